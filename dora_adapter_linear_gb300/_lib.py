@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora_gb300.so")
@@ -51,6 +51,36 @@ class LoraQkvShape(ctypes.Structure):
 
 class LoraAdapter(ctypes.Structure):
     _fields_ = [("A", c_void_p), ("B", c_void_p), ("s", c_float)]
+
+
+class LoraNormShape(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("D", c_int64), ("rows_per_gate", c_int64), ("ldx", c_int64), ("ldy", c_int64),
+                ("lddh", c_int64), ("lddz", c_int64), ("alpha", c_float), ("eps", c_float), ("w_offset", c_float),
+                ("post_norm", c_int32), ("dtype", c_int32)]
+
+
+LORA_ROTARY_HALF, LORA_ROTARY_INTERLEAVED = 0, 1
+
+
+class LoraRotaryShape(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("H", c_int64), ("head_dim", c_int64), ("rot_dim", c_int64), ("x_token", c_int64),
+                ("x_head", c_int64), ("y_token", c_int64), ("y_head", c_int64), ("scale", c_float),
+                ("layout", c_int32), ("pos_bits", c_int32), ("dtype", c_int32)]
+
+
+class LoraAdamwTensor(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("n", c_int64), ("lr_mul", c_float), ("weight_decay", c_float),
+                ("dtype", c_int32)]
+
+
+class LoraAdamwState(ctypes.Structure):
+    _fields_ = [("m", c_void_p), ("v", c_void_p), ("m_scale", c_void_p), ("v_scale", c_void_p),
+                ("master", c_void_p), ("ctl", c_void_p), ("bits", c_int32)]
+
+
+class LoraAdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("grad_scale", c_double), ("lr_device", c_void_p)]
 
 
 P = c_void_p
@@ -99,6 +129,17 @@ _SIGS = {
     "lora_qkv_fwd": (c_int, [POINTER(LoraQkvShape), P, P, POINTER(LoraAdapter), P, P, P, P, c_size_t, P]),
     "lora_qkv_bwd": (c_int, [POINTER(LoraQkvShape), P, P, POINTER(LoraAdapter), P, P, P, POINTER(c_void_p),
                              POINTER(c_void_p), P, P, c_size_t, P]),
+    "block_norm_fwd": (c_int, [POINTER(LoraNormShape), P, P, P, P, P, P, P, P, P, P]),
+    "block_norm_bwd_workspace_bytes": (c_size_t, [POINTER(LoraNormShape)]),
+    "block_norm_bwd": (c_int, [POINTER(LoraNormShape), P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P]),
+    "rotary_fwd": (c_int, [POINTER(LoraRotaryShape), P, P, P, P, P]),
+    "rotary_bwd": (c_int, [POINTER(LoraRotaryShape), P, P, P, P, P]),
+    "adamw_state_blocks": (c_int64, [POINTER(LoraAdamwTensor), c_int64]),
+    "adamw_norm_workspace_bytes": (c_size_t, [c_int64]),
+    "adamw_grad_norm": (c_int, [POINTER(LoraAdamwTensor), POINTER(c_void_p), c_int64, c_float, c_float, P, P,
+                                c_size_t, P]),
+    "adamw_step": (c_int, [POINTER(LoraAdamwTensor), POINTER(c_void_p), c_int64, POINTER(LoraAdamwState),
+                           POINTER(LoraAdamwHyper), P, P]),
     "lora_launch_count": (ctypes.c_uint64, []),
     "lora_prof_enable": (c_int, [c_int]),
     "lora_prof_gemm": (c_int, [POINTER(ctypes.c_double), POINTER(c_int64), POINTER(ctypes.c_double), c_int]),
@@ -387,3 +428,54 @@ def w8a8_lora_fwd_packed(M, d_in, d_out, r, Xcodes, sx, Wb, sw, Z, B, s, bias, Y
                                     ptr(B), float(s), ptr(bias), ptr(Y), ptr(acc_out), ptr(ws),
                                     0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
         "w8a8_lora_fwd_packed")
+
+
+def block_norm_fwd(sh, X, Y, w_pre, w_post, gate, Xout, H, r_pre, r_post, stream=None):
+    _ck(_lib().block_norm_fwd(ctypes.byref(sh), ptr(X), ptr(Y), ptr(w_pre), ptr(w_post), ptr(gate), ptr(Xout),
+                              ptr(H), ptr(r_pre), ptr(r_post), _stream(stream)), "block_norm_fwd")
+
+
+def block_norm_bwd_workspace_bytes(sh: LoraNormShape) -> int:
+    return _lib().block_norm_bwd_workspace_bytes(ctypes.byref(sh))
+
+
+def block_norm_bwd(sh, Xout, Y, w_pre, w_post, gate, r_pre, r_post, dH, dXout, dX, dY, dw_pre, dw_post, dgate, ws,
+                   stream=None):
+    _ck(_lib().block_norm_bwd(ctypes.byref(sh), ptr(Xout), ptr(Y), ptr(w_pre), ptr(w_post), ptr(gate), ptr(r_pre),
+                              ptr(r_post), ptr(dH), ptr(dXout), ptr(dX), ptr(dY), ptr(dw_pre), ptr(dw_post),
+                              ptr(dgate), ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                              _stream(stream)), "block_norm_bwd")
+
+
+def rotary_fwd(sh, X, pos, freq, Y, stream=None):
+    _ck(_lib().rotary_fwd(ctypes.byref(sh), ptr(X), ptr(pos), ptr(freq), ptr(Y), _stream(stream)), "rotary_fwd")
+
+
+def rotary_bwd(sh, dY, pos, freq, dX, stream=None):
+    _ck(_lib().rotary_bwd(ctypes.byref(sh), ptr(dY), ptr(pos), ptr(freq), ptr(dX), _stream(stream)), "rotary_bwd")
+
+
+def adamw_tensors(params, lr_mul, weight_decay):
+    """A ctypes array of lora_adamw_tensor for the tensors, with the factor and decay of each."""
+    return (LoraAdamwTensor * max(len(params), 1))(*[
+        LoraAdamwTensor(p.data_ptr(), p.numel(), a, d, dtype_code(p)) for p, a, d in zip(params, lr_mul, weight_decay)])
+
+
+def adamw_state_blocks(tensors, count) -> int:
+    return _lib().adamw_state_blocks(tensors, count)
+
+
+def adamw_norm_workspace_bytes(count) -> int:
+    return _lib().adamw_norm_workspace_bytes(count)
+
+
+def adamw_grad_norm(tensors, grads, count, grad_scale, max_norm, norm_coef, ws, stream=None):
+    """tensors: from adamw_tensors(); grads: a ctypes array of pointers."""
+    _ck(_lib().adamw_grad_norm(tensors, grads, count, float(grad_scale), float(max_norm), ptr(norm_coef), ptr(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+        "adamw_grad_norm")
+
+
+def adamw_step(tensors, grads, count, state, hyper, norm_coef, stream=None):
+    _ck(_lib().adamw_step(tensors, grads, count, ctypes.byref(state), ctypes.byref(hyper), ptr(norm_coef),
+                          _stream(stream)), "adamw_step")

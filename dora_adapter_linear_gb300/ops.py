@@ -5,6 +5,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .rotary import rotary_plan  # noqa: F401
 
 _WS = {}
 
@@ -396,3 +397,137 @@ def w8a8_lora_fwd_packed(Xc, sx, Wb, sw, Z, B, s, bias=None, want_acc=False, wan
     ws = workspace(L.w8a8_packed_workspace_bytes(M, d_out), Xc.device)
     L.w8a8_lora_fwd_packed(M, d_in, d_out, r, Xc, sx, Wb, sw, Z, B, s, bias, Y, acc, ws)
     return Y, acc
+
+
+def _row_stride(name, t, shape, X):
+    """The row stride of t: `shape` [M, D], X's dtype and device, rows of consecutive elements at
+    16-byte multiples (any row stride of at least D)."""
+    if tuple(t.shape) != shape or t.dtype != X.dtype or t.device != X.device:
+        raise ValueError(f"{name} must be a {shape} {X.dtype} tensor on {X.device}, got {tuple(t.shape)} {t.dtype} "
+                         f"on {t.device}")
+    if shape[0] <= 1:
+        ld = shape[1]
+    else:
+        ld = t.stride(0)
+    if (t.stride(1) != 1 and shape[1] > 1) or ld < shape[1]:
+        raise ValueError(f"{name} must have rows of consecutive elements that do not overlap, got strides {t.stride()}")
+    return ld
+
+
+def _need_cuda(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+
+
+def _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm):
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    M, D = X.shape
+    _check_vec("w_pre", w_pre, D, X, X.dtype)
+    _check_vec("w_post", w_post, D, X, X.dtype)
+    if w_post is not None and not post_norm:
+        raise ValueError("w_post needs post_norm=True")
+    if gate is not None:
+        if gate.dim() != 2 or (gate.shape[0] == 0 and M > 0):
+            raise ValueError("gate must be [rows, D]")
+        if rows_per_gate is None:
+            if gate.shape[0] and M % gate.shape[0]:
+                raise ValueError(f"{M} rows do not split evenly over {gate.shape[0]} gate rows: give rows_per_gate")
+            rows_per_gate = max(M // max(gate.shape[0], 1), 1)
+        if rows_per_gate < 1 or gate.shape[0] != -(-M // rows_per_gate):
+            raise ValueError(f"gate must have a row for every {rows_per_gate} of {M} rows, got {gate.shape[0]}")
+        _check_like("gate", gate, (gate.shape[0], D), X)
+    return L.LoraNormShape(M, D, rows_per_gate or 0, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0,
+                           L.dtype_code(X))
+
+
+def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=None, alpha=1.0, eps=1e-6,
+                   w_offset=0.0, pre_norm=True, post_norm=False):
+    """The end of one block and the start of the next: Xout = X + alpha gate o p with p the block
+    output Y, normed (RMS, weight w_post) first when post_norm, and H = the RMS norm of Xout (weight
+    w_pre) when pre_norm.  Weights are used as w + w_offset.  gate [G, D]: row i takes gate row
+    i // rows_per_gate (by default the rows split evenly over the gate's).  Returns
+    (Xout, H, r_pre, r_post); Xout is X when there is no Y, and what is not formed is None."""
+    sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
+    M, D = X.shape
+    if Y is None and (gate is not None or post_norm or not pre_norm):
+        raise ValueError("without a block output Y only the pre norm can be asked for")
+    if w_pre is not None and not pre_norm:
+        raise ValueError("w_pre needs pre_norm=True")
+    sh.ldx = _row_stride("X", X, (M, D), X)
+    if Y is not None:
+        sh.ldy = _row_stride("Y", Y, (M, D), X)
+    _need_cuda("X", X)
+    dev = X.device
+    Xout = torch.empty(M, D, dtype=X.dtype, device=dev) if Y is not None else None
+    H = torch.empty(M, D, dtype=X.dtype, device=dev) if pre_norm else None
+    r_pre = torch.empty(M, dtype=F32, device=dev) if pre_norm else None
+    r_post = torch.empty(M, dtype=F32, device=dev) if post_norm else None
+    L.block_norm_fwd(sh, X, Y, w_pre, w_post, gate, Xout, H, r_pre, r_post)
+    return X if Y is None else Xout, H, r_pre, r_post
+
+
+def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, gate=None, rows_per_gate=None,
+                   alpha=1.0, w_offset=0.0, post_norm=False, need_dx=True, need_dw=True, need_dgate=True):
+    """Gradients of block_norm_fwd from those of H (dH) and Xout (dXout; either may be None): returns
+    (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
+    and r_post."""
+    sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
+    M, D = Xout.shape
+    if dH is None and dXout is None:
+        raise ValueError("at least one of dH and dXout is needed")
+    if Y is None and (gate is not None or post_norm):
+        raise ValueError("a gate or post norm needs the block output Y")
+    _check_vec("r_pre", r_pre, M, Xout, F32)
+    _check_vec("r_post", r_post, M, Xout, F32)
+    if (dH is not None and r_pre is None) or (post_norm and r_post is None):
+        raise ValueError("r_pre (with dH) and r_post (with post_norm) come from the forward")
+    sh.ldx = _row_stride("Xout", Xout, (M, D), Xout)
+    for name, t, field in (("Y", Y, "ldy"), ("dH", dH, "lddh"), ("dXout", dXout, "lddz")):
+        if t is not None:
+            setattr(sh, field, _row_stride(name, t, (M, D), Xout))
+    _need_cuda("Xout", Xout)
+    dev = Xout.device
+    new = lambda: torch.empty(M, D, dtype=Xout.dtype, device=dev)  # noqa: E731
+    dX = new() if need_dx else None
+    dY = new() if Y is not None else None
+    dw_pre = torch.empty_like(w_pre) if need_dw and w_pre is not None else None
+    dw_post = torch.empty_like(w_post) if need_dw and w_post is not None else None
+    dgate = torch.empty_like(gate) if need_dgate and gate is not None else None
+    ws = workspace(L.block_norm_bwd_workspace_bytes(sh), dev)
+    L.block_norm_bwd(sh, Xout, Y, w_pre, w_post, gate, r_pre, r_post, dH, dXout, dX, dY, dw_pre, dw_post, dgate, ws)
+    return dX, dY, dw_pre, dw_post, dgate
+
+
+def _rotary(call, X, pos, plan, out):
+    if X.dim() != 3 or (X.stride(2) != 1 and X.shape[2] > 1):
+        raise ValueError(f"the heads must be a [tokens, heads, head_dim] tensor with consecutive elements in a head, "
+                         f"got {tuple(X.shape)} with strides {X.stride()}")
+    M, H, hd = X.shape
+    if pos.dtype not in (torch.int32, torch.int64) or tuple(pos.shape) != (M,) or not pos.is_contiguous():
+        raise ValueError(f"pos must be a contiguous [{M}] int32 or int64 tensor, got {tuple(pos.shape)} {pos.dtype}")
+    if pos.device != X.device or plan.freq.device != X.device:
+        raise ValueError(f"pos and the plan must be on {X.device}")
+    if plan.rot_dim > hd:
+        raise ValueError(f"the plan turns {plan.rot_dim} elements of a head, the heads have {hd}")
+    _need_cuda("X", X)
+    if out is None:
+        out = torch.empty(M, H, hd, dtype=X.dtype, device=X.device)
+    elif out.shape != X.shape or out.dtype != X.dtype or out.device != X.device or (out.stride(2) != 1 and hd > 1):
+        raise ValueError(f"out must be like the heads, {tuple(X.shape)} {X.dtype} on {X.device}")
+    sh = L.LoraRotaryShape(M, H, hd, plan.rot_dim, X.stride(0), X.stride(1), out.stride(0), out.stride(1), plan.scale,
+                           plan.layout, 8 * pos.element_size(), L.dtype_code(X))
+    call(sh, X, pos, plan.freq, out)
+    return out
+
+
+def rotary_fwd(X, pos, plan, out=None):
+    """Turns the heads X [tokens, heads, head_dim] (any token and head stride: the query and key heads
+    of a packed projection are one view) by their positions pos [tokens]; `plan` from rotary_plan.
+    out=X turns in place; by default a new contiguous tensor is returned."""
+    return _rotary(L.rotary_fwd, X, pos, plan, out)
+
+
+def rotary_bwd(dY, pos, plan, out=None):
+    """The gradient of rotary_fwd: the turn by the negative angle, with the same scale."""
+    return _rotary(L.rotary_bwd, dY, pos, plan, out)

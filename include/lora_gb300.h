@@ -5,7 +5,9 @@
  * without ever forming the dense update dW = B A or its gradient; the DoRA row-scale and
  * column-scale variants with their closed-form norms; a gated (SwiGLU / GeGLU) MLP built from
  * three such projections; a fused query/key/value projection with one adapter per leaf; and an
- * int8 (W8A8) base weight with a per-row dequant scale and a LoRA epilogue.
+ * int8 (W8A8) base weight with a per-row dequant scale and a LoRA epilogue.  Around it, for the
+ * adapter training step of a transformer block: the norms before and after a block with its gate
+ * and residual scale, rotary positions, and AdamW over all adapter tensors at once.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -16,8 +18,8 @@
  *  - dtype LORA_BF16: bf16 storage, fp32 accumulation, bf16 outputs/gradients.
  *    dtype LORA_F32: fp32 storage, fp32 FMA accumulation (no TF32), fp32 outputs.
  *  - s is the complete scale strength * alpha / r (the caller folds strength in).
- *  - Every pointer must be 16-byte aligned; d_in, d_out must be multiples of 8,
- *    r a multiple of 8 with 8 <= r <= 128 (LORA_BF16) or 1 <= r <= 128 (LORA_F32).
+ *  - Every pointer must be 16-byte aligned (the tensors of the rotary and AdamW calls: to their
+ *    element); d_in, d_out must be multiples of 8, r a multiple of 8 with 8 <= r <= 128 (LORA_BF16) or 1 <= r <= 128 (LORA_F32).
  *    M >= 0 (M == 0 is a no-op).  Violations return an error before anything is
  *    launched and leave every output untouched.
  *  - Work is enqueued asynchronously on `stream` (a cudaStream_t; NULL = legacy default
@@ -464,6 +466,126 @@ lora_status w8a8_lora_bwd(int64_t M, int64_t d_in, int64_t d_out, int64_t r, con
                           const float* sw, const void* A, const void* B, const void* Z_saved, const void* dY,
                           float s, void* dX, void* dA, void* dB, void* dbias, void* ws, size_t ws_bytes,
                           void* stream);
+
+/* ---------------------------------------------------------------- block norm
+ * The norms before and after a block of the model, fused with the block's gate and residual scale.
+ * Row i of M, D columns, gate row i / rows_per_gate, off = w_offset:
+ *   p = Y r_post (w_post + off), r_post = (mean(Y^2) + eps)^-1/2   (p = Y when post_norm is 0)
+ *   Xout = X + alpha gate o p
+ *   H = Xout r_pre (w_pre + off), r_pre = (mean(Xout^2) + eps)^-1/2
+ * Y is the output of the block that ends here, Xout the residual stream, H the input of the next
+ * block.  All sums and products are fp32; H is formed from Xout before its rounding.
+ *   X [M, D] (row stride ldx), Y [M, D] (ldy) or NULL (no block output yet: no Xout, gate or post
+ *   norm, H = norm of X); w_pre, w_post [D] or NULL (ones); gate [ceil(M / rows_per_gate), D] or
+ *   NULL (ones); Xout [M, D]; H [M, D] or NULL (no norm follows); r_pre, r_post [M] fp32 or NULL,
+ *   saved for the backward.  Xout may be X (ldx == D) and H may be Y (ldy == D); no other overlap.
+ *   dtype LORA_BF16 or LORA_F32 for every tensor but r_pre, r_post; D a multiple of 8; row strides
+ *   at least D and multiples of 16 bytes; eps > 0. */
+typedef struct {
+    int64_t M, D;
+    int64_t rows_per_gate;        /* rows that share a gate row: M one gate, 1 one for each row */
+    int64_t ldx, ldy, lddh, lddz; /* row strides of X (backward: Xout), Y, dH, dXout, in elements */
+    float alpha, eps, w_offset;
+    int32_t post_norm;            /* 1: Y is normed before the gate */
+    int32_t dtype;                /* lora_dtype */
+} lora_norm_shape;
+lora_status block_norm_fwd(const lora_norm_shape* sh, const void* X, const void* Y, const void* w_pre,
+                           const void* w_post, const void* gate, void* Xout, void* H, float* r_pre,
+                           float* r_post, void* stream);
+
+/* Bytes of workspace block_norm_bwd needs (0 on bad input). */
+size_t block_norm_bwd_workspace_bytes(const lora_norm_shape* sh);
+
+/* Backward of block_norm_fwd: dH (or NULL: no gradient through H) and dXout (or NULL: zero) are the
+ * gradients of its outputs.
+ *   dX, dY [M, D]; dw_pre, dw_post [D]; dgate as gate; each may be NULL.  dX may be the only one when
+ *   there was no Y.  The sums over rows are fp32 in a fixed order (the same bits call after call).
+ *   No output may overlap an input. */
+lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const void* Y, const void* w_pre,
+                           const void* w_post, const void* gate, const float* r_pre, const float* r_post,
+                           const void* dH, const void* dXout, void* dX, void* dY, void* dw_pre, void* dw_post,
+                           void* dgate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- rotary positions
+ * Pair j < rot_dim / 2 of each of the H heads of token i, (a, b), becomes
+ *   scale (a cos t - b sin t, b cos t + a sin t),  t = pos[i] theta_j;
+ * the rest of a head passes unchanged.  rotary_bwd applies the transpose (the turn by -t) to a
+ * gradient.  freq[j] = round(2^64 theta_j / (2 pi)) mod 2^64, a fraction of a turn per position, so
+ * the angle is exact for every position.
+ *   X, Y: element (i, h, c) at i * token stride + h * head stride + c, of dtype LORA_BF16 or
+ *   LORA_F32 and aligned to their element; a packed projection's query and key heads are one call.
+ *   Y == X (with equal strides) turns in place and leaves the rest of each head alone; otherwise X
+ *   and Y do not overlap, and no two elements of Y share an address.
+ *   pos [M] int32 or int64 (negative positions too); freq [rot_dim / 2], device memory. */
+typedef enum {
+    LORA_ROTARY_HALF = 0,         /* pairs (j, j + rot_dim / 2) */
+    LORA_ROTARY_INTERLEAVED = 1   /* pairs (2 j, 2 j + 1) */
+} lora_rotary_layout;
+typedef struct {
+    int64_t M, H, head_dim;
+    int64_t rot_dim;              /* even, 2 <= rot_dim <= head_dim <= 4096 */
+    int64_t x_token, x_head, y_token, y_head;   /* strides in elements */
+    float scale;
+    int32_t layout;               /* lora_rotary_layout */
+    int32_t pos_bits;             /* 32 or 64 */
+    int32_t dtype;                /* lora_dtype */
+} lora_rotary_shape;
+lora_status rotary_fwd(const lora_rotary_shape* sh, const void* X, const void* pos, const uint64_t* freq, void* Y,
+                       void* stream);
+lora_status rotary_bwd(const lora_rotary_shape* sh, const void* dY, const void* pos, const uint64_t* freq, void* dX,
+                       void* stream);
+
+/* ---------------------------------------------------------------- AdamW
+ * One step over a set of tensors, t = steps done + 1, g' = grad_scale * clip * g:
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,  lr_i = lr lr_mul_i,
+ *   p = p - lr_i weight_decay_i p - lr_i (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * `tensors` and `grads` are host arrays of `count` entries, read during the call.  p and grads[i] are
+ * contiguous device arrays of n elements of one dtype, aligned to their element (16-byte aligned
+ * ones are faster); grads[i] NULL leaves tensor i and its state as they are.  The state of all
+ * tensors is one array of 256-element blocks in the table's order; each tensor begins at a block of
+ * its own.  Zero it before the first step; what lies past a tensor's end stays zero. */
+typedef struct {
+    void* p;
+    int64_t n;
+    float lr_mul, weight_decay;
+    int32_t dtype;                /* lora_dtype of p and its gradient */
+} lora_adamw_tensor;
+/* bits 32: m, v fp32 [blocks, 256].  bits 8: m and sqrt(v) as e4m3 codes [blocks, 256], the value a
+ * code stands for times m_scale / v_scale [blocks] (absmax / 448 of the block); a sqrt(v) above zero
+ * keeps at least the smallest code.  master: fp32 [blocks, 256], the bf16 tensors' exact values (the
+ * caller fills it once), or NULL: bf16 tensors are updated from their rounded values.
+ * ctl: int32[2] {steps done, 0}, 8-byte aligned; the count moves on the device, so that a captured
+ * graph counts its replays.  m, v, scales and master 16-byte aligned. */
+typedef struct {
+    void *m, *v;
+    float *m_scale, *v_scale;
+    float* master;
+    int32_t* ctl;
+    int32_t bits;
+} lora_adamw_state;
+typedef struct {
+    double lr, beta1, beta2, eps, grad_scale;
+    const float* lr_device;       /* device scalar that replaces lr, or NULL */
+} lora_adamw_hyper;
+
+/* State blocks of the set: the sum of ceil(n / 256); -1 on bad input. */
+int64_t adamw_state_blocks(const lora_adamw_tensor* tensors, int64_t count);
+
+/* Bytes of workspace adamw_grad_norm needs for `count` tensors (0 on bad input). */
+size_t adamw_norm_workspace_bytes(int64_t count);
+
+/* norm_coef[0] = grad_scale |g| over the whole set, norm_coef[1] = grad_scale min(1, max_norm / (norm +
+ * 1e-6)), the factor for adamw_step (max_norm <= 0: grad_scale alone), NaN when the norm is not finite.
+ * Sums of squares in fp32 in a fixed order.  norm_coef: device float[2], 8-byte aligned. */
+lora_status adamw_grad_norm(const lora_adamw_tensor* tensors, const void* const* grads, int64_t count,
+                            float grad_scale, float max_norm, float* norm_coef, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* The step.  norm_coef: from adamw_grad_norm, or NULL: the factor is hyper->grad_scale.  When
+ * norm_coef[1] is not finite, parameters, state and step count stay as they are. */
+lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grads, int64_t count,
+                       const lora_adamw_state* state, const lora_adamw_hyper* hyper, const float* norm_coef,
+                       void* stream);
 
 /* Test hook for the bounded-wait machinery: launches one CTA that waits on an mbarrier
  * that nothing ever arrives on, with a limit of `timeout_us` microseconds; the kernel then
