@@ -10,6 +10,8 @@ import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora_gb300.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "lora_gb300.h")
@@ -136,10 +138,9 @@ _SIGS = {
     "rotary_bwd": (c_int, [POINTER(LoraRotaryShape), P, P, P, P, P]),
     "adamw_state_blocks": (c_int64, [POINTER(LoraAdamwTensor), c_int64]),
     "adamw_norm_workspace_bytes": (c_size_t, [c_int64]),
-    "adamw_grad_norm": (c_int, [POINTER(LoraAdamwTensor), POINTER(c_void_p), c_int64, c_float, c_float, P, P,
-                                c_size_t, P]),
-    "adamw_step": (c_int, [POINTER(LoraAdamwTensor), POINTER(c_void_p), c_int64, POINTER(LoraAdamwState),
-                           POINTER(LoraAdamwHyper), P, P]),
+    "adamw_grad_norm": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, c_float, c_float, P, P, c_size_t, P]),
+    "adamw_step": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, POINTER(LoraAdamwState), POINTER(LoraAdamwHyper), P,
+                           P]),
     "lora_launch_count": (ctypes.c_uint64, []),
     "lora_prof_enable": (c_int, [c_int]),
     "lora_prof_gemm": (c_int, [POINTER(ctypes.c_double), POINTER(c_int64), POINTER(ctypes.c_double), c_int]),
@@ -166,16 +167,21 @@ def _lib():
 
 def ptr(t):
     """Device pointer of a tensor (None -> NULL)."""
-    if t is None:
-        return None
-    return c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def current_stream(device=None) -> int:
+    """The handle of the device's current stream (by default the current device's), read without making
+    a Stream object, which alone would cost 3 us a call."""
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _stream(stream):
+    """The handle of `stream` (an int or a torch stream), by default that of the current stream."""
     if stream is not None:
-        return c_void_p(stream if isinstance(stream, int) else stream.cuda_stream)
-    import torch
-    return c_void_p(torch.cuda.current_stream().cuda_stream)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return current_stream()
 
 
 def _ck(status, where):
@@ -184,7 +190,6 @@ def _ck(status, where):
 
 
 def dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.bfloat16:
         return LORA_BF16
     if t.dtype == torch.float32:
@@ -470,7 +475,7 @@ def adamw_norm_workspace_bytes(count) -> int:
 
 
 def adamw_grad_norm(tensors, grads, count, grad_scale, max_norm, norm_coef, ws, stream=None):
-    """tensors: from adamw_tensors(); grads: a ctypes array of pointers."""
+    """tensors: from adamw_tensors(); grads: the address of an array of pointers, or a ctypes array."""
     _ck(_lib().adamw_grad_norm(tensors, grads, count, float(grad_scale), float(max_norm), ptr(norm_coef), ptr(ws),
                                0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
         "adamw_grad_norm")

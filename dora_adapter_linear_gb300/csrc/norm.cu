@@ -37,7 +37,15 @@ struct NormArgs {
   int parts;
   float *pw, *pp, *pg;          // partials [parts, D], [parts, D], [parts, 2, D]
   void *dw_pre, *dw_post, *dgate;
+  uint32_t* err;                // device error word and limit of the bounded waits
+  uint64_t timeout_ns;
 };
+
+// threads of a CTA that takes one row
+int row_threads(int64_t D) {
+  const int64_t n = (D / 8 + 31) / 32 * 32;
+  return (int)(n > 1024 ? 1024 : n);
+}
 
 template <typename T>
 __device__ __forceinline__ void weight8(const void* w, int64_t c, float off, float (&f)[8]) {
@@ -62,6 +70,22 @@ __device__ __forceinline__ void gate8(const NormArgs& a, const T* gate, int64_t 
     for (int i = 0; i < 8; ++i) g[i] = a.alpha;
   }
 }
+
+template <typename T>
+__device__ __forceinline__ void weight4x2(const void* w, int64_t c, float off, F2 (&f)[4]) {
+  if (w) load4x2(static_cast<const T*>(w) + c, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = w ? add2(f[i], f2(off)) : f2(1.f);
+}
+template <typename T>
+__device__ __forceinline__ void gate4x2(const T* gate, int64_t c, float alpha, F2 (&g)[4]) {
+  if (gate) load4x2(gate + c, g);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = gate ? mul2(g[i], f2(alpha)) : f2(alpha);
+}
+
+// what a launch has of a block output: none, one, one behind a post norm, or either of the last two
+enum { NO_Y = 0, PLAIN_Y = 1, POST_Y = 2, ANY_Y = 3 };
 
 // ------------------------------------------------------------------ forward, one CTA per row
 // The row is read again for each of its steps (it is in L1 or L2 by then), so D has no limit.
@@ -128,6 +152,288 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
       store8(static_cast<T*>(a.h_out) + row * a.D + c, v);
     }
   }
+}
+
+// ------------------------------------------------------------------ forward, the row in registers
+// A thread holds K vectors of 8 columns, so x and y are read once and all their loads are in flight
+// together.  G threads share a row: a whole CTA, or a warp with 8 rows a CTA.
+// The post norm would put a second block sum in the row's way, behind the first.  With q = alpha g w_p o y
+// the sum of z^2 is sum x^2 + 2 r_y sum x q + r_y^2 sum q^2, so one block sum of four values serves both
+// norms; a row where those terms cancel to less than a quarter of their size (their rounding would be
+// more than four times that of the plain sum) takes the plain sum after all.
+template <typename T, int K, bool WARP, int Y>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const NormArgs a) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  __shared__ __align__(16) float red[WARP ? 1 : 2 * 4 * 32];
+  const int t = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x, D = (int)a.D;
+  const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= a.M) return;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* y = Y ? static_cast<const T*>(a.y) + row * a.ldy : nullptr;
+  const T* gate = Y && a.gate ? static_cast<const T*>(a.gate) + row / a.rpg * D : nullptr;
+  const auto col = [&](int k) { return (k * group + t) * 8; };
+  Raw8<T> xr[K], yr[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (col(k) >= D) continue;
+    if (Y) stream8(y + col(k), yr[k]);
+    stream8(x + col(k), xr[k]);
+  }
+  auto row_sums = [&](float (&v)[4], int flip) {
+    if (WARP) spread<4>(warp_sums_of<4>(v), v);
+    else block_sums_of<4, 32>(v, red, flip);
+  };
+  F2 q[K][4], p[4], w[4];   // q: what r_y times is added to x; later z
+  F2 xx = f2(0.f), xq = f2(0.f), qq = f2(0.f), yy = f2(0.f);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (col(k) >= D) continue;
+    xr[k].get(w);
+    if (!Y) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[k][i] = w[i];
+        xx = fma2(w[i], w[i], xx);
+      }
+      continue;
+    }
+    yr[k].get(q[k]);
+    if (Y == POST_Y) {
+      weight4x2<T>(a.w_post, col(k), a.off, p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        yy = fma2(q[k][i], q[k][i], yy);
+        q[k][i] = mul2(q[k][i], p[i]);
+      }
+    }
+    gate4x2<T>(gate, col(k), a.alpha, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (Y == POST_Y) {
+        q[k][i] = mul2(q[k][i], p[i]);
+        xx = fma2(w[i], w[i], xx);
+        xq = fma2(w[i], q[k][i], xq);
+        qq = fma2(q[k][i], q[k][i], qq);
+      } else {
+        q[k][i] = fma2(p[i], q[k][i], w[i]);
+        xx = fma2(q[k][i], q[k][i], xx);
+      }
+    }
+    if (Y == PLAIN_Y) store4x2(static_cast<T*>(a.z_out) + row * D + col(k), q[k]);
+  }
+  if (Y != POST_Y && !a.h_out) return;
+  float s[4] = {sum2(xx), sum2(xq), sum2(qq), sum2(yy)};
+  row_sums(s, 0);
+  float zz = s[0];
+  if (Y == POST_Y) {
+    const float r_y = rsqrtf(s[3] / (float)D + a.eps), size = fmaf(r_y * r_y, s[2], s[0]);
+    if (t == 0 && a.r_post) a.r_post[row] = r_y;
+    xx = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (col(k) >= D) continue;
+      xr[k].get(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[k][i] = fma2(f2(r_y), q[k][i], w[i]);
+        xx = fma2(q[k][i], q[k][i], xx);
+      }
+      store4x2(static_cast<T*>(a.z_out) + row * D + col(k), q[k]);
+    }
+    if (!a.h_out) return;
+    zz = fmaf(2.f * r_y, s[1], size);
+    if (!(zz >= 0.25f * size)) {   // the same for the whole row
+      s[0] = sum2(xx), s[1] = s[2] = s[3] = 0.f;
+      row_sums(s, 1);
+      zz = s[0];
+    }
+  }
+  const float r_z = rsqrtf(zz / (float)D + a.eps);
+  if (t == 0 && a.r_pre) a.r_pre[row] = r_z;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (col(k) >= D) continue;
+    weight4x2<T>(a.w_pre, col(k), a.off, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = mul2(q[k][i], mul2(w[i], f2(r_z)));
+    store4x2(static_cast<T*>(a.h_out) + row * D + col(k), w);
+  }
+}
+
+template <typename T, int K, bool WARP>
+cudaError_t launch_held(const NormArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)(WARP ? (a.M + 7) / 8 : a.M));
+  const dim3 cta((unsigned)(WARP ? 256 : (a.D / 8 + 32 * K - 1) / (32 * K) * 32));
+  if (!a.y) return launch_pdl(norm_fwd_held_kernel<T, K, WARP, NO_Y>, grid, cta, 0, st, a);
+  if (!a.post) return launch_pdl(norm_fwd_held_kernel<T, K, WARP, PLAIN_Y>, grid, cta, 0, st, a);
+  return launch_pdl(norm_fwd_held_kernel<T, K, WARP, POST_Y>, grid, cta, 0, st, a);
+}
+
+// ------------------------------------------------------------------ forward with a post norm, many rows
+// A CTA walks over every gridDim-th row with the weights in registers, two vectors a thread, the sums as
+// above.  Each thread keeps its own columns of the next row (x, y and, with a gate row per row, the gate)
+// on their way into shared memory: no thread reads another's, so the copies need no barrier.  bf16, 16384 x
+// 4096: 83 us (85 with a gate per sequence, 107 per row; floors 79, 79, 99) against 87 (101, 140) of the held
+// kernel, which loads and unpacks the weights for every row.  Two rows of a CTA in flight are faster than
+// three or four (83 against 94 and 96 us) and neighbouring rows at a time than a part of its own for each CTA.
+constexpr int kWalkThreads = 512;   // an SM's, at 128 registers
+
+template <typename T, bool TOKEN>
+__global__ void __launch_bounds__(kWalkThreads) norm_fwd_walk_kernel(const NormArgs a) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  constexpr int A = TOKEN ? 3 : 2, K = 2, S = 2;   // arrays of a stage, vectors of a thread, stages
+  extern __shared__ __align__(16) char stages[];
+  __shared__ __align__(16) float red[2 * 4 * 16];
+  const int D = (int)a.D, c0 = (int)threadIdx.x * 8, hop = (int)blockDim.x * 8;   // columns c0 + k hop
+  const int64_t r0 = blockIdx.x, stride = gridDim.x;
+  const T* gate = static_cast<const T*>(a.gate);
+  T* const ring = reinterpret_cast<T*>(stages) + c0;
+  T *fill = ring, *use = ring, *const ring_end = ring + S * A * D;
+  // what moves from row to row is a pointer that is stepped
+  const T* src[A];
+  src[0] = static_cast<const T*>(a.x) + r0 * a.ldx + c0;
+  src[1] = static_cast<const T*>(a.y) + r0 * a.ldy + c0;
+  if (TOKEN) src[A - 1] = gate + r0 * D + c0;
+  auto issue = [&](bool more) {   // this thread's columns of the next row; a group even past the end
+    if (more) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (c0 + k * hop >= D) continue;
+#pragma unroll
+        for (int i = 0; i < A; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; e += 16 / (int)sizeof(T)) cp_async16(fill + i * D + k * hop + e, src[i] + k * hop + e, true);
+      }
+      src[0] += stride * a.ldx;
+      src[1] += stride * a.ldy;
+      if (TOKEN) src[A - 1] += stride * D;
+    }
+    cp_async_commit();
+    fill += A * D;
+    if (fill == ring_end) fill = ring;
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(r0 + i * stride < a.M);
+  F2 wz[K][4], u[K][4];   // u = alpha g w_p (TOKEN: alpha w_p)
+  auto group_weights = [&](const T* g) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (c0 + k * hop >= D) continue;
+      F2 w[4];
+      gate4x2<T>(g, c0 + k * hop, a.alpha, w);
+      weight4x2<T>(a.w_post, c0 + k * hop, a.off, u[k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], w[i]);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (c0 + k * hop < D) weight4x2<T>(a.w_pre, c0 + k * hop, a.off, wz[k]);
+  if (TOKEN || !gate) group_weights(nullptr);
+  const float inv_d = 1.f / (float)D;
+  T* zo = static_cast<T*>(a.z_out) + r0 * D + c0;
+  T* ho = a.h_out ? static_cast<T*>(a.h_out) + r0 * D + c0 : nullptr;
+  int64_t grp = -1;
+  int flip = 0;
+  for (int64_t row = r0; row < a.M; row += stride) {
+    if (!TOKEN && gate && row >= (grp + 1) * a.rpg) {   // uniform over the CTA
+      grp = row / a.rpg;
+      group_weights(gate + grp * D);
+    }
+    issue(row + (S - 1) * stride < a.M);   // into the stage that the last row left
+    cp_async_wait<S - 1>();
+    F2 x[K][4], q[K][4], g[4], xx = f2(0.f), xq = f2(0.f), qq = f2(0.f), yy = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (c0 + k * hop >= D) continue;
+      load4x2(use + k * hop, x[k]);
+      load4x2(use + D + k * hop, q[k]);
+      if (TOKEN) load4x2(use + 2 * D + k * hop, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        yy = fma2(q[k][i], q[k][i], yy);
+        q[k][i] = mul2(q[k][i], TOKEN ? mul2(u[k][i], g[i]) : u[k][i]);
+        xx = fma2(x[k][i], x[k][i], xx);
+        xq = fma2(x[k][i], q[k][i], xq);
+        qq = fma2(q[k][i], q[k][i], qq);
+      }
+    }
+    use += A * D;
+    if (use == ring_end) use = ring;
+    float s[4] = {sum2(xx), sum2(xq), sum2(qq), sum2(yy)};
+    block_sums_of<4, 16>(s, red, flip);
+    flip ^= 1;
+    const float r_y = rsqrtf(fmaf(s[3], inv_d, a.eps)), size = fmaf(r_y * r_y, s[2], s[0]);
+    if (threadIdx.x == 0 && a.r_post) a.r_post[row] = r_y;
+    xx = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (c0 + k * hop >= D) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[k][i] = fma2(f2(r_y), q[k][i], x[k][i]);
+        xx = fma2(x[k][i], x[k][i], xx);
+      }
+      store4x2(zo + k * hop, x[k]);
+    }
+    zo += stride * D;
+    if (!ho) continue;
+    float zz = fmaf(2.f * r_y, s[1], size);
+    if (!(zz >= 0.25f * size)) {   // the same for the whole row
+      s[0] = sum2(xx), s[1] = s[2] = s[3] = 0.f;
+      block_sums_of<4, 16>(s, red, flip);
+      flip ^= 1;
+      zz = s[0];
+    }
+    const float r_z = rsqrtf(fmaf(zz, inv_d, a.eps));
+    if (threadIdx.x == 0 && a.r_pre) a.r_pre[row] = r_z;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (c0 + k * hop >= D) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k][i] = mul2(x[k][i], mul2(wz[k][i], f2(r_z)));
+      store4x2(ho + k * hop, x[k]);
+    }
+    ho += stride * D;
+  }
+}
+
+template <typename T>
+cudaError_t launch_walk(const NormArgs& a, cudaStream_t st) {
+  const int threads = (int)((a.D / 8 + 63) / 64 * 32);
+  const int64_t most = (int64_t)(kWalkThreads / threads) * num_sms_current();
+  const bool token = a.gate && a.rpg == 1;
+  const size_t smem = 2 * (size_t)(token ? 3 : 2) * a.D * sizeof(T);   // at most 96 KB
+  auto go = [&](auto kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)(a.M < most ? a.M : most)), dim3((unsigned)threads), smem, st, a);
+  };
+  return token ? go(norm_fwd_walk_kernel<T, true>) : go(norm_fwd_walk_kernel<T, false>);
+}
+
+// Rows that are all resident at once (half the threads of the SMs) want the shortest chain: one vector a
+// thread (1 x 4096 bf16: 2.4 against 2.7 us with two; at 512 rows 5.7 against 4.7).  Beyond that:
+//   up to 256 columns a warp a row (16384 x 256 bf16: 7.6 us), for bf16 up to 512 (16384 x 512 without a post
+//   norm: 12.5 against 17 us);
+//   bf16 with a post norm the walk from 512 to 8192 columns (16384 x 512: 11.5 against 12.5 us with a warp a
+//   row, x 2048: 43 against 47, x 8192: 85 per 8192 rows against 97);
+//   fp32 one vector up to 2048 columns (8192 x 1024: 20 us against 21 with the walk and 28 with two vectors),
+//   then two (8192 x 4096: 86 against 94 with one or the walk);
+//   bf16 without a post norm two vectors (16384 x 4096: 79 us, the floor).
+template <typename T>
+cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
+  constexpr bool narrow = sizeof(T) == 2;
+  const int64_t vecs = a.D / 8;
+  if (vecs <= 32) return launch_held<T, 1, true>(a, st);
+  if (narrow && vecs < 64 + !(a.y && a.post)) return launch_held<T, 2, true>(a, st);
+  if (vecs <= 1024 && a.M * vecs <= 1024LL * num_sms_current()) return launch_held<T, 1, false>(a, st);
+  if (narrow && a.y && a.post && vecs >= 64 && vecs <= 1024) return launch_walk<bf16>(a, st);
+  if (!narrow && vecs <= 256) return launch_held<T, 1, false>(a, st);
+  if (vecs <= 2048) return launch_held<T, 2, false>(a, st);
+  return launch_pdl(norm_fwd_kernel<T>, dim3((unsigned)a.M), dim3((unsigned)row_threads(a.D)), 0, st, a);
 }
 
 // ------------------------------------------------------------------ backward, rows: dx, dy, c
@@ -293,51 +599,321 @@ __global__ void __launch_bounds__(32 * kColWarps) norm_bwd_cols_kernel(const Nor
   }
 }
 
-// ------------------------------------------------------------------ backward: sums of the partials
-// CTA (t, j): columns 32 t .. 32 t + 31, one per lane; the warps share the parts.  j = 0: dw_pre,
-// 1: dw_post, 2 + k: the gate row that crosses the boundary before part k + 1, if that is its first.
-template <typename T>
-__global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(const NormArgs a) {
+// ------------------------------------------------------------------ backward in one pass
+// One CTA takes the rows of a part in order, a thread always the same 8 columns: the column sums stay
+// in its registers for the whole part, the weights too, and every input is read once.  The rows
+// arrive by bulk copies in a ring of stages (z, y, dh, dz_in and, with a gate row per row, the gate).
+// A row's stage is refilled after the next row's barrier: no thread can still be reading it then.
+// While the gate row stays the same only N = sum dz y r_y is kept: dw_post += alpha g N and dgate =
+// alpha w_p N at the segment's end (the segments and their partials as in the column kernel above).
+struct RingPlan {
+  int threads, stages, ctas;          // ctas: per SM
+  int vectors, rows;                  // of 8 columns a thread, and rows a barrier
+  uint32_t row_bytes, stage_bytes;
+};
+constexpr int kMaxStages = 6, kRingThreads = 512;   // 16384 x 4096 bf16: 4 stages 172 us, 6 and more 128
+constexpr int kSmSmem = 227 * 1024, kRingStatic = 3 * 1024;   // of an SM; a CTA's share beside its ring
+
+// FULL: both gradients come in and dx and dy go out, so nothing of that is asked in the loop (126
+// against 140 us at 16384 x 4096 bf16).
+// K vectors of 8 columns a thread, R rows a barrier.
+template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
+__global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormArgs a, const RingPlan pl) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  __shared__ float acc[32][33];
+  constexpr int N = R == 1 ? 4 : 8;   // three sums a row, rounded up
+  constexpr bool HAS_Y = Y != NO_Y;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ __align__(16) float red[2 * 16 * N];
+  __shared__ int abort_flag;
+  const int part = blockIdx.x, S = pl.stages;
+  const int64_t r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
+  const bool post = Y == POST_Y || (Y == ANY_Y && a.post);
+  const bool has_dh = FULL || a.dh, has_dzi = FULL || a.dzi, has_dx = FULL || a.dx, has_dy = FULL || a.dy;
+  const T* gate = static_cast<const T*>(a.gate);
+
+  auto issue = [&](int64_t row, int s) {   // thread 0: the row's copies into stage s
+    if (row >= r1) return;
+    char* dst = ring + (size_t)s * pl.stage_bytes;
+    mbar_expect_tx(&full[s], pl.stage_bytes);
+    auto copy = [&](const void* src, int64_t ld) {
+      bulk_load(dst, static_cast<const T*>(src) + row * ld, pl.row_bytes, &full[s]);
+      dst += pl.row_bytes;
+    };
+    copy(a.x, a.ldx);
+    if (has_dh) copy(a.dh, a.ldh);
+    if (has_dzi) copy(a.dzi, a.ldo);
+    if (HAS_Y) copy(a.y, a.ldy);
+    if (TOKEN) copy(a.gate, a.D);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    mbar_fence_init();
+    abort_flag = 0;
+    for (int i = 0; i < S; ++i) issue(r0 + i, i);
+  }
+  __syncthreads();
+
+  // column of this thread's k-th vector; past D nothing is read or written
+  const auto col = [&](int k) { return (k * (int)blockDim.x + (int)threadIdx.x) * 8; };
+  const int D = (int)a.D;
+  F2 wz[K][4], u[K][4], dw[K][4], acc[K][4];   // u = alpha g w_p (TOKEN: alpha w_p); acc: N (TOKEN: dw_post)
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[k][i] = acc[k][i] = wz[k][i] = u[k][i] = f2(0.f);
+    if (col(k) >= D) continue;
+    weight4x2<T>(a.w_pre, col(k), a.off, wz[k]);
+    if (TOKEN) {
+      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, u[k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], f2(a.alpha));
+    }
+  }
+  auto begin_segment = [&](int64_t grp) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (col(k) >= D) continue;
+      F2 w[4];
+      gate4x2<T>(gate ? gate + grp * D : nullptr, col(k), a.alpha, u[k]);
+      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], w[i]);
+    }
+  };
+  auto end_segment = [&](int64_t seg0, int64_t grp) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (col(k) >= D) continue;
+      F2 w[4];
+      if (a.dgate) {
+        weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(w[i], f2(a.alpha)), acc[k][i]);
+        const int64_t g0 = grp * a.rpg, g1 = min(a.M, g0 + a.rpg);
+        if (g0 >= r0 && g1 <= r1) store4x2(static_cast<T*>(a.dgate) + grp * D + col(k), w);
+        else store4x2(a.pg + ((int64_t)part * 2 + (seg0 == r0 ? 0 : 1)) * D + col(k), w);
+      }
+      if (a.pp) {   // the part's own partial sum grows by a segment; no one else touches it
+        float* pp = a.pp + (int64_t)part * D + col(k);
+        F2 sum[4];
+        if (seg0 != r0) load4x2(pp, sum);
+        gate4x2<T>(gate ? gate + grp * D : nullptr, col(k), a.alpha, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = fma2(w[i], acc[k][i], seg0 != r0 ? sum[i] : f2(0.f));
+        store4x2(pp, sum);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[k][i] = f2(0.f);
+    }
+  };
+
+  // the arrays of a stage, in the order of the copies
+  const int at_o = 1 + has_dh, at_y = at_o + has_dzi;
+  const float inv_d = 1.f / (float)D;
+  float r_z[R], r_y[R], r_z2[R], r_y2[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t at = min(r0 + r, r1 - 1);
+    r_z2[r] = has_dh ? a.r_pre[at] : 0.f;
+    r_y2[r] = post ? a.r_post[at] : 1.f;
+  }
+  int s = 0, flip = 0, refill = 0;   // refill (thread 0): the stage of the next row to ask for, `next`
+  uint32_t parity = 0;
+  int64_t next = r0 + S;
+  int64_t row = r0, seg0 = r0, seg_end = r0, grp = 0;
+  int rows = 0;
+  for (; row < r1; row += rows) {
+    if (HAS_Y && !TOKEN && row == seg_end) {   // uniform over the CTA
+      if (row > r0) end_segment(seg0, grp);
+      grp = row / a.rpg;
+      seg0 = row;
+      seg_end = min(r1, (grp + 1) * a.rpg);
+      begin_segment(grp);
+    }
+    rows = (int)min((int64_t)R, (HAS_Y && !TOKEN ? seg_end : r1) - row);
+    bool bad = false;
+    float sums[N];   // of row r at 3 r: S1, S2, S3 of the row kernel above
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[i] = 0.f;
+    F2 z[4], t[R][4], y[4], g[4];
+    const T* st[R] = {};
+    // z, t = dz_in + r_z w_z dh and y of a vector; the first time also what the sums need of dh
+    auto load_zty = [&](int r, int k, F2* s0) {
+      load4x2(st[r] + col(k), z);
+      if (has_dzi) load4x2(st[r] + at_o * D + col(k), t[r]);
+      if (has_dh) {
+        F2 h[4];
+        load4x2(st[r] + D + col(k), h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 rh = mul2(h[i], f2(r_z[r])), wh = mul2(rh, wz[k][i]);
+          if (s0) {
+            *s0 = fma2(wh, z[i], *s0);
+            dw[k][i] = fma2(rh, z[i], dw[k][i]);
+          }
+          t[r][i] = has_dzi ? add2(t[r][i], wh) : wh;
+        }
+      }
+      if (HAS_Y) load4x2(st[r] + at_y * D + col(k), y);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      r_z[r] = r_z2[r], r_y[r] = r_y2[r];
+      const int64_t at = min(row + rows + r, r1 - 1);
+      r_z2[r] = has_dh ? a.r_pre[at] : 0.f;
+      r_y2[r] = post ? a.r_post[at] : 1.f;
+      const int sr = s + r < S ? s + r : s + r - S;
+      st[r] = reinterpret_cast<const T*>(ring + (size_t)sr * pl.stage_bytes);
+      if (r >= rows) continue;
+      bad |= !mbar_wait(&full[sr], s + r < S ? parity : parity ^ 1, a.timeout_ns, &abort_flag, a.err, 40);
+      if (bad) continue;
+      F2 s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (col(k) >= D) continue;
+        load_zty(r, k, &s0);
+        if (!post) continue;
+        if (TOKEN) load4x2(st[r] + (at_y + 1) * D + col(k), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 uy = mul2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], y[i]);
+          s1 = fma2(uy, t[r][i], s1);
+          s2 = fma2(uy, z[i], s2);
+        }
+      }
+      sums[3 * r] = sum2(s0);
+      sums[3 * r + 1] = sum2(s1);
+      sums[3 * r + 2] = sum2(s2);
+    }
+    if (block_sums_of<N, 16>(sums, red, flip, bad)) break;
+    flip ^= 1;
+    if (threadIdx.x == 0)   // the stages of all rows before `row` are free now
+      for (; next < row + S; ++next) {
+        issue(next, refill);
+        refill = refill + 1 < S ? refill + 1 : 0;
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rows) continue;
+      // s0 was summed over r_z w_z dh z
+      const float cz = r_z[r] * r_z[r] * (sums[3 * r] * inv_d);
+      const float cy = post ? r_y[r] * r_y[r] * r_y[r] * ((sums[3 * r + 1] - cz * sums[3 * r + 2]) * inv_d) : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (col(k) >= D) continue;
+        if (K > 1) {
+          load_zty(r, k, nullptr);
+        } else if (R > 1) {   // t stays in registers, z and y come from the stage again
+          load4x2(st[r] + col(k), z);
+          if (HAS_Y) load4x2(st[r] + at_y * D + col(k), y);
+        }
+        const int64_t at = (row + r) * D + col(k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[r][i] = fma2(f2(-cz), z[i], t[r][i]);
+        if (has_dx) store4x2(static_cast<T*>(a.dx) + at, t[r]);
+        if (!HAS_Y) continue;
+        if (TOKEN) load4x2(st[r] + (at_y + 1) * D + col(k), g);
+        if (TOKEN && a.dgate_rows) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = mul2(u[k][i], mul2(mul2(t[r][i], f2(r_y[r])), y[i]));
+          store4x2(static_cast<T*>(a.dgate_rows) + at, z);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 e = mul2(t[r][i], f2(r_y[r]));
+          if (TOKEN) acc[k][i] = fma2(mul2(mul2(g[i], f2(a.alpha)), e), y[i], acc[k][i]);
+          else acc[k][i] = fma2(e, y[i], acc[k][i]);
+          y[i] = fma2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], e, mul2(f2(-cy), y[i]));
+        }
+        if (has_dy) store4x2(static_cast<T*>(a.dy) + at, y);
+      }
+    }
+    s += rows;
+    if (s >= S) {
+      s -= S;
+      parity ^= 1;
+    }
+  }
+  if (row < r1) {   // a wait ran out (every thread is here): let the copies in flight land, then leave
+    if (threadIdx.x == 0)
+      for (int64_t k = row; k < min(r1, next); ++k)
+        mbar_wait_drain(&full[(k - r0) % S], (uint32_t)((k - r0) / S) & 1, 100000000ull);
+    return;
+  }
+  if (HAS_Y && !TOKEN) end_segment(seg0, grp);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (col(k) >= D) continue;
+    if (a.pw) store4x2(a.pw + (int64_t)part * D + col(k), dw[k]);
+    if (TOKEN && a.pp) store4x2(a.pp + (int64_t)part * D + col(k), acc[k]);
+  }
+}
+
+// ------------------------------------------------------------------ backward: sums of the partials
+// CTA (t, j): columns 32 t .. 32 t + 31, one per lane.  j = 0: dw_pre, 1: dw_post, the warps sharing
+// the parts.  Past that the gate rows that more than one part has rows of: with few gate rows one a
+// CTA, its parts shared by the warps; with as many as there are boundaries between parts, a warp takes
+// the gate row that crosses a boundary (it has few parts then), if that boundary is its first.
+constexpr int kFinishWarps = 32;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kFinishWarps) norm_bwd_finish_kernel(const NormArgs a, const int gate_rows) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  __shared__ float acc[kFinishWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
-  const int job = blockIdx.y;
-  int first = 0, last = a.parts - 1;
-  T* out = nullptr;
-  int64_t grp = 0;
-  if (job == 0) out = static_cast<T*>(a.dw_pre);
-  else if (job == 1) out = static_cast<T*>(a.dw_post);
-  else if (a.dgate) {
-    const int64_t b = (int64_t)(job - 1) * a.rp;   // the boundary's row
-    grp = b / a.rpg;
+  const int job = (int)blockIdx.y - 2;
+  // partials first, first + step, .. last of this warp; slot(p) is where part p keeps this sum
+  auto add = [&](int first, int last, int step, auto slot) {
+    float t = 0.f;
+    if (col < a.D)
+#pragma unroll 16
+      for (int p = first; p <= last; p += step) t += slot(p)[col];
+    return t;
+  };
+  auto parts_of = [&](int64_t grp, int& first, int& last) {
     const int64_t g0 = grp * a.rpg, g1 = min(a.M, g0 + a.rpg);
     first = (int)(g0 / a.rp);
     last = (int)((g1 - 1) / a.rp);
-    if (g0 < b && first == job - 2) out = static_cast<T*>(a.dgate) + grp * a.D;
-  }
-  if (!out) return;
-  float t = 0.f;
-  if (col < a.D) {
-    for (int p = first + warp; p <= last; p += 32) {
-      if (job == 0) t += a.pw[p * a.D + col];
-      else if (job == 1) t += a.pp[p * a.D + col];
-      else t += a.pg[((int64_t)p * 2 + ((int64_t)p * a.rp / a.rpg == grp ? 0 : 1)) * a.D + col];
-    }
+  };
+  auto gate_slot = [&](int64_t grp) {
+    return [&a, grp](int p) { return a.pg + ((int64_t)p * 2 + ((int64_t)p * a.rp / a.rpg == grp ? 0 : 1)) * a.D; };
+  };
+  T* out;
+  float t;
+  if (job < 0) {
+    const float* src = job == -2 ? a.pw : a.pp;
+    out = static_cast<T*>(job == -2 ? a.dw_pre : a.dw_post);
+    if (!out) return;
+    t = add(warp, a.parts - 1, kFinishWarps, [&](int p) { return src + (int64_t)p * a.D; });
+  } else if (gate_rows) {
+    int first, last;
+    parts_of(job, first, last);
+    if (first == last) return;   // written by its one part
+    out = static_cast<T*>(a.dgate) + (int64_t)job * a.D;
+    t = add(first + warp, last, kFinishWarps, gate_slot(job));
+  } else {
+    const int p = job * kFinishWarps + warp + 1;   // the boundary before part p
+    if (p >= a.parts) return;
+    int first, last;
+    const int64_t grp = (int64_t)p * a.rp / a.rpg;
+    parts_of(grp, first, last);
+    if (grp * a.rpg >= (int64_t)p * a.rp || first != p - 1) return;
+    t = add(first, last, 1, gate_slot(grp));
+    if (col < a.D) static_cast<T*>(a.dgate)[grp * a.D + col] = from_f<T>(t);
+    return;
   }
   acc[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && col < a.D) {
     t = 0.f;
-    for (int w = 0; w < 32; ++w) t += acc[w][lane];
+#pragma unroll
+    for (int w = 0; w < kFinishWarps; ++w) t += acc[w][lane];
     out[col] = from_f<T>(t);
   }
-}
-
-int row_threads(int64_t D) {
-  const int64_t n = (D / 8 + 31) / 32 * 32;
-  return (int)(n > 1024 ? 1024 : n);
 }
 
 lora_status check_norm(const lora_norm_shape* sh) {
@@ -355,11 +931,40 @@ lora_status check_norm(const lora_norm_shape* sh) {
   return LORA_OK;
 }
 
-// Row parts of the column sums: two CTAs per SM over all column tiles, at least 32 rows each.
-void norm_parts(const lora_norm_shape& sh, int64_t* rp, int* parts) {
-  const int64_t tiles = (sh.D + 255) / 256;
-  int64_t want = (4LL * num_sms_current() + tiles - 1) / tiles;
-  if (want > (sh.M + 31) / 32) want = (sh.M + 31) / 32;
+// Ring plan of the one-pass backward with n input rows a row, or threads == 0 where no variant holds
+// them: those take the row and column kernels.  Small rows get several CTAs an SM (the 128 registers a
+// thread allow 512 threads).  Two rows a barrier take four stages, one row three.
+RingPlan ring_plan(const lora_norm_shape& sh, int n) {
+  RingPlan p = {};
+  const int64_t es = sh.dtype == LORA_BF16 ? 2 : 4, vecs = sh.D / 8, stage = n * sh.D * es;
+  p.vectors = vecs <= kRingThreads ? 1 : 2;
+  const int64_t threads = (vecs + 32 * p.vectors - 1) / (32 * p.vectors) * 32;
+  if (threads > kRingThreads) return RingPlan{};
+  const auto budget = [](int ctas) { return (int64_t)(kSmSmem / ctas - kRingStatic); };
+  p.ctas = (int)(kRingThreads / threads < 16 ? kRingThreads / threads : 16);
+  while (p.ctas > 1 && 4 * stage > budget(p.ctas)) --p.ctas;
+  const int64_t fit = budget(p.ctas) / stage;
+  p.rows = p.vectors == 1 && fit >= 4 ? 2 : 1;
+  if (fit < 3 || (p.vectors == 2 && sh.dtype == LORA_F32)) return RingPlan{};
+  p.threads = (int)threads;
+  p.stages = (int)(fit < kMaxStages ? fit : kMaxStages);
+  p.row_bytes = (uint32_t)(sh.D * es);
+  p.stage_bytes = (uint32_t)stage;
+  return p;
+}
+
+// Row parts of the column sums: one a resident CTA in the one-pass backward; for the column kernel
+// four CTAs per SM over all column tiles, at least 32 rows each.
+void norm_parts(const lora_norm_shape& sh, const RingPlan& ring, int64_t* rp, int* parts) {
+  int64_t want;
+  if (ring.threads) {
+    want = (int64_t)ring.ctas * num_sms_current();
+    if (want > sh.M) want = sh.M;
+  } else {
+    const int64_t tiles = (sh.D + 255) / 256;
+    want = (4LL * num_sms_current() + tiles - 1) / tiles;
+    if (want > (sh.M + 31) / 32) want = (sh.M + 31) / 32;
+  }
   if (want < 1) want = 1;
   *rp = (sh.M + want - 1) / want;
   if (*rp < 1) *rp = 1;
@@ -367,19 +972,28 @@ void norm_parts(const lora_norm_shape& sh, int64_t* rp, int* parts) {
 }
 
 struct NormBwdWs {
+  uint32_t* err;
   float *crow, *pw, *pp, *pg;
 };
-size_t plan_norm_bwd(const lora_norm_shape& sh, char* base, NormBwdWs* w) {
-  int64_t rp;
-  int parts;
-  norm_parts(sh, &rp, &parts);
+size_t plan_norm_bwd(const lora_norm_shape& sh, char* base, int parts, NormBwdWs* w) {
   Carve c{base};
-  c.take<char>(kErrBytes);
+  w->err = c.take<uint32_t>(kErrBytes / 4);
   w->crow = c.take<float>((size_t)sh.M);
   w->pw = c.take<float>((size_t)parts * sh.D);
   w->pp = c.take<float>((size_t)parts * sh.D);
   w->pg = c.take<float>((size_t)parts * 2 * sh.D);
   return c.off;
+}
+// over every number of inputs a call may have: the plan depends on it
+int most_parts(const lora_norm_shape& sh) {
+  int most = 0;
+  for (int n = 1; n <= 5; ++n) {
+    int64_t rp;
+    int parts;
+    norm_parts(sh, ring_plan(sh, n), &rp, &parts);
+    if (parts > most) most = parts;
+  }
+  return most;
 }
 
 NormArgs norm_args(const lora_norm_shape& sh, const void* x, const void* y, const void* w_pre, const void* w_post,
@@ -393,16 +1007,55 @@ NormArgs norm_args(const lora_norm_shape& sh, const void* x, const void* y, cons
   return a;
 }
 
+template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
+cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
+  static bool set = false;
+  if (!set) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmSmem - kRingStatic);
+    if (e != cudaSuccess) return e;
+    set = true;
+  }
+  return launch_pdl(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>, dim3((unsigned)a.parts), dim3((unsigned)p.threads),
+                    (size_t)p.stages * p.stage_bytes, st, a, p);
+}
+template <typename T, int K, int R>
+cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
+  const bool token = a.gate && a.rpg == 1;
+  if (!a.y) return launch_ring<T, K, R, NO_Y, false, false>(a, p, st);
+  if (!(a.dh && a.dzi && a.dx && a.dy))
+    return token ? launch_ring<T, K, R, ANY_Y, true, false>(a, p, st) : launch_ring<T, K, R, ANY_Y, false, false>(a, p, st);
+  if (a.post)
+    return token ? launch_ring<T, K, R, POST_Y, true, true>(a, p, st) : launch_ring<T, K, R, POST_Y, false, true>(a, p, st);
+  return token ? launch_ring<T, K, R, PLAIN_Y, true, true>(a, p, st) : launch_ring<T, K, R, PLAIN_Y, false, true>(a, p, st);
+}
+// The variants that ring_plan can ask for: bf16 rows always fit four stages up to 4096 columns (one
+// vector a thread), fp32 ones do not fit three above them.
+inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_t st, bf16) {
+  return p.vectors == 2 ? launch_ring<bf16, 2, 1>(a, p, st) : launch_ring<bf16, 1, 2>(a, p, st);
+}
+inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_t st, float) {
+  return p.rows == 2 ? launch_ring<float, 1, 2>(a, p, st) : launch_ring<float, 1, 1>(a, p, st);
+}
+
 template <typename T>
-lora_status norm_bwd(NormArgs& a, cudaStream_t st) {
-  const dim3 row_cta(row_threads(a.D));
-  if (a.M > 0) CK(launch_pdl(norm_bwd_rows_kernel<T>, dim3((unsigned)a.M), row_cta, 0, st, a));
-  if (!a.dw_pre && !a.dw_post && !a.dgate) return LORA_OK;
-  if (a.parts > 0)
-    CK(launch_pdl(norm_bwd_cols_kernel<T>, dim3((unsigned)((a.D + 255) / 256), (unsigned)a.parts),
-                  dim3(32 * kColWarps), 0, st, a));
-  const int jobs = a.dgate && a.parts > 1 ? 2 + a.parts - 1 : 2;
-  CK(launch_pdl(norm_bwd_finish_kernel<T>, dim3((unsigned)((a.D + 31) / 32), (unsigned)jobs), dim3(1024), 0, st, a));
+lora_status norm_bwd(NormArgs& a, const RingPlan& ring, cudaStream_t st) {
+  const bool sums = a.dw_pre || a.dw_post || a.dgate;
+  if (a.M > 0 && ring.threads) {
+    CK(launch_plan(a, ring, st, T{}));
+  } else if (a.M > 0) {
+    CK(launch_pdl(norm_bwd_rows_kernel<T>, dim3((unsigned)a.M), dim3((unsigned)row_threads(a.D)), 0, st, a));
+    if (sums)
+      CK(launch_pdl(norm_bwd_cols_kernel<T>, dim3((unsigned)((a.D + 255) / 256), (unsigned)a.parts),
+                    dim3(32 * kColWarps), 0, st, a));
+  }
+  if (!sums) return LORA_OK;
+  // gate rows that may cross a boundary: few of them a CTA each, otherwise a warp for each boundary
+  const int64_t groups = a.dgate && a.parts > 1 ? (a.M + a.rpg - 1) / a.rpg : 0, bounds = a.parts - 1;
+  const bool each = groups <= (bounds + kFinishWarps - 1) / kFinishWarps;
+  const int64_t jobs = 2 + (groups == 0 ? 0 : each ? groups : (bounds + kFinishWarps - 1) / kFinishWarps);
+  CK(launch_pdl(norm_bwd_finish_kernel<T>, dim3((unsigned)((a.D + 31) / 32), (unsigned)jobs),
+                dim3(32 * kFinishWarps), 0, st, a, each ? 1 : 0));
   return LORA_OK;
 }
 
@@ -434,16 +1087,14 @@ lora_status block_norm_fwd(const lora_norm_shape* sh, const void* X, const void*
   if (sh->M == 0) return LORA_OK;
   NormArgs a = norm_args(*sh, X, Y, w_pre, w_post, gate);
   a.z_out = Xout, a.h_out = H, a.r_pre = r_pre, a.r_post = r_post;
-  const dim3 grid((unsigned)sh->M), cta(row_threads(sh->D));
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (sh->dtype == LORA_BF16) CK(launch_pdl(norm_fwd_kernel<bf16>, grid, cta, 0, st, a));
-  else CK(launch_pdl(norm_fwd_kernel<float>, grid, cta, 0, st, a));
+  CK(sh->dtype == LORA_BF16 ? norm_fwd<bf16>(a, st) : norm_fwd<float>(a, st));
   return LORA_OK;
 }
 
 size_t block_norm_bwd_workspace_bytes(const lora_norm_shape* sh) {
   NormBwdWs w;
-  return check_norm(sh) == LORA_OK ? plan_norm_bwd(*sh, nullptr, &w) : 0;
+  return check_norm(sh) == LORA_OK ? plan_norm_bwd(*sh, nullptr, most_parts(*sh), &w) : 0;
 }
 
 lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const void* Y, const void* w_pre,
@@ -468,24 +1119,24 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
                         (const void*)dgate})
     ALN(p);
   NormBwdWs w;
-  const lora_status ew = check_ws(ws, ws_bytes, plan_norm_bwd(*sh, static_cast<char*>(ws), &w));
+  const lora_status ew = check_ws(ws, ws_bytes, plan_norm_bwd(*sh, static_cast<char*>(ws), most_parts(*sh), &w));
   if (ew != LORA_OK) return ew;
   NormArgs a = norm_args(*sh, Xout, Y, w_pre, w_post, gate);
-  norm_parts(*sh, &a.rp, &a.parts);
+  const bool token = gate && sh->rows_per_gate == 1;
+  const RingPlan ring = ring_plan(*sh, 1 + (Y != nullptr) + (dH != nullptr) + (dXout != nullptr) + token);
+  norm_parts(*sh, ring, &a.rp, &a.parts);
   a.r_pre = const_cast<float*>(r_pre), a.r_post = const_cast<float*>(r_post);
   a.dh = dH, a.dzi = dXout, a.dx = dX, a.dy = dY;
   a.dw_pre = dw_pre, a.dw_post = dw_post;
   a.crow = w.crow;
-  if (gate && sh->rows_per_gate == 1) {
-    a.dgate_rows = dgate;   // a gate row per row: its gradient is an output of the row pass
-  } else {
-    a.dgate = dgate;
-  }
+  if (token) a.dgate_rows = dgate;   // a gate row per row: its gradient is an output of the row pass
+  else a.dgate = dgate;
+  a.err = w.err, a.timeout_ns = wait_timeout_ns();
   a.pw = dw_pre ? w.pw : nullptr;
   a.pp = dw_post ? w.pp : nullptr;
   a.pg = w.pg;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return sh->dtype == LORA_BF16 ? norm_bwd<bf16>(a, st) : norm_bwd<float>(a, st);
+  return sh->dtype == LORA_BF16 ? norm_bwd<bf16>(a, ring, st) : norm_bwd<float>(a, ring, st);
 }
 
 }  // extern "C"

@@ -12,7 +12,9 @@ _WS = {}
 
 def workspace(nbytes: int, device) -> torch.Tensor:
     """A cached, zero-initialised scratch buffer of at least nbytes (error word cleared)."""
-    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
+    if not isinstance(device, torch.device):
+        device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    key = (device, L.current_stream(device))
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -399,17 +401,16 @@ def w8a8_lora_fwd_packed(Xc, sx, Wb, sw, Z, B, s, bias=None, want_acc=False, wan
     return Y, acc
 
 
-def _row_stride(name, t, shape, X):
-    """The row stride of t: `shape` [M, D], X's dtype and device, rows of consecutive elements at
-    16-byte multiples (any row stride of at least D)."""
-    if tuple(t.shape) != shape or t.dtype != X.dtype or t.device != X.device:
-        raise ValueError(f"{name} must be a {shape} {X.dtype} tensor on {X.device}, got {tuple(t.shape)} {t.dtype} "
+def _row_stride(name, t, M, D, X):
+    """The row stride of t: a [M, D] tensor of X's dtype and device with rows of consecutive elements,
+    any stride of at least D between them."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != D or t.dtype is not X.dtype or t.device != X.device:
+        raise ValueError(f"{name} must be a {(M, D)} {X.dtype} tensor on {X.device}, got {tuple(t.shape)} {t.dtype} "
                          f"on {t.device}")
-    if shape[0] <= 1:
-        ld = shape[1]
-    else:
-        ld = t.stride(0)
-    if (t.stride(1) != 1 and shape[1] > 1) or ld < shape[1]:
+    ld, step = t.stride()
+    if M <= 1:
+        ld = D
+    if (step != 1 and D > 1) or ld < D:
         raise ValueError(f"{name} must have rows of consecutive elements that do not overlap, got strides {t.stride()}")
     return ld
 
@@ -419,26 +420,34 @@ def _need_cuda(name, t):
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
 
 
+def _gate_rows(gate, rows_per_gate, X):
+    """Rows that share a gate row; by default the rows of X split evenly over the gate's."""
+    M, D = X.shape
+    if gate.dim() != 2 or (gate.shape[0] == 0 and M > 0):
+        raise ValueError("gate must be [rows, D]")
+    G = gate.shape[0]
+    if rows_per_gate is None:
+        if G and M % G:
+            raise ValueError(f"{M} rows do not split evenly over {G} gate rows: give rows_per_gate")
+        rows_per_gate = max(M // max(G, 1), 1)
+    if rows_per_gate < 1 or G != -(-M // rows_per_gate):
+        raise ValueError(f"gate must have a row for every {rows_per_gate} of {M} rows, got {G}")
+    _check_like("gate", gate, (G, D), X)
+    return rows_per_gate
+
+
 def _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm):
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     M, D = X.shape
-    _check_vec("w_pre", w_pre, D, X, X.dtype)
-    _check_vec("w_post", w_post, D, X, X.dtype)
-    if w_post is not None and not post_norm:
-        raise ValueError("w_post needs post_norm=True")
-    if gate is not None:
-        if gate.dim() != 2 or (gate.shape[0] == 0 and M > 0):
-            raise ValueError("gate must be [rows, D]")
-        if rows_per_gate is None:
-            if gate.shape[0] and M % gate.shape[0]:
-                raise ValueError(f"{M} rows do not split evenly over {gate.shape[0]} gate rows: give rows_per_gate")
-            rows_per_gate = max(M // max(gate.shape[0], 1), 1)
-        if rows_per_gate < 1 or gate.shape[0] != -(-M // rows_per_gate):
-            raise ValueError(f"gate must have a row for every {rows_per_gate} of {M} rows, got {gate.shape[0]}")
-        _check_like("gate", gate, (gate.shape[0], D), X)
-    return L.LoraNormShape(M, D, rows_per_gate or 0, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0,
-                           L.dtype_code(X))
+    if w_pre is not None:
+        _check_vec("w_pre", w_pre, D, X, X.dtype)
+    if w_post is not None:
+        _check_vec("w_post", w_post, D, X, X.dtype)
+        if not post_norm:
+            raise ValueError("w_post needs post_norm=True")
+    per = 0 if gate is None else _gate_rows(gate, rows_per_gate, X)
+    return M, D, L.LoraNormShape(M, D, per, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0, L.dtype_code(X))
 
 
 def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=None, alpha=1.0, eps=1e-6,
@@ -448,15 +457,14 @@ def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=
     w_pre) when pre_norm.  Weights are used as w + w_offset.  gate [G, D]: row i takes gate row
     i // rows_per_gate (by default the rows split evenly over the gate's).  Returns
     (Xout, H, r_pre, r_post); Xout is X when there is no Y, and what is not formed is None."""
-    sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
-    M, D = X.shape
+    M, D, sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
     if Y is None and (gate is not None or post_norm or not pre_norm):
         raise ValueError("without a block output Y only the pre norm can be asked for")
     if w_pre is not None and not pre_norm:
         raise ValueError("w_pre needs pre_norm=True")
-    sh.ldx = _row_stride("X", X, (M, D), X)
+    sh.ldx = _row_stride("X", X, M, D, X)
     if Y is not None:
-        sh.ldy = _row_stride("Y", Y, (M, D), X)
+        sh.ldy = _row_stride("Y", Y, M, D, X)
     _need_cuda("X", X)
     dev = X.device
     Xout = torch.empty(M, D, dtype=X.dtype, device=dev) if Y is not None else None
@@ -472,8 +480,7 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     """Gradients of block_norm_fwd from those of H (dH) and Xout (dXout; either may be None): returns
     (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
     and r_post."""
-    sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
-    M, D = Xout.shape
+    M, D, sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
     if dH is None and dXout is None:
         raise ValueError("at least one of dH and dXout is needed")
     if Y is None and (gate is not None or post_norm):
@@ -482,10 +489,13 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     _check_vec("r_post", r_post, M, Xout, F32)
     if (dH is not None and r_pre is None) or (post_norm and r_post is None):
         raise ValueError("r_pre (with dH) and r_post (with post_norm) come from the forward")
-    sh.ldx = _row_stride("Xout", Xout, (M, D), Xout)
-    for name, t, field in (("Y", Y, "ldy"), ("dH", dH, "lddh"), ("dXout", dXout, "lddz")):
-        if t is not None:
-            setattr(sh, field, _row_stride(name, t, (M, D), Xout))
+    sh.ldx = _row_stride("Xout", Xout, M, D, Xout)
+    if Y is not None:
+        sh.ldy = _row_stride("Y", Y, M, D, Xout)
+    if dH is not None:
+        sh.lddh = _row_stride("dH", dH, M, D, Xout)
+    if dXout is not None:
+        sh.lddz = _row_stride("dXout", dXout, M, D, Xout)
     _need_cuda("Xout", Xout)
     dev = Xout.device
     new = lambda: torch.empty(M, D, dtype=Xout.dtype, device=dev)  # noqa: E731
@@ -500,23 +510,29 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
 
 
 def _rotary(call, X, pos, plan, out):
-    if X.dim() != 3 or (X.stride(2) != 1 and X.shape[2] > 1):
-        raise ValueError(f"the heads must be a [tokens, heads, head_dim] tensor with consecutive elements in a head, "
-                         f"got {tuple(X.shape)} with strides {X.stride()}")
+    if X.dim() != 3:
+        raise ValueError(f"the heads must be [tokens, heads, head_dim], got {tuple(X.shape)}")
     M, H, hd = X.shape
-    if pos.dtype not in (torch.int32, torch.int64) or tuple(pos.shape) != (M,) or not pos.is_contiguous():
+    xt, xh, step = X.stride()
+    if step != 1 and hd > 1:
+        raise ValueError(f"a head must be consecutive elements, got strides {X.stride()}")
+    wide = pos.dtype is torch.int64
+    if pos.dim() != 1 or pos.shape[0] != M or not (wide or pos.dtype is torch.int32) or not pos.is_contiguous():
         raise ValueError(f"pos must be a contiguous [{M}] int32 or int64 tensor, got {tuple(pos.shape)} {pos.dtype}")
-    if pos.device != X.device or plan.freq.device != X.device:
-        raise ValueError(f"pos and the plan must be on {X.device}")
+    dev = X.device
+    if pos.device != dev or plan.freq.device != dev:
+        raise ValueError(f"pos and the plan must be on {dev}")
     if plan.rot_dim > hd:
         raise ValueError(f"the plan turns {plan.rot_dim} elements of a head, the heads have {hd}")
     _need_cuda("X", X)
     if out is None:
-        out = torch.empty(M, H, hd, dtype=X.dtype, device=X.device)
-    elif out.shape != X.shape or out.dtype != X.dtype or out.device != X.device or (out.stride(2) != 1 and hd > 1):
-        raise ValueError(f"out must be like the heads, {tuple(X.shape)} {X.dtype} on {X.device}")
-    sh = L.LoraRotaryShape(M, H, hd, plan.rot_dim, X.stride(0), X.stride(1), out.stride(0), out.stride(1), plan.scale,
-                           plan.layout, 8 * pos.element_size(), L.dtype_code(X))
+        out = torch.empty(M, H, hd, dtype=X.dtype, device=dev)
+    elif out is not X and (out.shape != X.shape or out.dtype is not X.dtype or out.device != dev
+                           or (out.stride(2) != 1 and hd > 1)):
+        raise ValueError(f"out must be like the heads, {tuple(X.shape)} {X.dtype} on {dev}")
+    yt, yh = (xt, xh) if out is X else (out.stride(0), out.stride(1))
+    sh = L.LoraRotaryShape(M, H, hd, plan.rot_dim, xt, xh, yt, yh, plan.scale, plan.layout, 64 if wide else 32,
+                           L.dtype_code(X))
     call(sh, X, pos, plan.freq, out)
     return out
 

@@ -2,7 +2,7 @@
 from __future__ import annotations
 
 import math
-from ctypes import c_void_p
+from array import array
 from operator import attrgetter
 
 import torch
@@ -11,7 +11,8 @@ from . import _lib as L
 from .ops import workspace
 
 BLOCK = 256     # elements of a state block
-_META = attrgetter("shape", "dtype", "device")
+_SHAPE, _DTYPE = attrgetter("shape"), attrgetter("dtype")
+_Tensor = torch.Tensor
 
 
 def _each(name, value, count):
@@ -50,9 +51,9 @@ class AdamW:
             raise ValueError(f"betas must be in [0, 1) and eps above 0, got {betas}, {eps}")
         self.params, self.lr, self.betas, self.eps, self.state_bits = params, lr, (b1, b2), eps, state_bits
         n = len(params)
-        self._meta = list(map(_META, params))
+        self._shapes, self._dtypes = list(map(_SHAPE, params)), list(map(_DTYPE, params))
+        self._devices = list(map(_Tensor.get_device, params))
         self._tensors = L.adamw_tensors(params, _each("lr_mul", lr_mul, n), _each("weight_decay", weight_decay, n))
-        self._grads = c_void_p * n
         dev, blocks = params[0].device, L.adamw_state_blocks(self._tensors, n)
         code = torch.float8_e4m3fn if state_bits == 8 else torch.float32
         new = lambda dtype, width: torch.zeros(blocks, width, dtype=dtype, device=dev)  # noqa: E731
@@ -75,17 +76,20 @@ class AdamW:
         return int(self._ctl[0])
 
     def _pointers(self, grads):
-        """A ctypes array of the gradients' pointers; a None leaves its tensor alone."""
+        """The gradients' pointers, 0 for a None.  One pass over the list for each property, in C: a
+        loop with all checks in its body takes half as long again for hundreds of tensors."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
-        if not any(g is None for g in grads):
-            if list(map(_META, grads)) == self._meta and all(map(torch.Tensor.is_contiguous, grads)):
-                return self._grads(*map(torch.Tensor.data_ptr, grads))
-        for i, (g, meta) in enumerate(zip(grads, self._meta)):
-            if g is not None and (_META(g) != meta or not g.is_contiguous()):
-                raise ValueError(f"gradient {i} must be a contiguous {tuple(meta[0])} {meta[1]} tensor on {meta[2]}, "
+        if type(None) not in set(map(type, grads)) and (
+                list(map(_SHAPE, grads)) == self._shapes and list(map(_DTYPE, grads)) == self._dtypes
+                and list(map(_Tensor.get_device, grads)) == self._devices and all(map(_Tensor.is_contiguous, grads))):
+            return array("Q", map(_Tensor.data_ptr, grads))
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g is not None and (g.shape != p.shape or g.dtype != p.dtype or g.device != p.device
+                                  or not g.is_contiguous()):
+                raise ValueError(f"gradient {i} must be a contiguous {tuple(p.shape)} {p.dtype} tensor on {p.device}, "
                                  f"got {tuple(g.shape)} {g.dtype} on {g.device}")
-        return self._grads(*[None if g is None else g.data_ptr() for g in grads])
+        return array("Q", [0 if g is None else g.data_ptr() for g in grads])
 
     def step(self, grads, lr=None, max_norm=None, grad_scale=1.0):
         """One step from `grads`, a tensor (or None: its tensor stays) for each parameter, on the current
@@ -94,7 +98,8 @@ class AdamW:
         max_norm then clips their global norm.  With max_norm the norm before the clip is returned (a
         0-d tensor, nothing waits), and a step whose norm is not finite changes nothing and is not
         counted; max_norm=inf only guards."""
-        ptrs, n, norm = self._pointers(grads), len(self.params), None
+        pointers, n, norm = self._pointers(grads), len(self.params), None
+        at = pointers.buffer_info()[0]
         lr = self.lr if lr is None else lr
         lr_dev = None
         if isinstance(lr, torch.Tensor):
@@ -106,9 +111,9 @@ class AdamW:
             if not max_norm > 0:
                 raise ValueError(f"max_norm must be above 0, got {max_norm}")
             norm = torch.empty(2, dtype=torch.float32, device=self.params[0].device)
-            L.adamw_grad_norm(self._tensors, ptrs, n, grad_scale, max_norm, norm,
+            L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm,
                               workspace(self._ws_bytes, self.params[0].device))
-        L.adamw_step(self._tensors, ptrs, n, self._state, hyper, norm)
+        L.adamw_step(self._tensors, at, n, self._state, hyper, norm)
         return None if norm is None else norm[0]
 
     def state_dict(self):

@@ -122,6 +122,11 @@ NORM_CASES = [  # M, D, gate, post, kwargs
     (1031, 512, "row", True, {}), (640, 1536, "none", True, dict(pre=False)), (200, 4096, "seq", True, dict(rpg=300)),
     (65, 8200, "row", True, {}), (40, 11008, "none", False, {}), (21, 20488, "seq", True, dict(rpg=10)),
     (90, 1024, "none", False, dict(y=False)), (5, 5120, "none", False, dict(y=False, off=1.0)),
+    # enough rows that each variant walks, holds two vectors a thread, or takes two rows a barrier
+    (1100, 2048, "none", True, dict(off=1.0)), (1300, 1544, "token", True, {}), (1250, 2048, "seq", True, dict(rpg=101)),
+    (1500, 1032, "seq", False, dict(rpg=3)), (700, 4096, "row", False, {}), (2500, 520, "token", True, {}),
+    (310, 8192, "seq", True, dict(rpg=4)), (400, 6008, "token", False, {}), (170, 16384, "none", True, {}),
+    (350, 4104, "none", False, dict(y=False)), (3000, 400, "row", False, {}), (900, 504, "row", True, {}),
     (700, 128, "seq", True, dict(rpg=1)), (2000, 64, "seq", True, dict(rpg=3)), (9, 33000, "row", True, {}),
 ]
 
@@ -228,6 +233,18 @@ def test_norm_zero_rows_and_values_that_are_not_finite(ops):
     for a, b in zip(bad, got):
         assert torch.equal(a[rows], b[rows])
     assert bad[1][5].isnan().all() and bad[0][11, 3].isnan()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,D", [(30, 512), (24, 1024), (1200, 2048), (12, 200)])
+def test_norm_rows_that_cancel(ops, M, D, dtype):
+    """The block's output nearly takes the residual stream away: the sum of z^2 is far below those of
+    its terms, and r_pre keeps the precision of z itself."""
+    t, kw = norm_case(M, D, dtype, "none", True, seed=12)
+    p = f64(ops.block_norm_fwd(torch.zeros_like(t["X"]), t["Y"], **kw)[0].float())
+    keep = torch.from_numpy(np.where(np.arange(M) % 3 == 0, 1.0, np.where(np.arange(M) % 3 == 1, 0.97, 0.0)))
+    t["X"] = (-torch.from_numpy(p) * keep[:, None]).to(dtype).to(DEV) + 0.002 * t["X"]
+    check_norm_fwd(ops.block_norm_fwd(t["X"], t["Y"], eps=1e-5, **kw), t, kw, True, dtype, 1e-5)
 
 
 def test_norm_gradient_against_differences(ops):
