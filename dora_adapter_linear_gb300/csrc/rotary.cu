@@ -18,52 +18,178 @@ namespace lg {
 namespace {
 
 struct RotArgs {
-  int64_t M, H, hd, rot;
+  int64_t M;
+  int H, half, rest;            // heads, pairs of a head, elements past them to copy (0 in place)
   int64_t xt, xh, yt, yh;       // token and head strides of x and y, in elements
   const void *x, *pos;
   const uint64_t* freq;
   void* y;
   float scale;
-  int interleaved, pos64, inverse, copy_rest;
+  int pos64, inverse;
+  int tokens;                   // of a CTA
 };
 
-// scale cos t and scale sin t of one pair
-__device__ __forceinline__ float2 turn(const RotArgs& a, int64_t pos, int j) {
-  const int32_t half = (int32_t)(((uint64_t)pos * a.freq[j]) >> 32);   // 2 x the fraction, x 2^31, signed
-  float s, c;
-  sincospif((float)half * 0x1p-31f, &s, &c);
-  s *= a.scale;
-  return make_float2(c * a.scale, a.inverse ? -s : s);
+// B bytes as they lie in memory, and as fp32
+template <int B>
+struct Bytes {
+  uint32_t w[B < 4 ? 1 : B / 4];
+};
+template <int B, typename T>
+__device__ __forceinline__ void load_b(const T* p, Bytes<B>& r) {
+  if constexpr (B == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  } else if constexpr (B == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  } else if constexpr (B == 4) {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+template <int B, typename T>
+__device__ __forceinline__ void store_b(T* p, const Bytes<B>& r) {
+  if constexpr (B == 16) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  else if constexpr (B == 8) *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+  else if constexpr (B == 4) *reinterpret_cast<uint32_t*>(p) = r.w[0];
+  else *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+}
+template <int B, typename T>
+__device__ __forceinline__ void open_b(const Bytes<B>& r, float (&f)[B / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) f[i] = __uint_as_float(r.w[i]);
+  } else if constexpr (B == 2) {
+    f[0] = __uint_as_float(r.w[0] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) {
+      const float2 t = unpack_bf16x2(r.w[i]);
+      f[2 * i] = t.x, f[2 * i + 1] = t.y;
+    }
+  }
+}
+template <int B, typename T>
+__device__ __forceinline__ void close_b(const float (&f)[B / sizeof(T)], Bytes<B>& r) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) r.w[i] = __float_as_uint(f[i]);
+  } else if constexpr (B == 2) {
+    r.w[0] = pack_bf16x2(f[0], 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) r.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  }
 }
 
-// ------------------------------------------------------------------ any size and alignment
-// One CTA per token: the token's angles in shared memory, then a pair (or a passed element) a thread.
-template <typename T>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotArgs a) {
+// A CTA takes `tokens` tokens: their angles, one sincospif for each pair of a token whatever the number of
+// heads, go to shared memory; its threads walk over the items (token, head, vector).  An item is P pairs:
+// two accesses of B bytes in the half layout, one in the interleaved one (two where B is a single
+// element); the vectors of the passed part follow them.  A thread has U items on their way, the first of
+// them while the angles are formed.
+template <typename T, int B, bool INTER>
+__global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  extern __shared__ float2 cs[];
-  const int64_t tok = blockIdx.x;
-  const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.pos)[tok] : static_cast<const int32_t*>(a.pos)[tok];
-  const int half = (int)a.rot / 2, rest = a.copy_rest ? (int)(a.hd - a.rot) : 0, per = half + rest;
-  for (int j = threadIdx.x; j < half; j += blockDim.x) cs[j] = turn(a, pos, j);
-  __syncthreads();
-  const T* x = static_cast<const T*>(a.x) + tok * a.xt;
-  T* y = static_cast<T*>(a.y) + tok * a.yt;
-  for (int64_t i = threadIdx.x; i < a.H * per; i += blockDim.x) {
-    const int64_t h = i / per;
-    const int j = (int)(i - h * per);
-    const T* xh = x + h * a.xh;
-    T* yh = y + h * a.yh;
-    if (j >= half) {
-      yh[a.rot + j - half] = xh[a.rot + j - half];
-      continue;
+  constexpr int E = B / sizeof(T);
+  constexpr bool TWO = !INTER || E == 1;          // an item's pairs lie in two accesses
+  constexpr int P = TWO ? E : E / 2, U = 2;
+  extern __shared__ __align__(16) float2 cs[];    // [token][pair of the item][vector]: neighbours at neighbours
+  const int nv = a.half / P, per = nv + a.rest / E;
+  const int64_t tok0 = (int64_t)blockIdx.x * a.tokens;
+  const int toks = (int)min((int64_t)a.tokens, a.M - tok0);
+  // this thread's items: every blockDim-th, as (token, head, vector) with carries instead of divisions
+  const int all = toks * a.H * per, rows = a.H * per;
+  int i = threadIdx.x;
+  int t = i / rows, h = (i - t * rows) / per, v = i - t * rows - h * per;
+  const int st = blockDim.x / rows, sh = (blockDim.x - st * rows) / per, sv = blockDim.x - st * rows - sh * per;
+  const T* x = static_cast<const T*>(a.x) + tok0 * a.xt;
+  T* y = static_cast<T*>(a.y) + tok0 * a.yt;
+  Bytes<B> p[U], q[U];
+  T* out[U];
+  int at[U];              // where the item's angles begin; -1: a vector that passes, -2: none
+  auto fetch = [&]() {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = -2;
+      if (i < all) {
+        const bool turned = v < nv;
+        const int c = turned ? (INTER ? 2 * P * v : P * v) : 2 * a.half + (v - nv) * E;
+        const T* in = x + t * a.xt + h * a.xh + c;
+        out[u] = y + t * a.yt + h * a.yh + c;
+        load_b<B, T>(in, p[u]);
+        if (TWO && turned) load_b<B, T>(in + (INTER ? 1 : a.half), q[u]);
+        at[u] = turned ? t * a.half + v : -1;
+      }
+      i += blockDim.x;
+      v += sv;
+      if (v >= per) v -= per, ++h;
+      h += sh;
+      if (h >= a.H) h -= a.H, ++t;
+      t += st;
     }
-    const int ia = a.interleaved ? 2 * j : j, ib = a.interleaved ? 2 * j + 1 : j + half;
-    const float u = to_f<T>(xh[ia]), v = to_f<T>(xh[ib]);
-    yh[ia] = from_f<T>(u * cs[j].x - v * cs[j].y);
-    yh[ib] = from_f<T>(v * cs[j].x + u * cs[j].y);
+  };
+  fetch();
+  for (int k = threadIdx.x; k < toks * a.half; k += blockDim.x) {
+    const int tk = k / a.half, j = k - tk * a.half;
+    const int64_t pos = a.pos64 ? static_cast<const int64_t*>(a.pos)[tok0 + tk] : static_cast<const int32_t*>(a.pos)[tok0 + tk];
+    const int32_t turn = (int32_t)(((uint64_t)pos * a.freq[j]) >> 32);   // 2 x the fraction of a turn, x 2^31, signed
+    float s, c;
+    sincospif((float)turn * 0x1p-31f, &s, &c);
+    s *= a.scale;
+    cs[tk * a.half + (j % P) * nv + j / P] = make_float2(c * a.scale, a.inverse ? -s : s);
   }
+  __syncthreads();
+  while (at[0] != -2) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at[u] == -2) continue;
+      if (at[u] >= 0) {
+        float f[E], g[E];
+        open_b<B, T>(p[u], f);
+        if (TWO) open_b<B, T>(q[u], g);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const float2 r = cs[at[u] + e * nv];
+          float& m = TWO ? f[e] : f[2 * e];
+          float& n = TWO ? g[e] : f[(2 * e + 1) % E];
+          const float m0 = m;
+          // written out: the same bits whatever the variant
+          m = fmaf(m0, r.x, -(n * r.y));
+          n = fmaf(n, r.x, m0 * r.y);
+        }
+        close_b<B, T>(f, p[u]);
+        if (TWO) {
+          close_b<B, T>(g, q[u]);
+          store_b<B, T>(out[u] + (INTER ? 1 : a.half), q[u]);
+        }
+      }
+      store_b<B, T>(out[u], p[u]);
+    }
+    fetch();
+  }
+}
+
+template <typename T, int B>
+cudaError_t launch(const RotArgs& a, bool inter, cudaStream_t st) {
+  constexpr int E = B / (int)sizeof(T);
+  const int P = inter && E > 1 ? E / 2 : E;
+  const int64_t items = (int64_t)a.H * (a.half / P + a.rest / E);   // of a token
+  // A CTA reads about 40 KB (16384 x 40 heads of 128, bf16: 50 us in the half layout with 40 KB, 51 with 20 and
+  // 55 with 160; 54 us in the interleaved one with 40 KB, 58 with 20), but rather there are two for every SM.
+  RotArgs r = a;
+  int64_t tokens = 40960 / (items * B * (inter && E > 1 ? 1 : 2));
+  const int64_t fit = 16384 / (a.half * (int64_t)sizeof(float2)), spread = a.M / (2 * num_sms_current());
+  if (tokens > fit) tokens = fit;
+  if (tokens > spread) tokens = spread;
+  r.tokens = (int)(tokens < 1 ? 1 : tokens);
+  const int64_t mine = items * r.tokens;
+  const int threads = mine >= 512 ? 256 : (int)((mine + 31) / 32 * 32);
+  const dim3 grid((unsigned)((a.M + r.tokens - 1) / r.tokens));
+  const size_t smem = (size_t)r.tokens * a.half * sizeof(float2);
+  return inter ? launch_pdl(rotary_kernel<T, B, true>, grid, dim3((unsigned)threads), smem, st, r)
+               : launch_pdl(rotary_kernel<T, B, false>, grid, dim3((unsigned)threads), smem, st, r);
 }
 
 lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, const uint64_t* freq, void* Y,
@@ -75,7 +201,8 @@ lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, 
   if (sh->layout != LORA_ROTARY_HALF && sh->layout != LORA_ROTARY_INTERLEAVED) return LORA_ERR_INVALID_ARG;
   if (sh->pos_bits != 32 && sh->pos_bits != 64) return LORA_ERR_INVALID_ARG;
   if (!isfinite(sh->scale)) return LORA_ERR_INVALID_ARG;
-  if (sh->M > (1LL << 31) - 1 || sh->H > (1 << 20) || sh->head_dim > (1 << 12)) return LORA_ERR_UNSUPPORTED;
+  if (sh->M > (1LL << 31) - 1 || sh->head_dim > (1 << 12) || sh->H > (1LL << 30) / sh->head_dim)
+    return LORA_ERR_UNSUPPORTED;
   REQ(freq);
   if (sh->M > 0 && (!X || !pos || !Y)) return LORA_ERR_INVALID_ARG;
   // no two elements of y at one address (x may repeat a head or a token); in place: the same layout
@@ -93,15 +220,29 @@ lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, 
     return LORA_ERR_MISALIGNED;
   if (M == 0) return LORA_OK;
   RotArgs a = {};
-  a.M = M, a.H = H, a.hd = hd, a.rot = sh->rot_dim;
+  a.M = M, a.H = (int)H, a.half = (int)(sh->rot_dim / 2), a.rest = X != Y ? (int)(hd - sh->rot_dim) : 0;
   a.xt = sh->x_token, a.xh = sh->x_head, a.yt = sh->y_token, a.yh = sh->y_head;
   a.x = X, a.pos = pos, a.freq = freq, a.y = Y, a.scale = sh->scale;
-  a.interleaved = sh->layout == LORA_ROTARY_INTERLEAVED, a.pos64 = sh->pos_bits == 64;
-  a.inverse = inverse, a.copy_rest = X != Y;
-  const size_t smem = (size_t)sh->rot_dim / 2 * sizeof(float2);
+  a.pos64 = sh->pos_bits == 64, a.inverse = inverse;
+  const bool inter = sh->layout == LORA_ROTARY_INTERLEAVED;
+  // the widest access that every address of a vector is a multiple of
+  uintptr_t bits = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y) |
+                   (uintptr_t)(inter ? sh->rot_dim : sh->rot_dim / 2) * es | (uintptr_t)a.rest * es;
+  if (M > 1) bits |= (uintptr_t)(a.xt | a.yt) * es;
+  if (H > 1) bits |= (uintptr_t)(a.xh | a.yh) * es;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (sh->dtype == LORA_BF16) CK(launch_pdl(rotary_kernel<bf16>, dim3((unsigned)M), dim3(256), smem, st, a));
-  else CK(launch_pdl(rotary_kernel<float>, dim3((unsigned)M), dim3(256), smem, st, a));
+  cudaError_t e;
+  if (sh->dtype == LORA_BF16) {
+    if (bits % 16 == 0) e = launch<bf16, 16>(a, inter, st);
+    else if (bits % 8 == 0) e = launch<bf16, 8>(a, inter, st);
+    else if (bits % 4 == 0) e = launch<bf16, 4>(a, inter, st);
+    else e = launch<bf16, 2>(a, inter, st);
+  } else {
+    if (bits % 16 == 0) e = launch<float, 16>(a, inter, st);
+    else if (bits % 8 == 0) e = launch<float, 8>(a, inter, st);
+    else e = launch<float, 4>(a, inter, st);
+  }
+  CK(e);
   return LORA_OK;
 }
 
