@@ -10,12 +10,15 @@
 // their rounding make this step's update, and a sqrt(v) above zero is never stored as zero (an
 // element whose v vanished would be divided by eps alone).  sqrt(v) instead of v halves the range
 // that the 4 exponent bits have to span; the rounding is at most 2^-4 of a normal value.
-// Bound by memory: 28 bytes an element (bf16, fp32 master and states), 16 with 8-bit states.
+// 28 bytes an element (bf16, fp32 master and states), 16 with 8-bit states.  32-bit states are bound by memory:
+// 42 M bf16 elements 174 us, 6.7 TB/s.
 //
 // The table of tensors travels in the launch's parameters (up to 32 KB), so a step copies nothing and
 // is captured by a CUDA graph as it is.
 #include <cuda_fp8.h>
 #include <math.h>
+
+#include <type_traits>
 
 #include "checks.h"
 #include "vec.cuh"
@@ -27,6 +30,7 @@ namespace {
 constexpr int kBlock = 256;           // elements of a state block
 constexpr int kSmallTable = 64, kTable = 640;
 constexpr int kNormCtas = 608;        // gradient-norm CTAs of one launch, 4 per SM of a 152-SM part
+constexpr int kStepCtas = 4;          // step CTAs of an SM: 64 registers a thread
 constexpr float kMinTop = 0x1p-110f;  // a block whose largest value is below this is stored as zeros
 
 struct AdamEntry {
@@ -40,7 +44,7 @@ struct AdamEntry {
 };
 struct AdamArgs {
   int count;                          // tensors in this launch's table
-  int32_t blocks;                     // their blocks
+  int32_t blocks, rounds;             // their blocks; rounds of a chunk
   int advance;                        // the step's last launch: counts the step
   int bits;
   void *m, *v;
@@ -73,139 +77,309 @@ __device__ __forceinline__ int find_entry(const AdamTable<N>& t, int count, int3
   return lo;
 }
 
-// 8 elements at i of an array of n, zeros past its end; whole aligned groups as 16-byte loads
+// 8 elements as they lie in memory (bf16 takes the first half): a load that does not wait for its value
+struct Eight {
+  uint4 lo, hi;
+};
+// What a launch's tensors are, where that is known for all of them: bf16 with masters (KIND_BF16), fp32,
+// or either, asked for each.
+enum { KIND_ANY = 0, KIND_BF16 = 1, KIND_F32 = 2 };
+template <int KIND>
+__device__ __forceinline__ int type_of(const AdamEntry& e) {
+  return KIND == KIND_BF16 ? (int)LORA_BF16 : KIND == KIND_F32 ? (int)LORA_F32 : e.dtype;
+}
+template <int KIND>
+__device__ __forceinline__ bool has_master(const AdamArgs& a, int dtype) {
+  return KIND == KIND_BF16 || (KIND == KIND_ANY && a.master && dtype == LORA_BF16);
+}
+__device__ __forceinline__ void take(const void* base, int dtype, int64_t i, Eight& r) {
+  if (dtype == LORA_BF16) {
+    r.lo = __ldcs(reinterpret_cast<const uint4*>(static_cast<const bf16*>(base) + i));
+  } else {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + i);
+    r.lo = __ldcs(p);
+    r.hi = __ldcs(p + 1);
+  }
+}
+// the same element by element, zeros past the end of the array of n
 template <typename T>
-__device__ __forceinline__ void load8_of(const void* base, int64_t i, int64_t n, float (&f)[8]) {
+__device__ __forceinline__ void take_each(const void* base, int64_t i, int64_t n, Eight& r) {
   const T* p = static_cast<const T*>(base) + i;
-  if (i + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    load8(p, f);
+  uint32_t w[8];
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = i + k < n ? to_f<T>(p[k]) : 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    w[k] = sizeof(T) == 4 ? __float_as_uint(f[k]) : k < 4 ? pack_bf16x2(f[2 * k & 7], f[(2 * k + 1) & 7]) : 0u;
+  r.lo = make_uint4(w[0], w[1], w[2], w[3]);
+  r.hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void open8(const Eight& r, int dtype, F2 (&f)[4]) {
+  const uint32_t a[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, b[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+  if (dtype == LORA_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(a[i] << 16), __uint_as_float(a[i] & 0xffff0000u));
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = i + k < n ? to_f<T>(p[k]) : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      f[i] = f2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1]));
+      f[i + 2] = f2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]));
+    }
   }
 }
 template <typename T>
-__device__ __forceinline__ void store8_of(void* base, int64_t i, int64_t n, const float (&f)[8]) {
+__device__ __forceinline__ void put_each(void* base, int64_t i, int64_t n, const F2 (&f)[4]) {
   T* p = static_cast<T*>(base) + i;
-  if (i + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    store8(p, f);
-  } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i + k < n) p[k] = from_f<T>(f[k]);
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = unpack(f[k]);
+    if (i + 2 * k < n) p[2 * k] = from_f<T>(t.x);
+    if (i + 2 * k + 1 < n) p[2 * k + 1] = from_f<T>(t.y);
   }
 }
-__device__ __forceinline__ void load8_dt(const void* p, int dtype, int64_t i, int64_t n, float (&f)[8]) {
-  if (dtype == LORA_BF16) load8_of<bf16>(p, i, n, f);
-  else load8_of<float>(p, i, n, f);
+// whether the block of 256 elements from i on lies within the array of n, which begins at 16 bytes
+__device__ __forceinline__ bool whole(const void* base, int64_t i, int64_t n) {
+  return i + kBlock <= n && (reinterpret_cast<uintptr_t>(base) & 15) == 0;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-__device__ __forceinline__ void decode8(const uint8_t* p, float scale, float (&f)[8]) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
+// eight e4m3 codes times their block's scale
+__device__ __forceinline__ void decode8(uint2 w, float scale, F2 (&f)[4]) {
   const uint32_t u[2] = {w.x, w.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
     const float2 t = __half22float2(__half2(h));
-    f[2 * i] = t.x * scale;
-    f[2 * i + 1] = t.y * scale;
+    f[i] = mul2(f2(t.x, t.y), f2(scale));
   }
 }
-__device__ __forceinline__ void encode8(uint8_t* p, const float (&f)[8]) {
+// Codes and scale of one block from its values (8 a lane).  ROOT: values that are not negative, of which
+// none above zero may become the code 0.  The largest absolute value is found on the bit patterns, whose
+// order as integers is that of the numbers, with a NaN on top: a block with one becomes NaN as a whole.
+template <bool ROOT>
+__device__ __forceinline__ void encode_block(uint8_t* codes, float* scale, const F2 (&f)[4], int lane) {
+  float x[8];
+  uint32_t top_bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = unpack(f[i]);
+    x[2 * i] = t.x, x[2 * i + 1] = t.y;
+    top_bits = max(top_bits, max(__float_as_uint(t.x) & 0x7fffffffu, __float_as_uint(t.y) & 0x7fffffffu));
+  }
+  const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, top_bits));
+  const bool none = top < kMinTop;
+  const float inv = none ? 0.f : __fmul_rn(1.f / top, 448.f), low = none ? 0.f : 0x1p-9f;
   uint32_t u[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    u[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[2 * i], f[2 * i + 1]), __NV_SATFINITE, __NV_E4M3)
-                 << (16 * (i & 1));
-  *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-}
-// codes and scale of one block from its values (8 a lane); low: the least code of a value above zero
-__device__ __forceinline__ void encode_block(uint8_t* codes, float* scale, const float (&f)[8], float low, int lane) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-  top = warp_max(top);
-  const float inv = top >= kMinTop ? __fmul_rn(1.f / top, 448.f) : 0.f;
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    q[i] = f[i] * inv;
-    if (f[i] > 0.f && inv > 0.f) q[i] = fmaxf(q[i], low);
+  for (int i = 0; i < 4; ++i) {
+    float2 q = unpack(mul2(f[i], f2(inv)));
+    if (ROOT) {
+      if (x[2 * i] > 0.f) q.x = fmaxf(q.x, low);
+      if (x[2 * i + 1] > 0.f) q.y = fmaxf(q.y, low);
+    }
+    u[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
   }
-  encode8(codes, q);
-  if (lane == 0) *scale = inv > 0.f ? __fmul_rn(top, 1.f / 448.f) : 0.f;
+  *reinterpret_cast<uint2*>(codes) = make_uint2(u[0], u[1]);
+  if (lane == 0) *scale = none ? 0.f : __fmul_rn(top, 1.f / 448.f);
 }
 
 // b s + t, each operation rounded on its own: whether the compiler contracts a product into a sum does
 // not decide on which side of a rounding boundary an 8-bit state falls
-__device__ __forceinline__ float ema(float b, float s, float t) { return __fadd_rn(__fmul_rn(b, s), t); }
+__device__ __forceinline__ F2 ema(float b, F2 s, F2 t) {
+  const float2 x = unpack(s), y = unpack(t);
+  return f2(__fadd_rn(__fmul_rn(b, x.x), y.x), __fadd_rn(__fmul_rn(b, x.y), y.y));
+}
 
 // ------------------------------------------------------------------ the step
+// What a launch's steps have in common, formed once per thread.
+struct StepFactors {
+  float coef, i1, i2, lr;   // of the gradients, 1 / (1 - b1^t), (1 - b2^t)^-1/2, lr
+  int steps;
+  bool go;                  // gradients that are not finite leave everything as it was
+};
+__device__ __forceinline__ StepFactors step_factors(const AdamArgs& a) {
+  StepFactors f;
+  f.steps = a.ctl[0];
+  f.coef = a.norm_coef ? a.norm_coef[1] : a.grad_scale;
+  f.go = isfinite(f.coef);
+  // 1 - b^t = -expm1(t ln b): no cancellation for b near 1
+  const float t = (float)(f.steps + 1);
+  f.i1 = -1.f / expm1f(t * a.ln_b1);
+  f.i2 = rsqrtf(-expm1f(t * a.ln_b2));
+  f.lr = a.lr_dev ? *a.lr_dev : a.lr;
+  return f;
+}
+// the last CTA of the step's last launch counts the step: every CTA has read the count by then
+__device__ __forceinline__ void count_step(const AdamArgs& a, const StepFactors& f) {
+  if (!a.advance) return;
+  __syncthreads();
+  if (threadIdx.x == 0 && atomicAdd(a.ctl + 1, 1) == (int)gridDim.x - 1) {
+    a.ctl[1] = 0;
+    if (f.go) a.ctl[0] = f.steps + 1;
+  }
+}
+// m, v and p of eight elements; root becomes sqrt(v)
+__device__ __forceinline__ void update8(const AdamArgs& a, const StepFactors& f, const AdamEntry& e, const F2 (&g)[4],
+                                        F2 (&m)[4], F2 (&v)[4], F2 (&root)[4], F2 (&p)[4]) {
+  const float lr = f.lr * e.lr_mul, step = lr * f.i1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const F2 gs = mul2(g[j], f2(f.coef));
+    m[j] = ema(a.b1, m[j], mul2(f2(a.c1), gs));
+    v[j] = ema(a.b2, v[j], mul2(mul2(f2(a.c2), gs), gs));
+    const float2 vv = unpack(v[j]);
+    root[j] = f2(sqrtf(vv.x), sqrtf(vv.y));
+    // the quotient within 2 ulp: it is lr times smaller than what it is added to
+    const float2 den = unpack(fma2(root[j], f2(f.i2), f2(a.eps))), num = unpack(mul2(m[j], f2(step)));
+    p[j] = fma2(f2(-lr * e.decay), p[j], p[j]);
+    p[j] = add2(p[j], f2(-__fdividef(num.x, den.x), -__fdividef(num.y, den.y)));
+  }
+}
+// the gradient and the parameter's exact value (master, or the parameter itself)
+__device__ __forceinline__ void take_gp(const AdamArgs& a, const AdamEntry& e, int dtype, bool full, bool master,
+                                        int64_t i, int64_t si, Eight& ge, Eight& pe) {
+  if (full) take(e.g, dtype, i, ge);
+  else if (dtype == LORA_BF16) take_each<bf16>(e.g, i, e.n, ge);
+  else take_each<float>(e.g, i, e.n, ge);
+  if (master) take(a.master, LORA_F32, si, pe);
+  else if (full) take(e.p, dtype, i, pe);
+  else if (dtype == LORA_BF16) take_each<bf16>(e.p, i, e.n, pe);
+  else take_each<float>(e.p, i, e.n, pe);
+}
+__device__ __forceinline__ void put_p(const AdamArgs& a, const AdamEntry& e, int dtype, bool full, bool master, int64_t i,
+                                      int64_t si, const F2 (&p)[4]) {
+  if (master) store4x2(a.master + si, p);
+  if (dtype == LORA_BF16) {
+    if (full) store4x2(static_cast<bf16*>(e.p) + i, p);
+    else put_each<bf16>(e.p, i, e.n, p);
+  } else {
+    if (full) store4x2(static_cast<float*>(e.p) + i, p);
+    else put_each<float>(e.p, i, e.n, p);
+  }
+}
+// A warp's way through its blocks: chunks of 8 `rounds` consecutive blocks, every gridDim-th chunk for a
+// CTA; in a round each of its 8 warps has one, so a CTA touches 2048 neighbouring elements of every array.
+// The tensor is looked up once per chunk.
 template <int N>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamArgs a,
-                                                    const __grid_constant__ AdamTable<N> table) {
+struct Walk {
+  const AdamArgs& a;
+  const AdamTable<N>& table;
+  int64_t c0;
+  int32_t w, w1, end;
+  int k;
+  __device__ __forceinline__ Walk(const AdamArgs& args, const AdamTable<N>& t) : a(args), table(t) {
+    c0 = (int64_t)blockIdx.x * 8 * a.rounds;
+    begin();
+  }
+  __device__ __forceinline__ bool valid() const { return w < w1; }
+  __device__ __forceinline__ void begin() {
+    w = (int32_t)min(c0 + (threadIdx.x >> 5), (int64_t)INT32_MAX - 8);
+    w1 = (int32_t)min((int64_t)a.blocks, c0 + 8 * a.rounds);
+    if (!valid()) return;
+    k = find_entry(table, a.count, w);
+    end = k + 1 < a.count ? table.e[k + 1].first : a.blocks;
+  }
+  __device__ __forceinline__ void next() {
+    w += 8;
+    if (w >= w1) {
+      c0 += (int64_t)gridDim.x * 8 * a.rounds;
+      begin();
+      return;
+    }
+    while (w >= end) {
+      ++k;
+      end = k + 1 < a.count ? table.e[k + 1].first : a.blocks;
+    }
+  }
+};
+
+template <int N, int KIND>
+__global__ void __launch_bounds__(256, kStepCtas) adamw_kernel(const __grid_constant__ AdamArgs a,
+                                                       const __grid_constant__ AdamTable<N> table) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int steps = a.ctl[0];
-  const float coef = a.norm_coef ? a.norm_coef[1] : a.grad_scale;
-  const bool go = isfinite(coef);       // gradients that are not finite leave everything as it was
-  if (go && w < a.blocks) {
-    const AdamEntry& e = table.e[find_entry(table, a.count, (int32_t)w)];
-    const int32_t k0 = (int32_t)w - e.first, b = e.state + k0;
-    const int64_t i = (int64_t)k0 * kBlock + lane * 8, si = (int64_t)b * kBlock + lane * 8;
-    const float t = (float)(steps + 1);
-    // 1 - b^t = -expm1(t ln b): no cancellation for b near 1
-    const float i1 = -1.f / expm1f(t * a.ln_b1), i2 = rsqrtf(-expm1f(t * a.ln_b2));
-    const float lr = (a.lr_dev ? *a.lr_dev : a.lr) * e.lr_mul;
-    float g[8], m[8], v[8], p[8];
-    load8_dt(e.g, e.dtype, i, e.n, g);
-    if (a.bits == 8) {
-      decode8(static_cast<const uint8_t*>(a.m) + si, a.m_scale[b], m);
-      decode8(static_cast<const uint8_t*>(a.v) + si, a.v_scale[b], v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= v[k];
-    } else {
-      load8(static_cast<const float*>(a.m) + si, m);
-      load8(static_cast<const float*>(a.v) + si, v);
-    }
-    const bool master = a.master && e.dtype == LORA_BF16;
-    if (master) load8(a.master + si, p);
-    else load8_dt(e.p, e.dtype, i, e.n, p);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gs = g[k] * coef;
-      m[k] = ema(a.b1, m[k], __fmul_rn(a.c1, gs));
-      v[k] = ema(a.b2, v[k], __fmul_rn(__fmul_rn(a.c2, gs), gs));
-      g[k] = sqrtf(v[k]);
-      p[k] -= lr * e.decay * p[k] + lr * ((m[k] * i1) / fmaf(g[k], i2, a.eps));
-    }
-    if (master) store8(a.master + si, p);
-    if (e.dtype == LORA_BF16) store8_of<bf16>(e.p, i, e.n, p);
-    else store8_of<float>(e.p, i, e.n, p);
-    if (a.bits == 8) {
-      encode_block(static_cast<uint8_t*>(a.m) + si, a.m_scale + b, m, -448.f, lane);
-      encode_block(static_cast<uint8_t*>(a.v) + si, a.v_scale + b, g, 0x1p-9f, lane);
-    } else {
-      store8(static_cast<float*>(a.m) + si, m);
-      store8(static_cast<float*>(a.v) + si, v);
+  const StepFactors f = step_factors(a);
+  if (f.go) {
+    for (Walk<N> at(a, table); at.valid(); at.next()) {
+      const AdamEntry& e = table.e[at.k];
+      const int32_t b0 = at.w - e.first;
+      const int64_t i0 = (int64_t)b0 * kBlock, i = i0 + lane * 8, si = (int64_t)(e.state + b0) * kBlock + lane * 8;
+      const int dtype = type_of<KIND>(e);
+      const bool master = has_master<KIND>(a, dtype);
+      const bool full = whole(e.g, i0, e.n) && whole(e.p, i0, e.n);   // the same for the warp
+      Eight ge, pe;   // every load is on its way before the first value is opened
+      F2 g[4], m[4], v[4], p[4];
+      take_gp(a, e, dtype, full, master, i, si, ge, pe);
+      load4x2(static_cast<const float*>(a.m) + si, m);
+      load4x2(static_cast<const float*>(a.v) + si, v);
+      open8(ge, dtype, g);
+      open8(pe, master ? (int)LORA_F32 : dtype, p);
+      update8(a, f, e, g, m, v, g, p);
+      put_p(a, e, dtype, full, master, i, si, p);
+      store4x2(static_cast<float*>(a.m) + si, m);
+      store4x2(static_cast<float*>(a.v) + si, v);
     }
   }
-  // the last CTA of the step's last launch counts the step: every CTA has read the count by then
-  if (a.advance) {
-    __syncthreads();
-    if (threadIdx.x == 0 && atomicAdd(a.ctl + 1, 1) == (int)gridDim.x - 1) {
-      a.ctl[1] = 0;
-      if (go) a.ctl[0] = steps + 1;
+  count_step(a, f);
+}
+
+// ------------------------------------------------------------------ the step with 8-bit states
+// A block's arithmetic (square roots, quotients, two block maxima, the codes both ways: some 550 instructions
+// a warp) takes about as long as its 4 KB take from memory, so a warp must not wait for DRAM: it asks for its
+// next block in L2 while it works on this one.  168 M bf16 elements with masters: 473 us, 5.7 TB/s; without
+// the prefetch 570, with the next block's loads in registers (three CTAs an SM) 497, with asynchronous copies
+// into shared memory 690.  It issues 60% of the time: bound by the length of a block's chain, not by memory.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+template <int N, int KIND>
+__global__ void __launch_bounds__(256, kStepCtas) adamw8_kernel(const __grid_constant__ AdamArgs a,
+                                                        const __grid_constant__ AdamTable<N> table) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const StepFactors f = step_factors(a);
+  uint8_t *const mc = static_cast<uint8_t*>(a.m), *const vc = static_cast<uint8_t*>(a.v);
+  if (f.go) {
+    for (Walk<N> at(a, table); at.valid();) {
+      const AdamEntry& e = table.e[at.k];
+      const int32_t b0 = at.w - e.first, b = e.state + b0;
+      const int64_t i0 = (int64_t)b0 * kBlock, i = i0 + lane * 8, si = (int64_t)b * kBlock + lane * 8;
+      const int dtype = type_of<KIND>(e);
+      const bool master = has_master<KIND>(a, dtype);
+      const bool full = whole(e.g, i0, e.n) && whole(e.p, i0, e.n);   // the same for the warp
+      Eight ge, pe;   // every load is on its way before the first value is opened
+      take_gp(a, e, dtype, full, master, i, si, ge, pe);
+      const uint2 mw = *reinterpret_cast<const uint2*>(mc + si), vw = *reinterpret_cast<const uint2*>(vc + si);
+      const float ms = a.m_scale[b], vs = a.v_scale[b];
+      at.next();
+      if (at.valid() && lane < 4) {
+        const AdamEntry& n = table.e[at.k];
+        const int32_t nb0 = at.w - n.first;
+        const int64_t ns = (int64_t)(n.state + nb0) * kBlock;
+        const int ntype = type_of<KIND>(n), es = ntype == LORA_BF16 ? 2 : 4;
+        if (lane == 0) prefetch_l2(mc + ns, kBlock);
+        else if (lane == 1) prefetch_l2(vc + ns, kBlock);
+        else if (lane == 2 && has_master<KIND>(a, ntype)) prefetch_l2(a.master + ns, kBlock * 4);
+        else if (lane == 3 && whole(n.g, (int64_t)nb0 * kBlock, n.n))
+          prefetch_l2(static_cast<const char*>(n.g) + (int64_t)nb0 * kBlock * es, kBlock * es);
+      }
+      F2 g[4], m[4], v[4], p[4];
+      open8(ge, dtype, g);
+      open8(pe, master ? (int)LORA_F32 : dtype, p);
+      decode8(mw, ms, m);
+      decode8(vw, vs, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
+      update8(a, f, e, g, m, v, g, p);
+      put_p(a, e, dtype, full, master, i, si, p);
+      encode_block<false>(mc + si, a.m_scale + b, m, lane);
+      encode_block<true>(vc + si, a.v_scale + b, g, lane);
     }
   }
+  count_step(a, f);
 }
 
 // ------------------------------------------------------------------ gradient norm
@@ -217,16 +391,48 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
   __shared__ float red[2 * 32];
-  __shared__ double tot[256];
+  __shared__ double tot[8];
   __shared__ int last;
   const int lane = threadIdx.x & 31;
+  // a warp has a run of consecutive blocks and keeps four of them on their way
+  const int64_t warps = (int64_t)gridDim.x * 8, id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int32_t w = (int32_t)(id * a.blocks / warps);
+  const int32_t w1 = (int32_t)((id + 1) * a.blocks / warps);
   float s[1] = {0.f};
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < a.blocks; w += (int64_t)gridDim.x * 8) {
-    const AdamEntry& e = table.e[find_entry(table, a.count, (int32_t)w)];
-    float g[8];
-    load8_dt(e.g, e.dtype, (int64_t)((int32_t)w - e.first) * kBlock + lane * 8, e.n, g);
+  for (int k = w < w1 ? find_entry(table, a.count, w) : 0; w < w1; ++k) {
+    const AdamEntry& e = table.e[k];
+    const int32_t end = min(w1, k + 1 < a.count ? table.e[k + 1].first : a.blocks);
+    int64_t i = (int64_t)(w - e.first) * kBlock + lane * 8;
+    auto sum = [&](auto one) {
+      using T = decltype(one);
+      const T* p = static_cast<const T*>(e.g) + i;
+      if ((reinterpret_cast<uintptr_t>(p) & 15) == 0)
+        for (; w + 4 <= end && i - lane * 8 + 4 * kBlock <= e.n; w += 4, i += 4 * kBlock, p += 4 * kBlock) {
+          Raw8<T> r[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[0] = fmaf(g[k], g[k], s[0]);
+          for (int u = 0; u < 4; ++u) stream8(p + u * kBlock, r[u]);
+          F2 q = f2(0.f);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            F2 f[4];
+            r[u].get(f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q = fma2(f[j], f[j], q);
+          }
+          s[0] += sum2(q);
+        }
+      for (; w < end; ++w, i += kBlock) {
+        Eight r;
+        F2 f[4], q = f2(0.f);
+        take_each<T>(e.g, i, e.n, r);
+        open8(r, e.dtype, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q = fma2(f[j], f[j], q);
+        s[0] += sum2(q);
+      }
+    };
+    if (e.dtype == LORA_BF16) sum(bf16{});
+    else sum(float{});
   }
   block_sums<1>(s, red, 0);
   if (threadIdx.x == 0) {
@@ -245,17 +451,22 @@ __global__ void __launch_bounds__(256) adamw_norm_kernel(const __grid_constant__
   if (!last) return;
   double t = 0.0;
   for (int i = threadIdx.x; i < a.part_total; i += 256) t += (double)__ldcg(a.parts + i);
-  tot[threadIdx.x] = t;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) tot[threadIdx.x >> 5] = t;
   __syncthreads();
   if (threadIdx.x == 0) {
     t = 0.0;
-    for (int i = 0; i < 256; ++i) t += tot[i];
-    const float norm = (float)(sqrt(t) * fabs((double)a.grad_scale));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += tot[i];
+    const float norm = sqrtf((float)t) * fabsf(a.grad_scale);
     a.norm_out[0] = norm;
     const float clip = a.max_norm > 0.f ? fminf(1.f, a.max_norm / (norm + 1e-6f)) : 1.f;
     a.norm_out[1] = isfinite(norm) ? a.grad_scale * clip : nanf("");
   }
 }
+
+inline bool t_used(const lora_adamw_tensor& t, const void* grad) { return t.n > 0 && grad; }
 
 lora_status check_table(const lora_adamw_tensor* t, const void* const* grads, int64_t count, int64_t* used) {
   if (count < 0 || (count > 0 && (!t || !grads))) return LORA_ERR_INVALID_ARG;
@@ -266,7 +477,7 @@ lora_status check_table(const lora_adamw_tensor* t, const void* const* grads, in
     if (!isfinite(t[i].lr_mul) || !isfinite(t[i].weight_decay)) return LORA_ERR_INVALID_ARG;
     b += (t[i].n + kBlock - 1) / kBlock;
     if (b > (1LL << 31) - 1) return LORA_ERR_UNSUPPORTED;
-    if (t[i].n == 0 || !grads[i]) continue;
+    if (!t_used(t[i], grads[i])) continue;
     if (!t[i].p) return LORA_ERR_INVALID_ARG;
     const uintptr_t es = t[i].dtype == LORA_BF16 ? 2 : 4;
     if (reinterpret_cast<uintptr_t>(t[i].p) % es || reinterpret_cast<uintptr_t>(grads[i]) % es)
@@ -289,7 +500,7 @@ lora_status over_table(const lora_adamw_tensor* t, const void* const* grads, int
     a.blocks = 0;
     for (; i < count && a.count < N; ++i) {
       const int32_t nb = (int32_t)((t[i].n + kBlock - 1) / kBlock);
-      if (nb > 0 && grads[i]) {
+      if (t_used(t[i], grads[i])) {
         table.e[a.count++] =
             AdamEntry{t[i].p, grads[i], t[i].n, a.blocks, state, t[i].dtype, t[i].lr_mul, t[i].weight_decay};
         a.blocks += nb;
@@ -407,17 +618,34 @@ lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grad
   a.ln_b1 = (float)log(h.beta1), a.ln_b2 = (float)log(h.beta2);
   a.eps = (float)h.eps, a.grad_scale = (float)h.grad_scale;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const auto run = [&](auto kernel, AdamArgs& b, const auto& table) {
-    CK(launch_pdl(kernel, dim3((unsigned)((b.blocks + 7) / 8)), dim3(256), 0, st, b, table));
+  // Two rounds a chunk; with 32-bit states a CTA for each chunk (448 tensors of 42 M elements, bf16: 174 us;
+  // with one round 180, four 181, eight 188), with 8-bit ones as many CTAs as are resident, which know their
+  // next block (168 M elements: 473 us against 630).
+  const auto run = [&](auto kernel, AdamArgs& b, const auto& table, bool stay) {
+    const int64_t slots = kStepCtas * (int64_t)num_sms_current(), eights = (b.blocks + 7) / 8;
+    b.rounds = eights >= 2 * slots ? 2 : 1;
+    const int64_t chunks = (eights + b.rounds - 1) / b.rounds;
+    CK(launch_pdl(kernel, dim3((unsigned)(stay && chunks > slots ? slots : chunks)), dim3(256), 0, st, b, table));
     return LORA_OK;
   };
-  if (used <= kSmallTable)
-    return over_table<kSmallTable>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<kSmallTable>& t) {
-      return run(adamw_kernel<kSmallTable>, b, t);
+  int kind = a.master ? KIND_BF16 : KIND_ANY;
+  int64_t narrow = 0;
+  for (int64_t i = 0; i < count; ++i) narrow += t_used(tensors[i], grads[i]) && tensors[i].dtype == LORA_BF16;
+  if (narrow == 0) kind = KIND_F32;
+  else if (narrow != used) kind = KIND_ANY;
+  const auto step = [&](auto size, auto which) {
+    constexpr int N = decltype(size)::value, K = decltype(which)::value;
+    return over_table<N>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<N>& t) {
+      return b.bits == 8 ? run(adamw8_kernel<N, K>, b, t, true) : run(adamw_kernel<N, K>, b, t, false);
     });
-  return over_table<kTable>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<kTable>& t) {
-    return run(adamw_kernel<kTable>, b, t);
-  });
+  };
+  const auto sized = [&](auto which) {
+    if (used <= kSmallTable) return step(std::integral_constant<int, kSmallTable>{}, which);
+    return step(std::integral_constant<int, kTable>{}, which);
+  };
+  if (kind == KIND_BF16) return sized(std::integral_constant<int, KIND_BF16>{});
+  if (kind == KIND_F32) return sized(std::integral_constant<int, KIND_F32>{});
+  return sized(std::integral_constant<int, KIND_ANY>{});
 }
 
 }  // extern "C"
