@@ -174,7 +174,7 @@ def current_stream(device=None) -> int:
     """The handle of the device's current stream (by default the current device's), read without making
     a Stream object, which alone would cost 3 us a call."""
     index = None if device is None else device.index
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if index is None else index)
 
 
 def _stream(stream):

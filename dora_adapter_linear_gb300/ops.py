@@ -401,18 +401,24 @@ def w8a8_lora_fwd_packed(Xc, sx, Wb, sw, Z, B, s, bias=None, want_acc=False, wan
     return Y, acc
 
 
-def _row_stride(name, t, M, D, X):
-    """The row stride of t: a [M, D] tensor of X's dtype and device with rows of consecutive elements,
-    any stride of at least D between them."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != D or t.dtype is not X.dtype or t.device != X.device:
-        raise ValueError(f"{name} must be a {(M, D)} {X.dtype} tensor on {X.device}, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
+def _row_stride(name, t, X):
+    """The row stride of t: a tensor of X's shape [M, D], dtype and device with rows of consecutive
+    elements, any stride of at least D between them."""
+    if t.shape != X.shape or t.dtype is not X.dtype or t.device != X.device:
+        raise ValueError(f"{name} must be a {tuple(X.shape)} {X.dtype} tensor on {X.device}, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    M, D = t.shape
+    if t.is_contiguous() or M <= 1 and (D <= 1 or t.stride(1) == 1):
+        return D
     ld, step = t.stride()
-    if M <= 1:
-        ld = D
     if (step != 1 and D > 1) or ld < D:
         raise ValueError(f"{name} must have rows of consecutive elements that do not overlap, got strides {t.stride()}")
     return ld
+
+
+def _rows_like(X):
+    """A new contiguous tensor like X [M, D]."""
+    return torch.empty_like(X) if X.is_contiguous() else torch.empty(X.shape, dtype=X.dtype, device=X.device)
 
 
 def _need_cuda(name, t):
@@ -440,14 +446,15 @@ def _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, pos
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     M, D = X.shape
-    if w_pre is not None:
-        _check_vec("w_pre", w_pre, D, X, X.dtype)
-    if w_post is not None:
-        _check_vec("w_post", w_post, D, X, X.dtype)
-        if not post_norm:
-            raise ValueError("w_post needs post_norm=True")
+    for name, w in (("w_pre", w_pre), ("w_post", w_post)):
+        if w is not None and (w.shape != (D,) or w.dtype is not X.dtype or w.device != X.device
+                              or not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous [{D}] {X.dtype} tensor on {X.device}, got {tuple(w.shape)} "
+                             f"{w.dtype} on {w.device}")
+    if w_post is not None and not post_norm:
+        raise ValueError("w_post needs post_norm=True")
     per = 0 if gate is None else _gate_rows(gate, rows_per_gate, X)
-    return M, D, L.LoraNormShape(M, D, per, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0, L.dtype_code(X))
+    return L.LoraNormShape(M, D, per, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0, L.dtype_code(X))
 
 
 def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=None, alpha=1.0, eps=1e-6,
@@ -457,18 +464,18 @@ def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=
     w_pre) when pre_norm.  Weights are used as w + w_offset.  gate [G, D]: row i takes gate row
     i // rows_per_gate (by default the rows split evenly over the gate's).  Returns
     (Xout, H, r_pre, r_post); Xout is X when there is no Y, and what is not formed is None."""
-    M, D, sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
+    sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
     if Y is None and (gate is not None or post_norm or not pre_norm):
         raise ValueError("without a block output Y only the pre norm can be asked for")
     if w_pre is not None and not pre_norm:
         raise ValueError("w_pre needs pre_norm=True")
-    sh.ldx = _row_stride("X", X, M, D, X)
+    sh.ldx = _row_stride("X", X, X)
     if Y is not None:
-        sh.ldy = _row_stride("Y", Y, M, D, X)
+        sh.ldy = _row_stride("Y", Y, X)
     _need_cuda("X", X)
-    dev = X.device
-    Xout = torch.empty(M, D, dtype=X.dtype, device=dev) if Y is not None else None
-    H = torch.empty(M, D, dtype=X.dtype, device=dev) if pre_norm else None
+    M, dev = sh.M, X.device
+    Xout = None if Y is None else _rows_like(X)
+    H = _rows_like(X) if pre_norm else None
     r_pre = torch.empty(M, dtype=F32, device=dev) if pre_norm else None
     r_post = torch.empty(M, dtype=F32, device=dev) if post_norm else None
     L.block_norm_fwd(sh, X, Y, w_pre, w_post, gate, Xout, H, r_pre, r_post)
@@ -480,7 +487,8 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     """Gradients of block_norm_fwd from those of H (dH) and Xout (dXout; either may be None): returns
     (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
     and r_post."""
-    M, D, sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
+    sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
+    M = sh.M
     if dH is None and dXout is None:
         raise ValueError("at least one of dH and dXout is needed")
     if Y is None and (gate is not None or post_norm):
@@ -489,18 +497,17 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     _check_vec("r_post", r_post, M, Xout, F32)
     if (dH is not None and r_pre is None) or (post_norm and r_post is None):
         raise ValueError("r_pre (with dH) and r_post (with post_norm) come from the forward")
-    sh.ldx = _row_stride("Xout", Xout, M, D, Xout)
+    sh.ldx = _row_stride("Xout", Xout, Xout)
     if Y is not None:
-        sh.ldy = _row_stride("Y", Y, M, D, Xout)
+        sh.ldy = _row_stride("Y", Y, Xout)
     if dH is not None:
-        sh.lddh = _row_stride("dH", dH, M, D, Xout)
+        sh.lddh = _row_stride("dH", dH, Xout)
     if dXout is not None:
-        sh.lddz = _row_stride("dXout", dXout, M, D, Xout)
+        sh.lddz = _row_stride("dXout", dXout, Xout)
     _need_cuda("Xout", Xout)
     dev = Xout.device
-    new = lambda: torch.empty(M, D, dtype=Xout.dtype, device=dev)  # noqa: E731
-    dX = new() if need_dx else None
-    dY = new() if Y is not None else None
+    dX = _rows_like(Xout) if need_dx else None
+    dY = _rows_like(Xout) if Y is not None else None
     dw_pre = torch.empty_like(w_pre) if need_dw and w_pre is not None else None
     dw_post = torch.empty_like(w_post) if need_dw and w_post is not None else None
     dgate = torch.empty_like(gate) if need_dgate and gate is not None else None
