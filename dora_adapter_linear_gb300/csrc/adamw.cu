@@ -11,7 +11,7 @@
 // element whose v vanished would be divided by eps alone).  sqrt(v) instead of v halves the range
 // that the 4 exponent bits have to span; the rounding is at most 2^-4 of a normal value.
 // 28 bytes an element (bf16, fp32 master and states), 16 with 8-bit states.  32-bit states are bound by memory:
-// 42 M bf16 elements 174 us, 6.7 TB/s.
+// 42 M bf16 elements 174 to 177 us, 6.7 TB/s.
 //
 // The table of tensors travels in the launch's parameters (up to 32 KB), so a step copies nothing and
 // is captured by a CUDA graph as it is.
@@ -31,6 +31,7 @@ constexpr int kBlock = 256;           // elements of a state block
 constexpr int kSmallTable = 64, kTable = 640;
 constexpr int kNormCtas = 608;        // gradient-norm CTAs of one launch, 4 per SM of a 152-SM part
 constexpr int kStepCtas = 4;          // step CTAs of an SM: 64 registers a thread
+constexpr int kStep8Ctas = 2, kPair = 2;   // with 8-bit states; blocks that a warp takes at a time
 constexpr float kMinTop = 0x1p-110f;  // a block whose largest value is below this is stored as zeros
 
 struct AdamEntry {
@@ -325,58 +326,86 @@ __global__ void __launch_bounds__(256, kStepCtas) adamw_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ the step with 8-bit states
-// A block's arithmetic (square roots, quotients, two block maxima, the codes both ways: some 550 instructions
-// a warp) takes about as long as its 4 KB take from memory, so a warp must not wait for DRAM: it asks for its
-// next block in L2 while it works on this one.  168 M bf16 elements with masters: 473 us, 5.7 TB/s; without
-// the prefetch 570, with the next block's loads in registers (three CTAs an SM) 497, with asynchronous copies
-// into shared memory 690.  It issues 60% of the time: bound by the length of a block's chain, not by memory.
+// A block's arithmetic (square roots, quotients, two block maxima, the codes both ways) takes about as long
+// as its 4 KB take from memory, so nothing may stand between a warp and its next values: it takes two
+// blocks of a tensor at a time, all loads before the first use, and has asked L2 for the next two by then.
+// 168 M bf16 elements with masters: 414 us, 6.5 TB/s.  With one block at a time 617 us on two CTAs an SM and
+// 473 on four, with three or four 441 and 451, with two on three CTAs 463 (80 registers spill); one block
+// without the prefetch 570, one by asynchronous copies into shared memory 690.
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// a block's values as they are loaded
+struct Raw8Bit {
+  Eight g, p;
+  uint2 m, v;
+  float ms, vs;
+};
+
 template <int N, int KIND>
-__global__ void __launch_bounds__(256, kStepCtas) adamw8_kernel(const __grid_constant__ AdamArgs a,
-                                                        const __grid_constant__ AdamTable<N> table) {
+__global__ void __launch_bounds__(256, kStep8Ctas) adamw8_kernel(const __grid_constant__ AdamArgs a,
+                                                                 const __grid_constant__ AdamTable<N> table) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
   const int lane = threadIdx.x & 31;
   const StepFactors f = step_factors(a);
   uint8_t *const mc = static_cast<uint8_t*>(a.m), *const vc = static_cast<uint8_t*>(a.v);
+  // one block: i its lane's first element in the tensor, b its place in the state
+  auto load = [&](const AdamEntry& e, int dtype, bool full, int64_t i, int64_t b, Raw8Bit& r) {
+    const int64_t si = b * kBlock + lane * 8;
+    take_gp(a, e, dtype, full, has_master<KIND>(a, dtype), i, si, r.g, r.p);
+    r.m = *reinterpret_cast<const uint2*>(mc + si);
+    r.v = *reinterpret_cast<const uint2*>(vc + si);
+    r.ms = a.m_scale[b], r.vs = a.v_scale[b];
+  };
+  auto step = [&](const AdamEntry& e, int dtype, bool full, int64_t i, int64_t b, const Raw8Bit& r) {
+    const int64_t si = b * kBlock + lane * 8;
+    const bool master = has_master<KIND>(a, dtype);
+    F2 g[4], m[4], v[4], p[4];
+    open8(r.g, dtype, g);
+    open8(r.p, master ? (int)LORA_F32 : dtype, p);
+    decode8(r.m, r.ms, m);
+    decode8(r.v, r.vs, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
+    update8(a, f, e, g, m, v, g, p);
+    put_p(a, e, dtype, full, master, i, si, p);
+    encode_block<false>(mc + si, a.m_scale + b, m, lane);
+    encode_block<true>(vc + si, a.v_scale + b, g, lane);
+  };
   if (f.go) {
     for (Walk<N> at(a, table); at.valid();) {
       const AdamEntry& e = table.e[at.k];
-      const int32_t b0 = at.w - e.first, b = e.state + b0;
-      const int64_t i0 = (int64_t)b0 * kBlock, i = i0 + lane * 8, si = (int64_t)b * kBlock + lane * 8;
       const int dtype = type_of<KIND>(e);
-      const bool master = has_master<KIND>(a, dtype);
-      const bool full = whole(e.g, i0, e.n) && whole(e.p, i0, e.n);   // the same for the warp
-      Eight ge, pe;   // every load is on its way before the first value is opened
-      take_gp(a, e, dtype, full, master, i, si, ge, pe);
-      const uint2 mw = *reinterpret_cast<const uint2*>(mc + si), vw = *reinterpret_cast<const uint2*>(vc + si);
-      const float ms = a.m_scale[b], vs = a.v_scale[b];
+      const int64_t i0 = (int64_t)(at.w - e.first) * (kPair * kBlock), i = i0 + lane * 8;
+      const int64_t b = e.state + (int64_t)(at.w - e.first) * kPair;
       at.next();
-      if (at.valid() && lane < 4) {
-        const AdamEntry& n = table.e[at.k];
-        const int32_t nb0 = at.w - n.first;
-        const int64_t ns = (int64_t)(n.state + nb0) * kBlock;
-        const int ntype = type_of<KIND>(n), es = ntype == LORA_BF16 ? 2 : 4;
-        if (lane == 0) prefetch_l2(mc + ns, kBlock);
-        else if (lane == 1) prefetch_l2(vc + ns, kBlock);
-        else if (lane == 2 && has_master<KIND>(a, ntype)) prefetch_l2(a.master + ns, kBlock * 4);
-        else if (lane == 3 && whole(n.g, (int64_t)nb0 * kBlock, n.n))
-          prefetch_l2(static_cast<const char*>(n.g) + (int64_t)nb0 * kBlock * es, kBlock * es);
-      }
-      F2 g[4], m[4], v[4], p[4];
-      open8(ge, dtype, g);
-      open8(pe, master ? (int)LORA_F32 : dtype, p);
-      decode8(mw, ms, m);
-      decode8(vw, vs, v);
+      if (whole(e.g, i0 + (kPair - 1) * kBlock, e.n) && whole(e.p, i0 + (kPair - 1) * kBlock, e.n)) {   // both blocks; the same for the warp
+        Raw8Bit r[kPair];   // every load is on its way before the first value is opened
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], v[j]);
-      update8(a, f, e, g, m, v, g, p);
-      put_p(a, e, dtype, full, master, i, si, p);
-      encode_block<false>(mc + si, a.m_scale + b, m, lane);
-      encode_block<true>(vc + si, a.v_scale + b, g, lane);
+        for (int h = 0; h < kPair; ++h) load(e, dtype, true, i + h * kBlock, b + h, r[h]);
+        if (at.valid() && lane < 4) {
+          const AdamEntry& n = table.e[at.k];
+          const int ntype = type_of<KIND>(n), es = ntype == LORA_BF16 ? 2 : 4;
+          const int64_t n0 = (int64_t)(at.w - n.first) * (kPair * kBlock), ns = (int64_t)n.state * kBlock + n0;
+          if (whole(n.g, n0 + (kPair - 1) * kBlock, n.n)) {
+            if (lane == 0) prefetch_l2(mc + ns, kPair * kBlock);
+            else if (lane == 1) prefetch_l2(vc + ns, kPair * kBlock);
+            else if (lane == 2 && has_master<KIND>(a, ntype)) prefetch_l2(a.master + ns, kPair * kBlock * 4);
+            else if (lane == 3) prefetch_l2(static_cast<const char*>(n.g) + n0 * es, kPair * kBlock * es);
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < kPair; ++h) step(e, dtype, true, i + h * kBlock, b + h, r[h]);
+      } else {
+        for (int h = 0; h < kPair && i0 + h * kBlock < e.n; ++h) {
+          Raw8Bit r;
+          const bool full = whole(e.g, i0 + h * kBlock, e.n) && whole(e.p, i0 + h * kBlock, e.n);
+          load(e, dtype, full, i + h * kBlock, b + h, r);
+          step(e, dtype, full, i + h * kBlock, b + h, r);
+        }
+      }
     }
   }
   count_step(a, f);
@@ -489,9 +518,10 @@ lora_status check_table(const lora_adamw_tensor* t, const void* const* grads, in
 }
 
 // Runs `launch(args, table)` over the tensors that have a gradient, as many a launch as its table holds.
+// The launch's own numbering goes by `unit` blocks, the last of a tensor may be part of one.
 template <int N, typename F>
 lora_status over_table(const lora_adamw_tensor* t, const void* const* grads, int64_t count, int64_t used, AdamArgs a,
-                       F launch) {
+                       int unit, F launch) {
   AdamTable<N> table;
   int32_t state = 0;
   int64_t i = 0, left = used;
@@ -503,7 +533,7 @@ lora_status over_table(const lora_adamw_tensor* t, const void* const* grads, int
       if (t_used(t[i], grads[i])) {
         table.e[a.count++] =
             AdamEntry{t[i].p, grads[i], t[i].n, a.blocks, state, t[i].dtype, t[i].lr_mul, t[i].weight_decay};
-        a.blocks += nb;
+        a.blocks += (nb + unit - 1) / unit;
       }
       state += nb;
     }
@@ -574,10 +604,10 @@ lora_status adamw_grad_norm(const lora_adamw_tensor* tensors, const void* const*
     return LORA_OK;
   }
   if (used <= kSmallTable)
-    return over_table<kSmallTable>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<kSmallTable>& t) {
+    return over_table<kSmallTable>(tensors, grads, count, used, a, 1, [&](AdamArgs& b, const AdamTable<kSmallTable>& t) {
       return run(adamw_norm_kernel<kSmallTable>, b, t);
     });
-  return over_table<kTable>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<kTable>& t) {
+  return over_table<kTable>(tensors, grads, count, used, a, 1, [&](AdamArgs& b, const AdamTable<kTable>& t) {
     return run(adamw_norm_kernel<kTable>, b, t);
   });
 }
@@ -620,9 +650,9 @@ lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grad
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Two rounds a chunk; with 32-bit states a CTA for each chunk (448 tensors of 42 M elements, bf16: 174 us;
   // with one round 180, four 181, eight 188), with 8-bit ones as many CTAs as are resident, which know their
-  // next block (168 M elements: 473 us against 630).
+  // next blocks (168 M elements, one block at a time: 473 us against 630).
   const auto run = [&](auto kernel, AdamArgs& b, const auto& table, bool stay) {
-    const int64_t slots = kStepCtas * (int64_t)num_sms_current(), eights = (b.blocks + 7) / 8;
+    const int64_t slots = (stay ? kStep8Ctas : kStepCtas) * (int64_t)num_sms_current(), eights = (b.blocks + 7) / 8;
     b.rounds = eights >= 2 * slots ? 2 : 1;
     const int64_t chunks = (eights + b.rounds - 1) / b.rounds;
     CK(launch_pdl(kernel, dim3((unsigned)(stay && chunks > slots ? slots : chunks)), dim3(256), 0, st, b, table));
@@ -635,7 +665,7 @@ lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grad
   else if (narrow != used) kind = KIND_ANY;
   const auto step = [&](auto size, auto which) {
     constexpr int N = decltype(size)::value, K = decltype(which)::value;
-    return over_table<N>(tensors, grads, count, used, a, [&](AdamArgs& b, const AdamTable<N>& t) {
+    return over_table<N>(tensors, grads, count, used, a, a.bits == 8 ? kPair : 1, [&](AdamArgs& b, const AdamTable<N>& t) {
       return b.bits == 8 ? run(adamw8_kernel<N, K>, b, t, true) : run(adamw_kernel<N, K>, b, t, false);
     });
   };
