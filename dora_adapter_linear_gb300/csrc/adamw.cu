@@ -274,7 +274,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool valid() const { return w < w1; }
   __device__ __forceinline__ void begin() {
-    w = (int32_t)min(c0 + (threadIdx.x >> 5), (int64_t)INT32_MAX - 8);
+    w = (int32_t)min(c0, (int64_t)a.blocks) + (int32_t)(threadIdx.x >> 5);   // at most 2^30 blocks
     w1 = (int32_t)min((int64_t)a.blocks, c0 + 8 * a.rounds);
     if (!valid()) return;
     k = find_entry(table, a.count, w);
@@ -505,7 +505,7 @@ lora_status check_table(const lora_adamw_tensor* t, const void* const* grads, in
     if (t[i].dtype != LORA_F32 && t[i].dtype != LORA_BF16) return LORA_ERR_INVALID_ARG;
     if (!isfinite(t[i].lr_mul) || !isfinite(t[i].weight_decay)) return LORA_ERR_INVALID_ARG;
     b += (t[i].n + kBlock - 1) / kBlock;
-    if (b > (1LL << 31) - 1) return LORA_ERR_UNSUPPORTED;
+    if (b > 1LL << 30) return LORA_ERR_UNSUPPORTED;
     if (!t_used(t[i], grads[i])) continue;
     if (!t[i].p) return LORA_ERR_INVALID_ARG;
     const uintptr_t es = t[i].dtype == LORA_BF16 ? 2 : 4;

@@ -407,8 +407,10 @@ cudaError_t launch_walk(const NormArgs& a, cudaStream_t st) {
   const bool token = a.gate && a.rpg == 1;
   const size_t smem = 2 * (size_t)(token ? 3 : 2) * a.D * sizeof(T);   // at most 96 KB
   auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
     return launch_pdl(kernel, dim3((unsigned)(a.M < most ? a.M : most)), dim3((unsigned)threads), smem, st, a);
   };
   return token ? go(norm_fwd_walk_kernel<T, true>) : go(norm_fwd_walk_kernel<T, false>);

@@ -543,7 +543,8 @@ lora_status rotary_bwd(const lora_rotary_shape* sh, const void* dY, const void* 
  * contiguous device arrays of n elements of one dtype, aligned to their element (16-byte aligned
  * ones are faster); grads[i] NULL leaves tensor i and its state as they are.  The state of all
  * tensors is one array of 256-element blocks in the table's order; each tensor begins at a block of
- * its own.  Zero it before the first step; what lies past a tensor's end stays zero. */
+ * its own, at most 2^30 blocks in all.  Zero it before the first step; what lies past a tensor's end
+ * stays zero. */
 typedef struct {
     void* p;
     int64_t n;
