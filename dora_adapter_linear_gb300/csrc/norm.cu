@@ -855,25 +855,31 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
 
 // ------------------------------------------------------------------ backward: sums of the partials
 // CTA (t, j): columns 32 t .. 32 t + 31, one per lane.  j = 0: dw_pre, 1: dw_post, the warps sharing
-// the parts.  Past that the gate rows that more than one part has rows of: with few gate rows one a
-// CTA, its parts shared by the warps; with as many as there are boundaries between parts, a warp takes
-// the gate row that crosses a boundary (it has few parts then), if that boundary is its first.
-constexpr int kFinishWarps = 32;
+// the parts.  Past that the gate rows that more than one part has rows of: GATE_CTA one a CTA in the same way
+// (few gate rows, many parts each), GATE_WARP one a warp, GATE_BOUND (more gate rows than boundaries between
+// parts) a warp takes the gate row that crosses a boundary, if that boundary is its first.
+enum { GATE_NONE = 0, GATE_CTA = 1, GATE_WARP = 2, GATE_BOUND = 3 };
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kFinishWarps) norm_bwd_finish_kernel(const NormArgs a, const int gate_rows) {
+template <typename T, int HOW>
+__global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(const NormArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  __shared__ float acc[kFinishWarps][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float acc[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   const int job = (int)blockIdx.y - 2;
-  // partials first, first + step, .. last of this warp; slot(p) is where part p keeps this sum
+  // partials first, first + step, .. last of this warp, eight loads at a time; slot(p) is where part p keeps
+  // this sum
   auto add = [&](int first, int last, int step, auto slot) {
     float t = 0.f;
     if (col < a.D)
-#pragma unroll 16
-      for (int p = first; p <= last; p += step) t += slot(p)[col];
+      for (int p = first; p <= last; p += 8 * step) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p + j * step <= last ? slot(p + j * step)[col] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t += v[j];
+      }
     return t;
   };
   auto parts_of = [&](int64_t grp, int& first, int& last) {
@@ -881,30 +887,32 @@ __global__ void __launch_bounds__(32 * kFinishWarps) norm_bwd_finish_kernel(cons
     first = (int)(g0 / a.rp);
     last = (int)((g1 - 1) / a.rp);
   };
-  auto gate_slot = [&](int64_t grp) {
-    return [&a, grp](int p) { return a.pg + ((int64_t)p * 2 + ((int64_t)p * a.rp / a.rpg == grp ? 0 : 1)) * a.D; };
+  // its first part keeps a gate row in slot 1 unless it begins with it, the others begin with it
+  auto gate_slot = [&](int64_t grp, int first) {
+    const int late = grp * a.rpg > (int64_t)first * a.rp;
+    return [&a, first, late](int p) { return a.pg + ((int64_t)p * 2 + (p == first ? late : 0)) * a.D; };
   };
   T* out;
   float t;
-  if (job < 0) {
+  if (HOW == GATE_NONE || job < 0) {
     const float* src = job == -2 ? a.pw : a.pp;
     out = static_cast<T*>(job == -2 ? a.dw_pre : a.dw_post);
     if (!out) return;
-    t = add(warp, a.parts - 1, kFinishWarps, [&](int p) { return src + (int64_t)p * a.D; });
-  } else if (gate_rows) {
+    t = add(warp, a.parts - 1, warps, [&](int p) { return src + (int64_t)p * a.D; });
+  } else if (HOW == GATE_CTA) {
     int first, last;
     parts_of(job, first, last);
     if (first == last) return;   // written by its one part
     out = static_cast<T*>(a.dgate) + (int64_t)job * a.D;
-    t = add(first + warp, last, kFinishWarps, gate_slot(job));
+    t = add(first + warp, last, warps, gate_slot(job, first));
   } else {
-    const int p = job * kFinishWarps + warp + 1;   // the boundary before part p
-    if (p >= a.parts) return;
+    const int64_t item = (int64_t)job * warps + warp, b = (item + 1) * a.rp;   // b: the first row of part item + 1
+    const int64_t grp = HOW == GATE_WARP ? item : b / a.rpg;
+    if (grp * a.rpg >= a.M || (HOW == GATE_BOUND && item + 1 >= a.parts)) return;
     int first, last;
-    const int64_t grp = (int64_t)p * a.rp / a.rpg;
     parts_of(grp, first, last);
-    if (grp * a.rpg >= (int64_t)p * a.rp || first != p - 1) return;
-    t = add(first, last, 1, gate_slot(grp));
+    if (first == last || (HOW == GATE_BOUND && first != item)) return;
+    t = add(first, last, 1, gate_slot(grp, first));
     if (col < a.D) static_cast<T*>(a.dgate)[grp * a.D + col] = from_f<T>(t);
     return;
   }
@@ -912,8 +920,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) norm_bwd_finish_kernel(cons
   __syncthreads();
   if (warp == 0 && col < a.D) {
     t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kFinishWarps; ++w) t += acc[w][lane];
+    for (int w = 0; w < warps; ++w) t += acc[w][lane];
     out[col] = from_f<T>(t);
   }
 }
@@ -1052,12 +1059,24 @@ lora_status norm_bwd(NormArgs& a, const RingPlan& ring, cudaStream_t st) {
                     dim3(32 * kColWarps), 0, st, a));
   }
   if (!sums) return LORA_OK;
-  // gate rows that may cross a boundary: few of them a CTA each, otherwise a warp for each boundary
+  int warps = (a.parts + 7) / 8;   // eight partials a warp
+  warps = warps < 4 ? 4 : warps > 32 ? 32 : warps;
   const int64_t groups = a.dgate && a.parts > 1 ? (a.M + a.rpg - 1) / a.rpg : 0, bounds = a.parts - 1;
-  const bool each = groups <= (bounds + kFinishWarps - 1) / kFinishWarps;
-  const int64_t jobs = 2 + (groups == 0 ? 0 : each ? groups : (bounds + kFinishWarps - 1) / kFinishWarps);
-  CK(launch_pdl(norm_bwd_finish_kernel<T>, dim3((unsigned)((a.D + 31) / 32), (unsigned)jobs),
-                dim3(32 * kFinishWarps), 0, st, a, each ? 1 : 0));
+  int how = GATE_NONE;
+  int64_t jobs = 2;
+  if (groups > 0) {
+    how = groups > bounds ? GATE_BOUND : a.parts / groups > 64 ? GATE_CTA : GATE_WARP;
+    jobs += how == GATE_CTA ? groups : ((how == GATE_BOUND ? bounds : groups) + warps - 1) / warps;
+  }
+  auto finish = [&](auto kernel) {
+    return launch_pdl(kernel, dim3((unsigned)((a.D + 31) / 32), (unsigned)jobs), dim3(32 * warps), 0, st, a);
+  };
+  cudaError_t e;
+  if (how == GATE_NONE) e = finish(norm_bwd_finish_kernel<T, GATE_NONE>);
+  else if (how == GATE_CTA) e = finish(norm_bwd_finish_kernel<T, GATE_CTA>);
+  else if (how == GATE_WARP) e = finish(norm_bwd_finish_kernel<T, GATE_WARP>);
+  else e = finish(norm_bwd_finish_kernel<T, GATE_BOUND>);
+  CK(e);
   return LORA_OK;
 }
 
