@@ -7,6 +7,7 @@ raises LoraError on a non-OK status.  No arithmetic of the layer happens in Pyth
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
@@ -14,6 +15,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora_gb300.so")
+HOST_PATH = os.path.join(_HERE, "_host.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "lora_gb300.h")
 
 LORA_F32, LORA_BF16 = 0, 1
@@ -163,6 +165,26 @@ def _lib():
             f.argtypes = args
         _LIB = lib
     return _LIB
+
+
+_HOST = None
+
+
+def host():
+    """The module _host: operand checks, outputs and the C call of the short calls without Python in
+    between.  Loaded once, like the library, and bound to its entry points."""
+    global _HOST
+    if _HOST is None:
+        lib = _lib()
+        if not os.path.exists(HOST_PATH):
+            raise ImportError(f"{HOST_PATH} is missing; build it with dora_adapter_linear_gb300.build.build()")
+        spec = importlib.util.spec_from_file_location("_host", HOST_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(lib, name), c_void_p).value
+                      for name in ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd")])
+        _HOST = module
+    return _HOST
 
 
 def ptr(t):
@@ -475,7 +497,7 @@ def adamw_norm_workspace_bytes(count) -> int:
 
 
 def adamw_grad_norm(tensors, grads, count, grad_scale, max_norm, norm_coef, ws, stream=None):
-    """tensors: from adamw_tensors(); grads: the address of an array of pointers, or a ctypes array."""
+    """tensors: from adamw_tensors(); grads: an array of their addresses, as bytes or a ctypes array."""
     _ck(_lib().adamw_grad_norm(tensors, grads, count, float(grad_scale), float(max_norm), ptr(norm_coef), ptr(ws),
                                0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
         "adamw_grad_norm")

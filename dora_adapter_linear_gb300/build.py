@@ -1,7 +1,8 @@
-"""Build the C-ABI shared library liblora_gb300.so in-tree with nvcc (sm_103a only).
+"""Build the C-ABI shared library liblora_gb300.so in-tree with nvcc (sm_103a only), and _host.so, the
+host side of short calls against PyTorch's headers, with g++.
 
 Each translation unit under csrc/ is compiled in parallel, then linked with the static
-CUDA runtime.  The library is placed next to this file, where the binding loads it.
+CUDA runtime.  Both are placed next to this file, where the binding loads them.
 """
 from __future__ import annotations
 
@@ -10,11 +11,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liblora_gb300.so")
+HOST_SRC, HOST = os.path.join(CSRC, "host_path.cpp"), os.path.join(HERE, "_host.so")
 BUILD = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -33,12 +36,27 @@ def sources():
 
 
 def _stale(srcs) -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOST):
         return True
-    t = os.path.getmtime(LIB)
-    deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
+    deps = srcs + [HOST_SRC] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     deps.append(os.path.join(ROOT, "include", "lora_gb300.h"))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_host() -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = HOST + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(root, "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", cuda, HOST_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -60,8 +78,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(12, len(srcs) + 1)) as ex:
+        host = ex.submit(_build_host)
         objs = list(ex.map(compile_one, srcs))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,6 +2,8 @@
 the entry point of the same name.  PyTorch is used only for device memory and the stream."""
 from __future__ import annotations
 
+from functools import lru_cache
+
 import torch
 
 from . import _lib as L
@@ -457,6 +459,21 @@ def _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, pos
     return L.LoraNormShape(M, D, per, D, D, D, D, alpha, eps, w_offset, 1 if post_norm else 0, L.dtype_code(X))
 
 
+def _done(result, where):
+    """The outputs of a call that the host module has made, or its error."""
+    if type(result) is int:
+        raise L.LoraError(result, where)
+    return result
+
+
+@lru_cache(maxsize=256)
+def _norm_bwd_bytes(M, D, dtype):
+    if dtype not in (BF16, F32):
+        return 0
+    return L.block_norm_bwd_workspace_bytes(L.LoraNormShape(M, D, 1, D, D, D, D, 1.0, 1.0, 0.0, 0,
+                                                            L.LORA_BF16 if dtype == BF16 else L.LORA_F32))
+
+
 def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=None, alpha=1.0, eps=1e-6,
                    w_offset=0.0, pre_norm=True, post_norm=False):
     """The end of one block and the start of the next: Xout = X + alpha gate o p with p the block
@@ -464,6 +481,9 @@ def block_norm_fwd(X, Y=None, w_pre=None, w_post=None, gate=None, rows_per_gate=
     w_pre) when pre_norm.  Weights are used as w + w_offset.  gate [G, D]: row i takes gate row
     i // rows_per_gate (by default the rows split evenly over the gate's).  Returns
     (Xout, H, r_pre, r_post); Xout is X when there is no Y, and what is not formed is None."""
+    done = L.host().block_norm_fwd(X, Y, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, pre_norm, post_norm)
+    if done is not None:
+        return _done(done, "block_norm_fwd")
     sh = _norm_shape(X, w_pre, w_post, gate, rows_per_gate, alpha, eps, w_offset, post_norm)
     if Y is None and (gate is not None or post_norm or not pre_norm):
         raise ValueError("without a block output Y only the pre norm can be asked for")
@@ -487,6 +507,14 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     """Gradients of block_norm_fwd from those of H (dH) and Xout (dXout; either may be None): returns
     (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
     and r_post."""
+    if Xout.dim() == 2 and Xout.is_cuda:
+        need = _norm_bwd_bytes(*Xout.shape, Xout.dtype)
+        if need:
+            done = L.host().block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre, w_post, gate, rows_per_gate, alpha,
+                                           w_offset, post_norm, need_dx, need_dw, need_dgate,
+                                           workspace(need, Xout.device))
+            if done is not None:
+                return _done(done, "block_norm_bwd")
     sh = _norm_shape(Xout, w_pre, w_post, gate, rows_per_gate, alpha, 1.0, w_offset, post_norm)
     M = sh.M
     if dH is None and dXout is None:
@@ -516,7 +544,10 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     return dX, dY, dw_pre, dw_post, dgate
 
 
-def _rotary(call, X, pos, plan, out):
+def _rotary(inverse, X, pos, plan, out):
+    done = L.host().rotary(inverse, X, pos, plan.freq, plan.rot_dim, plan.scale, plan.layout, out)
+    if done is not None:
+        return _done(done, "rotary_bwd" if inverse else "rotary_fwd")
     if X.dim() != 3:
         raise ValueError(f"the heads must be [tokens, heads, head_dim], got {tuple(X.shape)}")
     M, H, hd = X.shape
@@ -540,7 +571,7 @@ def _rotary(call, X, pos, plan, out):
     yt, yh = (xt, xh) if out is X else (out.stride(0), out.stride(1))
     sh = L.LoraRotaryShape(M, H, hd, plan.rot_dim, xt, xh, yt, yh, plan.scale, plan.layout, 64 if wide else 32,
                            L.dtype_code(X))
-    call(sh, X, pos, plan.freq, out)
+    (L.rotary_bwd if inverse else L.rotary_fwd)(sh, X, pos, plan.freq, out)
     return out
 
 
@@ -548,9 +579,9 @@ def rotary_fwd(X, pos, plan, out=None):
     """Turns the heads X [tokens, heads, head_dim] (any token and head stride: the query and key heads
     of a packed projection are one view) by their positions pos [tokens]; `plan` from rotary_plan.
     out=X turns in place; by default a new contiguous tensor is returned."""
-    return _rotary(L.rotary_fwd, X, pos, plan, out)
+    return _rotary(False, X, pos, plan, out)
 
 
 def rotary_bwd(dY, pos, plan, out=None):
     """The gradient of rotary_fwd: the turn by the negative angle, with the same scale."""
-    return _rotary(L.rotary_bwd, dY, pos, plan, out)
+    return _rotary(True, dY, pos, plan, out)

@@ -2,8 +2,6 @@
 from __future__ import annotations
 
 import math
-from array import array
-from operator import attrgetter
 
 import torch
 
@@ -11,8 +9,6 @@ from . import _lib as L
 from .ops import workspace
 
 BLOCK = 256     # elements of a state block
-_SHAPE, _DTYPE = attrgetter("shape"), attrgetter("dtype")
-_Tensor = torch.Tensor
 
 
 def _each(name, value, count):
@@ -51,8 +47,6 @@ class AdamW:
             raise ValueError(f"betas must be in [0, 1) and eps above 0, got {betas}, {eps}")
         self.params, self.lr, self.betas, self.eps, self.state_bits = params, lr, (b1, b2), eps, state_bits
         n = len(params)
-        self._shapes, self._dtypes = list(map(_SHAPE, params)), list(map(_DTYPE, params))
-        self._devices = list(map(_Tensor.get_device, params))
         self._tensors = L.adamw_tensors(params, _each("lr_mul", lr_mul, n), _each("weight_decay", weight_decay, n))
         dev, blocks = params[0].device, L.adamw_state_blocks(self._tensors, n)
         code = torch.float8_e4m3fn if state_bits == 8 else torch.float32
@@ -76,20 +70,19 @@ class AdamW:
         return int(self._ctl[0])
 
     def _pointers(self, grads):
-        """The gradients' pointers, 0 for a None.  One pass over the list for each property, in C: a
-        loop with all checks in its body takes half as long again for hundreds of tensors."""
+        """The gradients' addresses, 0 for a None."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
-        if type(None) not in set(map(type, grads)) and (
-                list(map(_SHAPE, grads)) == self._shapes and list(map(_DTYPE, grads)) == self._dtypes
-                and list(map(_Tensor.get_device, grads)) == self._devices and all(map(_Tensor.is_contiguous, grads))):
-            return array("Q", map(_Tensor.data_ptr, grads))
+        at = L.host().pointers(grads, self.params)
+        if at is not None:
+            return at
+        grads = list(grads)
         for i, (g, p) in enumerate(zip(grads, self.params)):
             if g is not None and (g.shape != p.shape or g.dtype != p.dtype or g.device != p.device
                                   or not g.is_contiguous()):
                 raise ValueError(f"gradient {i} must be a contiguous {tuple(p.shape)} {p.dtype} tensor on {p.device}, "
                                  f"got {tuple(g.shape)} {g.dtype} on {g.device}")
-        return array("Q", [0 if g is None else g.data_ptr() for g in grads])
+        return L.host().pointers(grads, self.params)
 
     def step(self, grads, lr=None, max_norm=None, grad_scale=1.0):
         """One step from `grads`, a tensor (or None: its tensor stays) for each parameter, on the current
@@ -98,8 +91,7 @@ class AdamW:
         max_norm then clips their global norm.  With max_norm the norm before the clip is returned (a
         0-d tensor, nothing waits), and a step whose norm is not finite changes nothing and is not
         counted; max_norm=inf only guards."""
-        pointers, n, norm = self._pointers(grads), len(self.params), None
-        at = pointers.buffer_info()[0]
+        at, n, norm = self._pointers(grads), len(self.params), None
         lr = self.lr if lr is None else lr
         lr_dev = None
         if isinstance(lr, torch.Tensor):
