@@ -139,6 +139,7 @@ _SIGS = {
     "rotary_fwd": (c_int, [POINTER(LoraRotaryShape), P, P, P, P, P]),
     "rotary_bwd": (c_int, [POINTER(LoraRotaryShape), P, P, P, P, P]),
     "adamw_state_blocks": (c_int64, [POINTER(LoraAdamwTensor), c_int64]),
+    "adamw_fill_master": (c_int, [POINTER(LoraAdamwTensor), c_int64, P, P]),
     "adamw_norm_workspace_bytes": (c_size_t, [c_int64]),
     "adamw_grad_norm": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, c_float, c_float, P, P, c_size_t, P]),
     "adamw_step": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, POINTER(LoraAdamwState), POINTER(LoraAdamwHyper), P,
@@ -485,11 +486,15 @@ def rotary_bwd(sh, dY, pos, freq, dX, stream=None):
 def adamw_tensors(params, lr_mul, weight_decay):
     """A ctypes array of lora_adamw_tensor for the tensors, with the factor and decay of each."""
     return (LoraAdamwTensor * max(len(params), 1))(*[
-        LoraAdamwTensor(p.data_ptr(), p.numel(), a, d, dtype_code(p)) for p, a, d in zip(params, lr_mul, weight_decay)])
+        (p.data_ptr(), p.numel(), a, d, dtype_code(p)) for p, a, d in zip(params, lr_mul, weight_decay)])
 
 
 def adamw_state_blocks(tensors, count) -> int:
     return _lib().adamw_state_blocks(tensors, count)
+
+
+def adamw_fill_master(tensors, count, master, stream=None):
+    _ck(_lib().adamw_fill_master(tensors, count, ptr(master), _stream(stream)), "adamw_fill_master")
 
 
 def adamw_norm_workspace_bytes(count) -> int:

@@ -325,6 +325,27 @@ __global__ void __launch_bounds__(256, kStepCtas) adamw_kernel(const __grid_cons
   count_step(a, f);
 }
 
+// ------------------------------------------------------------------ masters from the parameters
+template <int N>
+__global__ void __launch_bounds__(256) adamw_master_kernel(const __grid_constant__ AdamArgs a,
+                                                           const __grid_constant__ AdamTable<N> table) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  for (Walk<N> at(a, table); at.valid(); at.next()) {
+    const AdamEntry& e = table.e[at.k];
+    if (e.dtype != LORA_BF16) continue;
+    const int32_t b0 = at.w - e.first;
+    const int64_t i0 = (int64_t)b0 * kBlock, i = i0 + lane * 8;
+    Eight r;
+    F2 f[4];
+    if (whole(e.p, i0, e.n)) take(e.p, LORA_BF16, i, r);
+    else take_each<bf16>(e.p, i, e.n, r);
+    open8(r, LORA_BF16, f);
+    store4x2(a.master + (int64_t)(e.state + b0) * kBlock + lane * 8, f);
+  }
+}
+
 // ------------------------------------------------------------------ the step with 8-bit states
 // A block's arithmetic (square roots, quotients, two block maxima, the codes both ways) takes about as long
 // as its 4 KB take from memory, so nothing may stand between a warp and its next values: it takes two
@@ -566,6 +587,32 @@ int64_t adamw_state_blocks(const lora_adamw_tensor* tensors, int64_t count) {
     b += (tensors[i].n + kBlock - 1) / kBlock;
   }
   return b;
+}
+
+lora_status adamw_fill_master(const lora_adamw_tensor* tensors, int64_t count, float* master, void* stream) {
+  if (count < 0 || (count > 0 && !tensors)) return LORA_ERR_INVALID_ARG;
+  // every tensor counts here: its own pointer stands in for a gradient
+  const void** self = static_cast<const void**>(malloc((size_t)(count > 0 ? count : 1) * sizeof(void*)));
+  if (!self) return LORA_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) self[i] = tensors[i].p;
+  int64_t used = 0;
+  lora_status e = check_table(tensors, self, count, &used);
+  for (int64_t i = 0; e == LORA_OK && i < count; ++i)
+    if (tensors[i].n > 0 && !tensors[i].p) e = LORA_ERR_INVALID_ARG;
+  if (e == LORA_OK && used > 0 && !master) e = LORA_ERR_INVALID_ARG;
+  if (e == LORA_OK && !al16(master)) e = LORA_ERR_MISALIGNED;
+  if (e == LORA_OK && used > 0) {
+    AdamArgs a = {};
+    a.master = master;
+    e = over_table<kTable>(tensors, self, count, used, a, 1, [&](AdamArgs& b, const AdamTable<kTable>& t) {
+      b.rounds = 1;
+      CK(launch_pdl(adamw_master_kernel<kTable>, dim3((unsigned)((b.blocks + 7) / 8)), dim3(256), 0,
+                    static_cast<cudaStream_t>(stream), b, t));
+      return LORA_OK;
+    });
+  }
+  free(self);
+  return e;
 }
 
 size_t adamw_norm_workspace_bytes(int64_t count) {

@@ -6,7 +6,6 @@ import math
 import torch
 
 from . import _lib as L
-from .ops import workspace
 
 BLOCK = 256     # elements of a state block
 
@@ -40,6 +39,9 @@ class AdamW:
                 raise ValueError(f"tensor {i} is on {p.device}, the first on {params[0].device}")
         if not params:
             raise ValueError("no tensors to optimise")
+        spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("two of the tensors share memory: each would be updated under the other's hands")
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         b1, b2 = betas
@@ -56,13 +58,13 @@ class AdamW:
         self.master = None
         if master and any(p.dtype == torch.bfloat16 for p in params):
             self.master = new(torch.float32, BLOCK)
-            rows = self.master.view(-1).split([-(-p.numel() // BLOCK) * BLOCK for p in params])
-            torch._foreach_copy_([r[:p.numel()] for r, p in zip(rows, params)], [p.view(-1) for p in params])
+            L.adamw_fill_master(self._tensors, n, self.master)
         self._ctl = torch.zeros(2, dtype=torch.int32, device=dev)
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._state = L.LoraAdamwState(ptr(self.m), ptr(self.v), ptr(self.m_scale), ptr(self.v_scale),
                                        ptr(self.master), ptr(self._ctl), state_bits)
-        self._ws_bytes = L.adamw_norm_workspace_bytes(n)
+        # of its own, so that a captured step keeps what it was captured with
+        self._ws = torch.zeros(L.adamw_norm_workspace_bytes(n), dtype=torch.uint8, device=dev)
 
     @property
     def steps(self) -> int:
@@ -103,18 +105,20 @@ class AdamW:
             if not max_norm > 0:
                 raise ValueError(f"max_norm must be above 0, got {max_norm}")
             norm = torch.empty(2, dtype=torch.float32, device=self.params[0].device)
-            L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm,
-                              workspace(self._ws_bytes, self.params[0].device))
+            L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm, self._ws)
         L.adamw_step(self._tensors, at, n, self._state, hyper, norm)
         return None if norm is None else norm[0]
 
     def state_dict(self):
         """The state as tensors (the optimiser's own, not copies) and the step count."""
         return {"step": self.steps, "m": self.m, "v": self.v, "m_scale": self.m_scale, "v_scale": self.v_scale,
-                "master": self.master}
+                "master": self.master, "sizes": [p.numel() for p in self.params]}
 
     def load_state_dict(self, state):
-        """Copies a state_dict() of an optimiser of the same tensors and state_bits into this one."""
+        """Copies a state_dict() of an optimiser of the same tensors and state_bits into this one.  The
+        tensors themselves are the caller's to restore; with masters the next step sets them from those."""
+        if state.get("sizes", [p.numel() for p in self.params]) != [p.numel() for p in self.params]:
+            raise ValueError("the state is of tensors of other sizes")
         for k in ("m", "v", "m_scale", "v_scale", "master"):
             mine, other = getattr(self, k), state[k]
             if (mine is None) != (other is None) or (mine is not None and (mine.shape != other.shape

@@ -553,8 +553,8 @@ typedef struct {
 } lora_adamw_tensor;
 /* bits 32: m, v fp32 [blocks, 256].  bits 8: m and sqrt(v) as e4m3 codes [blocks, 256], the value a
  * code stands for times m_scale / v_scale [blocks] (absmax / 448 of the block); a sqrt(v) above zero
- * keeps at least the smallest code.  master: fp32 [blocks, 256], the bf16 tensors' exact values (the
- * caller fills it once), or NULL: bf16 tensors are updated from their rounded values.
+ * keeps at least the smallest code.  master: fp32 [blocks, 256], the bf16 tensors' exact values
+ * (adamw_fill_master), or NULL: bf16 tensors are updated from their rounded values.
  * ctl: int32[2] {steps done, 0}, 8-byte aligned; the count moves on the device, so that a captured
  * graph counts its replays.  m, v, scales and master 16-byte aligned. */
 typedef struct {
@@ -571,6 +571,10 @@ typedef struct {
 
 /* State blocks of the set: the sum of ceil(n / 256); -1 on bad input. */
 int64_t adamw_state_blocks(const lora_adamw_tensor* tensors, int64_t count);
+
+/* master = the bf16 tensors' values in fp32, each from its own block on, zeros past its end (the blocks of
+ * fp32 tensors are left alone): once, before the first step.  master 16-byte aligned. */
+lora_status adamw_fill_master(const lora_adamw_tensor* tensors, int64_t count, float* master, void* stream);
 
 /* Bytes of workspace adamw_grad_norm needs for `count` tensors (0 on bad input). */
 size_t adamw_norm_workspace_bytes(int64_t count);

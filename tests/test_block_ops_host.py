@@ -331,6 +331,11 @@ def test_adamw_abi(lib):
     none = (ctypes.c_void_p * 1)(None)
     assert step(g=none) == 0 and step(count=0) == 0       # nothing has a gradient: nothing is launched
 
+    fill = lambda t=t, n=1, to=FAKE: lib.adamw_fill_master(t, n, to, None)  # noqa: E731
+    assert fill(t=None) == INVALID and fill(n=-1) == INVALID and fill(to=None) == INVALID and fill(to=ODD) == MISALIGNED
+    assert fill(t=_adamw_args(p=None)[0]) == INVALID and fill(t=_adamw_args(p=(1 << 20) + 1)[0]) == MISALIGNED
+    assert fill(n=0, to=None) == 0
+
     def norm(coef=FAKE, scale=1.0, most=1.0, ws=FAKE, size=1 << 30):
         return lib.adamw_grad_norm(t, g, 1, scale, most, coef, ws, size, None)
 

@@ -461,6 +461,18 @@ def test_adamw_steps(optim, dtypes, master, unaligned):
         assert not flat[used == 0].any()       # what lies past a tensor's end stays zero
 
 
+@pytest.mark.parametrize("unaligned", [False, True])
+@pytest.mark.parametrize("shapes", [SHAPES, [(5,)] * 700], ids=["few", "700"])
+def test_adamw_masters_are_the_parameters(optim, unaligned, shapes):
+    params, _ = adamw_set((BF16, F32, BF16), 12, unaligned, shapes)
+    opt = optim.AdamW(params)
+    left = opt.master.clone()
+    for p, m, rest in zip(params, rows(opt.master, params), rows(left, params)):
+        assert torch.equal(m, p.float()) if p.dtype == BF16 else not m.any()
+        rest.zero_()
+    assert not left.any()
+
+
 def encode_like(x, low):
     """The 8-bit blocks of fp32 values [blocks, 256], operation for operation."""
     top = x.abs().amax(1, keepdim=True)
@@ -601,6 +613,14 @@ def test_adamw_state_dict_and_refusals(optim):
             optim.AdamW([p.clone() for p in params], state_bits=40 - bits).load_state_dict(a.state_dict())
         with pytest.raises(ValueError):
             optim.AdamW(params[:2], state_bits=bits).load_state_dict(a.state_dict())
+    swapped = optim.AdamW([torch.zeros(512, device=DEV), torch.zeros(100, device=DEV)])
+    with pytest.raises(ValueError):     # as many blocks, other tensors
+        swapped.load_state_dict(optim.AdamW([torch.zeros(100, device=DEV), torch.zeros(512, device=DEV)]).state_dict())
+    flat = torch.zeros(100, device=DEV)
+    for shared in ([flat, flat], [flat[:60], flat[50:]]):
+        with pytest.raises(ValueError):
+            optim.AdamW(shared)
+    optim.AdamW([flat[:50], flat[50:], flat[:0]])
     opt = optim.AdamW(params)
     wrong = [grads[:-1], [grads[0].float()] + grads[1:], [grads[0].t().contiguous()] + grads[1:],
              [grads[0].cpu()] + grads[1:], [torch.zeros(520, 16, dtype=BF16, device=DEV).t()] + grads[1:]]
