@@ -86,17 +86,17 @@ __device__ __forceinline__ void close_b(const float (&f)[B / sizeof(T)], Bytes<B
 // A CTA takes `tokens` tokens: their angles, one sincospif for each pair of a token whatever the number of
 // heads, go to shared memory; its threads walk over the items (token, head, vector).  An item is P pairs:
 // two accesses of B bytes in the half layout, one in the interleaved one (two where B is a single
-// element); the vectors of the passed part follow them.  A thread has U items on their way, the first of
+// element); the vectors of the passed part (RB bytes) follow them.  A thread has U items on their way, the first of
 // them while the angles are formed.
-template <typename T, int B, bool INTER>
+template <typename T, int B, bool INTER, int RB>
 __global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  constexpr int E = B / sizeof(T);
+  constexpr int E = B / sizeof(T), ER = RB / sizeof(T);
   constexpr bool TWO = !INTER || E == 1;          // an item's pairs lie in two accesses
   constexpr int P = TWO ? E : E / 2, U = 2;
   extern __shared__ __align__(16) float2 cs[];    // [token][pair of the item][vector]: neighbours at neighbours
-  const int nv = a.half / P, per = nv + a.rest / E;
+  const int nv = a.half / P, per = nv + a.rest / ER;
   const int64_t tok0 = (int64_t)blockIdx.x * a.tokens;
   const int toks = (int)min((int64_t)a.tokens, a.M - tok0);
   // this thread's items: every blockDim-th, as (token, head, vector) with carries instead of divisions
@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
   const int st = blockDim.x / rows, sh = (blockDim.x - st * rows) / per, sv = blockDim.x - st * rows - sh * per;
   const T* x = static_cast<const T*>(a.x) + tok0 * a.xt;
   T* y = static_cast<T*>(a.y) + tok0 * a.yt;
-  Bytes<B> p[U], q[U];
+  static_assert(RB == B || RB == 2 * B, "the passed part is as wide or twice as wide");
+  Bytes<RB> p[U];
+  Bytes<B> q[U];
   T* out[U];
   int at[U];              // where the item's angles begin; -1: a vector that passes, -2: none
   auto fetch = [&]() {
@@ -115,10 +117,11 @@ __global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
       at[u] = -2;
       if (i < all) {
         const bool turned = v < nv;
-        const int c = turned ? (INTER ? 2 * P * v : P * v) : 2 * a.half + (v - nv) * E;
+        const int c = turned ? (INTER ? 2 * P * v : P * v) : 2 * a.half + (v - nv) * ER;
         const T* in = x + t * a.xt + h * a.xh + c;
         out[u] = y + t * a.yt + h * a.yh + c;
-        load_b<B, T>(in, p[u]);
+        if (RB == B || !turned) load_b<RB, T>(in, p[u]);
+        else load_b<B, T>(in, reinterpret_cast<Bytes<B>&>(p[u]));   // the first part of it
         if (TWO && turned) load_b<B, T>(in + (INTER ? 1 : a.half), q[u]);
         at[u] = turned ? t * a.half + v : -1;
       }
@@ -146,8 +149,9 @@ __global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
     for (int u = 0; u < U; ++u) {
       if (at[u] == -2) continue;
       if (at[u] >= 0) {
+        Bytes<B>& first = reinterpret_cast<Bytes<B>&>(p[u]);
         float f[E], g[E];
-        open_b<B, T>(p[u], f);
+        open_b<B, T>(first, f);
         if (TWO) open_b<B, T>(q[u], g);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
@@ -159,27 +163,28 @@ __global__ void __launch_bounds__(512) rotary_kernel(const RotArgs a) {
           m = fmaf(m0, r.x, -(n * r.y));
           n = fmaf(n, r.x, m0 * r.y);
         }
-        close_b<B, T>(f, p[u]);
+        close_b<B, T>(f, first);
         if (TWO) {
           close_b<B, T>(g, q[u]);
           store_b<B, T>(out[u] + (INTER ? 1 : a.half), q[u]);
         }
+        store_b<B, T>(out[u], first);
+      } else {
+        store_b<RB, T>(out[u], p[u]);
       }
-      store_b<B, T>(out[u], p[u]);
     }
     fetch();
   }
 }
 
-template <typename T, int B>
-cudaError_t launch(const RotArgs& a, bool inter, cudaStream_t st) {
-  constexpr int E = B / (int)sizeof(T);
-  const int P = inter && E > 1 ? E / 2 : E;
-  const int64_t items = (int64_t)a.H * (a.half / P + a.rest / E);   // of a token
+template <typename T, int B, bool INTER, int RB>
+cudaError_t launch(const RotArgs& a, cudaStream_t st) {
+  constexpr int E = B / (int)sizeof(T), ER = RB / (int)sizeof(T), P = INTER && E > 1 ? E / 2 : E;
+  const int64_t items = (int64_t)a.H * (a.half / P + a.rest / ER);   // of a token
   // A CTA reads about 40 KB (16384 x 40 heads of 128, bf16: 50 us in the half layout with 40 KB, 51 with 20 and
   // 55 with 160; 54 us in the interleaved one with 40 KB, 58 with 20), but rather there are two for every SM.
   RotArgs r = a;
-  int64_t tokens = 40960 / (items * B * (inter && E > 1 ? 1 : 2));
+  int64_t tokens = 40960 / (items * B * (INTER && E > 1 ? 1 : 2));
   const int64_t fit = 16384 / (a.half * (int64_t)sizeof(float2)), spread = a.M / (2 * num_sms_current());
   if (tokens > fit) tokens = fit;
   if (tokens > spread) tokens = spread;
@@ -188,8 +193,17 @@ cudaError_t launch(const RotArgs& a, bool inter, cudaStream_t st) {
   const int threads = mine >= 512 ? 256 : (int)((mine + 31) / 32 * 32);
   const dim3 grid((unsigned)((a.M + r.tokens - 1) / r.tokens));
   const size_t smem = (size_t)r.tokens * a.half * sizeof(float2);
-  return inter ? launch_pdl(rotary_kernel<T, B, true>, grid, dim3((unsigned)threads), smem, st, r)
-               : launch_pdl(rotary_kernel<T, B, false>, grid, dim3((unsigned)threads), smem, st, r);
+  return launch_pdl(rotary_kernel<T, B, INTER, RB>, grid, dim3((unsigned)threads), smem, st, r);
+}
+// heads: what the passed part's accesses have to divide.  It begins at twice a half, so where a half keeps
+// its accesses below 16 bytes the passed part may take twice as much (8192 x 12 heads of 72, 18 turned: 18.5
+// against 33 us).
+template <typename T, int B>
+cudaError_t launch(const RotArgs& a, bool inter, uintptr_t heads, cudaStream_t st) {
+  if (inter) return launch<T, B, true, B>(a, st);
+  if constexpr (B < 16)
+    if (a.rest && heads % (2 * B) == 0) return launch<T, B, false, 2 * B>(a, st);
+  return launch<T, B, false, B>(a, st);
 }
 
 lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, const uint64_t* freq, void* Y,
@@ -226,21 +240,21 @@ lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, 
   a.pos64 = sh->pos_bits == 64, a.inverse = inverse;
   const bool inter = sh->layout == LORA_ROTARY_INTERLEAVED;
   // the widest access that every address of a vector is a multiple of
-  uintptr_t bits = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y) |
-                   (uintptr_t)(inter ? sh->rot_dim : sh->rot_dim / 2) * es | (uintptr_t)a.rest * es;
-  if (M > 1) bits |= (uintptr_t)(a.xt | a.yt) * es;
-  if (H > 1) bits |= (uintptr_t)(a.xh | a.yh) * es;
+  uintptr_t heads = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Y) | (uintptr_t)a.rest * es;
+  if (M > 1) heads |= (uintptr_t)(a.xt | a.yt) * es;
+  if (H > 1) heads |= (uintptr_t)(a.xh | a.yh) * es;
+  const uintptr_t bits = heads | (uintptr_t)(inter ? sh->rot_dim : sh->rot_dim / 2) * es;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (sh->dtype == LORA_BF16) {
-    if (bits % 16 == 0) e = launch<bf16, 16>(a, inter, st);
-    else if (bits % 8 == 0) e = launch<bf16, 8>(a, inter, st);
-    else if (bits % 4 == 0) e = launch<bf16, 4>(a, inter, st);
-    else e = launch<bf16, 2>(a, inter, st);
+    if (bits % 16 == 0) e = launch<bf16, 16>(a, inter, heads, st);
+    else if (bits % 8 == 0) e = launch<bf16, 8>(a, inter, heads, st);
+    else if (bits % 4 == 0) e = launch<bf16, 4>(a, inter, heads, st);
+    else e = launch<bf16, 2>(a, inter, heads, st);
   } else {
-    if (bits % 16 == 0) e = launch<float, 16>(a, inter, st);
-    else if (bits % 8 == 0) e = launch<float, 8>(a, inter, st);
-    else e = launch<float, 4>(a, inter, st);
+    if (bits % 16 == 0) e = launch<float, 16>(a, inter, heads, st);
+    else if (bits % 8 == 0) e = launch<float, 8>(a, inter, heads, st);
+    else e = launch<float, 4>(a, inter, heads, st);
   }
   CK(e);
   return LORA_OK;
