@@ -611,14 +611,18 @@ __global__ void __launch_bounds__(32 * kColWarps) norm_bwd_cols_kernel(const Nor
 struct RingPlan {
   int threads, stages, ctas;          // ctas: per SM
   int vectors, rows;                  // of 8 columns a thread, and rows a barrier
-  uint32_t row_bytes, stage_bytes;
+  int arrays, half;                   // input rows a row; where a pair of CTAs splits it (0: one takes it all)
+  uint32_t stage_bytes;
 };
 constexpr int kMaxStages = 6, kRingThreads = 512;   // 16384 x 4096 bf16: 4 stages 172 us, 6 and more 128
 constexpr int kSmSmem = 227 * 1024, kRingStatic = 3 * 1024;   // of an SM; a CTA's share beside its ring
 
 // FULL: both gradients come in and dx and dy go out, so nothing of that is asked in the loop (126
 // against 140 us at 16384 x 4096 bf16).
-// K vectors of 8 columns a thread, R rows a barrier.
+// K vectors of 8 columns a thread, R rows a barrier.  pl.half != 0: a cluster of two CTAs shares a row, the
+// first takes its columns up to half; each adds the other's sums to its own, which they leave in each other's
+// shared memory (4096 x 8192 fp32: 179 us against 290 with a pass over rows and one over columns; the cluster barrier is about
+// 1 us a row).
 template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormArgs a, const RingPlan pl) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
@@ -629,7 +633,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
   __shared__ __align__(8) uint64_t full[kMaxStages];
   __shared__ __align__(16) float red[2 * 16 * N];
   __shared__ int abort_flag;
-  const int part = blockIdx.x, S = pl.stages;
+  __shared__ float other[2][N + 1];   // the other CTA's sums, and whether it has to stop
+  const int rank = pl.half ? (int)cluster_ctarank() : 0, part = pl.half ? blockIdx.x >> 1 : blockIdx.x, S = pl.stages;
+  const int D = (int)a.D, base = rank ? pl.half : 0, mine = !pl.half ? D : rank ? D - pl.half : pl.half;
   const int64_t r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
   const bool post = Y == POST_Y || (Y == ANY_Y && a.post);
   const bool has_dh = FULL || a.dh, has_dzi = FULL || a.dzi, has_dx = FULL || a.dx, has_dy = FULL || a.dy;
@@ -638,10 +644,11 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
   auto issue = [&](int64_t row, int s) {   // thread 0: the row's copies into stage s
     if (row >= r1) return;
     char* dst = ring + (size_t)s * pl.stage_bytes;
-    mbar_expect_tx(&full[s], pl.stage_bytes);
+    const uint32_t bytes = (uint32_t)mine * sizeof(T);
+    mbar_expect_tx(&full[s], pl.arrays * bytes);
     auto copy = [&](const void* src, int64_t ld) {
-      bulk_load(dst, static_cast<const T*>(src) + row * ld, pl.row_bytes, &full[s]);
-      dst += pl.row_bytes;
+      bulk_load(dst, static_cast<const T*>(src) + row * ld + base, bytes, &full[s]);
+      dst += bytes;
     };
     copy(a.x, a.ldx);
     if (has_dh) copy(a.dh, a.ldh);
@@ -656,19 +663,20 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
     for (int i = 0; i < S; ++i) issue(r0 + i, i);
   }
   __syncthreads();
+  if (R == 1 && pl.half) cluster_sync_all();   // before anything is left in the other CTA it has to run
 
-  // column of this thread's k-th vector; past D nothing is read or written
+  // column of this thread's k-th vector among the CTA's, past `mine` nothing is read or written; and in the row
   const auto col = [&](int k) { return (k * (int)blockDim.x + (int)threadIdx.x) * 8; };
-  const int D = (int)a.D;
+  const auto gcol = [&](int k) { return base + col(k); };
   F2 wz[K][4], u[K][4], dw[K][4], acc[K][4];   // u = alpha g w_p (TOKEN: alpha w_p); acc: N (TOKEN: dw_post)
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[k][i] = acc[k][i] = wz[k][i] = u[k][i] = f2(0.f);
-    if (col(k) >= D) continue;
-    weight4x2<T>(a.w_pre, col(k), a.off, wz[k]);
+    if (col(k) >= mine) continue;
+    weight4x2<T>(a.w_pre, gcol(k), a.off, wz[k]);
     if (TOKEN) {
-      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, u[k]);
+      weight4x2<T>(post ? a.w_post : nullptr, gcol(k), a.off, u[k]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], f2(a.alpha));
     }
@@ -676,10 +684,10 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
   auto begin_segment = [&](int64_t grp) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (col(k) >= D) continue;
+      if (col(k) >= mine) continue;
       F2 w[4];
-      gate4x2<T>(gate ? gate + grp * D : nullptr, col(k), a.alpha, u[k]);
-      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, w);
+      gate4x2<T>(gate ? gate + grp * D : nullptr, gcol(k), a.alpha, u[k]);
+      weight4x2<T>(post ? a.w_post : nullptr, gcol(k), a.off, w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], w[i]);
     }
@@ -687,21 +695,21 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
   auto end_segment = [&](int64_t seg0, int64_t grp) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (col(k) >= D) continue;
+      if (col(k) >= mine) continue;
       F2 w[4];
       if (a.dgate) {
-        weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, w);
+        weight4x2<T>(post ? a.w_post : nullptr, gcol(k), a.off, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = mul2(mul2(w[i], f2(a.alpha)), acc[k][i]);
         const int64_t g0 = grp * a.rpg, g1 = min(a.M, g0 + a.rpg);
-        if (g0 >= r0 && g1 <= r1) store4x2(static_cast<T*>(a.dgate) + grp * D + col(k), w);
-        else store4x2(a.pg + ((int64_t)part * 2 + (seg0 == r0 ? 0 : 1)) * D + col(k), w);
+        if (g0 >= r0 && g1 <= r1) store4x2(static_cast<T*>(a.dgate) + grp * D + gcol(k), w);
+        else store4x2(a.pg + ((int64_t)part * 2 + (seg0 == r0 ? 0 : 1)) * D + gcol(k), w);
       }
       if (a.pp) {   // the part's own partial sum grows by a segment; no one else touches it
-        float* pp = a.pp + (int64_t)part * D + col(k);
+        float* pp = a.pp + (int64_t)part * D + gcol(k);
         F2 sum[4];
         if (seg0 != r0) load4x2(pp, sum);
-        gate4x2<T>(gate ? gate + grp * D : nullptr, col(k), a.alpha, w);
+        gate4x2<T>(gate ? gate + grp * D : nullptr, gcol(k), a.alpha, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = fma2(w[i], acc[k][i], seg0 != r0 ? sum[i] : f2(0.f));
         store4x2(pp, sum);
@@ -744,10 +752,10 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
     // z, t = dz_in + r_z w_z dh and y of a vector; the first time also what the sums need of dh
     auto load_zty = [&](int r, int k, F2* s0) {
       load4x2(st[r] + col(k), z);
-      if (has_dzi) load4x2(st[r] + at_o * D + col(k), t[r]);
+      if (has_dzi) load4x2(st[r] + at_o * mine + col(k), t[r]);
       if (has_dh) {
         F2 h[4];
-        load4x2(st[r] + D + col(k), h);
+        load4x2(st[r] + mine + col(k), h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F2 rh = mul2(h[i], f2(r_z[r])), wh = mul2(rh, wz[k][i]);
@@ -758,7 +766,7 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
           t[r][i] = has_dzi ? add2(t[r][i], wh) : wh;
         }
       }
-      if (HAS_Y) load4x2(st[r] + at_y * D + col(k), y);
+      if (HAS_Y) load4x2(st[r] + at_y * mine + col(k), y);
     };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -774,10 +782,10 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
       F2 s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (col(k) >= D) continue;
+        if (col(k) >= mine) continue;
         load_zty(r, k, &s0);
         if (!post) continue;
-        if (TOKEN) load4x2(st[r] + (at_y + 1) * D + col(k), g);
+        if (TOKEN) load4x2(st[r] + (at_y + 1) * mine + col(k), g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F2 uy = mul2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], y[i]);
@@ -789,8 +797,23 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
       sums[3 * r + 1] = sum2(s1);
       sums[3 * r + 2] = sum2(s2);
     }
-    if (block_sums_of<N, 16>(sums, red, flip, bad)) break;
+    bool stop = block_sums_of<N, 16>(sums, red, flip, bad);
+    if (R == 1 && pl.half) {   // uniform over the cluster; only the variants with one row a barrier come in pairs
+      if (threadIdx.x == 0) {
+        const uint32_t to = mapa_shared(smem_u32(other[flip]), rank ^ 1);
+#pragma unroll
+        for (int i = 0; i <= N; ++i)
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(i < N ? sums[i] : stop ? 1.f : 0.f)
+                       : "memory");
+      }
+      __syncwarp();
+      cluster_sync_all();
+#pragma unroll
+      for (int i = 0; i < N; ++i) sums[i] += other[flip][i];
+      stop |= other[flip][N] != 0.f;
+    }
     flip ^= 1;
+    if (stop) break;
     if (threadIdx.x == 0)   // the stages of all rows before `row` are free now
       for (; next < row + S; ++next) {
         issue(next, refill);
@@ -804,19 +827,19 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
       const float cy = post ? r_y[r] * r_y[r] * r_y[r] * ((sums[3 * r + 1] - cz * sums[3 * r + 2]) * inv_d) : 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (col(k) >= D) continue;
+        if (col(k) >= mine) continue;
         if (K > 1) {
           load_zty(r, k, nullptr);
         } else if (R > 1) {   // t stays in registers, z and y come from the stage again
           load4x2(st[r] + col(k), z);
-          if (HAS_Y) load4x2(st[r] + at_y * D + col(k), y);
+          if (HAS_Y) load4x2(st[r] + at_y * mine + col(k), y);
         }
-        const int64_t at = (row + r) * D + col(k);
+        const int64_t at = (row + r) * D + gcol(k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[r][i] = fma2(f2(-cz), z[i], t[r][i]);
         if (has_dx) store4x2(static_cast<T*>(a.dx) + at, t[r]);
         if (!HAS_Y) continue;
-        if (TOKEN) load4x2(st[r] + (at_y + 1) * D + col(k), g);
+        if (TOKEN) load4x2(st[r] + (at_y + 1) * mine + col(k), g);
         if (TOKEN && a.dgate_rows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) z[i] = mul2(u[k][i], mul2(mul2(t[r][i], f2(r_y[r])), y[i]));
@@ -842,14 +865,18 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
     if (threadIdx.x == 0)
       for (int64_t k = row; k < min(r1, next); ++k)
         mbar_wait_drain(&full[(k - r0) % S], (uint32_t)((k - r0) / S) & 1, 100000000ull);
+    __syncthreads();
+    if (R == 1 && pl.half) cluster_sync_all();
     return;
   }
+  __syncthreads();
+  if (R == 1 && pl.half) cluster_sync_all();   // the other CTA may still write here
   if (HAS_Y && !TOKEN) end_segment(seg0, grp);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (col(k) >= D) continue;
-    if (a.pw) store4x2(a.pw + (int64_t)part * D + col(k), dw[k]);
-    if (TOKEN && a.pp) store4x2(a.pp + (int64_t)part * D + col(k), acc[k]);
+    if (col(k) >= mine) continue;
+    if (a.pw) store4x2(a.pw + (int64_t)part * D + gcol(k), dw[k]);
+    if (TOKEN && a.pp) store4x2(a.pp + (int64_t)part * D + gcol(k), acc[k]);
   }
 }
 
@@ -942,24 +969,31 @@ lora_status check_norm(const lora_norm_shape* sh) {
 
 // Ring plan of the one-pass backward with n input rows a row, or threads == 0 where no variant holds
 // them: those take the row and column kernels.  Small rows get several CTAs an SM (the 128 registers a
-// thread allow 512 threads).  Two rows a barrier take four stages, one row three.
+// thread allow 512 threads), rows too long for one CTA a pair of them.  Two rows a barrier take four
+// stages, one row three.
 RingPlan ring_plan(const lora_norm_shape& sh, int n) {
-  RingPlan p = {};
-  const int64_t es = sh.dtype == LORA_BF16 ? 2 : 4, vecs = sh.D / 8, stage = n * sh.D * es;
-  p.vectors = vecs <= kRingThreads ? 1 : 2;
-  const int64_t threads = (vecs + 32 * p.vectors - 1) / (32 * p.vectors) * 32;
-  if (threads > kRingThreads) return RingPlan{};
+  const bool narrow = sh.dtype == LORA_BF16;
+  const int64_t es = narrow ? 2 : 4;
   const auto budget = [](int ctas) { return (int64_t)(kSmSmem / ctas - kRingStatic); };
-  p.ctas = (int)(kRingThreads / threads < 16 ? kRingThreads / threads : 16);
-  while (p.ctas > 1 && 4 * stage > budget(p.ctas)) --p.ctas;
-  const int64_t fit = budget(p.ctas) / stage;
-  p.rows = p.vectors == 1 && fit >= 4 ? 2 : 1;
-  if (fit < 3 || (p.vectors == 2 && sh.dtype == LORA_F32)) return RingPlan{};
-  p.threads = (int)threads;
-  p.stages = (int)(fit < kMaxStages ? fit : kMaxStages);
-  p.row_bytes = (uint32_t)(sh.D * es);
-  p.stage_bytes = (uint32_t)stage;
-  return p;
+  for (int pair = 0; pair < 2; ++pair) {
+    const int64_t vecs = pair ? (sh.D / 8 + 1) / 2 : sh.D / 8, stage = n * vecs * 8 * es;
+    RingPlan p = {};
+    p.vectors = vecs <= kRingThreads && !(pair && narrow) ? 1 : 2;
+    if (p.vectors == 2 && !narrow) continue;   // three stages of fp32 do not fit then
+    p.threads = (int)((vecs + 32 * p.vectors - 1) / (32 * p.vectors) * 32);
+    if (p.threads > kRingThreads) continue;
+    p.ctas = pair ? 1 : (int)(kRingThreads / p.threads < 16 ? kRingThreads / p.threads : 16);
+    while (p.ctas > 1 && 4 * stage > budget(p.ctas)) --p.ctas;
+    const int64_t fit = budget(p.ctas) / stage;
+    p.rows = p.vectors == 1 && fit >= 4 && !pair ? 2 : 1;
+    if (fit < 3) continue;
+    p.stages = (int)(fit < kMaxStages ? fit : kMaxStages);
+    p.arrays = n;
+    p.half = pair ? (int)vecs * 8 : 0;
+    p.stage_bytes = (uint32_t)stage;
+    return p;
+  }
+  return RingPlan{};
 }
 
 // Row parts of the column sums: one a resident CTA in the one-pass backward; for the column kernel
@@ -967,7 +1001,7 @@ RingPlan ring_plan(const lora_norm_shape& sh, int n) {
 void norm_parts(const lora_norm_shape& sh, const RingPlan& ring, int64_t* rp, int* parts) {
   int64_t want;
   if (ring.threads) {
-    want = (int64_t)ring.ctas * num_sms_current();
+    want = (int64_t)ring.ctas * num_sms_current() / (ring.half ? 2 : 1);
     if (want > sh.M) want = sh.M;
   } else {
     const int64_t tiles = (sh.D + 255) / 256;
@@ -1025,8 +1059,24 @@ cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set = true;
   }
-  return launch_pdl(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>, dim3((unsigned)a.parts), dim3((unsigned)p.threads),
-                    (size_t)p.stages * p.stage_bytes, st, a, p);
+  const size_t smem = (size_t)p.stages * p.stage_bytes;
+  if (!p.half)
+    return launch_pdl(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>, dim3((unsigned)a.parts), dim3((unsigned)p.threads),
+                      smem, st, a, p);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(2 * (unsigned)a.parts);
+  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>, a, p);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <typename T, int K, int R>
 cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
@@ -1039,7 +1089,7 @@ cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
   return token ? launch_ring<T, K, R, PLAIN_Y, true, true>(a, p, st) : launch_ring<T, K, R, PLAIN_Y, false, true>(a, p, st);
 }
 // The variants that ring_plan can ask for: bf16 rows always fit four stages up to 4096 columns (one
-// vector a thread), fp32 ones do not fit three above them.
+// vector a thread) and come in pairs above 8192, fp32 ones above 4096.
 inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_t st, bf16) {
   return p.vectors == 2 ? launch_ring<bf16, 2, 1>(a, p, st) : launch_ring<bf16, 1, 2>(a, p, st);
 }
