@@ -621,8 +621,8 @@ constexpr int kSmSmem = 227 * 1024, kRingStatic = 3 * 1024;   // of an SM; a CTA
 // against 140 us at 16384 x 4096 bf16).
 // K vectors of 8 columns a thread, R rows a barrier.  pl.half != 0: a cluster of two CTAs shares a row, the
 // first takes its columns up to half; each adds the other's sums to its own, which they leave in each other's
-// shared memory (4096 x 8192 fp32: 179 us against 290 with a pass over rows and one over columns; the cluster barrier is about
-// 1 us a row).
+// shared memory (4096 x 8192 fp32: 179 us against 290 with a pass over rows and one over columns; the cluster
+// barrier is about 1 us a row).
 template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
 __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormArgs a, const RingPlan pl) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
