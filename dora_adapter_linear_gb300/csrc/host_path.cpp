@@ -95,7 +95,7 @@ bool norm_shape(lora_norm_shape* sh, const Tensor& x, const Arg& w_pre, const Ar
       per = PyLong_AsLongLong(rows_per_gate);
       if (per == -1 && PyErr_Occurred()) PyErr_Clear();
     }
-    if (per < 1 || G != (M + per - 1) / per) return false;
+    if (per < 1 || G != (M - 1) / per + 1) return false;
   }
   *sh = lora_norm_shape{M, D, per, D, D, D, D, (float)alpha, (float)eps, (float)off, post ? 1 : 0, dtype_of(x)};
   return true;

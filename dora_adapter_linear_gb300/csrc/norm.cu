@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
 // The post norm would put a second block sum in the row's way, behind the first.  With q = alpha g w_p o y
 // the sum of z^2 is sum x^2 + 2 r_y sum x q + r_y^2 sum q^2, so one block sum of four values serves both
 // norms; a row where those terms cancel to less than a quarter of their size (their rounding would be
-// more than four times that of the plain sum) takes the plain sum after all.
+// more than four times that of the plain sum) takes the plain sum after all, and so does one where they
+// overflow (sum q^2 can without sum z^2 doing so).
 template <typename T, int K, bool WARP, int Y>
 __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const NormArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const 
     }
     if (!a.h_out) return;
     zz = fmaf(2.f * r_y, s[1], size);
-    if (!(zz >= 0.25f * size)) {   // the same for the whole row
+    if (!(zz >= 0.25f * size) || isinf(size)) {   // the same for the whole row
       s[0] = sum2(xx), s[1] = s[2] = s[3] = 0.f;
       row_sums(s, 1);
       zz = s[0];
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kWalkThreads) norm_fwd_walk_kernel(const NormA
     zo += stride * D;
     if (!ho) continue;
     float zz = fmaf(2.f * r_y, s[1], size);
-    if (!(zz >= 0.25f * size)) {   // the same for the whole row
+    if (!(zz >= 0.25f * size) || isinf(size)) {   // the same for the whole row
       s[0] = sum2(xx), s[1] = s[2] = s[3] = 0.f;
       block_sums_of<4, 16>(s, red, flip);
       flip ^= 1;
@@ -1043,7 +1044,8 @@ NormArgs norm_args(const lora_norm_shape& sh, const void* x, const void* y, cons
                    const void* gate) {
   NormArgs a = {};
   a.M = sh.M, a.D = sh.D;
-  a.rpg = gate ? sh.rows_per_gate : (sh.M > 0 ? sh.M : 1);
+  a.rpg = sh.M > 0 ? sh.M : 1;   // more rows a gate row than there are rows are all of them
+  if (gate && sh.rows_per_gate < a.rpg) a.rpg = sh.rows_per_gate;
   a.ldx = sh.ldx, a.ldy = sh.ldy, a.ldh = sh.lddh, a.ldo = sh.lddz;
   a.x = x, a.y = y, a.w_pre = w_pre, a.w_post = w_post, a.gate = gate;
   a.alpha = sh.alpha, a.eps = sh.eps, a.off = sh.w_offset, a.post = sh.post_norm != 0;
@@ -1193,7 +1195,7 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
   const lora_status ew = check_ws(ws, ws_bytes, plan_norm_bwd(*sh, static_cast<char*>(ws), most_parts(*sh), &w));
   if (ew != LORA_OK) return ew;
   NormArgs a = norm_args(*sh, Xout, Y, w_pre, w_post, gate);
-  const bool token = gate && sh->rows_per_gate == 1;
+  const bool token = gate && a.rpg == 1;
   const RingPlan ring = ring_plan(*sh, 1 + (Y != nullptr) + (dH != nullptr) + (dXout != nullptr) + token);
   norm_parts(*sh, ring, &a.rp, &a.parts);
   a.r_pre = const_cast<float*>(r_pre), a.r_post = const_cast<float*>(r_post);

@@ -247,6 +247,27 @@ def test_norm_rows_that_cancel(ops, M, D, dtype):
     check_norm_fwd(ops.block_norm_fwd(t["X"], t["Y"], eps=1e-5, **kw), t, kw, True, dtype, 1e-5)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,D", [(6, 200), (30, 512), (1200, 2048)])
+def test_norm_large_output_with_a_large_weight(ops, M, D, dtype):
+    """sum (w_post y)^2 is past the fp32 range, sum y^2 and sum z^2 are not."""
+    t, kw = norm_case(M, D, dtype, "none", True, seed=21)
+    t["Y"] = t["Y"] * 1e16
+    kw["w_post"] = kw["w_post"] * 1e4
+    check_norm_fwd(ops.block_norm_fwd(t["X"], t["Y"], eps=1e-5, **kw), t, kw, True, dtype, 1e-5)
+
+
+@pytest.mark.parametrize("M,D", [(1, 512), (7, 512), (300, 4104), (40, 20488)])
+@pytest.mark.parametrize("per", [8192, 1 << 40, 1 << 60, (1 << 63) - 1])
+def test_norm_one_gate_row_for_more_rows_than_there_are(ops, M, D, per):
+    t, kw = norm_case(M, D, F32, "row", True, seed=22)
+    wide = {**kw, "rows_per_gate": per}
+    one, other = (ops.block_norm_fwd(t["X"], t["Y"], **k) for k in (kw, wide))
+    grads = [ops.block_norm_bwd(one[0], t["Y"], one[2], one[3], t["dH"], t["dXout"], **k) for k in (kw, wide)]
+    for a, b in zip((*one, *grads[0]), (*other, *grads[1])):
+        assert torch.equal(a, b)
+
+
 def test_norm_gradient_against_differences(ops):
     """fp32: the step's directional derivative by central differences of the forward itself."""
     t, kw = norm_case(24, 128, F32, "seq", True, seed=10, rpg=5, alpha=0.6)
