@@ -52,7 +52,7 @@ def _build_host() -> None:
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(root, "include"),
            "-I", sysconfig.get_paths()["include"], "-I", cuda, HOST_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
