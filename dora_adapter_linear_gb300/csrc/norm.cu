@@ -881,6 +881,212 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
   }
 }
 
+// ------------------------------------------------------------------ backward in one pass, short rows
+// G lanes take a row, so its sums need no barrier; the L groups of a CTA's eight warps take every L-th row of its
+// part.  Each lane keeps its own columns of its next rows on their way into shared memory, as the walk of the
+// forward does.  The column sums stay in registers and are added over the groups when the gate row changes (N,
+// as above) and at the end, so a CTA leaves one partial.  Against the ring of a CTA a row, whose barriers bound it:
+// bf16, 131072 x 64 22 against 78 us, x 128 39 against 79, 16384 x 256 14.7 against 25, x 512 25.6 against 29, 2000 x
+// 256 with a gate per row 5.6 against 10.8; fp32 16384 x 256 19 against 26.  Bound by memory where rows are many
+// (131072 x 128: 5.1 TB/s).  A whole warp for 128 columns takes 59 us there; three CTAs an SM spill registers.
+constexpr int kShortThreads = 256;
+template <typename T, int K, bool TOKEN>
+constexpr int short_stages() { return sizeof(T) == 2 && K == 1 ? 4 : TOKEN ? 2 : 3; }
+template <typename T, int K, int G, bool TOKEN>
+size_t short_smem(int64_t D) {
+  return kShortThreads / G * D * (short_stages<T, K, TOKEN>() * (TOKEN ? 5 : 4) * sizeof(T) + sizeof(float));
+}
+
+template <typename T, int K, int G, bool TOKEN>
+__global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const NormArgs a) {
+  pdl_wait();   // inputs may come from the previous kernel in the stream
+  if (threadIdx.x == 0) pdl_trigger();
+  constexpr int L = kShortThreads / G, S = short_stages<T, K, TOKEN>(), A = TOKEN ? 5 : 4;   // z, dh, dz_in, y, gate
+  extern __shared__ __align__(16) char stages[];
+  const int D = (int)a.D, lane = threadIdx.x % G, group = threadIdx.x / G;
+  const int64_t part = blockIdx.x, r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
+  const bool post = a.y && a.post;
+  const T* gate = static_cast<const T*>(a.gate);
+  float* const sums = reinterpret_cast<float*>(stages + (size_t)L * S * A * D * sizeof(T));   // [L][D]
+  T* const ring = reinterpret_cast<T*>(stages) + group * S * A * D;
+  int fill = 0, used = 0;   // where in the ring the next row goes, and the row in hand is
+  const auto col = [&](int k) { return (k * G + lane) * 8; };
+  auto issue = [&](int64_t row) {   // this lane's columns of a row; a group even past the end
+    if (row < r1) {
+      auto copy = [&](int at, const void* src, int64_t ld) {
+        const T* from = static_cast<const T*>(src) + row * ld;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (col(k) >= D) continue;
+#pragma unroll
+          for (int e = 0; e < 8; e += 16 / (int)sizeof(T)) cp_async16(ring + fill + at * D + col(k) + e, from + col(k) + e, true);
+        }
+      };
+      copy(0, a.x, a.ldx);
+      if (a.dh) copy(1, a.dh, a.ldh);
+      if (a.dzi) copy(2, a.dzi, a.ldo);
+      if (a.y) copy(3, a.y, a.ldy);
+      if (TOKEN) copy(4, a.gate, a.D);
+    }
+    cp_async_commit();
+    fill += A * D;
+    if (fill == S * A * D) fill = 0;
+  };
+  int64_t row = r0 + group;
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(row + i * L);
+  F2 wz[K][4], u[K][4], dw[K][4], acc[K][4];   // u = alpha g w_p (TOKEN: alpha w_p); acc: N (TOKEN: dw_post)
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[k][i] = acc[k][i] = f2(0.f);
+    if (col(k) < D) weight4x2<T>(a.w_pre, col(k), a.off, wz[k]);
+  }
+  // thread t: the sums over the groups of columns t, t + 256
+  auto over_groups = [&](F2 (&v)[K][4], float (&t)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (col(k) < D) store4x2(sums + group * D + col(k), v[k]);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = k * kShortThreads + (int)threadIdx.x;
+      t[k] = 0.f;
+      if (c < D)
+#pragma unroll 8
+        for (int l = 0; l < L; ++l) t[k] += sums[l * D + c];
+    }
+    __syncthreads();
+  };
+  const float inv_d = 1.f / (float)D;
+  float dpost[K], t1[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) dpost[k] = 0.f;
+  const auto factor = [&](const float* r, bool has, float other, int64_t at) { return has ? r[min(at, r1 - 1)] : other; };
+  float r_z2 = factor(a.r_pre, a.dh, 0.f, row), r_y2 = factor(a.r_post, post, 1.f, row);
+  for (int64_t seg0 = r0, seg_end; seg0 < r1; seg0 = seg_end) {   // rows of one gate row, uniform over the CTA
+    const int64_t grp = TOKEN ? 0 : seg0 / a.rpg;
+    seg_end = TOKEN ? r1 : min(r1, (grp + 1) * a.rpg);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (col(k) >= D) continue;
+      F2 w[4];
+      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, u[k]);
+      gate4x2<T>(!TOKEN && gate ? gate + grp * D : nullptr, col(k), a.alpha, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], w[i]);
+    }
+    // a warp stays while one of its groups has a row
+    for (bool mine; mine = row < seg_end, G == 32 ? mine : __any_sync(0xffffffffu, mine);) {
+      const float r_z = r_z2, r_y = r_y2;
+      const T* use = ring + used;
+      if (mine) {
+        issue(row + (S - 1) * L);   // into the stage that the last row left
+        r_z2 = factor(a.r_pre, a.dh, 0.f, row + L), r_y2 = factor(a.r_post, post, 1.f, row + L);
+        cp_async_wait<S - 1>();
+      }
+      F2 z[4], y[4], g[4], t[4], s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
+      auto load_zt = [&](int k, bool first) {   // z and t = dz_in + r_z w_z dh; the first time also what the sums need of dh
+        load4x2(use + col(k), z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = f2(0.f);
+        if (a.dzi) load4x2(use + 2 * D + col(k), t);
+        if (!a.dh) return;
+        load4x2(use + D + col(k), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 rh = mul2(g[i], f2(r_z)), wh = mul2(rh, wz[k][i]);
+          if (first) {
+            s0 = fma2(wh, z[i], s0);
+            dw[k][i] = fma2(rh, z[i], dw[k][i]);
+          }
+          t[i] = add2(t[i], wh);
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!mine || col(k) >= D) continue;
+        load_zt(k, true);
+        if (!post) continue;
+        load4x2(use + 3 * D + col(k), y);
+        if (TOKEN) load4x2(use + 4 * D + col(k), g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 uy = mul2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], y[i]);
+          s1 = fma2(uy, t[i], s1);
+          s2 = fma2(uy, z[i], s2);
+        }
+      }
+      float s[4] = {sum2(s0), sum2(s1), sum2(s2), 0.f};
+      spread<4, G>(warp_sums_of<4, G>(s), s);
+      if (K > 1) __syncwarp();   // z and y are read again rather than kept: 128 registers hold no more
+      const float cz = r_z * r_z * (s[0] * inv_d);   // s0 was summed over r_z w_z dh z
+      const float cy = post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_d) : 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!mine || col(k) >= D) continue;
+        if (K > 1) load_zt(k, false);
+        const int64_t at = row * D + col(k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = fma2(f2(-cz), z[i], t[i]);
+        if (a.dx) store4x2(static_cast<T*>(a.dx) + at, t);
+        if (!a.y) continue;
+        if (K > 1 || !post) load4x2(use + 3 * D + col(k), y);
+        if (TOKEN && (K > 1 || !post)) load4x2(use + 4 * D + col(k), g);
+        if (TOKEN && a.dgate_rows) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = mul2(u[k][i], mul2(mul2(t[i], f2(r_y)), y[i]));
+          store4x2(static_cast<T*>(a.dgate_rows) + at, z);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F2 e = mul2(t[i], f2(r_y));
+          if (TOKEN) acc[k][i] = fma2(mul2(mul2(g[i], f2(a.alpha)), e), y[i], acc[k][i]);
+          else acc[k][i] = fma2(e, y[i], acc[k][i]);
+          y[i] = fma2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], e, mul2(f2(-cy), y[i]));
+        }
+        if (a.dy) store4x2(static_cast<T*>(a.dy) + at, y);
+      }
+      if (!mine) continue;
+      row += L;
+      used += A * D;
+      if (used == S * A * D) used = 0;
+    }
+    if (TOKEN || !(a.dgate || a.pp)) continue;
+    over_groups(acc, t1);
+    const int64_t g0 = grp * a.rpg, g1 = min(a.M, g0 + a.rpg);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[k][i] = f2(0.f);
+      const int c = k * kShortThreads + (int)threadIdx.x;
+      if (c >= D) continue;
+      const float gc = gate ? to_f<T>(gate[grp * D + c]) : 1.f;
+      dpost[k] = fmaf(a.alpha * gc, t1[k], dpost[k]);
+      if (!a.dgate) continue;
+      const float wp = post && a.w_post ? to_f<T>(static_cast<const T*>(a.w_post)[c]) + a.off : 1.f;
+      const float dg = a.alpha * wp * t1[k];
+      if (g0 >= r0 && g1 <= r1) static_cast<T*>(a.dgate)[grp * D + c] = from_f<T>(dg);
+      else a.pg[(part * 2 + (seg0 == r0 ? 0 : 1)) * D + c] = dg;
+    }
+  }
+  auto leave = [&](float* to, const float (&v)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = k * kShortThreads + (int)threadIdx.x;
+      if (c < D) to[part * D + c] = v[k];
+    }
+  };
+  if (a.pp) {
+    if (TOKEN) over_groups(acc, dpost);
+    leave(a.pp, dpost);
+  }
+  if (a.pw) {
+    over_groups(dw, t1);
+    leave(a.pw, t1);
+  }
+}
+
 // ------------------------------------------------------------------ backward: sums of the partials
 // CTA (t, j): columns 32 t .. 32 t + 31, one per lane.  j = 0: dw_pre, 1: dw_post, the warps sharing
 // the parts.  Past that the gate rows that more than one part has rows of: GATE_CTA one a CTA in the same way
@@ -997,11 +1203,23 @@ RingPlan ring_plan(const lora_norm_shape& sh, int n) {
   return RingPlan{};
 }
 
-// Row parts of the column sums: one a resident CTA in the one-pass backward; for the column kernel
+// Whether the rows are short (rpg: rows that share a gate row, 0 without a gate): a group's columns fit two vectors
+// a lane, one of fp32, and a gate row's rows are all, or enough that the sum over the groups at its end costs less
+// than it saves: with 16 rows a gate 16384 x 256 takes 20 us against 27 (x 128: 15 against 25) and with 4 35 against
+// 29; above 256 columns 64 rows break even (16384 x 512: 30 against 31, with 16 39 against 32).
+bool short_rows(const lora_norm_shape& sh, int64_t rpg) {
+  if (sh.D > (sh.dtype == LORA_BF16 ? 512 : 256)) return false;
+  return rpg <= 1 || rpg >= (sh.D > 256 ? 64 : 16) || rpg >= sh.M;
+}
+
+// Row parts of the column sums: one a resident CTA in the one-pass backwards; for the column kernel
 // four CTAs per SM over all column tiles, at least 32 rows each.
-void norm_parts(const lora_norm_shape& sh, const RingPlan& ring, int64_t* rp, int* parts) {
+void norm_parts(const lora_norm_shape& sh, bool brief, const RingPlan& ring, int64_t* rp, int* parts) {
   int64_t want;
-  if (ring.threads) {
+  if (brief) {
+    want = 2 * num_sms_current();
+    if (want > (sh.M + 7) / 8) want = (sh.M + 7) / 8;
+  } else if (ring.threads) {
     want = (int64_t)ring.ctas * num_sms_current() / (ring.half ? 2 : 1);
     if (want > sh.M) want = sh.M;
   } else {
@@ -1028,13 +1246,13 @@ size_t plan_norm_bwd(const lora_norm_shape& sh, char* base, int parts, NormBwdWs
   w->pg = c.take<float>((size_t)parts * 2 * sh.D);
   return c.off;
 }
-// over every number of inputs a call may have: the plan depends on it
+// over the variants that a call may take: they depend on its inputs
 int most_parts(const lora_norm_shape& sh) {
   int most = 0;
-  for (int n = 1; n <= 5; ++n) {
+  for (int n = 0; n <= 5; ++n) {
     int64_t rp;
     int parts;
-    norm_parts(sh, ring_plan(sh, n), &rp, &parts);
+    norm_parts(sh, n == 0 && short_rows(sh, 0), n ? ring_plan(sh, n) : RingPlan{}, &rp, &parts);
     if (parts > most) most = parts;
   }
   return most;
@@ -1099,10 +1317,35 @@ inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_
   return p.rows == 2 ? launch_ring<float, 1, 2>(a, p, st) : launch_ring<float, 1, 1>(a, p, st);
 }
 
+template <typename T, int K, int G, bool TOKEN>
+cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
+  const size_t smem = short_smem<T, K, G, TOKEN>(a.D);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_bwd_short_kernel<T, K, G, TOKEN>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(norm_bwd_short_kernel<T, K, G, TOKEN>, dim3((unsigned)a.parts), dim3(kShortThreads), smem, st, a);
+}
+template <typename T, int K, int G>
+cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
+  return a.gate && a.rpg == 1 ? launch_short<T, K, G, true>(a, st) : launch_short<T, K, G, false>(a, st);
+}
 template <typename T>
-lora_status norm_bwd(NormArgs& a, const RingPlan& ring, cudaStream_t st) {
+cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
+  if (a.D <= 64) return launch_short<T, 1, 8>(a, st);
+  if (a.D <= 128) return launch_short<T, 1, 16>(a, st);
+  if constexpr (sizeof(T) == 2)
+    if (a.D > 256) return launch_short<T, 2, 32>(a, st);
+  return launch_short<T, 1, 32>(a, st);
+}
+
+template <typename T>
+lora_status norm_bwd(NormArgs& a, bool brief, const RingPlan& ring, cudaStream_t st) {
   const bool sums = a.dw_pre || a.dw_post || a.dgate;
-  if (a.M > 0 && ring.threads) {
+  if (a.M > 0 && brief) {
+    CK(launch_short<T>(a, st));
+  } else if (a.M > 0 && ring.threads) {
     CK(launch_plan(a, ring, st, T{}));
   } else if (a.M > 0) {
     CK(launch_pdl(norm_bwd_rows_kernel<T>, dim3((unsigned)a.M), dim3((unsigned)row_threads(a.D)), 0, st, a));
@@ -1197,7 +1440,8 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
   NormArgs a = norm_args(*sh, Xout, Y, w_pre, w_post, gate);
   const bool token = gate && a.rpg == 1;
   const RingPlan ring = ring_plan(*sh, 1 + (Y != nullptr) + (dH != nullptr) + (dXout != nullptr) + token);
-  norm_parts(*sh, ring, &a.rp, &a.parts);
+  const bool brief = short_rows(*sh, gate ? a.rpg : 0);
+  norm_parts(*sh, brief, ring, &a.rp, &a.parts);
   a.r_pre = const_cast<float*>(r_pre), a.r_post = const_cast<float*>(r_post);
   a.dh = dH, a.dzi = dXout, a.dx = dX, a.dy = dY;
   a.dw_pre = dw_pre, a.dw_post = dw_post;
@@ -1209,7 +1453,7 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
   a.pp = dw_post ? w.pp : nullptr;
   a.pg = w.pg;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return sh->dtype == LORA_BF16 ? norm_bwd<bf16>(a, ring, st) : norm_bwd<float>(a, ring, st);
+  return sh->dtype == LORA_BF16 ? norm_bwd<bf16>(a, brief, ring, st) : norm_bwd<float>(a, brief, ring, st);
 }
 
 }  // extern "C"

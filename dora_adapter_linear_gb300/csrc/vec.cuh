@@ -71,15 +71,6 @@ struct Raw8;
 template <>
 struct Raw8<bf16> {
   uint4 v;
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 t = unpack_bf16x2(w[i]);
-      f[2 * i] = t.x;
-      f[2 * i + 1] = t.y;
-    }
-  }
   __device__ __forceinline__ void get(F2 (&f)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -89,10 +80,6 @@ struct Raw8<bf16> {
 template <>
 struct Raw8<float> {
   float4 a, b;
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  }
   __device__ __forceinline__ void get(F2 (&f)[4]) const {
     f[0] = f2(a.x, a.y), f[1] = f2(a.z, a.w), f[2] = f2(b.x, b.y), f[3] = f2(b.z, b.w);
   }
@@ -102,12 +89,6 @@ __device__ __forceinline__ void stream8(const bf16* p, Raw8<bf16>& r) { r.v = __
 __device__ __forceinline__ void stream8(const float* p, Raw8<float>& r) {
   r.a = __ldcs(reinterpret_cast<const float4*>(p));
   r.b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-}
-
-__device__ __forceinline__ void shared8(const bf16* p, Raw8<bf16>& r) { r.v = *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void shared8(const float* p, Raw8<float>& r) {
-  r.a = *reinterpret_cast<const float4*>(p);
-  r.b = *(reinterpret_cast<const float4*>(p) + 1);
 }
 
 // Sums of N values over the block (a multiple of 32 threads, at most 1024), given to every thread
@@ -160,29 +141,14 @@ __device__ __forceinline__ void store4x2(float* p, const F2 (&f)[4]) {
   *(reinterpret_cast<ulonglong2*>(p) + 1) = make_ulonglong2(f[2].v, f[3].v);
 }
 
-// streaming stores: rows that this kernel does not read again
-__device__ __forceinline__ void stream4x2(bf16* p, const F2 (&f)[4]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = unpack(f[i]);
-    w[i] = pack_bf16x2(t.x, t.y);
-  }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-}
-__device__ __forceinline__ void stream4x2(float* p, const F2 (&f)[4]) {
-  const float2 a = unpack(f[0]), b = unpack(f[1]), c = unpack(f[2]), d = unpack(f[3]);
-  __stcs(reinterpret_cast<float4*>(p), make_float4(a.x, a.y, b.x, b.y));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(c.x, c.y, d.x, d.y));
-}
-
-// Sums of N (4 or 8) values over a warp: value i ends up in the lanes i Q .. i Q + Q - 1, Q = 32 / N.
-// Each of the first steps halves the values that a lane still carries: 9 shuffles for 8 values, not 40.
-template <int N>
+// Sums of N (4 or 8) values over each G neighbouring lanes of a warp: value i ends up in their lanes i Q ..
+// i Q + Q - 1, Q = G / N.  Each of the first steps halves the values that a lane still carries: 9 shuffles for
+// 8 values of a warp, not 40.
+template <int N, int G = 32>
 __device__ __forceinline__ float warp_sums_of(float (&v)[N]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
+  for (int n = N / 2, o = G / 2; n >= 1; n /= 2, o /= 2) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
@@ -192,13 +158,13 @@ __device__ __forceinline__ float warp_sums_of(float (&v)[N]) {
   }
   float t = v[0];
 #pragma unroll
-  for (int o = 16 / N; o >= 1; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+  for (int o = G / 2 / N; o >= 1; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
 }
-template <int N>
+template <int N, int G = 32>
 __device__ __forceinline__ void spread(float t, float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * (32 / N));
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t, i * (G / N), G);
 }
 
 // Sums of N (4 or 8) values over a block of at most W warps (16 or 32), all of them given to every

@@ -148,6 +148,46 @@ def test_norm(ops, M, D, gate, post, more, dtype):
         assert (a is None and b is None) or torch.equal(a, b)      # sums in a fixed order
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,D,gate,post,more", [
+    (1, 64, "token", True, {}), (3, 8, "row", True, {}), (7, 128, "none", False, {}), (2500, 72, "none", True, dict(off=1.0)),
+    (2600, 136, "seq", True, dict(rpg=16)), (10001, 64, "seq", False, dict(rpg=17)), (9000, 128, "token", True, {}),
+    (5003, 256, "token", False, dict(alpha=-0.3)), (4099, 264, "seq", True, dict(rpg=64)), (4100, 512, "row", True, {}),
+    (2700, 512, "token", True, dict(off=1.0)), (3000, 504, "none", False, dict(y=False)), (640, 40, "seq", True, dict(rpg=5)),
+    (33, 256, "seq", True, dict(rpg=32)), (20000, 16, "none", True, {}), (700, 96, "none", False, dict(y=False)),
+])
+def test_norm_backward_of_short_rows(ops, M, D, gate, post, more, dtype):
+    test_norm(ops, M, D, gate, post, more, dtype)
+
+
+@pytest.mark.parametrize("D", [64, 120, 256, 512])
+@pytest.mark.parametrize("which", ["dH", "dXout", "dX", "dw", "dgate"])
+@pytest.mark.parametrize("gate", ["token", "seq"])
+def test_norm_backward_of_short_rows_in_part(ops, D, which, gate):
+    t, kw = norm_case(333, D, BF16, gate, True, seed=23, rpg=100)
+    Xout, _, r_pre, r_post = ops.block_norm_fwd(t["X"], t["Y"], **kw)
+    full = ops.block_norm_bwd(Xout, t["Y"], r_pre, r_post, t["dH"], t["dXout"], **kw)
+    if which in t:
+        t[which] = None
+        check_norm_bwd(ops.block_norm_bwd(Xout, t["Y"], r_pre, r_post, t["dH"], t["dXout"], **kw), Xout, t, kw, r_pre,
+                       r_post, BF16)
+        return
+    got = ops.block_norm_bwd(Xout, t["Y"], r_pre, r_post, t["dH"], t["dXout"], need_dx=which != "dX",
+                             need_dw=which != "dw", need_dgate=which != "dgate", **kw)
+    for name, a, b in zip(("dX", "dY", "dw", "dw", "dgate"), got, full):
+        assert a is None if name == which else torch.equal(a, b)
+
+
+def test_norm_backward_of_short_rows_past_32_bit_offsets(ops):
+    M, D, ld = 3, 256, (1 << 30) + 8
+    t, kw = norm_case(M, D, BF16, "none", True, seed=24)
+    X = torch.empty(2 * ld + D, dtype=BF16, device=DEV).as_strided((M, D), (ld, 1))
+    X.copy_(t["X"])
+    _, _, r_pre, r_post = ops.block_norm_fwd(t["X"], t["Y"], **kw)
+    a, b = (ops.block_norm_bwd(x, t["Y"], r_pre, r_post, t["dH"], t["dXout"], **kw) for x in (X, t["X"]))
+    assert all(torch.equal(a[i], b[i]) for i in range(4))
+
+
 @pytest.mark.parametrize("which", ["dH", "dXout"])
 def test_norm_backward_with_one_gradient(ops, which):
     t, kw = norm_case(50, 520, BF16, "row", True, seed=4)
