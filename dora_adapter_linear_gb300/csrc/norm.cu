@@ -1360,7 +1360,9 @@ lora_status norm_bwd(NormArgs& a, bool brief, const RingPlan& ring, cudaStream_t
   int how = GATE_NONE;
   int64_t jobs = 2;
   if (groups > 0) {
-    how = groups > bounds ? GATE_BOUND : a.parts / groups > 64 ? GATE_CTA : GATE_WARP;
+    // with 64 parts a gate row a warp takes longer than the CTAs do to come and go (2000 x 256, 4 gate rows: 11.1
+    // against 7.4 us), with 38 not (16384 x 4096: 130.6 against 131.5)
+    how = groups > bounds ? GATE_BOUND : a.parts / groups > 48 ? GATE_CTA : GATE_WARP;
     jobs += how == GATE_CTA ? groups : ((how == GATE_BOUND ? bounds : groups) + warps - 1) / warps;
   }
   auto finish = [&](auto kernel) {
