@@ -156,24 +156,25 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormArgs a) {
 
 // ------------------------------------------------------------------ forward, the row in registers
 // A thread holds K vectors of 8 columns, so x and y are read once and all their loads are in flight
-// together.  G threads share a row: a whole CTA, or a warp with 8 rows a CTA.
+// together.  G lanes of a warp share a row, or a whole CTA (G = 0).
 // The post norm would put a second block sum in the row's way, behind the first.  With q = alpha g w_p o y
 // the sum of z^2 is sum x^2 + 2 r_y sum x q + r_y^2 sum q^2, so one block sum of four values serves both
 // norms; a row where those terms cancel to less than a quarter of their size (their rounding would be
 // more than four times that of the plain sum) takes the plain sum after all, and so does one where they
 // overflow (sum q^2 can without sum z^2 doing so).
-template <typename T, int K, bool WARP, int Y>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const NormArgs a) {
+template <typename T, int K, int G, int Y>
+__global__ void __launch_bounds__(G ? 256 : 1024) norm_fwd_held_kernel(const NormArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  __shared__ __align__(16) float red[WARP ? 1 : 2 * 4 * 32];
-  const int t = WARP ? threadIdx.x & 31 : threadIdx.x, group = WARP ? 32 : blockDim.x, D = (int)a.D;
-  const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && row >= a.M) return;
+  __shared__ __align__(16) float red[G ? 1 : 2 * 4 * 32];
+  const int t = G ? threadIdx.x % G : threadIdx.x, group = G ? G : blockDim.x, D = (int)a.D;
+  const int64_t at = G ? (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G : blockIdx.x;
+  const bool mine = !G || at < a.M;   // a group past the last row goes along for its warp's shuffles
+  const int64_t row = mine ? at : 0;
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const T* y = Y ? static_cast<const T*>(a.y) + row * a.ldy : nullptr;
   const T* gate = Y && a.gate ? static_cast<const T*>(a.gate) + row / a.rpg * D : nullptr;
-  const auto col = [&](int k) { return (k * group + t) * 8; };
+  const auto col = [&](int k) { return mine ? (k * group + t) * 8 : D; };
   Raw8<T> xr[K], yr[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const 
     stream8(x + col(k), xr[k]);
   }
   auto row_sums = [&](float (&v)[4], int flip) {
-    if (WARP) spread<4>(warp_sums_of<4>(v), v);
+    if (G) spread<4, G ? G : 32>(warp_sums_of<4, G ? G : 32>(v), v);
     else block_sums_of<4, 32>(v, red, flip);
   };
   F2 q[K][4], p[4], w[4];   // q: what r_y times is added to x; later z
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const 
   float zz = s[0];
   if (Y == POST_Y) {
     const float r_y = rsqrtf(s[3] / (float)D + a.eps), size = fmaf(r_y * r_y, s[2], s[0]);
-    if (t == 0 && a.r_post) a.r_post[row] = r_y;
+    if (t == 0 && mine && a.r_post) a.r_post[row] = r_y;
     xx = f2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -244,14 +245,15 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const 
     }
     if (!a.h_out) return;
     zz = fmaf(2.f * r_y, s[1], size);
-    if (!(zz >= 0.25f * size) || isinf(size)) {   // the same for the whole row
+    const bool plain = !(zz >= 0.25f * size) || isinf(size);   // the same for the whole row
+    if (G && G < 32 ? __any_sync(0xffffffffu, plain) : plain) {
       s[0] = sum2(xx), s[1] = s[2] = s[3] = 0.f;
       row_sums(s, 1);
-      zz = s[0];
+      if (plain) zz = s[0];
     }
   }
   const float r_z = rsqrtf(zz / (float)D + a.eps);
-  if (t == 0 && a.r_pre) a.r_pre[row] = r_z;
+  if (t == 0 && mine && a.r_pre) a.r_pre[row] = r_z;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (col(k) >= D) continue;
@@ -262,13 +264,13 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) norm_fwd_held_kernel(const 
   }
 }
 
-template <typename T, int K, bool WARP>
+template <typename T, int K, int G>
 cudaError_t launch_held(const NormArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)(WARP ? (a.M + 7) / 8 : a.M));
-  const dim3 cta((unsigned)(WARP ? 256 : (a.D / 8 + 32 * K - 1) / (32 * K) * 32));
-  if (!a.y) return launch_pdl(norm_fwd_held_kernel<T, K, WARP, NO_Y>, grid, cta, 0, st, a);
-  if (!a.post) return launch_pdl(norm_fwd_held_kernel<T, K, WARP, PLAIN_Y>, grid, cta, 0, st, a);
-  return launch_pdl(norm_fwd_held_kernel<T, K, WARP, POST_Y>, grid, cta, 0, st, a);
+  const dim3 grid((unsigned)(G ? (a.M + 256 / (G ? G : 1) - 1) / (256 / (G ? G : 1)) : a.M));
+  const dim3 cta((unsigned)(G ? 256 : (a.D / 8 + 32 * K - 1) / (32 * K) * 32));
+  if (!a.y) return launch_pdl(norm_fwd_held_kernel<T, K, G, NO_Y>, grid, cta, 0, st, a);
+  if (!a.post) return launch_pdl(norm_fwd_held_kernel<T, K, G, PLAIN_Y>, grid, cta, 0, st, a);
+  return launch_pdl(norm_fwd_held_kernel<T, K, G, POST_Y>, grid, cta, 0, st, a);
 }
 
 // ------------------------------------------------------------------ forward with a post norm, many rows
@@ -419,7 +421,8 @@ cudaError_t launch_walk(const NormArgs& a, cudaStream_t st) {
 
 // Rows that are all resident at once (half the threads of the SMs) want the shortest chain: one vector a
 // thread (1 x 4096 bf16: 2.4 against 2.7 us with two; at 512 rows 5.7 against 4.7).  Beyond that:
-//   up to 256 columns a warp a row (16384 x 256 bf16: 7.6 us), for bf16 up to 512 (16384 x 512 without a post
+//   up to 256 columns a warp a row (16384 x 256 bf16: 7.6 us), up to 128 and 64 a half and a quarter of one
+//   (131072 x 128 25 us against 44 with a warp, x 64 13 against 43), for bf16 up to 512 (16384 x 512 without a post
 //   norm: 12.5 against 17 us);
 //   bf16 with a post norm the walk from 512 to 8192 columns (16384 x 512: 11.5 against 12.5 us with a warp a
 //   row, x 2048: 43 against 47, x 8192: 85 per 8192 rows against 97);
@@ -430,12 +433,14 @@ template <typename T>
 cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   constexpr bool narrow = sizeof(T) == 2;
   const int64_t vecs = a.D / 8;
-  if (vecs <= 32) return launch_held<T, 1, true>(a, st);
-  if (narrow && vecs < 64 + !(a.y && a.post)) return launch_held<T, 2, true>(a, st);
-  if (vecs <= 1024 && a.M * vecs <= 1024LL * num_sms_current()) return launch_held<T, 1, false>(a, st);
+  if (vecs <= 8) return launch_held<T, 1, 8>(a, st);
+  if (vecs <= 16) return launch_held<T, 1, 16>(a, st);
+  if (vecs <= 32) return launch_held<T, 1, 32>(a, st);
+  if (narrow && vecs < 64 + !(a.y && a.post)) return launch_held<T, 2, 32>(a, st);
+  if (vecs <= 1024 && a.M * vecs <= 1024LL * num_sms_current()) return launch_held<T, 1, 0>(a, st);
   if (narrow && a.y && a.post && vecs >= 64 && vecs <= 1024) return launch_walk<bf16>(a, st);
-  if (!narrow && vecs <= 256) return launch_held<T, 1, false>(a, st);
-  if (vecs <= 2048) return launch_held<T, 2, false>(a, st);
+  if (!narrow && vecs <= 256) return launch_held<T, 1, 0>(a, st);
+  if (vecs <= 2048) return launch_held<T, 2, 0>(a, st);
   return launch_pdl(norm_fwd_kernel<T>, dim3((unsigned)a.M), dim3((unsigned)row_threads(a.D)), 0, st, a);
 }
 

@@ -308,6 +308,14 @@ def test_norm_one_gate_row_for_more_rows_than_there_are(ops, M, D, per):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,D", [(13, 8), (77, 64), (501, 40), (50, 72), (333, 128), (9, 256)])
+def test_norm_forward_of_short_rows(ops, M, D, dtype):
+    """Several rows a warp, of which some take the plain sum and some the one from its terms."""
+    test_norm_rows_that_cancel(ops, M, D, dtype)
+    test_norm_large_output_with_a_large_weight(ops, M, D, dtype)
+
+
 def test_norm_gradient_against_differences(ops):
     """fp32: the step's directional derivative by central differences of the forward itself."""
     t, kw = norm_case(24, 128, F32, "seq", True, seed=10, rpg=5, alpha=0.6)
