@@ -225,6 +225,18 @@ PyObject* py_pointers(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (tensor): a 0-d fp32 tensor next to it whose storage holds two values, the second behind the one it shows
+PyObject* py_pair(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 1) return not_here();
+  const Arg like(a[0]);
+  if (!like || !(*like).is_cuda()) return not_here();
+  const Tensor t = fresh(*like, {2}, at::kFloat);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({});
+  return THPVariable_Wrap(t);
+  END_HANDLE_TH_ERRORS
+}
+
 // (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd): addresses in the loaded library
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   void* at[4];
@@ -249,6 +261,7 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), "take the library's entry point
                          {"block_norm_fwd", FAST(py_norm_fwd), "ops.block_norm_fwd"},
                          {"block_norm_bwd", FAST(py_norm_bwd), "ops.block_norm_bwd"},
                          {"rotary", FAST(py_rotary), "ops.rotary_fwd and rotary_bwd"},
+                         {"pair", FAST(py_pair), "an optimiser's norm and factor"},
                          {"pointers", FAST(py_pointers), "addresses of an optimiser's gradients"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", "host side of short calls", -1, methods, nullptr, nullptr, nullptr,

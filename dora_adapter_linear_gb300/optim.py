@@ -104,10 +104,10 @@ class AdamW:
         if max_norm is not None:
             if not max_norm > 0:
                 raise ValueError(f"max_norm must be above 0, got {max_norm}")
-            norm = torch.empty(2, dtype=torch.float32, device=self.params[0].device)
+            norm = L.host().pair(self.params[0])   # shows the norm, the factor lies behind it
             L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm, self._ws)
         L.adamw_step(self._tensors, at, n, self._state, hyper, norm)
-        return None if norm is None else norm[0]
+        return norm
 
     def state_dict(self):
         """The state as tensors (the optimiser's own, not copies) and the step count."""

@@ -127,3 +127,15 @@ def test_gradient_addresses(ops):
     for bad in (g[:1], [g[0].t(), g[1]], [g[0].double(), g[1]], [g[0].cpu(), g[1]], [1, g[1]],
                 [torch.zeros(5, 3, device=DEV).t(), g[1]]):
         assert at(bad, p) is None
+
+
+def test_norms_of_consecutive_steps_are_their_own(ops):
+    from dora_adapter_linear_gb300 import optim
+    p = [torch.zeros(40, 8, device="cuda")]
+    opt = optim.AdamW(p)
+    norms = [opt.step([torch.full_like(p[0], float(i))], max_norm=1.0) for i in range(1, 6)]
+    assert all(n.shape == () and n.dtype is torch.float32 and n.is_cuda for n in norms)
+    want = torch.arange(1, 6) * 320 ** 0.5
+    assert torch.allclose(torch.stack(norms).cpu(), want, rtol=1e-6)
+    copy = norms[2].clone()
+    assert copy.item() == norms[2].item() and norms[2].view(1).sum().item() == copy.item()
