@@ -422,8 +422,9 @@ cudaError_t launch_walk(const NormArgs& a, cudaStream_t st) {
 // Rows that are all resident at once (half the threads of the SMs) want the shortest chain: one vector a
 // thread (1 x 4096 bf16: 2.4 against 2.7 us with two; at 512 rows 5.7 against 4.7).  Beyond that:
 //   up to 256 columns a warp a row (16384 x 256 bf16: 7.6 us), up to 128 and 64 a half and a quarter of one
-//   (131072 x 128 25 us against 44 with a warp, x 64 13 against 43), for bf16 up to 512 (16384 x 512 without a post
-//   norm: 12.5 against 17 us);
+//   (131072 x 128 25 us against 44 with a warp, x 64 13 against 43); two vectors a lane for bf16 up to 512 (16384 x
+//   512 without a post norm: 12.5 against 17 us) and fp32 up to 384 (11274 x 264: 9.8 against 12.1, x 384: 11.6
+//   against 12.3, x 504: 15.2 against 14.0);
 //   bf16 with a post norm the walk from 512 to 8192 columns (16384 x 512: 11.5 against 12.5 us with a warp a
 //   row, x 2048: 43 against 47, x 8192: 85 per 8192 rows against 97);
 //   fp32 one vector up to 2048 columns (8192 x 1024: 20 us against 21 with the walk and 28 with two vectors),
@@ -436,8 +437,8 @@ cudaError_t norm_fwd(const NormArgs& a, cudaStream_t st) {
   if (vecs <= 8) return launch_held<T, 1, 8>(a, st);
   if (vecs <= 16) return launch_held<T, 1, 16>(a, st);
   if (vecs <= 32) return launch_held<T, 1, 32>(a, st);
-  if (narrow && vecs < 64 + !(a.y && a.post)) return launch_held<T, 2, 32>(a, st);
   if (vecs <= 1024 && a.M * vecs <= 1024LL * num_sms_current()) return launch_held<T, 1, 0>(a, st);
+  if (vecs < (narrow ? 64 + !(a.y && a.post) : 49)) return launch_held<T, 2, 32>(a, st);
   if (narrow && a.y && a.post && vecs >= 64 && vecs <= 1024) return launch_walk<bf16>(a, st);
   if (!narrow && vecs <= 256) return launch_held<T, 1, 0>(a, st);
   if (vecs <= 2048) return launch_held<T, 2, 0>(a, st);

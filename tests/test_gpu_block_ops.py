@@ -309,7 +309,8 @@ def test_norm_one_gate_row_for_more_rows_than_there_are(ops, M, D, per):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("M,D", [(13, 8), (77, 64), (501, 40), (50, 72), (333, 128), (9, 256)])
+@pytest.mark.parametrize("M,D", [(13, 8), (77, 64), (501, 40), (50, 72), (333, 128), (9, 256), (8000, 264),
+                                 (5001, 384)])
 def test_norm_forward_of_short_rows(ops, M, D, dtype):
     """Several rows a warp, of which some take the plain sum and some the one from its terms."""
     test_norm_rows_that_cancel(ops, M, D, dtype)
