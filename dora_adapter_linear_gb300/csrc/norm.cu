@@ -892,9 +892,10 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
 // part.  Each lane keeps its own columns of its next rows on their way into shared memory, as the walk of the
 // forward does.  The column sums stay in registers and are added over the groups when the gate row changes (N,
 // as above) and at the end, so a CTA leaves one partial.  Against the ring of a CTA a row, whose barriers bound it:
-// bf16, 131072 x 64 22 against 78 us, x 128 39 against 79, 16384 x 256 14.7 against 25, x 512 25.6 against 29, 2000 x
-// 256 with a gate per row 5.6 against 10.8; fp32 16384 x 256 19 against 26.  Bound by memory where rows are many
-// (131072 x 128: 5.1 TB/s).  A whole warp for 128 columns takes 59 us there; three CTAs an SM spill registers.
+// bf16, 131072 x 64 22 against 78 us, x 128 39 against 79, 16384 x 256 13 against 25, x 512 25 against 29, 2000 x
+// 256 with a gate per row 5.4 against 10.8; fp32 16384 x 256 19 against 26.  Bound by memory where rows are many
+// (131072 x 128: 5.2 TB/s).  A whole warp for 128 columns takes 59 us there; three CTAs an SM spill registers.
+// FULL as above (16384 x 256: 13.2 against 14.7 us).
 constexpr int kShortThreads = 256;
 template <typename T, int K, bool TOKEN>
 constexpr int short_stages() { return sizeof(T) == 2 && K == 1 ? 4 : TOKEN ? 2 : 3; }
@@ -903,7 +904,7 @@ size_t short_smem(int64_t D) {
   return kShortThreads / G * D * (short_stages<T, K, TOKEN>() * (TOKEN ? 5 : 4) * sizeof(T) + sizeof(float));
 }
 
-template <typename T, int K, int G, bool TOKEN>
+template <typename T, int K, int G, bool TOKEN, bool FULL>
 __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const NormArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
@@ -911,7 +912,8 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
   extern __shared__ __align__(16) char stages[];
   const int D = (int)a.D, lane = threadIdx.x % G, group = threadIdx.x / G;
   const int64_t part = blockIdx.x, r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
-  const bool post = a.y && a.post;
+  const bool has_y = FULL || a.y, has_dh = FULL || a.dh, has_dzi = FULL || a.dzi, has_dx = FULL || a.dx, has_dy = FULL || a.dy;
+  const bool post = has_y && a.post;
   const T* gate = static_cast<const T*>(a.gate);
   float* const sums = reinterpret_cast<float*>(stages + (size_t)L * S * A * D * sizeof(T));   // [L][D]
   T* const ring = reinterpret_cast<T*>(stages) + group * S * A * D;
@@ -929,9 +931,9 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
         }
       };
       copy(0, a.x, a.ldx);
-      if (a.dh) copy(1, a.dh, a.ldh);
-      if (a.dzi) copy(2, a.dzi, a.ldo);
-      if (a.y) copy(3, a.y, a.ldy);
+      if (has_dh) copy(1, a.dh, a.ldh);
+      if (has_dzi) copy(2, a.dzi, a.ldo);
+      if (has_y) copy(3, a.y, a.ldy);
       if (TOKEN) copy(4, a.gate, a.D);
     }
     cp_async_commit();
@@ -969,7 +971,7 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
 #pragma unroll
   for (int k = 0; k < K; ++k) dpost[k] = 0.f;
   const auto factor = [&](const float* r, bool has, float other, int64_t at) { return has ? r[min(at, r1 - 1)] : other; };
-  float r_z2 = factor(a.r_pre, a.dh, 0.f, row), r_y2 = factor(a.r_post, post, 1.f, row);
+  float r_z2 = factor(a.r_pre, has_dh, 0.f, row), r_y2 = factor(a.r_post, post, 1.f, row);
   for (int64_t seg0 = r0, seg_end; seg0 < r1; seg0 = seg_end) {   // rows of one gate row, uniform over the CTA
     const int64_t grp = TOKEN ? 0 : seg0 / a.rpg;
     seg_end = TOKEN ? r1 : min(r1, (grp + 1) * a.rpg);
@@ -988,7 +990,7 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
       const T* use = ring + used;
       if (mine) {
         issue(row + (S - 1) * L);   // into the stage that the last row left
-        r_z2 = factor(a.r_pre, a.dh, 0.f, row + L), r_y2 = factor(a.r_post, post, 1.f, row + L);
+        r_z2 = factor(a.r_pre, has_dh, 0.f, row + L), r_y2 = factor(a.r_post, post, 1.f, row + L);
         cp_async_wait<S - 1>();
       }
       F2 z[4], y[4], g[4], t[4], s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
@@ -996,8 +998,8 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
         load4x2(use + col(k), z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = f2(0.f);
-        if (a.dzi) load4x2(use + 2 * D + col(k), t);
-        if (!a.dh) return;
+        if (has_dzi) load4x2(use + 2 * D + col(k), t);
+        if (!has_dh) return;
         load4x2(use + D + col(k), g);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1035,8 +1037,8 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
         const int64_t at = row * D + col(k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = fma2(f2(-cz), z[i], t[i]);
-        if (a.dx) store4x2(static_cast<T*>(a.dx) + at, t);
-        if (!a.y) continue;
+        if (has_dx) store4x2(static_cast<T*>(a.dx) + at, t);
+        if (!has_y) continue;
         if (K > 1 || !post) load4x2(use + 3 * D + col(k), y);
         if (TOKEN && (K > 1 || !post)) load4x2(use + 4 * D + col(k), g);
         if (TOKEN && a.dgate_rows) {
@@ -1051,7 +1053,7 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
           else acc[k][i] = fma2(e, y[i], acc[k][i]);
           y[i] = fma2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], e, mul2(f2(-cy), y[i]));
         }
-        if (a.dy) store4x2(static_cast<T*>(a.dy) + at, y);
+        if (has_dy) store4x2(static_cast<T*>(a.dy) + at, y);
       }
       if (!mine) continue;
       row += L;
@@ -1323,19 +1325,22 @@ inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_
   return p.rows == 2 ? launch_ring<float, 1, 2>(a, p, st) : launch_ring<float, 1, 1>(a, p, st);
 }
 
-template <typename T, int K, int G, bool TOKEN>
+template <typename T, int K, int G, bool TOKEN, bool FULL>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
   const size_t smem = short_smem<T, K, G, TOKEN>(a.D);
+  const auto kernel = norm_bwd_short_kernel<T, K, G, TOKEN, FULL>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_bwd_short_kernel<T, K, G, TOKEN>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(norm_bwd_short_kernel<T, K, G, TOKEN>, dim3((unsigned)a.parts), dim3(kShortThreads), smem, st, a);
+  return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(kShortThreads), smem, st, a);
 }
 template <typename T, int K, int G>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
-  return a.gate && a.rpg == 1 ? launch_short<T, K, G, true>(a, st) : launch_short<T, K, G, false>(a, st);
+  const bool token = a.gate && a.rpg == 1;
+  if (a.y && a.dh && a.dzi && a.dx && a.dy)
+    return token ? launch_short<T, K, G, true, true>(a, st) : launch_short<T, K, G, false, true>(a, st);
+  return token ? launch_short<T, K, G, true, false>(a, st) : launch_short<T, K, G, false, false>(a, st);
 }
 template <typename T>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
