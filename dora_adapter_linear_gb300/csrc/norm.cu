@@ -888,47 +888,46 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
 }
 
 // ------------------------------------------------------------------ backward in one pass, short rows
-// G lanes take a row, so its sums need no barrier; the L groups of a CTA's eight warps take every L-th row of its
-// part.  Each lane keeps its own columns of its next rows on their way into shared memory, as the walk of the
-// forward does.  The column sums stay in registers and are added over the groups when the gate row changes (N,
-// as above) and at the end, so a CTA leaves one partial.  Against the ring of a CTA a row, whose barriers bound it:
-// bf16, 131072 x 64 22 against 78 us, x 128 39 against 79, 16384 x 256 13 against 25, x 512 25 against 29, 2000 x
-// 256 with a gate per row 5.4 against 10.8; fp32 16384 x 256 19 against 26.  Bound by memory where rows are many
-// (131072 x 128: 5.2 TB/s).  A whole warp for 128 columns takes 59 us there; three CTAs an SM spill registers.
-// FULL as above (16384 x 256: 13.2 against 14.7 us).
+// G lanes take a row, so its sums need no barrier, or one among the warps of a group; the L groups of a CTA's
+// eight warps take every L-th row of its part.  Each lane keeps its own columns of its next rows on their way into
+// shared memory, as the walk of the forward does.  The column sums stay in registers and are added over the groups
+// when the gate row changes (N, as above) and at the end, so a CTA leaves one partial.  Against the ring, whose
+// CTAs are many for short rows and leave a partial each: bf16, 131072 x 64 22 against 78 us, x 128 39 against 79,
+// 16384 x 256 13 against 25, x 512 21 against 29, x 1024 38 against 41, 2000 x 256 with a gate per row 5.4 against
+// 10.8; fp32 16384 x 256 19 against 26, x 512 36 against 40.  Bound by memory where rows are many (65536 x 512: 6.0
+// TB/s).  A whole warp for 128 columns takes 59 us at 131072 rows, one for 512 (two vectors a lane, registers
+// spilled) 25 at 16384; three CTAs an SM spill registers.  FULL as above (16384 x 256: 13.2 against 14.7 us).
 constexpr int kShortThreads = 256;
-template <typename T, int K, bool TOKEN>
-constexpr int short_stages() { return sizeof(T) == 2 && K == 1 ? 4 : TOKEN ? 2 : 3; }
-template <typename T, int K, int G, bool TOKEN>
+template <typename T, bool TOKEN>
+constexpr int short_stages() { return sizeof(T) == 2 ? 4 : TOKEN ? 2 : 3; }
+template <typename T, int G, bool TOKEN>
 size_t short_smem(int64_t D) {
-  return kShortThreads / G * D * (short_stages<T, K, TOKEN>() * (TOKEN ? 5 : 4) * sizeof(T) + sizeof(float));
+  return kShortThreads / G * D * (short_stages<T, TOKEN>() * (TOKEN ? 5 : 4) * sizeof(T) + sizeof(float));
 }
 
-template <typename T, int K, int G, bool TOKEN, bool FULL>
+template <typename T, int G, bool TOKEN, bool FULL>
 __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const NormArgs a) {
   pdl_wait();   // inputs may come from the previous kernel in the stream
   if (threadIdx.x == 0) pdl_trigger();
-  constexpr int L = kShortThreads / G, S = short_stages<T, K, TOKEN>(), A = TOKEN ? 5 : 4;   // z, dh, dz_in, y, gate
+  constexpr int L = kShortThreads / G, Q = G > 32 ? G / 32 : 1;   // groups; columns a thread adds over them
+  constexpr int S = short_stages<T, TOKEN>(), A = TOKEN ? 5 : 4;   // z, dh, dz_in, y, gate
   extern __shared__ __align__(16) char stages[];
-  const int D = (int)a.D, lane = threadIdx.x % G, group = threadIdx.x / G;
+  __shared__ __align__(16) float4 red[2][kShortThreads / 32];   // of a warp, for groups of several
+  const int D = (int)a.D, lane = threadIdx.x % G, group = threadIdx.x / G, c = lane * 8;   // c: this lane's columns
+  const bool in = c < D;
   const int64_t part = blockIdx.x, r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
   const bool has_y = FULL || a.y, has_dh = FULL || a.dh, has_dzi = FULL || a.dzi, has_dx = FULL || a.dx, has_dy = FULL || a.dy;
   const bool post = has_y && a.post;
   const T* gate = static_cast<const T*>(a.gate);
   float* const sums = reinterpret_cast<float*>(stages + (size_t)L * S * A * D * sizeof(T));   // [L][D]
-  T* const ring = reinterpret_cast<T*>(stages) + group * S * A * D;
+  T* const ring = reinterpret_cast<T*>(stages) + group * S * A * D + c;
   int fill = 0, used = 0;   // where in the ring the next row goes, and the row in hand is
-  const auto col = [&](int k) { return (k * G + lane) * 8; };
   auto issue = [&](int64_t row) {   // this lane's columns of a row; a group even past the end
-    if (row < r1) {
+    if (row < r1 && in) {
       auto copy = [&](int at, const void* src, int64_t ld) {
-        const T* from = static_cast<const T*>(src) + row * ld;
+        const T* from = static_cast<const T*>(src) + row * ld + c;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (col(k) >= D) continue;
-#pragma unroll
-          for (int e = 0; e < 8; e += 16 / (int)sizeof(T)) cp_async16(ring + fill + at * D + col(k) + e, from + col(k) + e, true);
-        }
+        for (int e = 0; e < 8; e += 16 / (int)sizeof(T)) cp_async16(ring + fill + at * D + e, from + e, true);
       };
       copy(0, a.x, a.ldx);
       if (has_dh) copy(1, a.dh, a.ldh);
@@ -943,49 +942,43 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
   int64_t row = r0 + group;
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(row + i * L);
-  F2 wz[K][4], u[K][4], dw[K][4], acc[K][4];   // u = alpha g w_p (TOKEN: alpha w_p); acc: N (TOKEN: dw_post)
+  F2 wz[4], u[4], dw[4], acc[4];   // u = alpha g w_p (TOKEN: alpha w_p); acc: N (TOKEN: dw_post)
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dw[k][i] = acc[k][i] = f2(0.f);
-    if (col(k) < D) weight4x2<T>(a.w_pre, col(k), a.off, wz[k]);
-  }
-  // thread t: the sums over the groups of columns t, t + 256
-  auto over_groups = [&](F2 (&v)[K][4], float (&t)[K]) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (col(k) < D) store4x2(sums + group * D + col(k), v[k]);
+  for (int i = 0; i < 4; ++i) dw[i] = acc[i] = f2(0.f);
+  if (in) weight4x2<T>(a.w_pre, c, a.off, wz);
+  // thread t: the sums over the groups of columns t, t + 256, ..
+  auto over_groups = [&](F2 (&v)[4], float (&t)[Q]) {
+    if (in) store4x2(sums + group * D + c, v);
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = k * kShortThreads + (int)threadIdx.x;
-      t[k] = 0.f;
-      if (c < D)
+    for (int q = 0; q < Q; ++q) {
+      const int col = q * kShortThreads + (int)threadIdx.x;
+      t[q] = 0.f;
+      if (col < D)
 #pragma unroll 8
-        for (int l = 0; l < L; ++l) t[k] += sums[l * D + c];
+        for (int l = 0; l < L; ++l) t[q] += sums[l * D + col];
     }
     __syncthreads();
   };
   const float inv_d = 1.f / (float)D;
-  float dpost[K], t1[K];
+  float dpost[Q], t1[Q];
 #pragma unroll
-  for (int k = 0; k < K; ++k) dpost[k] = 0.f;
+  for (int q = 0; q < Q; ++q) dpost[q] = 0.f;
+  int flip = 0;
   const auto factor = [&](const float* r, bool has, float other, int64_t at) { return has ? r[min(at, r1 - 1)] : other; };
   float r_z2 = factor(a.r_pre, has_dh, 0.f, row), r_y2 = factor(a.r_post, post, 1.f, row);
   for (int64_t seg0 = r0, seg_end; seg0 < r1; seg0 = seg_end) {   // rows of one gate row, uniform over the CTA
     const int64_t grp = TOKEN ? 0 : seg0 / a.rpg;
     seg_end = TOKEN ? r1 : min(r1, (grp + 1) * a.rpg);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (col(k) >= D) continue;
+    if (in) {
       F2 w[4];
-      weight4x2<T>(post ? a.w_post : nullptr, col(k), a.off, u[k]);
-      gate4x2<T>(!TOKEN && gate ? gate + grp * D : nullptr, col(k), a.alpha, w);
+      weight4x2<T>(post ? a.w_post : nullptr, c, a.off, u);
+      gate4x2<T>(!TOKEN && gate ? gate + grp * D : nullptr, c, a.alpha, w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[k][i] = mul2(u[k][i], w[i]);
+      for (int i = 0; i < 4; ++i) u[i] = mul2(u[i], w[i]);
     }
     // a warp stays while one of its groups has a row
-    for (bool mine; mine = row < seg_end, G == 32 ? mine : __any_sync(0xffffffffu, mine);) {
+    for (bool mine; mine = row < seg_end, G >= 32 ? mine : __any_sync(0xffffffffu, mine);) {
       const float r_z = r_z2, r_y = r_y2;
       const T* use = ring + used;
       if (mine) {
@@ -993,69 +986,71 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
         r_z2 = factor(a.r_pre, has_dh, 0.f, row + L), r_y2 = factor(a.r_post, post, 1.f, row + L);
         cp_async_wait<S - 1>();
       }
-      F2 z[4], y[4], g[4], t[4], s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
-      auto load_zt = [&](int k, bool first) {   // z and t = dz_in + r_z w_z dh; the first time also what the sums need of dh
-        load4x2(use + col(k), z);
+      F2 z[4], y[4], g[4], t[4], s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);   // t = dz_in + r_z w_z dh
+      if (mine && in) {
+        load4x2(use, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = f2(0.f);
-        if (has_dzi) load4x2(use + 2 * D + col(k), t);
-        if (!has_dh) return;
-        load4x2(use + D + col(k), g);
+        if (has_dzi) load4x2(use + 2 * D, t);
+        if (has_dh) {
+          load4x2(use + D, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const F2 rh = mul2(g[i], f2(r_z)), wh = mul2(rh, wz[k][i]);
-          if (first) {
+          for (int i = 0; i < 4; ++i) {
+            const F2 rh = mul2(g[i], f2(r_z)), wh = mul2(rh, wz[i]);
             s0 = fma2(wh, z[i], s0);
-            dw[k][i] = fma2(rh, z[i], dw[k][i]);
+            dw[i] = fma2(rh, z[i], dw[i]);
+            t[i] = add2(t[i], wh);
           }
-          t[i] = add2(t[i], wh);
         }
-      };
+        if (has_y) load4x2(use + 3 * D, y);
+        if (TOKEN) load4x2(use + 4 * D, g);
+        if (post)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (!mine || col(k) >= D) continue;
-        load_zt(k, true);
-        if (!post) continue;
-        load4x2(use + 3 * D + col(k), y);
-        if (TOKEN) load4x2(use + 4 * D + col(k), g);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const F2 uy = mul2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], y[i]);
-          s1 = fma2(uy, t[i], s1);
-          s2 = fma2(uy, z[i], s2);
-        }
+          for (int i = 0; i < 4; ++i) {
+            const F2 uy = mul2(TOKEN ? mul2(u[i], g[i]) : u[i], y[i]);
+            s1 = fma2(uy, t[i], s1);
+            s2 = fma2(uy, z[i], s2);
+          }
       }
       float s[4] = {sum2(s0), sum2(s1), sum2(s2), 0.f};
-      spread<4, G>(warp_sums_of<4, G>(s), s);
-      if (K > 1) __syncwarp();   // z and y are read again rather than kept: 128 registers hold no more
+      if (G <= 32) {
+        spread<4, G <= 32 ? G : 32>(warp_sums_of<4, G <= 32 ? G : 32>(s), s);
+      } else {   // one barrier a row of the group's warps: a warp that runs ahead writes the other half
+        spread<4>(warp_sums_of<4>(s), s);
+        if ((threadIdx.x & 31) == 0) red[flip][threadIdx.x >> 5] = make_float4(s[0], s[1], s[2], 0.f);
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(G) : "memory");
+        s[0] = s[1] = s[2] = 0.f;
+#pragma unroll
+        for (int w = 0; w < Q; ++w) {
+          const float4 o = red[flip][group * Q + w];
+          s[0] += o.x, s[1] += o.y, s[2] += o.z;
+        }
+        flip ^= 1;
+      }
+      if (!mine) continue;
       const float cz = r_z * r_z * (s[0] * inv_d);   // s0 was summed over r_z w_z dh z
       const float cy = post ? r_y * r_y * r_y * ((s[1] - cz * s[2]) * inv_d) : 0.f;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (!mine || col(k) >= D) continue;
-        if (K > 1) load_zt(k, false);
-        const int64_t at = row * D + col(k);
+      if (in) {
+        const int64_t at = row * D + c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) t[i] = fma2(f2(-cz), z[i], t[i]);
         if (has_dx) store4x2(static_cast<T*>(a.dx) + at, t);
-        if (!has_y) continue;
-        if (K > 1 || !post) load4x2(use + 3 * D + col(k), y);
-        if (TOKEN && (K > 1 || !post)) load4x2(use + 4 * D + col(k), g);
         if (TOKEN && a.dgate_rows) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = mul2(u[k][i], mul2(mul2(t[i], f2(r_y)), y[i]));
+          for (int i = 0; i < 4; ++i) z[i] = mul2(u[i], mul2(mul2(t[i], f2(r_y)), y[i]));
           store4x2(static_cast<T*>(a.dgate_rows) + at, z);
         }
+        if (has_y) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const F2 e = mul2(t[i], f2(r_y));
-          if (TOKEN) acc[k][i] = fma2(mul2(mul2(g[i], f2(a.alpha)), e), y[i], acc[k][i]);
-          else acc[k][i] = fma2(e, y[i], acc[k][i]);
-          y[i] = fma2(TOKEN ? mul2(u[k][i], g[i]) : u[k][i], e, mul2(f2(-cy), y[i]));
+          for (int i = 0; i < 4; ++i) {
+            const F2 e = mul2(t[i], f2(r_y));
+            if (TOKEN) acc[i] = fma2(mul2(mul2(g[i], f2(a.alpha)), e), y[i], acc[i]);
+            else acc[i] = fma2(e, y[i], acc[i]);
+            y[i] = fma2(TOKEN ? mul2(u[i], g[i]) : u[i], e, mul2(f2(-cy), y[i]));
+          }
+          if (has_dy) store4x2(static_cast<T*>(a.dy) + at, y);
         }
-        if (has_dy) store4x2(static_cast<T*>(a.dy) + at, y);
       }
-      if (!mine) continue;
       row += L;
       used += A * D;
       if (used == S * A * D) used = 0;
@@ -1064,25 +1059,25 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
     over_groups(acc, t1);
     const int64_t g0 = grp * a.rpg, g1 = min(a.M, g0 + a.rpg);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int i = 0; i < 4; ++i) acc[i] = f2(0.f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[k][i] = f2(0.f);
-      const int c = k * kShortThreads + (int)threadIdx.x;
-      if (c >= D) continue;
-      const float gc = gate ? to_f<T>(gate[grp * D + c]) : 1.f;
-      dpost[k] = fmaf(a.alpha * gc, t1[k], dpost[k]);
+    for (int q = 0; q < Q; ++q) {
+      const int col = q * kShortThreads + (int)threadIdx.x;
+      if (col >= D) continue;
+      const float gc = gate ? to_f<T>(gate[grp * D + col]) : 1.f;
+      dpost[q] = fmaf(a.alpha * gc, t1[q], dpost[q]);
       if (!a.dgate) continue;
-      const float wp = post && a.w_post ? to_f<T>(static_cast<const T*>(a.w_post)[c]) + a.off : 1.f;
-      const float dg = a.alpha * wp * t1[k];
-      if (g0 >= r0 && g1 <= r1) static_cast<T*>(a.dgate)[grp * D + c] = from_f<T>(dg);
-      else a.pg[(part * 2 + (seg0 == r0 ? 0 : 1)) * D + c] = dg;
+      const float wp = post && a.w_post ? to_f<T>(static_cast<const T*>(a.w_post)[col]) + a.off : 1.f;
+      const float dg = a.alpha * wp * t1[q];
+      if (g0 >= r0 && g1 <= r1) static_cast<T*>(a.dgate)[grp * D + col] = from_f<T>(dg);
+      else a.pg[(part * 2 + (seg0 == r0 ? 0 : 1)) * D + col] = dg;
     }
   }
-  auto leave = [&](float* to, const float (&v)[K]) {
+  auto leave = [&](float* to, const float (&v)[Q]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = k * kShortThreads + (int)threadIdx.x;
-      if (c < D) to[part * D + c] = v[k];
+    for (int q = 0; q < Q; ++q) {
+      const int col = q * kShortThreads + (int)threadIdx.x;
+      if (col < D) to[part * D + col] = v[q];
     }
   };
   if (a.pp) {
@@ -1211,13 +1206,13 @@ RingPlan ring_plan(const lora_norm_shape& sh, int n) {
   return RingPlan{};
 }
 
-// Whether the rows are short (rpg: rows that share a gate row, 0 without a gate): a group's columns fit two vectors
-// a lane, one of fp32, and a gate row's rows are all, or enough that the sum over the groups at its end costs less
-// than it saves: with 16 rows a gate 16384 x 256 takes 20 us against 27 (x 128: 15 against 25) and with 4 35 against
-// 29; above 256 columns 64 rows break even (16384 x 512: 30 against 31, with 16 39 against 32).
+// Whether the rows are short (rpg: rows that share a gate row, 0 without a gate): half a CTA holds one, and a gate
+// row's rows are all, or enough that the sum over the groups at its end costs less than it saves (16384 x 1024 bf16
+// with 16 rows a gate 48 against 50 us with the ring, with 8 53 against 53; x 256 20 against 27, with 4 34 against 29).
+// Five fp32 arrays of more than 512 columns leave too few rows on their way (16384 x 1024: 93 against 87 us).
 bool short_rows(const lora_norm_shape& sh, int64_t rpg) {
-  if (sh.D > (sh.dtype == LORA_BF16 ? 512 : 256)) return false;
-  return rpg <= 1 || rpg >= (sh.D > 256 ? 64 : 16) || rpg >= sh.M;
+  if (sh.D > (sh.dtype == LORA_F32 && rpg == 1 ? 512 : 1024)) return false;
+  return rpg <= 1 || rpg >= 16 || rpg >= sh.M;
 }
 
 // Row parts of the column sums: one a resident CTA in the one-pass backwards; for the column kernel
@@ -1226,7 +1221,8 @@ void norm_parts(const lora_norm_shape& sh, bool brief, const RingPlan& ring, int
   int64_t want;
   if (brief) {
     want = 2 * num_sms_current();
-    if (want > (sh.M + 7) / 8) want = (sh.M + 7) / 8;
+    const int64_t least = sh.D > 512 ? 2 : sh.D > 256 ? 4 : 8;   // rows, one for each group of long rows
+    if (want > (sh.M + least - 1) / least) want = (sh.M + least - 1) / least;
   } else if (ring.threads) {
     want = (int64_t)ring.ctas * num_sms_current() / (ring.half ? 2 : 1);
     if (want > sh.M) want = sh.M;
@@ -1325,30 +1321,30 @@ inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_
   return p.rows == 2 ? launch_ring<float, 1, 2>(a, p, st) : launch_ring<float, 1, 1>(a, p, st);
 }
 
-template <typename T, int K, int G, bool TOKEN, bool FULL>
+template <typename T, int G, bool TOKEN, bool FULL>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
-  const size_t smem = short_smem<T, K, G, TOKEN>(a.D);
-  const auto kernel = norm_bwd_short_kernel<T, K, G, TOKEN, FULL>;
+  const size_t smem = short_smem<T, G, TOKEN>(a.D);
+  const auto kernel = norm_bwd_short_kernel<T, G, TOKEN, FULL>;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(kShortThreads), smem, st, a);
 }
-template <typename T, int K, int G>
+template <typename T, int G>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
   const bool token = a.gate && a.rpg == 1;
   if (a.y && a.dh && a.dzi && a.dx && a.dy)
-    return token ? launch_short<T, K, G, true, true>(a, st) : launch_short<T, K, G, false, true>(a, st);
-  return token ? launch_short<T, K, G, true, false>(a, st) : launch_short<T, K, G, false, false>(a, st);
+    return token ? launch_short<T, G, true, true>(a, st) : launch_short<T, G, false, true>(a, st);
+  return token ? launch_short<T, G, true, false>(a, st) : launch_short<T, G, false, false>(a, st);
 }
 template <typename T>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
-  if (a.D <= 64) return launch_short<T, 1, 8>(a, st);
-  if (a.D <= 128) return launch_short<T, 1, 16>(a, st);
-  if constexpr (sizeof(T) == 2)
-    if (a.D > 256) return launch_short<T, 2, 32>(a, st);
-  return launch_short<T, 1, 32>(a, st);
+  if (a.D <= 64) return launch_short<T, 8>(a, st);
+  if (a.D <= 128) return launch_short<T, 16>(a, st);
+  if (a.D <= 256) return launch_short<T, 32>(a, st);
+  if (a.D <= 512) return launch_short<T, 64>(a, st);
+  return launch_short<T, 128>(a, st);
 }
 
 template <typename T>
