@@ -893,8 +893,8 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
 // shared memory, as the walk of the forward does.  The column sums stay in registers and are added over the groups
 // when the gate row changes (N, as above) and at the end, so a CTA leaves one partial.  Against the ring, whose
 // CTAs are many for short rows and leave a partial each: bf16, 131072 x 64 22 against 78 us, x 128 39 against 79,
-// 16384 x 256 13 against 25, x 512 21 against 29, x 1024 38 against 41, 2000 x 256 with a gate per row 5.4 against
-// 10.8; fp32 16384 x 256 19 against 26, x 512 36 against 40.  Bound by memory where rows are many (65536 x 512: 6.0
+// 16384 x 256 13 against 25, x 512 20 against 29, x 1024 38 against 41, 2000 x 256 with a gate per row 5.4 against
+// 10.8; fp32 16384 x 256 19 against 26, x 512 36 against 40.  Bound by memory where rows are many (65536 x 512: 6.2
 // TB/s).  A whole warp for 128 columns takes 59 us at 131072 rows, one for 512 (two vectors a lane, registers
 // spilled) 25 at 16384; three CTAs an SM spill registers.  FULL as above (16384 x 256: 13.2 against 14.7 us).
 constexpr int kShortThreads = 256;
@@ -1105,17 +1105,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_finish_kernel(const NormArgs a)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   const int job = (int)blockIdx.y - 2;
-  // partials first, first + step, .. last of this warp, eight loads at a time; slot(p) is where part p keeps
-  // this sum
+  // partials first, first + step, .. last of this warp, ten loads at a time, so that 32 warps have 320 on their
+  // way (304 parts: 24.6 against 25.4 us with eight, 4096 x 2048); slot(p) is where part p keeps this sum
   auto add = [&](int first, int last, int step, auto slot) {
     float t = 0.f;
     if (col < a.D)
-      for (int p = first; p <= last; p += 8 * step) {
-        float v[8];
+      for (int p = first; p <= last; p += 10 * step) {
+        float v[10];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p + j * step <= last ? slot(p + j * step)[col] : 0.f;
+        for (int j = 0; j < 10; ++j) v[j] = p + j * step <= last ? slot(p + j * step)[col] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t += v[j];
+        for (int j = 0; j < 10; ++j) t += v[j];
       }
     return t;
   };
@@ -1221,7 +1221,7 @@ void norm_parts(const lora_norm_shape& sh, bool brief, const RingPlan& ring, int
   int64_t want;
   if (brief) {
     want = 2 * num_sms_current();
-    const int64_t least = sh.D > 512 ? 2 : sh.D > 256 ? 4 : 8;   // rows, one for each group of long rows
+    const int64_t least = sh.D > 512 ? 4 : 8;   // rows (300 x 1024: 5.3 us with 2 and 4, 6.4 with 8; 2000 x 512: 7.4 with 4, 6.8 with 8)
     if (want > (sh.M + least - 1) / least) want = (sh.M + least - 1) / least;
   } else if (ring.threads) {
     want = (int64_t)ring.ctas * num_sms_current() / (ring.half ? 2 : 1);
@@ -1361,7 +1361,7 @@ lora_status norm_bwd(NormArgs& a, bool brief, const RingPlan& ring, cudaStream_t
                     dim3(32 * kColWarps), 0, st, a));
   }
   if (!sums) return LORA_OK;
-  int warps = (a.parts + 7) / 8;   // eight partials a warp
+  int warps = (a.parts + 9) / 10;   // ten partials a warp
   warps = warps < 4 ? 4 : warps > 32 ? 32 : warps;
   const int64_t groups = a.dgate && a.parts > 1 ? (a.M + a.rpg - 1) / a.rpg : 0, bounds = a.parts - 1;
   int how = GATE_NONE;

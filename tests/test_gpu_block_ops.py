@@ -155,12 +155,14 @@ def test_norm(ops, M, D, gate, post, more, dtype):
     (5003, 256, "token", False, dict(alpha=-0.3)), (4099, 264, "seq", True, dict(rpg=64)), (4100, 512, "row", True, {}),
     (2700, 512, "token", True, dict(off=1.0)), (3000, 504, "none", False, dict(y=False)), (640, 40, "seq", True, dict(rpg=5)),
     (33, 256, "seq", True, dict(rpg=32)), (20000, 16, "none", True, {}), (700, 96, "none", False, dict(y=False)),
+    (2503, 1024, "token", True, {}), (1501, 648, "seq", True, dict(rpg=16)), (702, 1000, "row", False, {}),
+    (3, 1024, "none", True, {}), (1300, 776, "token", False, dict(off=1.0)), (2100, 392, "seq", False, dict(rpg=301)),
 ])
 def test_norm_backward_of_short_rows(ops, M, D, gate, post, more, dtype):
     test_norm(ops, M, D, gate, post, more, dtype)
 
 
-@pytest.mark.parametrize("D", [64, 120, 256, 512])
+@pytest.mark.parametrize("D", [64, 120, 256, 512, 1024])
 @pytest.mark.parametrize("which", ["dH", "dXout", "dX", "dw", "dgate"])
 @pytest.mark.parametrize("gate", ["token", "seq"])
 def test_norm_backward_of_short_rows_in_part(ops, D, which, gate):
