@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(256, kStep8Ctas) adamw8_kernel(const __grid_co
     const int64_t i0 = (int64_t)(at.w - e.first) * (kPair * kBlock), i = i0 + lane * 8;
     const int64_t b = e.state + (int64_t)(at.w - e.first) * kPair;
     at.next();
-    if (whole(e.g, i0 + (kPair - 1) * kBlock, e.n) && whole(e.p, i0 + (kPair - 1) * kBlock, e.n)) {   // both blocks; the same for the warp
+    // both blocks; the same for the warp
+    if (whole(e.g, i0 + (kPair - 1) * kBlock, e.n) && whole(e.p, i0 + (kPair - 1) * kBlock, e.n)) {
       Raw8Bit r[kPair];   // every load is on its way before the first value is opened
 #pragma unroll
       for (int h = 0; h < kPair; ++h) load(e, dtype, true, i + h * kBlock, b + h, r[h]);

@@ -916,7 +916,8 @@ __global__ void __launch_bounds__(kShortThreads, 2) norm_bwd_short_kernel(const 
   const int D = (int)a.D, lane = threadIdx.x % G, group = threadIdx.x / G, c = lane * 8;   // c: this lane's columns
   const bool in = c < D;
   const int64_t part = blockIdx.x, r0 = part * a.rp, r1 = min(a.M, r0 + a.rp);
-  const bool has_y = FULL || a.y, has_dh = FULL || a.dh, has_dzi = FULL || a.dzi, has_dx = FULL || a.dx, has_dy = FULL || a.dy;
+  const bool has_y = FULL || a.y, has_dh = FULL || a.dh, has_dzi = FULL || a.dzi;
+  const bool has_dx = FULL || a.dx, has_dy = FULL || a.dy;
   const bool post = has_y && a.post;
   const T* gate = static_cast<const T*>(a.gate);
   float* const sums = reinterpret_cast<float*>(stages + (size_t)L * S * A * D * sizeof(T));   // [L][D]
@@ -1221,7 +1222,8 @@ void norm_parts(const lora_norm_shape& sh, bool brief, const RingPlan& ring, int
   int64_t want;
   if (brief) {
     want = 2 * num_sms_current();
-    const int64_t least = sh.D > 512 ? 4 : 8;   // rows (300 x 1024: 5.3 us with 2 and 4, 6.4 with 8; 2000 x 512: 7.4 with 4, 6.8 with 8)
+    // least rows of a part (300 x 1024: 5.3 us with 2 and 4, 6.4 with 8; 2000 x 512: 7.4 with 4, 6.8 with 8)
+    const int64_t least = sh.D > 512 ? 4 : 8;
     if (want > (sh.M + least - 1) / least) want = (sh.M + least - 1) / least;
   } else if (ring.threads) {
     want = (int64_t)ring.ctas * num_sms_current() / (ring.half ? 2 : 1);
