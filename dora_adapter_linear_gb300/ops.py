@@ -2,6 +2,7 @@
 the entry point of the same name.  PyTorch is used only for device memory and the stream."""
 from __future__ import annotations
 
+import threading
 from functools import lru_cache
 
 import torch
@@ -13,10 +14,12 @@ _WS = {}
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
-    """A cached, zero-initialised scratch buffer of at least nbytes (error word cleared)."""
+    """A cached, zero-initialised scratch buffer of at least nbytes (error word cleared), of this thread and
+    stream: a call's launches run without the interpreter's lock, so those of two threads' calls on one
+    stream come in any order, and each has to find the partial results of its own call."""
     if not isinstance(device, torch.device):
         device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
-    key = (device, L.current_stream(device))
+    key = (device, L.current_stream(device), threading.get_ident())
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
