@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
-from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 import torch
 
@@ -95,6 +95,7 @@ _SIGS = {
     "lora_mlp_workspace_bytes": (c_size_t, [c_int, POINTER(LoraMlpShape)]),
     "lora_clear_device_error": (c_int, [P, P]),
     "lora_check_device_error": (c_int, [P, P]),
+    "lora_capture_id": (c_uint64, [P]),
     "lora_linear_fwd": (c_int, [POINTER(LoraShape), P, P, P, P, P, c_float, P, P, P, c_size_t, P]),
     "lora_linear_bwd": (c_int, [POINTER(LoraShape), P, P, P, P, P, P, c_float, P, P, P, P, P, c_size_t, P]),
     "lora_linear_dropout_fwd": (c_int, [POINTER(LoraShape), P, P, c_float, P, P, P, P, c_float, P, P, P, c_size_t,
@@ -198,6 +199,12 @@ def current_stream(device=None) -> int:
     a Stream object, which alone would cost 3 us a call."""
     index = None if device is None else device.index
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if index is None else index)
+
+
+def capture_id(stream: int) -> int:
+    """The number of the capture that the current stream, of this handle, takes part in, or 0.  The default
+    stream, 0, cannot be captured."""
+    return _lib().lora_capture_id(stream) if stream and torch._C._cuda_isCurrentStreamCapturing() else 0
 
 
 def _stream(stream):

@@ -636,6 +636,16 @@ lora_status lora_clear_device_error(void* ws, void* stream) {
   return LORA_OK;
 }
 
+uint64_t lora_capture_id(void* stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo((cudaStream_t)stream, &status, &id) != cudaSuccess) {
+    cudaGetLastError();   // of this query only
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? id : 0;
+}
+
 lora_status lora_check_device_error(const void* ws, void* stream) {
   REQ(ws);
   CK(cudaStreamSynchronize((cudaStream_t)stream));

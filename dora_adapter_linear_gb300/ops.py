@@ -14,15 +14,24 @@ _WS = {}
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
-    """A cached, zero-initialised scratch buffer of at least nbytes (error word cleared), of this thread and
-    stream: a call's launches run without the interpreter's lock, so those of two threads' calls on one
-    stream come in any order, and each has to find the partial results of its own call."""
+    """A cached scratch buffer of at least nbytes, its error word cleared when it is made.  It belongs to
+      this thread and stream: a call's launches run without the interpreter's lock, so those of two threads'
+        calls on one stream come in any order, and each has to find the partial results of its own call;
+      this graph capture, if the stream is in one: the graph keeps the address, in memory from its own pool,
+        whatever is called later, and no other graph or call writes there."""
     if not isinstance(device, torch.device):
         device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
-    key = (device, L.current_stream(device), threading.get_ident())
+    stream = L.current_stream(device)
+    capture, thread = L.capture_id(stream), threading.get_ident()
+    key = (device, stream, thread, capture)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        for k in [k for k in list(_WS) if k[2] == thread and k[3] not in (0, capture)]:
+            del _WS[k]          # of captures that have ended: their graphs' pools keep the memory
+        new = torch.empty if capture else torch.zeros       # in a graph: the error word's 256 bytes alone
+        buf = new(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if capture:
+            buf[:256].zero_()
         _WS[key] = buf
     return buf
 

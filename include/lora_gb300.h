@@ -137,6 +137,10 @@ size_t lora_qkv_workspace_bytes(int op, const lora_qkv_shape* sh);
 /* Zero the device error word at the head of `ws` (asynchronous on `stream`). */
 lora_status lora_clear_device_error(void* ws, void* stream);
 
+/* A number of the graph capture that `stream` takes part in, another for every capture; 0 when it takes part
+ * in none.  A captured graph keeps the addresses it was captured with, so its workspaces have to be its own. */
+uint64_t lora_capture_id(void* stream);
+
 /* Synchronise `stream`, then read the device error word of `ws`:
  * LORA_OK if clear, LORA_ERR_DEVICE_TIMEOUT if a kernel recorded a timed-out wait. */
 lora_status lora_check_device_error(const void* ws, void* stream);

@@ -11,6 +11,7 @@ from dora_adapter_linear_gb300 import ops
 @pytest.fixture(autouse=True)
 def made_up_stream(monkeypatch):
     monkeypatch.setattr(L, "current_stream", lambda device=None: 7)
+    monkeypatch.setattr(L, "capture_id", lambda stream: 0, raising=False)
     monkeypatch.setattr(ops, "_WS", {})
 
 
@@ -40,3 +41,19 @@ def test_two_threads_on_one_stream_have_a_buffer_each():
         t.join()
     assert len({mine, *others}) == 3
     assert address() == mine
+
+
+def test_a_capture_has_a_buffer_of_its_own(monkeypatch):
+    """A graph writes where it was captured: neither a later call, however large, nor another graph may be there."""
+    eager = ops.workspace(1024, torch.device("cpu"))
+    captured = {}
+    for number in (11, 12):
+        monkeypatch.setattr(L, "capture_id", lambda stream: number)
+        captured[number] = ops.workspace(1024, torch.device("cpu"))
+        assert not captured[number][:256].any()
+        assert address() == captured[number].data_ptr()         # calls of one capture follow one another
+    assert len({eager.data_ptr(), *(t.data_ptr() for t in captured.values())}) == 3
+    monkeypatch.setattr(L, "capture_id", lambda stream: 0)
+    assert address() == eager.data_ptr()
+    assert address(1 << 20) not in (eager.data_ptr(), *(t.data_ptr() for t in captured.values()))
+    assert len(ops._WS) == 1            # what ended captures used is left to their graphs
