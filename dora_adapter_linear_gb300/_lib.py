@@ -194,11 +194,24 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def current_device() -> int:
+    """The index of the current device, whose streams the calls run on."""
+    return torch._C._cuda_getDevice()
+
+
+def need_current(name, device):
+    """The calls run on the current device's current stream: operands of another device would be read
+    without any order to that device's own work, or not be reachable at all."""
+    if device.type == "cuda" and device.index is not None and device.index != current_device():
+        raise ValueError(f"{name} must be on the current device, cuda:{current_device()}, got {device}: make it the "
+                         f"current one around the call")
+
+
 def current_stream(device=None) -> int:
     """The handle of the device's current stream (by default the current device's), read without making
     a Stream object, which alone would cost 3 us a call."""
     index = None if device is None else device.index
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice() if index is None else index)
+    return torch._C._cuda_getCurrentRawStream(current_device() if index is None else index)
 
 
 def capture_id(stream: int) -> int:

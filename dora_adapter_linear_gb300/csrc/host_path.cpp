@@ -6,6 +6,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -39,6 +40,8 @@ struct Arg {
 int dtype_of(const Tensor& x) {
   return x.scalar_type() == at::kBFloat16 ? LORA_BF16 : x.scalar_type() == at::kFloat ? LORA_F32 : -1;
 }
+// the calls run on the current device's current stream
+bool here(const Tensor& x) { return x.is_cuda() && x.device().index() == c10::cuda::current_device(); }
 bool strided(const Tensor& t) { return t.layout() == at::kStrided; }
 bool same_kind(const Tensor& t, const Tensor& x) {
   return strided(t) && t.scalar_type() == x.scalar_type() && t.device() == x.device();
@@ -83,7 +86,7 @@ PyObject* tuple_of(const Ts&... ts) {
 // The shape both norm calls share; false: not for here.
 bool norm_shape(lora_norm_shape* sh, const Tensor& x, const Arg& w_pre, const Arg& w_post, const Arg& gate,
                 PyObject* rows_per_gate, double alpha, double eps, double off, bool post) {
-  if (!x.is_cuda() || !strided(x) || x.dim() != 2 || dtype_of(x) < 0) return false;
+  if (!here(x) || !strided(x) || x.dim() != 2 || dtype_of(x) < 0) return false;
   const int64_t M = x.size(0), D = x.size(1);
   if (M < 1 || D < 1) return false;
   if (w_pre && !dense(*w_pre, x, x.scalar_type(), {D})) return false;
@@ -180,7 +183,7 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(a[5]);
   const long layout = PyLong_AsLong(a[6]);
   if (PyErr_Occurred()) return nullptr;
-  if (!x.is_cuda() || !strided(x) || x.dim() != 3 || dtype_of(x) < 0 || x.size(0) < 1 || x.size(1) < 1 || x.stride(2) != 1)
+  if (!here(x) || !strided(x) || x.dim() != 3 || dtype_of(x) < 0 || x.size(0) < 1 || x.size(1) < 1 || x.stride(2) != 1)
     return not_here();
   const bool wide = p.scalar_type() == at::kLong;
   if (!(wide || p.scalar_type() == at::kInt) || !dense(p, x, p.scalar_type(), {x.size(0)}) || rot > x.size(2) ||

@@ -21,6 +21,7 @@ def workspace(nbytes: int, device) -> torch.Tensor:
         whatever is called later, and no other graph or call writes there."""
     if not isinstance(device, torch.device):
         device = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    L.need_current("the operands", device)
     stream = L.current_stream(device)
     capture, thread = L.capture_id(stream), threading.get_ident()
     key = (device, stream, thread, capture)
@@ -191,6 +192,7 @@ def lora_linear_dropout_bwd(X, mask, keep_scale, W0, A, B, Z, dY, s, need_dx=Tru
 
 
 def dora_rownorm2(W0):
+    _need_cuda("W0", W0)
     sh = L.shape(0, W0.shape[1], W0.shape[0], 8, L.dtype_code(W0))
     r0 = torch.empty(W0.shape[0], dtype=torch.float32, device=W0.device)
     L.dora_rownorm2(sh, W0, r0)
@@ -229,6 +231,7 @@ def dora_linear_bwd(X, W0, A, B, m, bias, Y, Z, n, V, dY, s, eps=1e-12, need_dx=
 
 
 def dora_colnorm2(W0):
+    _need_cuda("W0", W0)
     sh = L.shape(0, W0.shape[1], W0.shape[0], 8, L.dtype_code(W0))
     c0 = torch.empty(W0.shape[1], dtype=torch.float32, device=W0.device)
     L.dora_colnorm2(sh, W0, c0)
@@ -306,6 +309,7 @@ def w8a8_quantize_rows(X, A=None):
         raise ValueError("X must be 2-D")
     rows, cols = X.shape
     _check_shapes(X, X=(X, (rows, cols), BF16), A=(A, (None if A is None else A.shape[0], cols), BF16))
+    _need_cuda("X", X)
     Xq = torch.empty(rows, cols, dtype=torch.int8, device=X.device)
     sx = torch.empty(rows, dtype=torch.float32, device=X.device)
     Z = torch.empty(rows, A.shape[0], dtype=X.dtype, device=X.device) if A is not None else None
@@ -379,6 +383,7 @@ def w8a8_quantize_rows_bf16(X, A=None):
         raise ValueError("X must be 2-D")
     rows, cols = X.shape
     _check_shapes(X, X=(X, (rows, cols), BF16), A=(A, (None if A is None else A.shape[0], cols), BF16))
+    _need_cuda("X", X)
     Xc = torch.empty(rows, cols, dtype=torch.bfloat16, device=X.device)
     sx = torch.empty(rows, dtype=torch.float32, device=X.device)
     Z = torch.empty(rows, A.shape[0], dtype=X.dtype, device=X.device) if A is not None else None
@@ -393,6 +398,7 @@ def w8a8_prepack_weight(Wq, sw, codes=True, dequant=True):
         raise ValueError("Wq must be a 2-D int8 tensor")
     d_out, d_in = Wq.shape
     _check_shapes(Wq, Wq=(Wq, (d_out, d_in), torch.int8), sw=(sw, (d_out,), F32))
+    _need_cuda("Wq", Wq)
     mk = lambda: torch.empty(d_out, d_in, dtype=torch.bfloat16, device=Wq.device)  # noqa: E731
     Wb = mk() if codes else None
     Wd = mk() if dequant else None
@@ -436,8 +442,10 @@ def _rows_like(X):
 
 
 def _need_cuda(name, t):
+    """t must be where the call runs."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got one on {t.device}")
+    L.need_current(name, t.device)
 
 
 def _gate_rows(gate, rows_per_gate, X):
