@@ -7,11 +7,27 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 namespace lg {
 
 typedef __nv_bfloat16 bf16;
 
 int num_sms_current();
+// Allows the kernel `bytes` (always the same) of dynamic shared memory on the current device.  The runtime keeps
+// that by device, so it is asked once on each.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> asked[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && asked[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) asked[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 // Fills *a with the programmatic-stream-serialization launch attribute and returns 1, or returns 0
 // when LORA_GB300_PDL=0.  Only kernels that call pdl_wait() before touching global memory use it.
 int pdl_attr(cudaLaunchAttribute* a);

@@ -1278,13 +1278,8 @@ NormArgs norm_args(const lora_norm_shape& sh, const void* x, const void* y, cons
 
 template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
 cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
-  static bool set = false;
-  if (!set) {
-    const cudaError_t e = cudaFuncSetAttribute(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmSmem - kRingStatic);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  const cudaError_t allowed = allow_smem<norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>>(kSmSmem - kRingStatic);
+  if (allowed != cudaSuccess) return allowed;
   const size_t smem = (size_t)p.stages * p.stage_bytes;
   if (!p.half)
     return launch_pdl(norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>, dim3((unsigned)a.parts), dim3((unsigned)p.threads),

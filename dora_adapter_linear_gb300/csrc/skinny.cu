@@ -238,12 +238,8 @@ template <int R, bool KR, bool MASK = false>
 static cudaError_t rowproj_launch(const RowProjDesc& d, cudaStream_t st) {
   using C = rp::Cfg<R, KR, MASK>;
   auto k = rowproj_kernel<R, KR, MASK>;
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  const cudaError_t allowed = allow_smem<rowproj_kernel<R, KR, MASK>>(C::SMEM);
+  if (allowed != cudaSuccess) return allowed;
   RpParams P;
   memset(&P, 0, sizeof(P));
   P.d = d;
@@ -556,12 +552,8 @@ template <int R, bool HAS_Y, bool SUMS, bool MASK = false>
 static cudaError_t colreduce_launch(const ColReduceDesc& d, cudaStream_t st) {
   using C = cr::Cfg<R, HAS_Y, MASK>;
   auto k = colreduce_kernel<R, HAS_Y, SUMS, MASK>;
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  const cudaError_t allowed = allow_smem<colreduce_kernel<R, HAS_Y, SUMS, MASK>>(C::SMEM);
+  if (allowed != cudaSuccess) return allowed;
   CrParams P;
   memset(&P, 0, sizeof(P));
   P.d = d;
@@ -907,12 +899,8 @@ template <int R, bool ROW, bool SUMS>
 static cudaError_t rowcol_launch(const RowColDesc& d, cudaStream_t st) {
   using C = rc::Cfg<R>;
   auto k = rowcol_kernel<R, ROW, SUMS>;
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  const cudaError_t allowed = allow_smem<rowcol_kernel<R, ROW, SUMS>>(C::SMEM);
+  if (allowed != cudaSuccess) return allowed;
   RcParams P;
   memset(&P, 0, sizeof(P));
   P.d = d;

@@ -254,12 +254,8 @@ cudaError_t w8a8_gemm(int64_t M, int64_t K, int64_t N, int r, const int8_t* Xq, 
                       int32_t* acc_out, cudaStream_t st) {
   if (M <= 0 || N <= 0) return cudaSuccess;
   const int smem = w8::STAGES * w8::STAGE_BYTES;
-  static bool set = false;
-  if (!set) {
-    cudaError_t e = cudaFuncSetAttribute(w8a8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    set = true;
-  }
+  const cudaError_t allowed = allow_smem<w8a8_gemm_kernel>(smem);
+  if (allowed != cudaSuccess) return allowed;
   dim3 grid((unsigned)((N + w8::BN - 1) / w8::BN), (unsigned)((M + w8::BM - 1) / w8::BM));
   w8a8_gemm_kernel<<<grid, 256, smem, st>>>(M, K, N, r, Xq, sx, Wq, sw, Z, B, s, bias, Y, acc_out);
   count_launch();
