@@ -487,7 +487,8 @@ def _done(result, where):
 
 
 @lru_cache(maxsize=256)
-def _norm_bwd_bytes(M, D, dtype):
+def _norm_bwd_bytes(M, D, dtype, device):
+    """Bytes of workspace; they go by the multiprocessors of the current device, of index `device`."""
     if dtype not in (BF16, F32):
         return 0
     return L.block_norm_bwd_workspace_bytes(L.LoraNormShape(M, D, 1, D, D, D, D, 1.0, 1.0, 0.0, 0,
@@ -528,7 +529,8 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
     and r_post."""
     if Xout.dim() == 2 and Xout.is_cuda:
-        need = _norm_bwd_bytes(*Xout.shape, Xout.dtype)
+        _need_cuda("Xout", Xout)
+        need = _norm_bwd_bytes(*Xout.shape, Xout.dtype, Xout.device.index)
         if need:
             done = L.host().block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre, w_post, gate, rows_per_gate, alpha,
                                            w_offset, post_norm, need_dx, need_dw, need_dgate,

@@ -70,6 +70,21 @@ def test_a_step_under_another_device_is_refused(without_gpu, monkeypatch):
             opt.step([elsewhere(4, 4)])
 
 
+def test_workspace_sizes_are_of_a_device(without_gpu, monkeypatch):
+    """A larger device has more parts, and each of them partial sums of its own."""
+    current, asked = [0], []
+    monkeypatch.setattr(L, "current_device", lambda: current[0])
+    monkeypatch.setattr(L, "block_norm_bwd_workspace_bytes", lambda sh: (1 + current[0]) << 20)
+    monkeypatch.setattr(ops, "workspace", lambda nbytes, device: asked.append(nbytes))
+    monkeypatch.setattr(L, "block_norm_bwd", lambda *a: None)
+    monkeypatch.setattr(L, "host", lambda: type("Host", (), {"block_norm_bwd": lambda *a: (None,) * 5}))
+    for current[0] in (0, 1, 0):
+        with FakeTensorMode():
+            t = lambda *s, dtype=BF16: torch.zeros(*s, dtype=dtype, device=f"cuda:{current[0]}")  # noqa: B023,E731
+            ops.block_norm_bwd(t(9, 48), t(9, 48), t(9, dtype=F32), None, t(9, 48), t(9, 48))
+    assert asked == [1 << 20, 2 << 20, 1 << 20]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["norm forward", "norm backward", "rotary forward", "rotary backward"])
 def test_refused_by_the_native_calls(name):
