@@ -2,6 +2,7 @@
 The tensors are made up (shapes and devices without memory), so no second device is needed."""
 import pytest
 import torch
+from torch._subclasses import fake_tensor
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 from dora_adapter_linear_gb300 import _lib as L
@@ -16,6 +17,11 @@ class NoHost:
 
     def __getattr__(self, name):
         return lambda *a: None
+
+
+@pytest.fixture(autouse=True)
+def no_context_of_a_made_up_device(monkeypatch):
+    monkeypatch.setattr(fake_tensor, "init_gpu_context", lambda device: None, raising=False)
 
 
 @pytest.fixture
