@@ -60,6 +60,11 @@ Tensor fresh(const Tensor& x, at::IntArrayRef sizes, at::ScalarType type) {
   return at::detail::empty_cuda(sizes, type, x.device(), std::nullopt);
 }
 Tensor fresh(const Tensor& x, at::IntArrayRef sizes) { return fresh(x, sizes, x.scalar_type()); }
+// Other Python threads run while this one allocates and launches: either may have to wait for the device.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 PyObject* not_here() { Py_RETURN_NONE; }
 PyObject* wrap(const Tensor& t) {
@@ -123,12 +128,16 @@ PyObject* py_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return not_here();
   if ((sh.ldx = row_stride(*X, *X)) < 0 || (Y && (sh.ldy = row_stride(*Y, *X)) < 0)) return not_here();
   Tensor z, h, r_pre, r_post;
-  if (Y) z = fresh(*X, {sh.M, sh.D});
-  if (pre) h = fresh(*X, {sh.M, sh.D}), r_pre = fresh(*X, {sh.M}, at::kFloat);
-  if (post) r_post = fresh(*X, {sh.M}, at::kFloat);
-  const auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-  const int e = norm_fwd_call(&sh, X.ptr(), Y.ptr(), w_pre.ptr(), w_post.ptr(), gate.ptr(), p(z), p(h),
-                              static_cast<float*>(p(r_pre)), static_cast<float*>(p(r_post)), stream());
+  int e;
+  {
+    const Unlocked unlocked;
+    if (Y) z = fresh(*X, {sh.M, sh.D});
+    if (pre) h = fresh(*X, {sh.M, sh.D}), r_pre = fresh(*X, {sh.M}, at::kFloat);
+    if (post) r_post = fresh(*X, {sh.M}, at::kFloat);
+    const auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    e = norm_fwd_call(&sh, X.ptr(), Y.ptr(), w_pre.ptr(), w_post.ptr(), gate.ptr(), p(z), p(h),
+                      static_cast<float*>(p(r_pre)), static_cast<float*>(p(r_post)), stream());
+  }
   if (e != LORA_OK) return PyLong_FromLong(e);
   return tuple_of(Y ? z : *X, h, r_pre, r_post);
   END_HANDLE_TH_ERRORS
@@ -157,16 +166,19 @@ PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       (dH && (sh.lddh = row_stride(*dH, *X)) < 0) || (dZ && (sh.lddz = row_stride(*dZ, *X)) < 0))
     return not_here();
   Tensor dX, dY, dw_pre, dw_post, dgate;
-  if (need_dx) dX = fresh(*X, {sh.M, sh.D});
-  if (Y) dY = fresh(*X, {sh.M, sh.D});
-  if (need_dw && w_pre) dw_pre = fresh(*X, {sh.D});
-  if (need_dw && w_post) dw_post = fresh(*X, {sh.D});
-  if (need_dgate && gate) dgate = fresh(*X, (*gate).sizes());
-  const auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-  const int e = norm_bwd_call(&sh, X.ptr(), Y.ptr(), w_pre.ptr(), w_post.ptr(), gate.ptr(),
-                              static_cast<const float*>(r_pre.ptr()), static_cast<const float*>(r_post.ptr()), dH.ptr(),
-                              dZ.ptr(), p(dX), p(dY), p(dw_pre), p(dw_post), p(dgate), ws.ptr(), (*ws).nbytes(),
-                              stream());
+  int e;
+  {
+    const Unlocked unlocked;
+    if (need_dx) dX = fresh(*X, {sh.M, sh.D});
+    if (Y) dY = fresh(*X, {sh.M, sh.D});
+    if (need_dw && w_pre) dw_pre = fresh(*X, {sh.D});
+    if (need_dw && w_post) dw_post = fresh(*X, {sh.D});
+    if (need_dgate && gate) dgate = fresh(*X, (*gate).sizes());
+    const auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    e = norm_bwd_call(&sh, X.ptr(), Y.ptr(), w_pre.ptr(), w_post.ptr(), gate.ptr(),
+                      static_cast<const float*>(r_pre.ptr()), static_cast<const float*>(r_post.ptr()), dH.ptr(),
+                      dZ.ptr(), p(dX), p(dY), p(dw_pre), p(dw_post), p(dgate), ws.ptr(), (*ws).nbytes(), stream());
+  }
   if (e != LORA_OK) return PyLong_FromLong(e);
   return tuple_of(dX, dY, dw_pre, dw_post, dgate);
   END_HANDLE_TH_ERRORS
@@ -189,15 +201,17 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!(wide || p.scalar_type() == at::kInt) || !dense(p, x, p.scalar_type(), {x.size(0)}) || rot > x.size(2) ||
       !dense(*freq, x, at::kLong, {rot / 2}))
     return not_here();
-  Tensor y;
-  if (!out) y = fresh(x, x.sizes());
-  else if (!same_kind(*out, x) || (*out).sizes() != x.sizes() || (*out).stride(2) != 1) return not_here();
-  else y = *out;
-  const lora_rotary_shape sh{x.size(0), x.size(1), x.size(2), rot, x.stride(0), x.stride(1), y.stride(0), y.stride(1),
-                             (float)scale, (int32_t)layout, wide ? 64 : 32, dtype_of(x)};
+  if (out && (!same_kind(*out, x) || (*out).sizes() != x.sizes() || (*out).stride(2) != 1)) return not_here();
   const auto call = PyObject_IsTrue(a[0]) == 1 ? rotary_bwd_call : rotary_fwd_call;
-  const int e = call(&sh, x.data_ptr(), p.data_ptr(), static_cast<const uint64_t*>((*freq).data_ptr()), y.data_ptr(),
-                     stream());
+  Tensor y;
+  int e;
+  {
+    const Unlocked unlocked;
+    y = out ? *out : fresh(x, x.sizes());
+    const lora_rotary_shape sh{x.size(0), x.size(1), x.size(2), rot, x.stride(0), x.stride(1), y.stride(0), y.stride(1),
+                               (float)scale, (int32_t)layout, wide ? 64 : 32, dtype_of(x)};
+    e = call(&sh, x.data_ptr(), p.data_ptr(), static_cast<const uint64_t*>((*freq).data_ptr()), y.data_ptr(), stream());
+  }
   if (e != LORA_OK) return PyLong_FromLong(e);
   if (!out) return THPVariable_Wrap(y);
   Py_INCREF(a[7]);
@@ -234,7 +248,11 @@ PyObject* py_pair(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 1) return not_here();
   const Arg like(a[0]);
   if (!like || !(*like).is_cuda()) return not_here();
-  const Tensor t = fresh(*like, {2}, at::kFloat);
+  Tensor t;
+  {
+    const Unlocked unlocked;
+    t = fresh(*like, {2}, at::kFloat);
+  }
   t.unsafeGetTensorImpl()->set_sizes_contiguous({});
   return THPVariable_Wrap(t);
   END_HANDLE_TH_ERRORS
