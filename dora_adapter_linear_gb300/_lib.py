@@ -202,7 +202,8 @@ def current_device() -> int:
 def need_current(name, device):
     """The calls run on the current device's current stream: operands of another device would be read
     without any order to that device's own work, or not be reachable at all."""
-    if device.type == "cuda" and device.index is not None and device.index != current_device():
+    index = device.index        # None: the current one, or the CPU
+    if index is not None and index != current_device() and device.type == "cuda":
         raise ValueError(f"{name} must be on the current device, cuda:{current_device()}, got {device}: make it the "
                          f"current one around the call")
 

@@ -529,8 +529,7 @@ def block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre=None, w_post=None, g
     (dX, dY, dw_pre, dw_post, dgate), None for what is not asked for or has no input.  eps is in r_pre
     and r_post."""
     if Xout.dim() == 2 and Xout.is_cuda:
-        _need_cuda("Xout", Xout)
-        need = _norm_bwd_bytes(*Xout.shape, Xout.dtype, Xout.device.index)
+        need = _norm_bwd_bytes(*Xout.shape, Xout.dtype, L.current_device())
         if need:
             done = L.host().block_norm_bwd(Xout, Y, r_pre, r_post, dH, dXout, w_pre, w_post, gate, rows_per_gate, alpha,
                                            w_offset, post_norm, need_dx, need_dw, need_dgate,

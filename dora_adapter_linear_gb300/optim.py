@@ -39,7 +39,8 @@ class AdamW:
                 raise ValueError(f"tensor {i} is on {p.device}, the first on {params[0].device}")
         if not params:
             raise ValueError("no tensors to optimise")
-        L.need_current("the tensors", params[0].device)
+        self._device = params[0].device
+        L.need_current("the tensors", self._device)
         spans = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size()) for p in params if p.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("two of the tensors share memory: each would be updated under the other's hands")
@@ -94,7 +95,7 @@ class AdamW:
         max_norm then clips their global norm.  With max_norm the norm before the clip is returned (a
         0-d tensor, nothing waits), and a step whose norm is not finite changes nothing and is not
         counted; max_norm=inf only guards."""
-        L.need_current("the tensors", self.params[0].device)
+        L.need_current("the tensors", self._device)
         at, n, norm = self._pointers(grads), len(self.params), None
         lr = self.lr if lr is None else lr
         lr_dev = None

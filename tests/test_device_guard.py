@@ -70,7 +70,7 @@ def test_refused_by_the_wrappers(without_gpu, name):
 def test_a_step_under_another_device_is_refused(without_gpu, monkeypatch):
     opt = optim.AdamW.__new__(optim.AdamW)      # one that was made while its device was the current one
     with FakeTensorMode():
-        opt.params = [elsewhere(4, 4)]
+        opt.params, opt._device = [elsewhere(4, 4)], torch.device("cuda", 1)
         monkeypatch.setattr(optim.AdamW, "_pointers", lambda self, grads: pytest.fail("the step went on"))
         with pytest.raises(ValueError, match="current device"):
             opt.step([elsewhere(4, 4)])
