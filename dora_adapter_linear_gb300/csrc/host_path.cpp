@@ -65,6 +65,10 @@ struct Unlocked {
   PyThreadState* const state = PyEval_SaveThread();
   ~Unlocked() { PyEval_RestoreThread(state); }
 };
+// A kernel has written t: autograd notices if it had kept t for a backward.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 PyObject* not_here() { Py_RETURN_NONE; }
 PyObject* wrap(const Tensor& t) {
@@ -214,6 +218,7 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   if (e != LORA_OK) return PyLong_FromLong(e);
   if (!out) return THPVariable_Wrap(y);
+  written(y);
   Py_INCREF(a[7]);
   return a[7];
   END_HANDLE_TH_ERRORS
@@ -239,6 +244,22 @@ PyObject* py_pointers(PyObject*, PyObject* const* a, Py_ssize_t n) {
     memcpy(to + i * sizeof at, &at, sizeof at);
   }
   return bytes;
+  END_HANDLE_TH_ERRORS
+}
+
+// (tensors, addresses): the tensors whose gradients' addresses, from pointers(), are not 0 have been written
+PyObject* py_written(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 2 || !PyList_Check(a[0]) || !PyBytes_Check(a[1])) return not_here();
+  const Py_ssize_t count = PyList_GET_SIZE(a[0]);
+  if (PyBytes_GET_SIZE(a[1]) != count * (Py_ssize_t)sizeof(uint64_t)) return not_here();
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    uint64_t at;
+    memcpy(&at, PyBytes_AS_STRING(a[1]) + i * sizeof at, sizeof at);
+    const Arg t(PyList_GET_ITEM(a[0], i));
+    if (at && t) written(*t);
+  }
+  Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
 
@@ -284,6 +305,7 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), "take the library's entry point
                          {"rotary", FAST(py_rotary), "ops.rotary_fwd and rotary_bwd"},
                          {"pair", FAST(py_pair), "an optimiser's norm and factor"},
                          {"pointers", FAST(py_pointers), "addresses of an optimiser's gradients"},
+                         {"written", FAST(py_written), "an optimiser's tensors after its step"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", "host side of short calls", -1, methods, nullptr, nullptr, nullptr,
                       nullptr};

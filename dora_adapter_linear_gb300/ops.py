@@ -584,6 +584,7 @@ def _rotary(inverse, X, pos, plan, out):
     if plan.rot_dim > hd:
         raise ValueError(f"the plan turns {plan.rot_dim} elements of a head, the heads have {hd}")
     _need_cuda("X", X)
+    given = out
     if out is None:
         out = torch.empty(M, H, hd, dtype=X.dtype, device=dev)
     elif out is not X and (out.shape != X.shape or out.dtype is not X.dtype or out.device != dev
@@ -593,6 +594,8 @@ def _rotary(inverse, X, pos, plan, out):
     sh = L.LoraRotaryShape(M, H, hd, plan.rot_dim, xt, xh, yt, yh, plan.scale, plan.layout, 64 if wide else 32,
                            L.dtype_code(X))
     (L.rotary_bwd if inverse else L.rotary_fwd)(sh, X, pos, plan.freq, out)
+    if given is not None and not out.is_inference():
+        torch.autograd.graph.increment_version(out)     # autograd notices if it had kept it for a backward
     return out
 
 

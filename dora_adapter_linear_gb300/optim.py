@@ -110,6 +110,7 @@ class AdamW:
             norm = L.host().pair(self.params[0])   # shows the norm, the factor lies behind it
             L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm, self._ws)
         L.adamw_step(self._tensors, at, n, self._state, hyper, norm)
+        L.host().written(self.params, at)
         return norm
 
     def state_dict(self):
