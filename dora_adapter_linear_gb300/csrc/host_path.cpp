@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -205,7 +206,9 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!(wide || p.scalar_type() == at::kInt) || !dense(p, x, p.scalar_type(), {x.size(0)}) || rot > x.size(2) ||
       !dense(*freq, x, at::kLong, {rot / 2}))
     return not_here();
-  if (out && (!same_kind(*out, x) || (*out).sizes() != x.sizes() || (*out).stride(2) != 1)) return not_here();
+  if (out && (!same_kind(*out, x) || (*out).sizes() != x.sizes() || (*out).stride(2) != 1 ||
+              ((*out).requires_grad() && at::GradMode::is_enabled())))
+    return not_here();
   const auto call = PyObject_IsTrue(a[0]) == 1 ? rotary_bwd_call : rotary_fwd_call;
   Tensor y;
   int e;

@@ -581,6 +581,8 @@ def _rotary(inverse, X, pos, plan, out):
     dev = X.device
     if pos.device != dev or plan.freq.device != dev:
         raise ValueError(f"pos and the plan must be on {dev}")
+    if out is not None and out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out needs a gradient, which would not be that of this call: call it under torch.no_grad()")
     if plan.rot_dim > hd:
         raise ValueError(f"the plan turns {plan.rot_dim} elements of a head, the heads have {hd}")
     _need_cuda("X", X)

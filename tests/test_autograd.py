@@ -72,3 +72,29 @@ def test_a_step_moves_its_parameters_versions(ops):
     with pytest.raises(ops.L.LoraError):
         opt.step(grads, lr=float("nan"))    # refused: nothing was written
     assert [p._version - b for p, b in zip(params, before)] == [1, 0, 1]
+
+
+def test_rotary_into_a_tensor_that_needs_a_gradient_is_refused(ops):
+    plan, pos = ops.rotary_plan(32, device="cpu"), torch.arange(6)
+    out = torch.zeros(6, 2, 32, requires_grad=True)
+    for call in (ops.rotary_fwd, ops.rotary_bwd):
+        with pytest.raises(ValueError, match="gradient"):
+            call(torch.zeros(6, 2, 32), pos, plan, out=out)
+
+
+@pytest.mark.gpu
+def test_rotary_into_a_tensor_that_needs_a_gradient(ops):
+    plan, pos = ops.rotary_plan(32, device=DEV), torch.arange(6, device=DEV)
+    W = torch.randn(64, 64, device=DEV, requires_grad=True)
+    X = torch.randn(6, 64, device=DEV) @ W
+    heads = X.view(6, 2, 32)
+    before = heads.detach().clone()
+    for call in (ops.rotary_fwd, ops.rotary_bwd):
+        with pytest.raises(ValueError, match="gradient"):
+            call(heads, pos, plan, out=heads)
+        assert torch.equal(heads, before)
+    with torch.no_grad():
+        assert ops.rotary_fwd(heads, pos, plan, out=heads) is heads
+    assert not torch.equal(heads, before)
+    ops.rotary_fwd(before, pos, plan, out=before)
+    assert torch.equal(heads, before)
