@@ -581,6 +581,7 @@ def _rotary(inverse, X, pos, plan, out):
     dev = X.device
     if pos.device != dev or plan.freq.device != dev:
         raise ValueError(f"pos and the plan must be on {dev}")
+    _check_shapes(X, **{"the plan's freq": (plan.freq, (plan.rot_dim // 2,), torch.int64)})
     if out is not None and out.requires_grad and torch.is_grad_enabled():
         raise ValueError("out needs a gradient, which would not be that of this call: call it under torch.no_grad()")
     if plan.rot_dim > hd:
