@@ -206,6 +206,48 @@ cudaError_t launch(const RotArgs& a, bool inter, uintptr_t heads, cudaStream_t s
   return launch<T, B, false, B>(a, st);
 }
 
+// Whether a head of x and one of y, which begins d elements after x, share an element.  A head is hd consecutive
+// elements, and y's heads are apart: o is the dimension of its larger stride, i the other.  A head of x at p, counted
+// from y's begin, can only meet y's rows (over o) at p / stride and at the next one.  With the same outer stride in
+// both, as columns of one packed projection have, all rows of x are alike and one stands for them; with the same
+// inner one as well, so are all heads of a row.
+struct Dim {
+  int64_t n, stride;
+};
+bool heads_meet(Dim xo, Dim xi, Dim yo, Dim yi, int64_t hd, int64_t d) {
+  typedef __int128 wide;    // a caller's strides are not bounded
+  for (Dim* t : {&xo, &xi})
+    if (t->stride == 0) t->n = 1;         // the same head again and again
+  for (Dim* t : {&xo, &xi, &yo, &yi})
+    if (t->n == 1) t->stride = INT64_MAX;   // of no use: 0 is its only index
+  const auto span = [](Dim t) { return (wide)(t.n - 1) * (t.n == 1 ? 0 : t.stride); };
+  if (d >= span(xo) + span(xi) + hd || d + span(yo) + span(yi) + hd <= 0) return false;
+  const bool alike = xo.n == yo.n && xo.stride == yo.stride, all_alike = alike && xi.n == yi.n && xi.stride == yi.stride;
+  const auto floor_div = [](wide a, wide b) { return a >= 0 ? a / b : -((b - 1 - a) / b); };
+  const auto row_meets = [&](wide p) {   // a head at p and the heads of y's row that begins at 0
+    if (p + hd <= 0) return false;
+    wide j = (p + hd - 1) / yi.stride;   // the last one that begins before the head ends
+    if (j > yi.n - 1) j = yi.n - 1;
+    return j * yi.stride + hd > p;
+  };
+  if (all_alike) {   // m heads and k rows between two that meet
+    const wide rows = floor_div(-(wide)d, yo.stride);
+    for (wide k = rows - 1; k <= rows + 1; ++k) {
+      const wide r = -d - k * yo.stride, heads = floor_div(-r, yi.stride);
+      for (wide m = heads; m <= heads + 1; ++m)
+        if (k > -yo.n && k < yo.n && m > -yi.n && m < yi.n && m * yi.stride + r < hd && m * yi.stride + r > -hd) return true;
+    }
+    return false;
+  }
+  for (int64_t a = 0; a < (alike ? 1 : xo.n); ++a)
+    for (int64_t b = 0; b < xi.n; ++b) {
+      const wide p = (wide)a * xo.stride + (wide)b * xi.stride - d, first = floor_div(p, yo.stride);
+      for (wide k = first; k <= first + 1; ++k)
+        if ((alike ? k > -yo.n && k < yo.n : k >= 0 && k < yo.n) && row_meets(p - k * yo.stride)) return true;
+    }
+  return false;
+}
+
 lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, const uint64_t* freq, void* Y,
                    bool inverse, void* stream) {
   if (!sh) return LORA_ERR_INVALID_ARG;
@@ -223,7 +265,8 @@ lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, 
   const auto apart = [](int64_t n, int64_t s, int64_t inner) { return n <= 1 || s >= inner; };
   const int64_t hd = sh->head_dim, M = sh->M, H = sh->H;
   if (sh->x_token < 0 || sh->x_head < 0 || sh->y_token < 0 || sh->y_head < 0) return LORA_ERR_INVALID_ARG;
-  if (!(apart(H, sh->y_head, hd) && apart(M, sh->y_token, (H - 1) * sh->y_head + hd)) &&
+  const bool token_outer = apart(H, sh->y_head, hd) && apart(M, sh->y_token, (H - 1) * sh->y_head + hd);
+  if (!token_outer &&
       !(apart(M, sh->y_token, hd) && apart(H, sh->y_head, (M - 1) * sh->y_token + hd)))
     return LORA_ERR_INVALID_ARG;
   if (X == Y && ((M > 1 && sh->x_token != sh->y_token) || (H > 1 && sh->x_head != sh->y_head)))
@@ -233,6 +276,11 @@ lora_status rotary(const lora_rotary_shape* sh, const void* X, const void* pos, 
       reinterpret_cast<uintptr_t>(freq) % 8 || reinterpret_cast<uintptr_t>(pos) % (sh->pos_bits / 8))
     return LORA_ERR_MISALIGNED;
   if (M == 0) return LORA_OK;
+  if (X != Y) {
+    const int64_t d = (int64_t)((uintptr_t)Y - (uintptr_t)X) / (int64_t)es;
+    const Dim xt{M, sh->x_token}, xh{H, sh->x_head}, yt{M, sh->y_token}, yh{H, sh->y_head};
+    if (token_outer ? heads_meet(xt, xh, yt, yh, hd, d) : heads_meet(xh, xt, yh, yt, hd, d)) return LORA_ERR_INVALID_ARG;
+  }
   RotArgs a = {};
   a.M = M, a.H = (int)H, a.half = (int)(sh->rot_dim / 2), a.rest = X != Y ? (int)(hd - sh->rot_dim) : 0;
   a.xt = sh->x_token, a.xh = sh->x_head, a.yt = sh->y_token, a.yh = sh->y_head;

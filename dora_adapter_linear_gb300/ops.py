@@ -605,7 +605,8 @@ def _rotary(inverse, X, pos, plan, out):
 def rotary_fwd(X, pos, plan, out=None):
     """Turns the heads X [tokens, heads, head_dim] (any token and head stride: the query and key heads
     of a packed projection are one view) by their positions pos [tokens]; `plan` from rotary_plan.
-    out=X turns in place; by default a new contiguous tensor is returned."""
+    out=X turns in place; by default a new contiguous tensor is returned.  Any other out may not have an
+    element of X among its own."""
     return _rotary(False, X, pos, plan, out)
 
 

@@ -518,8 +518,9 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
  * the angle is exact for every position.
  *   X, Y: element (i, h, c) at i * token stride + h * head stride + c, of dtype LORA_BF16 or
  *   LORA_F32 and aligned to their element; a packed projection's query and key heads are one call.
- *   Y == X (with equal strides) turns in place and leaves the rest of each head alone; otherwise X
- *   and Y do not overlap, and no two elements of Y share an address.
+ *   Y == X (with equal strides) turns in place and leaves the rest of each head alone; otherwise no
+ *   element of X is one of Y (they may lie between one another, as columns of one packed projection do),
+ *   and no two elements of Y share an address: LORA_ERR_INVALID_ARG.
  *   pos [M] int32 or int64 (negative positions too); freq [rot_dim / 2], device memory. */
 typedef enum {
     LORA_ROTARY_HALF = 0,         /* pairs (j, j + rot_dim / 2) */

@@ -1,32 +1,13 @@
 """The host side of the entry points on two devices, over a stand-in for the CUDA runtime (fake_cudart.cpp)."""
 import ctypes
-import os
-import shutil
-import subprocess
 
 import pytest
 
 from dora_adapter_linear_gb300 import _lib as L
-from dora_adapter_linear_gb300 import build as B
+from fake_runtime import fake  # noqa: F401
 
 AT = 1 << 20        # never dereferenced
 WS, SIZE = 1 << 30, 1 << 40
-
-
-@pytest.fixture(scope="module")
-def fake(tmp_path_factory):
-    objects = [os.path.join(B.BUILD, os.path.basename(s) + ".o") for s in B.sources()]
-    B.build(force=not all(map(os.path.exists, objects)))
-    so = str(tmp_path_factory.mktemp("fake") / "fake.so")
-    include = os.path.join(os.path.dirname(os.path.dirname(B.nvcc())), "include")
-    source = os.path.join(os.path.dirname(os.path.abspath(__file__)), "fake_cudart.cpp")
-    # -Bsymbolic: the library's calls go to the stand-in, whatever runtime the process has loaded
-    subprocess.run([shutil.which("g++") or "g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-I", include, source, *objects,
-                    "-Wl,-Bsymbolic", "-o", so], check=True)
-    lib = ctypes.CDLL(so)
-    for name, (res, args) in L._SIGS.items():
-        getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
-    return lib
 
 
 def norm_bwd(lib, dtype, M, D, per, post=1):
@@ -64,7 +45,7 @@ CALLS = {
 
 
 @pytest.mark.parametrize("name", CALLS)
-def test_a_call_on_a_second_device_asks_for_its_shared_memory_there(fake, name):
+def test_a_call_on_a_second_device_asks_for_its_shared_memory_there(fake, name):  # noqa: F811
     before = fake.fake_launches()
     for device in (0, 1, 0):
         fake.fake_device(device)
