@@ -16,6 +16,7 @@
 // The table of tensors travels in the launch's parameters (up to 32 KB), so a step copies nothing and
 // is captured by a CUDA graph as it is.
 #include <cuda_fp8.h>
+#include <float.h>
 #include <math.h>
 
 #include <type_traits>
@@ -684,7 +685,9 @@ lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grad
     if (state->bits == 8 && (!state->m_scale || !state->v_scale)) return LORA_ERR_INVALID_ARG;
   }
   if (!(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0)) return LORA_ERR_INVALID_ARG;
-  if (!(h.eps > 0.0) || !isfinite(h.eps) || !isfinite(h.lr) || !isfinite(h.grad_scale)) return LORA_ERR_INVALID_ARG;
+  // as the kernels have them; an eps below the normal numbers leaves elements without a gradient 0 / 0
+  if (!((float)h.eps >= FLT_MIN) || !isfinite((float)h.eps) || !isfinite((float)h.lr) || !isfinite((float)h.grad_scale))
+    return LORA_ERR_INVALID_ARG;
   for (const void* p : {(const void*)state->m, (const void*)state->v, (const void*)state->m_scale,
                         (const void*)state->v_scale, (const void*)state->master})
     ALN(p);

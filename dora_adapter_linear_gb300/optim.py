@@ -47,8 +47,8 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         b1, b2 = betas
-        if not (0.0 <= b1 < 1.0 and 0.0 <= b2 < 1.0 and eps > 0.0 and math.isfinite(eps)):
-            raise ValueError(f"betas must be in [0, 1) and eps above 0, got {betas}, {eps}")
+        if not (0.0 <= b1 < 1.0 and 0.0 <= b2 < 1.0 and 2.0 ** -126 <= eps < 2.0 ** 128):
+            raise ValueError(f"betas must be in [0, 1) and eps a normal fp32 number, got {betas}, {eps}")
         self.params, self.lr, self.betas, self.eps, self.state_bits = params, lr, (b1, b2), eps, state_bits
         n = len(params)
         self._tensors = L.adamw_tensors(params, _each("lr_mul", lr_mul, n), _each("weight_decay", weight_decay, n))

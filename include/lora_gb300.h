@@ -569,6 +569,8 @@ typedef struct {
     int32_t* ctl;
     int32_t bits;
 } lora_adamw_state;
+/* The arithmetic is fp32: lr, eps and grad_scale are rounded to it and have to be finite there, eps a normal
+ * number (at least 2^-126). */
 typedef struct {
     double lr, beta1, beta2, eps, grad_scale;
     const float* lr_device;       /* device scalar that replaces lr, or NULL */
