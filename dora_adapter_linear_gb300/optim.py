@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import math
+from ctypes import c_float
 
 import torch
 
@@ -105,8 +106,8 @@ class AdamW:
             lr, lr_dev = 0.0, lr.data_ptr()
         hyper = L.LoraAdamwHyper(lr, *self.betas, self.eps, grad_scale, lr_dev)
         if max_norm is not None:
-            if not max_norm > 0:
-                raise ValueError(f"max_norm must be above 0, got {max_norm}")
+            if not c_float(max_norm).value > 0:     # as the kernels have it; 0 there is no clip at all
+                raise ValueError(f"max_norm must be above 0 in fp32, got {max_norm}")
             norm = L.host().pair(self.params[0])   # shows the norm, the factor lies behind it
             L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm, self._ws)
         L.adamw_step(self._tensors, at, n, self._state, hyper, norm)

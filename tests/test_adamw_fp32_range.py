@@ -45,3 +45,19 @@ def test_elements_without_a_gradient_stay(bits):
         with pytest.raises(L.LoraError):
             opt.step([torch.zeros_like(p)], **bad)
     assert opt.steps == 1
+
+
+@pytest.mark.parametrize("max_norm", [1e-50, 1e-46, 0.0, -1.0, float("nan")])
+def test_a_clip_that_fp32_does_not_hold_is_refused(monkeypatch, max_norm):
+    """It would be 0 in the kernels, where 0 stands for no clip."""
+    from dora_adapter_linear_gb300 import optim
+    opt = optim.AdamW.__new__(optim.AdamW)
+    opt.params, opt._device = [torch.zeros(4)], torch.device("cpu")
+    opt.lr, opt.betas, opt.eps, opt._tensors, opt._ws, opt._state = 1e-3, (0.9, 0.999), 1e-8, None, None, None
+    monkeypatch.setattr(L, "host", lambda: type("Host", (), {"pair": lambda *a: torch.zeros(()), "pointers": lambda *a: b"",
+                                                             "written": lambda *a: None}))
+    for name in ("adamw_grad_norm", "adamw_step"):
+        monkeypatch.setattr(L, name, lambda *a: None)
+    opt.step([torch.zeros(4)], max_norm=1e-40)      # held, if with fewer bits
+    with pytest.raises(ValueError, match="max_norm"):
+        opt.step([torch.zeros(4)], max_norm=max_norm)
