@@ -71,6 +71,12 @@ void written(const Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
+// the truth of a flag; false: it has none, and the error is set
+bool truth(PyObject* o, bool* value) {
+  const int v = PyObject_IsTrue(o);
+  *value = v == 1;
+  return v >= 0;
+}
 PyObject* not_here() { Py_RETURN_NONE; }
 PyObject* wrap(const Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
@@ -126,7 +132,8 @@ PyObject* py_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Arg X(a[0]), Y(a[1]), w_pre(a[2]), w_post(a[3]), gate(a[4]);
   const double alpha = PyFloat_AsDouble(a[6]), eps = PyFloat_AsDouble(a[7]), off = PyFloat_AsDouble(a[8]);
   if (PyErr_Occurred()) return nullptr;
-  const bool pre = PyObject_IsTrue(a[9]) == 1, post = PyObject_IsTrue(a[10]) == 1;
+  bool pre, post;
+  if (!truth(a[9], &pre) || !truth(a[10], &post)) return nullptr;
   lora_norm_shape sh;
   if (!X || !Y.ok || !w_pre.ok || !w_post.ok || !gate.ok || (!Y && (gate || post || !pre)) || (w_pre && !pre) ||
       !norm_shape(&sh, *X, w_pre, w_post, gate, a[5], alpha, eps, off, post))
@@ -157,8 +164,8 @@ PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws(a[16]);
   const double alpha = PyFloat_AsDouble(a[10]), off = PyFloat_AsDouble(a[11]);
   if (PyErr_Occurred()) return nullptr;
-  const bool post = PyObject_IsTrue(a[12]) == 1, need_dx = PyObject_IsTrue(a[13]) == 1,
-             need_dw = PyObject_IsTrue(a[14]) == 1, need_dgate = PyObject_IsTrue(a[15]) == 1;
+  bool post, need_dx, need_dw, need_dgate;
+  if (!truth(a[12], &post) || !truth(a[13], &need_dx) || !truth(a[14], &need_dw) || !truth(a[15], &need_dgate)) return nullptr;
   for (const Arg* t : {&Y, &r_pre, &r_post, &dH, &dZ, &w_pre, &w_post, &gate})
     if (!t->ok) return not_here();
   lora_norm_shape sh;
@@ -209,7 +216,9 @@ PyObject* py_rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (out && (!same_kind(*out, x) || (*out).sizes() != x.sizes() || (*out).stride(2) != 1 ||
               ((*out).requires_grad() && at::GradMode::is_enabled())))
     return not_here();
-  const auto call = PyObject_IsTrue(a[0]) == 1 ? rotary_bwd_call : rotary_fwd_call;
+  bool inverse;
+  if (!truth(a[0], &inverse)) return nullptr;
+  const auto call = inverse ? rotary_bwd_call : rotary_fwd_call;
   Tensor y;
   int e;
   {
