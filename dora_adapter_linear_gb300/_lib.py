@@ -9,13 +9,15 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sys
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int8, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora_gb300.so")
-HOST_PATH = os.path.join(_HERE, "_host.so")
+# built against the private headers of one PyTorch and one Python: another of either finds no module, not this one
+HOST_PATH = os.path.join(_HERE, f"_host.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "lora_gb300.h")
 
 LORA_F32, LORA_BF16 = 0, 1

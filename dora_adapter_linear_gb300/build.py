@@ -1,5 +1,5 @@
-"""Build the C-ABI shared library liblora_gb300.so in-tree with nvcc (sm_103a only), and _host.so, the
-host side of short calls against PyTorch's headers, with g++.
+"""Build the C-ABI shared library liblora_gb300.so in-tree with nvcc (sm_103a only), and the module _host,
+the host side of short calls against PyTorch's headers, with g++.
 
 Each translation unit under csrc/ is compiled in parallel, then linked with the static
 CUDA runtime.  Both are placed next to this file, where the binding loads them.
@@ -13,11 +13,13 @@ import subprocess
 import sys
 import sysconfig
 
+from ._lib import HOST_PATH as HOST
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liblora_gb300.so")
-HOST_SRC, HOST = os.path.join(CSRC, "host_path.cpp"), os.path.join(HERE, "_host.so")
+HOST_SRC = os.path.join(CSRC, "host_path.cpp")
 BUILD = os.path.join(ROOT, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
