@@ -4,9 +4,11 @@
 // (2 j, 2 j + 1) in the interleaved one; the rest of a head passes unchanged.
 //
 // The angle is kept in turns: freq[j] = theta_j / (2 pi) as a 64-bit binary fraction, so the low 64
-// bits of pos freq[j] are the fraction of a turn, exact for every 64-bit position (an fp32 product
+// bits of pos freq[j] are the fraction of a turn, without a rounding of the product (an fp32 one
 // would be off by 2^-24 of the angle: 0.008 rad at position 131072).  Its upper 32 bits, as a signed
-// half-turn in [-1, 1), go to sincospif: the angle is within pi 2^-25 of the true one.
+// half-turn in [-1, 1), go to sincospif: the angle is within pi 2^-25 of pos times the one that freq[j]
+// stands for.  What freq[j] itself is off by grows with the position: from fp64 arithmetic 1.5 2^-53 theta_j (2^-30
+// rad at position 2^22, as much as pi 2^-25 at 2^29) and half a unit of the fraction, pi 2^-64.
 // Bound by memory: each rotated element is read and written once.
 #include <math.h>
 

@@ -13,7 +13,8 @@ LAYOUTS = {"half": L.LORA_ROTARY_HALF, "interleaved": L.LORA_ROTARY_INTERLEAVED}
 
 @dataclass(frozen=True)
 class RotaryPlan:
-    """freq: [rot_dim / 2] fractions of a turn per position in units of 2^-64 (int64 bit patterns);
+    """freq: [rot_dim / 2] fractions of a turn per position in units of 2^-64 (int64 bit patterns), from fp64
+    arithmetic: within 1.5 2^-53 of theta_j / (2 pi) and half a unit;
     scale: factor on the rotated values; layout: the C ABI's lora_rotary_layout."""
     freq: torch.Tensor
     rot_dim: int

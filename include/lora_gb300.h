@@ -514,8 +514,8 @@ lora_status block_norm_bwd(const lora_norm_shape* sh, const void* Xout, const vo
  * Pair j < rot_dim / 2 of each of the H heads of token i, (a, b), becomes
  *   scale (a cos t - b sin t, b cos t + a sin t),  t = pos[i] theta_j;
  * the rest of a head passes unchanged.  rotary_bwd applies the transpose (the turn by -t) to a
- * gradient.  freq[j] = round(2^64 theta_j / (2 pi)) mod 2^64, a fraction of a turn per position, so
- * the angle is exact for every position.
+ * gradient.  freq[j] = round(2^64 theta_j / (2 pi)) mod 2^64, a fraction of a turn per position: the
+ * angle is within pi 2^-25 + |pos| pi 2^-64 of pos theta_j (more where freq[j] is not the nearest fraction).
  *   X, Y: element (i, h, c) at i * token stride + h * head stride + c, of dtype LORA_BF16 or
  *   LORA_F32 and aligned to their element; a packed projection's query and key heads are one call.
  *   Y == X (with equal strides) turns in place and leaves the rest of each head alone; otherwise no
