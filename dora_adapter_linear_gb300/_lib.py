@@ -196,9 +196,7 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def current_device() -> int:
-    """The index of the current device, whose streams the calls run on."""
-    return torch._C._cuda_getDevice()
+current_device = torch._C._cuda_getDevice    # the index of the device whose streams the calls run on
 
 
 def need_current(name, device):
