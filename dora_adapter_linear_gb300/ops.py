@@ -30,11 +30,28 @@ def workspace(nbytes: int, device) -> torch.Tensor:
         for k in [k for k in list(_WS) if k[2] == thread and k[3] not in (0, capture)]:
             del _WS[k]          # of captures that have ended: their graphs' pools keep the memory
         new = torch.empty if capture else torch.zeros       # in a graph: the error word's 256 bytes alone
-        buf = new(max(nbytes, 256), dtype=torch.uint8, device=device)
+        old, buf = buf, new(max(nbytes, 256), dtype=torch.uint8, device=device)
         if capture:
             buf[:256].zero_()
+        elif old is not None:
+            buf[:256].copy_(old[:256])          # an error that has not been looked at yet
         _WS[key] = buf
     return buf
+
+
+def check_device_errors():
+    """Waits for the device, then raises LoraError if a wait inside a kernel ran out since the last check: calls
+    launch and return, so this is where it shows, and the outputs of the calls before are not to be used.
+    Looks at the calls of every thread and stream, of captured ones at those of the last capture."""
+    torch.cuda.synchronize()
+    failed = 0
+    for buf in list(_WS.values()):
+        status = L.lora_check_device_error(buf)
+        if status:
+            failed = status
+            L.lora_clear_device_error(buf)
+    if failed:
+        raise L.LoraError(failed, "a call since the last check")
 
 
 def _shape_of(X, W0, A):

@@ -57,3 +57,38 @@ def test_a_capture_has_a_buffer_of_its_own(monkeypatch):
     assert address() == eager.data_ptr()
     assert address(1 << 20) not in (eager.data_ptr(), *(t.data_ptr() for t in captured.values()))
     assert len(ops._WS) == 1            # what ended captures used is left to their graphs
+
+
+def test_an_error_that_nobody_has_looked_at_outlives_its_buffer(monkeypatch):
+    first = ops.workspace(1024, torch.device("cpu"))
+    first[0], first[300] = 1, 9
+    larger = ops.workspace(4096, torch.device("cpu"))
+    assert larger.data_ptr() != first.data_ptr() and larger[0] == 1 and not larger[1:].any()
+    cleared = []
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: None)
+    monkeypatch.setattr(L, "lora_check_device_error", lambda buf: 6 if buf[0] else 0)
+    monkeypatch.setattr(L, "lora_clear_device_error", lambda buf: cleared.append(buf[:256].zero_()))
+    with pytest.raises(L.LoraError) as e:
+        ops.check_device_errors()
+    assert e.value.status == 6 and len(cleared) == 1
+    ops.check_device_errors()
+
+
+@pytest.mark.gpu
+def test_a_wait_that_ran_out_shows(monkeypatch):
+    """The test hook's wait on a barrier that nothing arrives on, in the workspace of one of three streams."""
+    monkeypatch.undo()
+    from dora_adapter_linear_gb300.build import build
+    build()
+    device, streams = torch.device("cuda", 0), [torch.cuda.Stream() for _ in range(3)]
+    ops.check_device_errors()
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            ws = ops.workspace(256, device)
+            if i == 1:
+                L.lora_debug_wait_timeout(ws, 2000)
+                assert ops.workspace(1 << 22, device).data_ptr() != ws.data_ptr()
+    with pytest.raises(L.LoraError) as e:
+        ops.check_device_errors()
+    assert e.value.status == 6
+    ops.check_device_errors()
