@@ -19,6 +19,10 @@ namespace lg {
 
 namespace {
 
+constexpr int kSmSmem = 227 * 1024, kRingStatic = 3 * 1024;   // of an SM; what a CTA has beside its dynamic part
+// asked for by every kernel with a dynamic part: up to 48 KB go without, but a kernel's own arrays count among them
+constexpr int kDynamicSmem = kSmSmem - kRingStatic;
+
 struct NormArgs {
   int64_t M, D, rpg;            // rpg: rows that share a gate row
   int64_t ldx, ldy, ldh, ldo;   // row strides of x (or z), y, dh, dz_in
@@ -409,14 +413,11 @@ cudaError_t launch_walk(const NormArgs& a, cudaStream_t st) {
   const int64_t most = (int64_t)(kWalkThreads / threads) * num_sms_current();
   const bool token = a.gate && a.rpg == 1;
   const size_t smem = 2 * (size_t)(token ? 3 : 2) * a.D * sizeof(T);   // at most 96 KB
-  auto go = [&](auto kernel) {
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(kernel, dim3((unsigned)(a.M < most ? a.M : most)), dim3((unsigned)threads), smem, st, a);
-  };
-  return token ? go(norm_fwd_walk_kernel<T, true>) : go(norm_fwd_walk_kernel<T, false>);
+  const cudaError_t allowed = token ? allow_smem<norm_fwd_walk_kernel<T, true>>(kDynamicSmem)
+                                    : allow_smem<norm_fwd_walk_kernel<T, false>>(kDynamicSmem);
+  if (allowed != cudaSuccess) return allowed;
+  return launch_pdl(token ? norm_fwd_walk_kernel<T, true> : norm_fwd_walk_kernel<T, false>,
+                    dim3((unsigned)(a.M < most ? a.M : most)), dim3((unsigned)threads), smem, st, a);
 }
 
 // Rows that are all resident at once (half the threads of the SMs) want the shortest chain: one vector a
@@ -622,7 +623,6 @@ struct RingPlan {
   uint32_t stage_bytes;
 };
 constexpr int kMaxStages = 6, kRingThreads = 512;   // 16384 x 4096 bf16: 4 stages 172 us, 6 and more 128
-constexpr int kSmSmem = 227 * 1024, kRingStatic = 3 * 1024;   // of an SM; a CTA's share beside its ring
 
 // FULL: both gradients come in and dx and dy go out, so nothing of that is asked in the loop (126
 // against 140 us at 16384 x 4096 bf16).
@@ -1278,7 +1278,7 @@ NormArgs norm_args(const lora_norm_shape& sh, const void* x, const void* y, cons
 
 template <typename T, int K, int R, int Y, bool TOKEN, bool FULL>
 cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
-  const cudaError_t allowed = allow_smem<norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>>(kSmSmem - kRingStatic);
+  const cudaError_t allowed = allow_smem<norm_bwd_ring_kernel<T, K, R, Y, TOKEN, FULL>>(kDynamicSmem);
   if (allowed != cudaSuccess) return allowed;
   const size_t smem = (size_t)p.stages * p.stage_bytes;
   if (!p.half)
@@ -1322,10 +1322,8 @@ template <typename T, int G, bool TOKEN, bool FULL>
 cudaError_t launch_short(const NormArgs& a, cudaStream_t st) {
   const size_t smem = short_smem<T, G, TOKEN>(a.D);
   const auto kernel = norm_bwd_short_kernel<T, G, TOKEN, FULL>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t allowed = allow_smem<norm_bwd_short_kernel<T, G, TOKEN, FULL>>(kDynamicSmem);
+  if (allowed != cudaSuccess) return allowed;
   return launch_pdl(kernel, dim3((unsigned)a.parts), dim3(kShortThreads), smem, st, a);
 }
 template <typename T, int G>
