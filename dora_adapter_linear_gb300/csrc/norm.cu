@@ -1309,8 +1309,9 @@ cudaError_t launch_ring(const NormArgs& a, const RingPlan& p, cudaStream_t st) {
     return token ? launch_ring<T, K, R, POST_Y, true, true>(a, p, st) : launch_ring<T, K, R, POST_Y, false, true>(a, p, st);
   return token ? launch_ring<T, K, R, PLAIN_Y, true, true>(a, p, st) : launch_ring<T, K, R, PLAIN_Y, false, true>(a, p, st);
 }
-// The variants that ring_plan can ask for: bf16 rows always fit four stages up to 4096 columns (one
-// vector a thread) and come in pairs above 8192, fp32 ones above 4096.
+// The variants that ring_plan can ask for: bf16 rows always fit four stages up to 4096 columns (one vector a
+// thread) and come in pairs above 8192, with all five inputs (a gate row per row) above 7640; fp32 ones above 4096 and
+// 3816.  Beyond 16384 (15280) bf16 or 8192 (7632) fp32 columns there is none.
 inline cudaError_t launch_plan(const NormArgs& a, const RingPlan& p, cudaStream_t st, bf16) {
   return p.vectors == 2 ? launch_ring<bf16, 2, 1>(a, p, st) : launch_ring<bf16, 1, 2>(a, p, st);
 }
