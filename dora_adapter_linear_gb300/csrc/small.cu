@@ -723,13 +723,8 @@ cudaError_t add_masked_rank_bf16(bf16* dX, const bf16* G, const bf16* A, const u
   if (rows <= 0 || cols <= 0) return cudaSuccess;
   if (r < 1 || r > 128 || cols % 8) return cudaErrorInvalidValue;   // A slice + G rows: at most 80 KB
   const size_t smem = (size_t)r * kAmrCols * 2 + (size_t)kAmrRows * r * 4;
-  static size_t opted = 48 * 1024;
-  if (smem > opted) {
-    const cudaError_t e = cudaFuncSetAttribute(add_masked_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
-    if (e != cudaSuccess) return e;
-    opted = smem;
-  }
+  const cudaError_t allowed = allow_smem<add_masked_rank_kernel>(128 * (kAmrCols * 2 + kAmrRows * 4));   // at r = 128
+  if (allowed != cudaSuccess) return allowed;
   const dim3 grid((unsigned)((rows + kAmrRows - 1) / kAmrRows), (unsigned)((cols + kAmrCols - 1) / kAmrCols));
   return launch_pdl(add_masked_rank_kernel, dim3(grid), dim3(256), smem, st, dX, G, A, mask, scale, rows, cols, r);
 }

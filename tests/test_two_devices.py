@@ -40,6 +40,8 @@ CALLS = {
     "walk": lambda lib: norm_fwd(lib, L.LORA_BF16, 16384, 8192, 1),
     "linear forward": lambda lib: linear(lib, 64, False),
     "linear backward": lambda lib: linear(lib, 64, True),
+    "dropout backward": lambda lib: lib.lora_linear_dropout_bwd(
+        ctypes.byref(L.shape(512, 1024, 2048, 128, L.LORA_BF16)), AT, AT, 1.0, *[AT] * 5, 1.0, *[AT] * 4, WS, SIZE, None),
     "int8 product": lambda lib: lib.w8a8_lora_fwd(512, 1024, 2048, 16, *[AT] * 6, 1.0, *[AT] * 3, WS, SIZE, None),
 }
 
