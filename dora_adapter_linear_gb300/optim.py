@@ -75,12 +75,10 @@ class AdamW:
         return int(self._ctl[0])
 
     def _pointers(self, grads):
-        """The gradients' addresses, 0 for a None."""
+        """The gradients' addresses, 0 for a None, of other sequences than lists and tuples; what does not fit is
+        named."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} tensors")
-        at = L.host().pointers(grads, self.params)
-        if at is not None:
-            return at
         grads = list(grads)
         for i, (g, p) in enumerate(zip(grads, self.params)):
             if g is not None and (g.shape != p.shape or g.dtype != p.dtype or g.device != p.device
@@ -97,7 +95,10 @@ class AdamW:
         0-d tensor, nothing waits), and a step whose norm is not finite changes nothing and is not
         counted; max_norm=inf only guards."""
         L.need_current("the tensors", self._device)
-        at, n, norm = self._pointers(grads), len(self.params), None
+        host, n, norm = L.host(), len(self.params), None
+        at = host.pointers(grads, self.params)
+        if at is None:
+            at = self._pointers(grads)
         lr = self.lr if lr is None else lr
         lr_dev = None
         if isinstance(lr, torch.Tensor):
@@ -108,10 +109,10 @@ class AdamW:
         if max_norm is not None:
             if not c_float(max_norm).value > 0:     # as the kernels have it; 0 there is no clip at all
                 raise ValueError(f"max_norm must be above 0 in fp32, got {max_norm}")
-            norm = L.host().pair(self.params[0])   # shows the norm, the factor lies behind it
+            norm = host.pair(self.params[0])   # shows the norm, the factor lies behind it
             L.adamw_grad_norm(self._tensors, at, n, grad_scale, max_norm, norm, self._ws)
         L.adamw_step(self._tensors, at, n, self._state, hyper, norm)
-        L.host().written(self.params, at)
+        host.written(self.params, at)
         return norm
 
     def state_dict(self):
