@@ -624,6 +624,8 @@ struct RingPlan {
 };
 constexpr int kMaxStages = 6, kRingThreads = 512;   // 16384 x 4096 bf16: 4 stages 172 us, 6 and more 128
 
+// The column sums are formed also for a call that asks for none (16384 x 4096 bf16, frozen weights: 122.6 us, and
+// 126.6 with both weights' gradients; floor 118).
 // FULL: both gradients come in and dx and dy go out, so nothing of that is asked in the loop (126
 // against 140 us at 16384 x 4096 bf16).
 // K vectors of 8 columns a thread, R rows a barrier.  pl.half != 0: a cluster of two CTAs shares a row, the
@@ -896,7 +898,9 @@ __global__ void __launch_bounds__(kRingThreads) norm_bwd_ring_kernel(const NormA
 // 16384 x 256 13 against 25, x 512 20 against 29, x 1024 38 against 41, 2000 x 256 with a gate per row 5.4 against
 // 10.8; fp32 16384 x 256 19 against 26, x 512 36 against 40.  Bound by memory where rows are many (65536 x 512: 6.2
 // TB/s).  A whole warp for 128 columns takes 59 us at 131072 rows, one for 512 (two vectors a lane, registers
-// spilled) 25 at 16384; three CTAs an SM spill registers.  FULL as above (16384 x 256: 13.2 against 14.7 us).
+// spilled) 25 at 16384; three CTAs an SM spill registers.  The groups of four warps (520 columns on) spill 16 to 32 bytes as they
+// are, but with a gate row per row.  FULL as above (16384 x 256: 13.2 against 14.7 us).  The column sums are formed
+// also for a call that asks for none of them (16384 x 256: 9.6 us then, 12.4 with them and the second launch).
 constexpr int kShortThreads = 256;
 template <typename T, bool TOKEN>
 constexpr int short_stages() { return sizeof(T) == 2 ? 4 : TOKEN ? 2 : 3; }

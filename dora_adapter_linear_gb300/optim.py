@@ -27,7 +27,8 @@ class AdamW:
     sqrt(v) with a scale for every 256 elements.  master: bf16 tensors keep their exact values in fp32.
 
     State, on the device: m, v (and m_scale, v_scale, master) with 256 elements a row, each tensor from
-    a row of its own, and the number of steps done."""
+    a row of its own, and the number of steps done.  The steps are the set's: a tensor that had no gradient
+    for some of them comes back with the bias correction of all."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, lr_mul=1.0, state_bits=32,
                  master=True):
