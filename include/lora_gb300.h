@@ -588,7 +588,8 @@ size_t adamw_norm_workspace_bytes(int64_t count);
 
 /* norm_coef[0] = grad_scale |g| over the whole set, norm_coef[1] = grad_scale min(1, max_norm / (norm +
  * 1e-6)), the factor for adamw_step (max_norm <= 0: grad_scale alone), NaN when the norm is not finite.
- * Sums of squares in fp32 in a fixed order: a norm from about 2^63 on counts as not finite.  norm_coef: device float[2], 8-byte aligned. */
+ * Sums of squares in fp32 in a fixed order: a norm from about 2^63 on counts as not finite.  norm_coef:
+ * device float[2], 8-byte aligned. */
 lora_status adamw_grad_norm(const lora_adamw_tensor* tensors, const void* const* grads, int64_t count,
                             float grad_scale, float max_norm, float* norm_coef, void* ws, size_t ws_bytes,
                             void* stream);
