@@ -59,6 +59,10 @@ class LoraAdapter(ctypes.Structure):
     _fields_ = [("A", c_void_p), ("B", c_void_p), ("s", c_float)]
 
 
+class LoraMultiShape(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("d_in", c_int64), ("d_out", c_int64), ("r", c_int64), ("n", c_int64), ("dtype", c_int32)]
+
+
 class LoraNormShape(ctypes.Structure):
     _fields_ = [("M", c_int64), ("D", c_int64), ("rows_per_gate", c_int64), ("ldx", c_int64), ("ldy", c_int64),
                 ("lddh", c_int64), ("lddz", c_int64), ("alpha", c_float), ("eps", c_float), ("w_offset", c_float),
@@ -147,6 +151,11 @@ _SIGS = {
     "adamw_grad_norm": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, c_float, c_float, P, P, c_size_t, P]),
     "adamw_step": (c_int, [POINTER(LoraAdamwTensor), P, c_int64, POINTER(LoraAdamwState), POINTER(LoraAdamwHyper), P,
                            P]),
+    "lora_multi_plan_bytes": (c_size_t, [c_int64, c_int64]),
+    "lora_multi_plan": (c_int, [c_int64, c_int64, P, c_int, P, c_size_t, P]),
+    "lora_multi_workspace_bytes": (c_size_t, [c_int, POINTER(LoraMultiShape)]),
+    "lora_multi_fwd": (c_int, [POINTER(LoraMultiShape), P, P, P, P, P, c_float, P, P, P, P, P, c_size_t, P]),
+    "lora_multi_bwd": (c_int, [POINTER(LoraMultiShape), P, P, P, P, P, P, c_float, P, P, P, P, P, P, P, c_size_t, P]),
     "lora_launch_count": (ctypes.c_uint64, []),
     "lora_prof_enable": (c_int, [c_int]),
     "lora_prof_gemm": (c_int, [POINTER(ctypes.c_double), POINTER(c_int64), POINTER(ctypes.c_double), c_int]),
@@ -532,3 +541,34 @@ def adamw_grad_norm(tensors, grads, count, grad_scale, max_norm, norm_coef, ws, 
 def adamw_step(tensors, grads, count, state, hyper, norm_coef, stream=None):
     _ck(_lib().adamw_step(tensors, grads, count, ctypes.byref(state), ctypes.byref(hyper), ptr(norm_coef),
                           _stream(stream)), "adamw_step")
+
+
+def lora_multi_plan_bytes(M, n) -> int:
+    return _lib().lora_multi_plan_bytes(M, n)
+
+
+def lora_multi_plan(M, n, ids, plan, stream=None):
+    """ids: an int32 or int64 tensor."""
+    _ck(_lib().lora_multi_plan(M, n, ptr(ids), 8 * ids.element_size(), ptr(plan), plan.numel() * plan.element_size(),
+                               _stream(stream)), "lora_multi_plan")
+
+
+def lora_multi_workspace_bytes(backward, sh: LoraMultiShape) -> int:
+    return _lib().lora_multi_workspace_bytes(1 if backward else 0, ctypes.byref(sh))
+
+
+def _multi_scale(s):
+    """(number, device address) of a scale: a number, or a tensor with one for each adapter."""
+    return (0.0, s.data_ptr()) if isinstance(s, torch.Tensor) else (float(s), None)
+
+
+def lora_multi_fwd(sh, X, W0, A, B, bias, s, plan, Y, Z_save, ws, stream=None):
+    _ck(_lib().lora_multi_fwd(ctypes.byref(sh), ptr(X), ptr(W0), ptr(A), ptr(B), ptr(bias), *_multi_scale(s), ptr(plan),
+                              ptr(Y), ptr(Z_save), ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                              _stream(stream)), "lora_multi_fwd")
+
+
+def lora_multi_bwd(sh, X, W0, A, B, Z_saved, dY, s, plan, dX, dA, dB, dbias, ws, stream=None):
+    _ck(_lib().lora_multi_bwd(ctypes.byref(sh), ptr(X), ptr(W0), ptr(A), ptr(B), ptr(Z_saved), ptr(dY),
+                              *_multi_scale(s), ptr(plan), ptr(dX), ptr(dA), ptr(dB), ptr(dbias), ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "lora_multi_bwd")

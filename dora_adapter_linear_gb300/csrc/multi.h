@@ -1,0 +1,59 @@
+// Layout of an adapter plan and the launches that use it (not part of the ABI).
+#pragma once
+
+#include "checks.h"
+
+namespace lg {
+
+constexpr int kItemRows = 32;     // rows of an item: consecutive rows of one adapter in the plan's order
+constexpr int kPieceRows = 512;   // rows of a piece, the share of one adapter's gradients that is summed at once
+constexpr int kTileRows = 256;    // rows of a tile, whose adapters and row masks the GEMMs take
+
+enum { kHeadItems = 0, kHeadPieces = 1, kHeadRows = 2, kHeadWords = 64 };
+
+// An adapter plan of M rows and n adapters: int32 words on the device.
+struct MultiPlan {
+  int64_t M = 0;
+  int n = 0;
+  int32_t* head = nullptr;     // kHead*: items, pieces, rows that have an adapter
+  int32_t* ids = nullptr;      // [M] the row's adapter, -1 for none
+  int32_t* order = nullptr;    // [M] rows by adapter, in their own order within one; those without one last
+  int32_t* other = nullptr;    // [M] the sort's second buffer
+  int32_t* start = nullptr;    // [n + 1] where an adapter's rows begin in `order`
+  int32_t* istart = nullptr;   // [n + 1] its first item
+  int32_t* pstart = nullptr;   // [n + 1] its first piece
+  int4* items = nullptr;       // {adapter, first of its rows in `order`, their count, 0}
+  int4* pieces = nullptr;      // {adapter, first, count, partial or -1: the adapter's only piece}
+  int32_t* tcount = nullptr;   // [tiles] adapters among a tile's rows
+  int32_t* tlist = nullptr;    // [tiles, kTileRows] which, by their first row
+  uint32_t* tmask = nullptr;   // [tiles, kTileRows, 8] the tile's rows that are NOT this adapter's
+};
+inline int64_t multi_tiles(int64_t M) { return (M + kTileRows - 1) / kTileRows; }
+inline int64_t multi_used(int64_t M, int64_t n) { return M < n ? M : n; }   // adapters that may have rows
+inline int64_t multi_items(int64_t M, int64_t n) { return M / kItemRows + multi_used(M, n); }
+inline int64_t multi_pieces(int64_t M, int64_t n) { return M / kPieceRows + multi_used(M, n); }
+// pieces that are not their adapter's only one: at most twice the whole pieces that there are
+inline int64_t multi_partials(int64_t M) { return 2 * (M / kPieceRows); }
+
+inline size_t multi_plan_layout(int64_t M, int64_t n, char* base, MultiPlan* p) {
+  Carve c{base};
+  p->M = M;
+  p->n = (int)n;
+  p->head = c.take<int32_t>(kHeadWords);
+  p->ids = c.take<int32_t>(M);
+  p->order = c.take<int32_t>(M);
+  p->other = c.take<int32_t>(M);
+  p->start = c.take<int32_t>(n + 1);
+  p->istart = c.take<int32_t>(n + 1);
+  p->pstart = c.take<int32_t>(n + 1);
+  p->items = c.take<int4>(multi_items(M, n));
+  p->pieces = c.take<int4>(multi_pieces(M, n));
+  p->tcount = c.take<int32_t>(multi_tiles(M));
+  p->tlist = c.take<int32_t>(multi_tiles(M) * kTileRows);
+  p->tmask = c.take<uint32_t>(multi_tiles(M) * kTileRows * 8);
+  return c.off;
+}
+
+cudaError_t multi_plan(const MultiPlan& p, const void* ids, int id_bits, cudaStream_t st);
+
+}  // namespace lg

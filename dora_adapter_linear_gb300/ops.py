@@ -2,12 +2,14 @@
 the entry point of the same name.  PyTorch is used only for device memory and the stream."""
 from __future__ import annotations
 
+import math
 import threading
 from functools import lru_cache
 
 import torch
 
 from . import _lib as L
+from .adapters import AdapterPlan, adapter_plan  # noqa: F401
 from .rotary import rotary_plan  # noqa: F401
 
 _WS = {}
@@ -630,3 +632,52 @@ def rotary_fwd(X, pos, plan, out=None):
 def rotary_bwd(dY, pos, plan, out=None):
     """The gradient of rotary_fwd: the turn by the negative angle, with the same scale."""
     return _rotary(True, dY, pos, plan, out)
+
+
+def _multi_shape(X, W0, A, B, s, plan, bias=None, Z=None, dY=None):
+    """The shape of a call with a stack of adapters, its operands checked against X [M, in], W0 [out, in] and
+    A [n, r, in]."""
+    if X.dim() != 2 or W0.dim() != 2 or A.dim() != 3:
+        raise ValueError("X and W0 must be 2-D and A a stack of adapters [n, r, in]")
+    if not isinstance(plan, AdapterPlan):
+        raise ValueError("plan must come from adapter_plan()")
+    M, d_in = X.shape
+    d_out, (n, r, _) = W0.shape[0], A.shape
+    for name, t, shape in (("X", X, (M, d_in)), ("W0", W0, (d_out, d_in)), ("A", A, (n, r, d_in)),
+                           ("B", B, (n, d_out, r)), ("bias", bias, (d_out,)), ("Z", Z, (M, r)), ("dY", dY, (M, d_out))):
+        _check_like(name, t, shape, X)
+    if isinstance(s, torch.Tensor):
+        _check_vec("s", s, n, X, F32)
+    elif not math.isfinite(s):
+        raise ValueError(f"s must be finite, got {s}")
+    if plan.rows != M or plan.adapters != n:
+        raise ValueError(f"the plan is of {plan.rows} rows and {plan.adapters} adapters, the call has {M} and {n}")
+    if plan.buffer.device != X.device:
+        raise ValueError(f"the plan must be on {X.device}, it is on {plan.buffer.device}")
+    return L.LoraMultiShape(M, d_in, d_out, r, n, L.dtype_code(X))
+
+
+def lora_multi_fwd(X, W0, A, B, s, plan, bias=None, save_z=True):
+    """The projection of a batch whose rows have different adapters: row i takes adapter ids[i] of the stacks
+    A [n, r, in] and B [n, out, r], or the frozen base alone where it has none; `plan` from
+    adapter_plan(ids, n).  s: a number, or an fp32 tensor [n] with one for each adapter.  Returns (Y, Z)."""
+    sh = _multi_shape(X, W0, A, B, s, plan, bias)
+    _need_cuda("X", X)
+    Y = torch.empty(sh.M, sh.d_out, dtype=X.dtype, device=X.device)
+    Z = torch.empty(sh.M, sh.r, dtype=X.dtype, device=X.device) if save_z else None
+    ws = workspace(L.lora_multi_workspace_bytes(False, sh), X.device)
+    L.lora_multi_fwd(sh, X, W0, A, B, bias, s, plan.buffer, Y, Z, ws)
+    return Y, Z
+
+
+def lora_multi_bwd(X, W0, A, B, Z, dY, s, plan, need_dx=True, need_dbias=False):
+    """Gradients of lora_multi_fwd with W0 frozen: (dX, dA, dB, dbias), dA and dB stacks like A and B, zeros
+    for an adapter without rows.  Z: from the forward, or None to recompute it."""
+    sh = _multi_shape(X, W0, A, B, s, plan, Z=Z, dY=dY)
+    _need_cuda("X", X)
+    dX = torch.empty_like(X) if need_dx else None
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    dbias = torch.empty(sh.d_out, dtype=X.dtype, device=X.device) if need_dbias else None
+    ws = workspace(L.lora_multi_workspace_bytes(True, sh), X.device)
+    L.lora_multi_bwd(sh, X, W0, A, B, Z, dY, s, plan.buffer, dX, dA, dB, dbias, ws)
+    return dX, dA, dB, dbias

@@ -7,7 +7,9 @@
  * three such projections; a fused query/key/value projection with one adapter per leaf; and an
  * int8 (W8A8) base weight with a per-row dequant scale and a LoRA epilogue.  Around it, for the
  * adapter training step of a transformer block: the norms before and after a block with its gate
- * and residual scale, rotary positions, and AdamW over all adapter tensors at once.
+ * and residual scale, rotary positions, and AdamW over all adapter tensors at once.  And for many
+ * adapters of one base: the projection of a batch whose rows have different adapters, forward and
+ * backward.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -599,6 +601,46 @@ lora_status adamw_grad_norm(const lora_adamw_tensor* tensors, const void* const*
 lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grads, int64_t count,
                        const lora_adamw_state* state, const lora_adamw_hyper* hyper, const float* norm_coef,
                        void* stream);
+
+/* ---------------------------------------------------------------- many adapters beside one projection
+ * Row i of a batch has adapter a = ids[i] of n, or none (an id outside 0 .. n - 1): the requests of several
+ * fine-tunes of one base served together, or several adapters trained in one batch.
+ *   forward:   z_i = x_i A_a^T,  y_i = x_i W0^T + s_a z_i B_a^T (+ bias)
+ *   backward:  g_i = s_a dy_i B_a,  dx_i = dy_i W0 + g_i A_a,  dA_a = sum g_i^T x_i,  dB_a = s_a sum dy_i^T z_i
+ *              over the rows of a,  dbias = sum of all dy_i.
+ * A row without adapter has z = 0 and takes the frozen base alone; an adapter without rows has zero
+ * gradients.  A row is formed from its own adapter alone: what is not finite in another adapter or in
+ * another row does not reach it.
+ *   A [n, r, d_in], B [n, d_out, r]: stacks; an adapter of lower rank has zeros in its last rows of A and
+ *   columns of B.  1 <= n <= 65535, M <= 2^24, d_in, d_out and r as above (LORA_BF16: r a multiple of 8).
+ *   s_each: device fp32 [n], read when the call runs, or NULL: s for all. */
+typedef struct {
+    int64_t M, d_in, d_out, r, n;
+    int32_t dtype;                /* lora_dtype */
+} lora_multi_shape;
+
+/* The plan of a batch: its rows by adapter and the adapters of every tile, made on the device from the ids
+ * (int32 or int64, id_bits), without a synchronisation.  One plan serves every projection of the batch, in
+ * both directions; it is read by calls with the same M and n.  `plan`: lora_multi_plan_bytes() of device
+ * memory (0 on bad input), 256-byte aligned; a call on another stream than the plan's has to be ordered
+ * behind it. */
+size_t lora_multi_plan_bytes(int64_t M, int64_t n);
+lora_status lora_multi_plan(int64_t M, int64_t n, const void* ids, int id_bits, void* plan, size_t plan_bytes,
+                            void* stream);
+
+/* Bytes of workspace of lora_multi_fwd (backward == 0) or lora_multi_bwd.  0 on bad input. */
+size_t lora_multi_workspace_bytes(int backward, const lora_multi_shape* sh);
+
+/* Y [M, d_out]; Z_save [M, r] or NULL; bias [d_out] or NULL. */
+lora_status lora_multi_fwd(const lora_multi_shape* sh, const void* X, const void* W0, const void* A, const void* B,
+                           const void* bias, float s, const float* s_each, const void* plan, void* Y, void* Z_save,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Z_saved [M, r] from the forward, or NULL to recompute it; dX [M, d_in] or NULL; dA, dB as A, B;
+ * dbias [d_out] or NULL.  The sums over rows are fp32 in a fixed order. */
+lora_status lora_multi_bwd(const lora_multi_shape* sh, const void* X, const void* W0, const void* A, const void* B,
+                           const void* Z_saved, const void* dY, float s, const float* s_each, const void* plan, void* dX,
+                           void* dA, void* dB, void* dbias, void* ws, size_t ws_bytes, void* stream);
 
 /* Test hook for the bounded-wait machinery: launches one CTA that waits on an mbarrier
  * that nothing ever arrives on, with a limit of `timeout_us` microseconds; the kernel then

@@ -1,0 +1,261 @@
+"""The many-adapter projection against its fp64 reference, element by element."""
+import numpy as np
+import pytest
+import torch
+
+from dora_adapter_linear_gb300 import _lib as L
+from dora_adapter_linear_gb300 import ops
+import multi_cases as C
+
+pytestmark = pytest.mark.gpu
+
+
+def cuda(c):
+    g = {k: v.cuda() if torch.is_tensor(v) else v for k, v in c.items()}
+    g["ids"] = torch.from_numpy(np.asarray(c["ids"], np.int64)).cuda()
+    return g
+
+
+def fwd(g, plan=None, **kw):
+    plan = plan or ops.adapter_plan(g["ids"], g["A"].shape[0])
+    return ops.lora_multi_fwd(g["X"], g["W0"], g["A"], g["B"], g["s"], plan, bias=g["bias"], **kw)
+
+
+def bwd(g, Z, plan=None, **kw):
+    plan = plan or ops.adapter_plan(g["ids"], g["A"].shape[0])
+    return ops.lora_multi_bwd(g["X"], g["W0"], g["A"], g["B"], Z, g["dY"], g["s"], plan, need_dbias=True, **kw)
+
+
+SIZES = [  # M, d_in, d_out, r, n, ids
+    (0, 64, 72, 8, 3, "one"), (1, 8, 8, 8, 1, "one"), (1, 4096, 72, 16, 4, "rows"), (1, 64, 4104, 16, 2, "none"),
+    (2, 264, 1000, 24, 300, "rows"), (7, 72, 8, 128, 5, "bare"), (16, 1000, 264, 16, 16, "rows"), (17, 520, 136, 64, 9, "rows"),
+    (31, 512, 512, 40, 3, "runs"), (33, 128, 256, 8, 40, "rows"), (64, 1024, 520, 16, 64, "rows"), (65, 72, 64, 72, 2, "bare"),
+    (128, 264, 392, 16, 7, "runs"), (130, 64, 1032, 32, 130, "rows"), (255, 40, 264, 16, 1, "one"), (256, 64, 256, 128, 3, "bare"),
+    (257, 520, 8, 8, 600, "rows"), (300, 128, 264, 16, 5, "runs"), (511, 72, 328, 104, 6, "runs"), (513, 200, 72, 56, 4, "runs"),
+    (700, 64, 512, 16, 2, "none"), (1029, 72, 136, 24, 3, "runs"), (1500, 16, 24, 64, 100, "rows"), (2600, 24, 40, 8, 2, "one"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,d_in,d_out,r,n,style", SIZES)
+def test_forward_and_backward(M, d_in, d_out, r, n, style, dtype):
+    r -= 3 if dtype == "f32" and r > 8 else 0            # fp32: any rank
+    c = C.inputs(M, d_in, d_out, r, n, style, dtype, seed=M + r)
+    g = cuda(c)
+    Y, Z = fwd(g)
+    ref = C.reference_fwd(c, dtype)
+    C.near(Y, ref["Y"], "Y")
+    C.near(Z, ref["Z"], "Z")
+    grads = dict(zip(("dX", "dA", "dB", "dbias"), bwd(g, Z)))
+    for k, v in C.reference_bwd(c, Z, dtype).items():
+        C.near(grads[k], v, k)
+    ops.check_device_errors()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_options(dtype):
+    """No bias, a number as scale, 32-bit ids, no saved Z, no dX, Z recomputed."""
+    c = C.inputs(90, 136, 72, 16, 4, "runs", dtype, bias=False)
+    g = cuda(c)
+    plan = ops.adapter_plan(g["ids"].int(), 4)
+    c["s"] = torch.full((4,), 0.75)
+    args = g["X"], g["W0"], g["A"], g["B"]
+    Y, Z = ops.lora_multi_fwd(*args, 0.75, plan)
+    C.near(Y, C.reference_fwd(c, dtype)["Y"], "Y")
+    Y2, none = ops.lora_multi_fwd(*args, 0.75, plan, save_z=False)
+    assert none is None and torch.equal(Y, Y2)
+    dX, dA, dB, db = ops.lora_multi_bwd(*args, Z, g["dY"], 0.75, plan)
+    assert db is None
+    none, dA2, dB2, db2 = ops.lora_multi_bwd(*args, None, g["dY"], 0.75, plan, need_dx=False, need_dbias=True)
+    assert none is None and torch.equal(dA, dA2) and torch.equal(dB, dB2)      # the recomputed Z has the same bits
+    ref = C.reference_bwd(c, Z, dtype)
+    for k, v in (("dX", dX), ("dA", dA), ("dB", dB), ("dbias", db2)):
+        C.near(v, ref[k], k)
+
+
+@pytest.mark.parametrize("M,r", [(40, 16), (300, 16), (600, 72)])
+def test_what_is_not_finite_stays_with_its_adapter(M, r):
+    """Adapter 1 holds NaN and infinities, row 5 too: other rows and other adapters' gradients keep their bits."""
+    c = C.inputs(M, 136, 264, r, 4, "rows", "bf16")
+    g = cuda(c)
+    plan = ops.adapter_plan(g["ids"], 4)
+    Y0, Z0 = fwd(g, plan)
+    d0 = bwd(g, Z0, plan)
+    g2 = {k: v.clone() if torch.is_tensor(v) else v for k, v in g.items()}
+    g2["A"][1, :, ::3], g2["B"][1, ::2], g2["s"][1] = float("nan"), float("inf"), float("nan")
+    bad = c["ids"] == 1
+    sick = int(np.flatnonzero(c["ids"] == 2)[1])         # one row of adapter 2
+    g2["X"][sick], g2["dY"][sick] = float("inf"), float("nan")
+    Y, Z = fwd(g2, plan)
+    fine = torch.from_numpy(~bad).cuda()
+    fine[sick] = False
+    assert torch.equal(Y[fine], Y0[fine]) and torch.equal(Z[fine], Z0[fine])
+    assert Y[torch.from_numpy(bad).cuda()].isnan().any(1).all()
+    Zb = torch.where(fine[:, None], Z0, float("nan"))
+    dX, dA, dB, _ = bwd(g2, Zb, plan)
+    assert torch.equal(dX[fine], d0[0][fine])
+    for a in (0, 3):
+        assert torch.equal(dA[a], d0[1][a]) and torch.equal(dB[a], d0[2][a])
+
+
+def test_same_bits_again_and_rows_of_any_order():
+    """Sums have one order: a call repeats its bits, and a row's output does not depend on its neighbours."""
+    c = C.inputs(700, 136, 264, 16, 5, "rows", "bf16")
+    g = cuda(c)
+    Y, Z = fwd(g)
+    first = bwd(g, Z)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, bwd(g, Z)))
+    perm = torch.randperm(700, generator=torch.Generator().manual_seed(1)).cuda()
+    h = dict(g, X=g["X"][perm], ids=g["ids"][perm])
+    Y2, Z2 = fwd(h)
+    assert torch.equal(Y2, Y[perm]) and torch.equal(Z2, Z[perm])
+
+
+@pytest.mark.parametrize("M", [5, 70, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nothing_outside_of_the_outputs_is_written(M, dtype):
+    d_in, d_out, r, n = 72, 136, 24, 3
+    c = C.inputs(M, d_in, d_out, r, n, "runs", dtype)
+    g, dt = cuda(c), C.DTYPES[dtype]
+    plan = ops.adapter_plan(g["ids"], n)
+    sh = L.LoraMultiShape(M, d_in, d_out, r, n, L.dtype_code(g["X"]))
+    sizes = {"Y": M * d_out, "Z": M * r, "dX": M * d_in, "dA": n * r * d_in, "dB": n * d_out * r, "db": d_out}
+    bufs = {k: torch.full((v + 512,), 7.0, dtype=dt, device="cuda") for k, v in sizes.items()}
+    out = {k: bufs[k][256:256 + v] for k, v in sizes.items()}
+    for back in (False, True):
+        need = L.lora_multi_workspace_bytes(back, sh)
+        ws = torch.full((need + 4096,), 0x55, dtype=torch.uint8, device="cuda")
+        ws[:256] = 0
+        if back:
+            L.lora_multi_bwd(sh, g["X"], g["W0"], g["A"], g["B"], out["Z"], g["dY"], g["s"], plan.buffer, out["dX"],
+                             out["dA"], out["dB"], out["db"], ws[:need])
+        else:
+            L.lora_multi_fwd(sh, g["X"], g["W0"], g["A"], g["B"], g["bias"], g["s"], plan.buffer, out["Y"], out["Z"],
+                             ws[:need])
+        assert (ws[need:] == 0x55).all()
+    for k, b in bufs.items():
+        assert (b[:256] == 7).all() and (b[256 + sizes[k]:] == 7).all(), k
+    Y, Z = fwd(g, plan)
+    assert torch.equal(out["Y"].view(M, d_out), Y) and torch.equal(out["Z"].view(M, r), Z)
+
+
+@pytest.mark.parametrize("rows,n", [(1, 1), (31, 2), (300, 5), (1000, 255), (1000, 256), (5000, 700), (70000, 65535)])
+def test_plan(rows, n):
+    """Rows by adapter in their own order, items, pieces and tiles."""
+    rng = np.random.default_rng(rows)
+    ids = rng.integers(-2, n + 2, rows)
+    ids[rng.random(rows) < 0.3] = n - 1
+    buf = ops.adapter_plan(torch.from_numpy(ids).cuda(), n).buffer.cpu().numpy()
+    at = 0
+
+    def take(count, words=1):
+        nonlocal at
+        v = buf[at:at + 4 * count * words].view(np.int32)
+        at += (4 * count * words + 255) // 256 * 256
+        return v.reshape(count, words) if words > 1 else v
+
+    used, tiles = min(rows, n), (rows + 255) // 256
+    head, kept, order, _, start, istart, pstart = (take(k) for k in (64, rows, rows, rows, n + 1, n + 1, n + 1))
+    items, pieces = take(rows // 32 + used, 4), take(rows // 512 + used, 4)
+    tcount, tlist, tmask = take(tiles), take(tiles * 256).reshape(tiles, 256), take(tiles * 256 * 8).reshape(tiles, 256, 8)
+    assert at == L.lora_multi_plan_bytes(rows, n)
+    real = np.where((ids >= 0) & (ids < n), ids, -1)
+    assert (kept == real).all()
+    key = np.where(real < 0, n, real)
+    assert (order == np.argsort(key, kind="stable")).all()
+    assert (start == np.searchsorted(np.sort(key), np.arange(n + 1))).all()
+    slots = 0
+    for first, list_, size in ((istart, items, 32), (pstart, pieces, 512)):
+        count = -(-np.diff(start) // size)
+        assert (first == np.concatenate(([0], np.cumsum(count)))).all()
+        k = 0
+        for a in np.flatnonzero(count):
+            for b in range(start[a], start[a + 1], size):
+                want = [a, b, min(size, start[a + 1] - b), 0]
+                if size == 512:
+                    want[3] = -1 if count[a] == 1 else slots
+                    slots += count[a] > 1
+                assert list_[k].tolist() == want
+                k += 1
+        assert head[0 if size == 32 else 1] == k <= len(list_)
+    assert slots <= 2 * (rows // 512) and head[2] == start[n]
+    for t in range(tiles):
+        mine = np.full(256, -1)
+        mine[:len(real[256 * t:256 * t + 256])] = real[256 * t:256 * t + 256]
+        seen = list(dict.fromkeys(mine[mine >= 0].tolist()))
+        assert tlist[t, :tcount[t]].tolist() == seen
+        for k, a in enumerate(seen):
+            bits = np.unpackbits(tmask[t, k].copy().view(np.uint8), bitorder="little")
+            assert (bits == (mine != a)).all()
+
+
+def test_captured_step_follows_its_ids():
+    """Plan, forward and backward in one graph, replayed with other ids and inputs in the same buffers."""
+    for M in (24, 300):
+        cases = [C.inputs(M, 72, 136, 16, 4, style, "bf16", seed=k) for k, style in enumerate(("runs", "rows", "none"))]
+        g = cuda(cases[0])
+        plan = ops.adapter_plan(g["ids"], 4)
+        Y, Z = fwd(g, plan)
+        bwd(g, Z, plan)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            plan.update(g["ids"])
+            Y, Z = fwd(g, plan)
+            grads = bwd(g, Z, plan)
+        for c in cases[1:] + cases[:1]:
+            for k, v in cuda(c).items():
+                if torch.is_tensor(v):
+                    g[k].copy_(v)
+            other = fwd(g)[0]                            # a call beside the graph's
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(other, Y)
+            C.near(Y, C.reference_fwd(c, "bf16")["Y"], "Y")
+            for k, v in C.reference_bwd(c, Z, "bf16").items():
+                C.near(dict(zip(("dX", "dA", "dB", "dbias"), grads))[k], v, k)
+
+
+def test_another_stream():
+    c = C.inputs(300, 136, 264, 16, 5, "runs", "bf16")
+    g = cuda(c)
+    Y0, Z0 = fwd(g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        Y, Z = fwd(g)
+        grads = bwd(g, Z)
+    side.synchronize()
+    assert torch.equal(Y, Y0) and all(torch.equal(a, b) for a, b in zip(grads, bwd(g, Z0)))
+
+
+def test_offsets_past_32_bits():
+    """Stacks of more than 2^31 elements, and as many outputs: the last adapters and rows are right."""
+    n, r, d = 1030, 128, 16392
+    A, B = torch.zeros(n, r, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 72, r, dtype=torch.bfloat16, device="cuda")
+    c = C.inputs(40, d, 72, r, 3, "rows", "bf16")
+    A[-3:], B[-3:] = c["A"].cuda(), c["B"].cuda()
+    g = dict(cuda(c), A=A, B=B, s=torch.cat((torch.zeros(n - 3), c["s"])).cuda())
+    g["ids"] += n - 3
+    Y, Z = fwd(g)
+    ref = C.reference_fwd(c, "bf16")
+    C.near(Y, ref["Y"], "Y")
+    C.near(Z, ref["Z"], "Z")
+    dX, dA, dB, _ = bwd(g, Z)
+    ref = C.reference_bwd(c, Z, "bf16")
+    C.near(dX, ref["dX"], "dX")
+    C.near(dA[-3:], ref["dA"], "dA")
+    C.near(dB[-3:], ref["dB"], "dB")
+    assert not dA[:-3].any() and not dB[:-3].any()
+    del A, B, g, dA, dB
+    M, d_out = 2 ** 18 + 37, 8200
+    c = C.inputs(64, 8, d_out, 8, 3, "rows", "bf16")
+    g = cuda(c)
+    g["X"] = torch.cat((torch.zeros(M - 64, 8, dtype=torch.bfloat16, device="cuda"), g["X"]))
+    g["ids"] = torch.cat((torch.full((M - 64,), -1, device="cuda"), g["ids"]))
+    Y, Z = fwd(g)
+    ref = C.reference_fwd(c, "bf16")
+    C.near(Y[-64:], ref["Y"], "Y")
+    assert torch.equal(Y[:M - 64:4099], g["bias"].expand(len(Y[:M - 64:4099]), -1))
