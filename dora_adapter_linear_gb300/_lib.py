@@ -63,6 +63,10 @@ class LoraMultiShape(ctypes.Structure):
     _fields_ = [("M", c_int64), ("d_in", c_int64), ("d_out", c_int64), ("r", c_int64), ("n", c_int64), ("dtype", c_int32)]
 
 
+class LoraGradTensor(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("n", c_int64), ("group", c_int32), ("dtype", c_int32)]
+
+
 class LoraNormShape(ctypes.Structure):
     _fields_ = [("M", c_int64), ("D", c_int64), ("rows_per_gate", c_int64), ("ldx", c_int64), ("ldy", c_int64),
                 ("lddh", c_int64), ("lddz", c_int64), ("alpha", c_float), ("eps", c_float), ("w_offset", c_float),
@@ -156,6 +160,8 @@ _SIGS = {
     "lora_multi_workspace_bytes": (c_size_t, [c_int, POINTER(LoraMultiShape)]),
     "lora_multi_fwd": (c_int, [POINTER(LoraMultiShape), P, P, P, P, P, c_float, P, P, P, P, P, c_size_t, P]),
     "lora_multi_bwd": (c_int, [POINTER(LoraMultiShape), P, P, P, P, P, P, c_float, P, P, P, P, P, P, P, c_size_t, P]),
+    "grad_clip_workspace_bytes": (c_size_t, [POINTER(LoraGradTensor), c_int64, c_int64, c_int]),
+    "grad_clip": (c_int, [POINTER(LoraGradTensor), c_int64, c_int64, c_int, c_float, P, P, c_size_t, P]),
     "lora_launch_count": (ctypes.c_uint64, []),
     "lora_prof_enable": (c_int, [c_int]),
     "lora_prof_gemm": (c_int, [POINTER(ctypes.c_double), POINTER(c_int64), POINTER(ctypes.c_double), c_int]),
@@ -195,7 +201,8 @@ def host():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(lib, name), c_void_p).value
-                      for name in ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd")])
+                      for name in ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd",
+                                   "grad_clip_workspace_bytes", "grad_clip")])
         _HOST = module
     return _HOST
 
@@ -572,3 +579,13 @@ def lora_multi_bwd(sh, X, W0, A, B, Z_saved, dY, s, plan, dX, dA, dB, dbias, ws,
     _ck(_lib().lora_multi_bwd(ctypes.byref(sh), ptr(X), ptr(W0), ptr(A), ptr(B), ptr(Z_saved), ptr(dY),
                               *_multi_scale(s), ptr(plan), ptr(dX), ptr(dA), ptr(dB), ptr(dbias), ptr(ws),
                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "lora_multi_bwd")
+
+
+def grad_clip_workspace_bytes(tensors, count, groups, stacked) -> int:
+    return _lib().grad_clip_workspace_bytes(tensors, count, groups, 1 if stacked else 0)
+
+
+def grad_clip(tensors, count, groups, stacked, max_norm, norms, ws, stream=None):
+    """tensors: a ctypes array of LoraGradTensor."""
+    _ck(_lib().grad_clip(tensors, count, groups, 1 if stacked else 0, float(max_norm), ptr(norms), ptr(ws),
+                         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)), "grad_clip")

@@ -12,6 +12,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <vector>
+
 #include "../../include/lora_gb300.h"
 
 namespace {
@@ -23,6 +25,8 @@ decltype(&block_norm_fwd) norm_fwd_call = nullptr;
 decltype(&block_norm_bwd) norm_bwd_call = nullptr;
 decltype(&rotary_fwd) rotary_fwd_call = nullptr;
 decltype(&rotary_bwd) rotary_bwd_call = nullptr;
+decltype(&grad_clip_workspace_bytes) clip_bytes_call = nullptr;
+decltype(&grad_clip) clip_call = nullptr;
 
 // a tensor argument: absent (None), a tensor, or something else
 struct Arg {
@@ -291,14 +295,66 @@ PyObject* py_pair(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd): addresses in the loaded library
+// (gradients, groups, count, max_norm): the norms of optim.clip_grads, or a status.  groups: a list with the
+// group of each gradient, or None: each is a stack of `count` groups.
+PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 4 || !(PyList_Check(a[0]) || PyTuple_Check(a[0]))) return not_here();
+  const bool stacked = a[1] == Py_None;
+  if (!stacked && !PyList_Check(a[1])) return not_here();
+  const Py_ssize_t all = PySequence_Fast_GET_SIZE(a[0]);
+  if (!stacked && PyList_GET_SIZE(a[1]) != all) return not_here();
+  const int64_t count = PyLong_AsLongLong(a[2]);
+  const double max_norm = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) return nullptr;
+  if (count < 1 || count > 65535) return not_here();
+  std::vector<lora_grad_tensor> table;
+  std::vector<Tensor> kept;           // the list may change while other threads run
+  table.reserve(all);
+  kept.reserve(all);
+  for (Py_ssize_t i = 0; i < all; ++i) {
+    const Arg g(PySequence_Fast_ITEMS(a[0])[i]);
+    if (!g.ok) return not_here();
+    if (!g) continue;
+    const Tensor& t = *g;
+    if (!here(t) || !strided(t) || dtype_of(t) < 0 || !t.is_contiguous()) return not_here();
+    if (stacked && (t.dim() < 1 || t.size(0) != count)) return not_here();
+    int64_t group = 0;
+    if (!stacked) {
+      group = PyLong_AsLongLong(PyList_GET_ITEM(a[1], i));
+      if (PyErr_Occurred()) return nullptr;
+      if (group < 0 || group >= count) return not_here();
+    }
+    table.push_back(lora_grad_tensor{t.data_ptr(), stacked ? t.numel() / count : t.numel(), (int32_t)group, dtype_of(t)});
+    kept.push_back(t);
+  }
+  if (kept.empty()) return not_here();
+  Tensor norms;
+  int e;
+  {
+    const Unlocked unlocked;
+    norms = fresh(kept[0], {count}, at::kFloat);
+    const size_t need = clip_bytes_call(table.data(), (int64_t)table.size(), count, stacked);
+    const Tensor ws = fresh(kept[0], {(int64_t)(need ? need : 1)}, at::kByte);
+    e = clip_call(table.data(), (int64_t)table.size(), count, stacked, (float)max_norm,
+                  static_cast<float*>(norms.data_ptr()), ws.data_ptr(), need, stream());
+  }
+  if (e != LORA_OK) return PyLong_FromLong(e);
+  if (max_norm > 0)
+    for (const Tensor& t : kept) written(t);
+  return THPVariable_Wrap(norms);
+  END_HANDLE_TH_ERRORS
+}
+
+// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd, grad_clip_workspace_bytes, grad_clip): addresses in the
+// loaded library
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* at[4];
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "four addresses");
+  void* at[6];
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "six addresses");
     return nullptr;
   }
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 6; ++i)
     if (!(at[i] = PyLong_AsVoidPtr(a[i]))) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is zero");
       return nullptr;
@@ -307,6 +363,8 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   norm_bwd_call = reinterpret_cast<decltype(norm_bwd_call)>(at[1]);
   rotary_fwd_call = reinterpret_cast<decltype(rotary_fwd_call)>(at[2]);
   rotary_bwd_call = reinterpret_cast<decltype(rotary_bwd_call)>(at[3]);
+  clip_bytes_call = reinterpret_cast<decltype(clip_bytes_call)>(at[4]);
+  clip_call = reinterpret_cast<decltype(clip_call)>(at[5]);
   Py_RETURN_NONE;
 }
 
@@ -315,6 +373,7 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), "take the library's entry point
                          {"block_norm_fwd", FAST(py_norm_fwd), "ops.block_norm_fwd"},
                          {"block_norm_bwd", FAST(py_norm_bwd), "ops.block_norm_bwd"},
                          {"rotary", FAST(py_rotary), "ops.rotary_fwd and rotary_bwd"},
+                         {"clip_grads", FAST(py_clip_grads), "optim.clip_grads"},
                          {"pair", FAST(py_pair), "an optimiser's norm and factor"},
                          {"pointers", FAST(py_pointers), "addresses of an optimiser's gradients"},
                          {"written", FAST(py_written), "an optimiser's tensors after its step"},

@@ -135,3 +135,57 @@ class AdamW:
             if state[k] is not None:
                 getattr(self, k).copy_(state[k])
         self._ctl.copy_(torch.tensor([state["step"], 0], dtype=torch.int32))
+
+
+def clip_grads(grads, max_norm, groups=None):
+    """Scales gradients in place by min(1, max_norm / (norm + 1e-6)) of their group's norm, and returns the
+    norms before that, fp32 [groups] on the device; nothing waits.  grads: contiguous fp32 or bf16 CUDA
+    tensors (or None); groups: None, one group of all; a list with the number of each tensor's group, 0 to
+    the largest; or a number G: every tensor is a stack of G groups along its first dimension, as the
+    gradients of ops.lora_multi_bwd are.  A group whose norm is not finite (from about 2^63 on) becomes
+    zeros, the others go on.  max_norm None: the norms alone; infinity: only such groups change."""
+    grads = grads if isinstance(grads, (list, tuple)) else list(grads)
+    each = None
+    if groups is None:
+        count, each = 1, [0] * len(grads)
+    elif isinstance(groups, int):
+        count = groups
+    else:
+        each = list(groups)
+        if len(each) != len(grads):
+            raise ValueError(f"{len(each)} groups for {len(grads)} gradients")
+        count = max(each, default=0) + 1
+    if max_norm is None:
+        limit = 0.0
+    elif c_float(max_norm).value > 0:       # as the kernels have it
+        limit = max_norm
+    else:
+        raise ValueError(f"max_norm must be above 0 in fp32, got {max_norm}")
+    norms = L.host().clip_grads(grads, each, count, limit)
+    if norms is None:
+        _check_grads(grads, each, count)
+        raise ValueError("no gradients to clip")
+    if isinstance(norms, int):
+        if norms == 1:
+            raise ValueError("two of the gradients share memory: each would be scaled under the other's hands")
+        raise L.LoraError(norms, "grad_clip")
+    return norms
+
+
+def _check_grads(grads, each, count):
+    """Names what clip_grads cannot take."""
+    if not 1 <= count <= 65535:
+        raise ValueError(f"there must be 1 to 65535 groups, got {count}")
+    for i, g in enumerate(grads):
+        if g is None:
+            continue
+        if not isinstance(g, torch.Tensor):
+            raise ValueError(f"gradient {i} must be a tensor or None, got {type(g).__name__}")
+        if g.dtype not in (torch.float32, torch.bfloat16) or not g.is_cuda or g.layout != torch.strided \
+                or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be a contiguous fp32 or bf16 CUDA tensor, got {g.dtype} on {g.device}")
+        L.need_current(f"gradient {i}", g.device)
+        if each is None and (g.dim() < 1 or g.shape[0] != count):
+            raise ValueError(f"gradient {i} must be a stack of {count} groups, got {tuple(g.shape)}")
+        if each is not None and not 0 <= each[i] < count:
+            raise ValueError(f"group {each[i]} of gradient {i} is not in 0 to {count - 1}")

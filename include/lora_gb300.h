@@ -9,7 +9,7 @@
  * adapter training step of a transformer block: the norms before and after a block with its gate
  * and residual scale, rotary positions, and AdamW over all adapter tensors at once.  And for many
  * adapters of one base: the projection of a batch whose rows have different adapters, forward and
- * backward.
+ * backward, and the norms and clipping of each adapter's gradients.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -641,6 +641,28 @@ lora_status lora_multi_fwd(const lora_multi_shape* sh, const void* X, const void
 lora_status lora_multi_bwd(const lora_multi_shape* sh, const void* X, const void* W0, const void* A, const void* B,
                            const void* Z_saved, const void* dY, float s, const float* s_each, const void* plan, void* dX,
                            void* dA, void* dB, void* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- clipping by groups
+ * norms[k] = sqrt(sum of x^2 over group k), and in place x = x min(1, max_norm / (norms[k] + 1e-6)) for the
+ * elements of group k: one group for each adapter of a set that is trained together, so that one adapter's
+ * spike does not scale the others.  A group whose norm is not finite becomes zeros (its norm shows it, the
+ * others go on).  max_norm <= 0: the norms alone; infinity: only such groups change.
+ * Squares are summed in fp32 in a fixed order, a group's sums in fp64: a norm from about 2^63 on counts as not
+ * finite, values below about 2^-75 add nothing.
+ * `tensors` is a host array of `count` entries, read during the call; g: contiguous device array, aligned to
+ * its element (16-byte aligned ones are faster), of one dtype.  stacked 0: n elements of group `group`.
+ * stacked 1: a stack of all `groups` groups behind one another, n elements each (`group` is not read).  No two
+ * tensors share memory (LORA_ERR_INVALID_ARG).  1 <= groups <= 65535; norms: device fp32 [groups]. */
+typedef struct {
+    void* g;
+    int64_t n;
+    int32_t group;
+    int32_t dtype;                /* lora_dtype */
+} lora_grad_tensor;
+/* Bytes of workspace (its first 256 are not an error word: nothing waits).  0 on bad input. */
+size_t grad_clip_workspace_bytes(const lora_grad_tensor* tensors, int64_t count, int64_t groups, int stacked);
+lora_status grad_clip(const lora_grad_tensor* tensors, int64_t count, int64_t groups, int stacked, float max_norm,
+                      float* norms, void* ws, size_t ws_bytes, void* stream);
 
 /* Test hook for the bounded-wait machinery: launches one CTA that waits on an mbarrier
  * that nothing ever arrives on, with a limit of `timeout_us` microseconds; the kernel then

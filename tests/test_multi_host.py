@@ -8,7 +8,7 @@ import torch
 
 import oracle as O1
 from dora_adapter_linear_gb300 import _lib as L
-from dora_adapter_linear_gb300 import adapters, ops
+from dora_adapter_linear_gb300 import adapters, ops, optim
 from oracle import multi_oracle as O
 
 
@@ -153,3 +153,64 @@ def test_entry_points_check_before_they_launch():
     assert plan(M=-1) == 1 and plan(n=0) == 1 and plan(n=65536) == 2 and plan(M=2 ** 24 + 1) == 2
     assert plan(ids=None) == 1 and plan(bits=16) == 1 and plan(ids=odd) == 3 and plan(p=None) == 4
     assert plan(p=odd) == 3 and plan(size=L.lora_multi_plan_bytes(4, 3) - 1) == 4 and plan(M=0, ids=None) == 0
+
+
+# ------------------------------------------------------------------ clipping by groups
+def test_clip_reference():
+    g = np.random.default_rng(0)
+    grads = [g.normal(size=(3, 4)) * 10, g.normal(size=5) * 0.01, g.normal(size=2) * 10]
+    norms, out = O.clip(grads, 1.0, [0, 1, 0], 3)
+    t = [torch.nn.Parameter(torch.zeros(v.shape)) for v in (grads[0], grads[2])]
+    for p, v in zip(t, (grads[0], grads[2])):
+        p.grad = torch.from_numpy(v.copy()).float()
+    total = torch.nn.utils.clip_grad_norm_(t, 1.0)
+    assert abs(norms[0] - float(total)) < 1e-5 * norms[0] and norms[2] == 0
+    np.testing.assert_allclose(out[0], t[0].grad.numpy(), rtol=1e-5)
+    np.testing.assert_allclose(out[2], t[1].grad.numpy(), rtol=1e-5)
+    assert (out[1] == grads[1]).all()
+    grads[1][0] = np.inf
+    norms, out = O.clip(grads, 1.0, [0, 1, 0], 3)
+    assert not out[1].any() and np.isinf(norms[1]) and abs(np.sqrt((out[0] ** 2).sum() + (out[2] ** 2).sum()) - 1) < 1e-6
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(grads=[torch.zeros(4)], max_norm=1.0), "CUDA"),
+    (dict(grads=[3.0], max_norm=1.0), "tensor or None"),
+    (dict(grads=[], max_norm=1.0), "no gradients"),
+    (dict(grads=[None], max_norm=1.0), "no gradients"),
+    (dict(grads=[torch.zeros(4)], max_norm=0.0), "max_norm"),
+    (dict(grads=[torch.zeros(4)], max_norm=-1.0), "max_norm"),
+    (dict(grads=[torch.zeros(4)], max_norm=float("nan")), "max_norm"),
+    (dict(grads=[torch.zeros(4)], max_norm=1e-60), "max_norm"),
+    (dict(grads=[torch.zeros(4)], max_norm=1.0, groups=[0, 1]), "2 groups"),
+    (dict(grads=[torch.zeros(4)], max_norm=1.0, groups=0), "1 to 65535"),
+    (dict(grads=[torch.zeros(4)], max_norm=1.0, groups=70000), "1 to 65535"),
+    (dict(grads=[None, None], max_norm=1.0, groups=[0, 70000]), "1 to 65535"),
+])
+def test_clip_refuses(kw, what):
+    with pytest.raises(ValueError, match=what):
+        optim.clip_grads(**kw)
+
+
+def test_clip_entry_point_checks_before_it_launches():
+    lib = L._lib()
+    p = ctypes.c_void_p(1 << 20)
+
+    def call(*tensors, groups=2, stacked=0, max_norm=1.0, norms=p, ws=p, size=1 << 30, count=None):
+        t = (L.LoraGradTensor * max(len(tensors), 1))(*tensors)
+        return lib.grad_clip(t, len(tensors) if count is None else count, groups, stacked, max_norm, norms, ws, size, None)
+
+    a, b = (1 << 20, 100, 0, 0), (1 << 21, 64, 1, 1)
+    assert call(a, groups=0) == 1 and call(a, groups=65536) == 2 and call(a, count=-1) == 1
+    assert call((1 << 20, -1, 0, 0)) == 1 and call((None, 4, 0, 0)) == 1 and call((1 << 20, 4, 0, 2)) == 1
+    assert call((1 << 20, 4, 2, 0)) == 1 and call((1 << 20, 4, -1, 0)) == 1       # the group
+    assert call(((1 << 20) + 2, 4, 0, 0)) == 3 and call(((1 << 20) + 1, 4, 0, 1)) == 3
+    assert call(a, a) == 1 and call(a, b, ((1 << 20) + 396, 8, 1, 0)) == 1       # shared memory
+    assert call(((1 << 21) - 384, 100, 0, 1), b, stacked=1) == 1       # 2 groups of 200 bytes
+    assert call(a, b, norms=None) == 1 and call(a, b, norms=ctypes.c_void_p(2)) == 3 and call(a, b, max_norm=float("nan")) == 1
+    t = (L.LoraGradTensor * 2)(a, b)
+    need = L.grad_clip_workspace_bytes(t, 2, 2, False)
+    assert need > 0 and call(a, b, size=need - 1) == 4 and call(a, b, ws=None) == 4
+    assert call(a, b, ws=ctypes.c_void_p((1 << 20) + 8)) == 3
+    assert L.grad_clip_workspace_bytes(t, 2, 0, False) == 0
+    assert call((1 << 20, 2 ** 46, 0, 0)) == 2                          # more units than are counted
