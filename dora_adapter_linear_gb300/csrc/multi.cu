@@ -141,72 +141,135 @@ __global__ void __launch_bounds__(256) multi_reduce_kernel(MultiPlan p, int64_t 
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) multi_colsum_kernel(int64_t M, int64_t K, const T* S, T* out) {
+__global__ void __launch_bounds__(128) colsum_f32_kernel(int64_t M, int64_t K, const float* S, float* out) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   const int64_t k = (int64_t)blockIdx.x * 128 + threadIdx.x;
   if (k >= K) return;
   float t = 0.f;
-  for (int64_t i = 0; i < M; ++i) t += to_f(S[i * K + k]);
-  out[k] = from_f<T>(t);
+  for (int64_t i = 0; i < M; ++i) t += S[i * K + k];
+  out[k] = t;
 }
 
 // ------------------------------------------------------------------ launch sequences
 struct MultiWs {
   uint32_t* err;
-  float* P;       // [M, r] z, or s g
-  void* Z;        // [M, r] z recomputed by the backward
+  void* P;                    // [M, r] z or s g; bf16: s z or s g
+  void* Z;                    // [M, r] z recomputed by the backward
+  float *pa, *pb, *csum;      // bf16 backward: partials of dA and dB, column sums
 };
 size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   Carve c{base};
-  const size_t es = sh.dtype == LORA_BF16 ? 2 : 4;
+  const bool bf = sh.dtype == LORA_BF16;
+  const size_t rank = (size_t)sh.M * sh.r * (bf ? 2 : 4), parts = (size_t)multi_partials(sh.M) * sh.r;
   w->err = c.take<uint32_t>(kErrBytes / 4);
-  w->P = c.take<float>((size_t)sh.M * sh.r);
-  w->Z = bwd ? c.take<char>((size_t)sh.M * sh.r * es) : nullptr;
+  w->P = c.take<char>(rank);
+  w->Z = bwd ? c.take<char>(rank) : nullptr;
+  w->pa = bwd && bf ? c.take<float>(parts * sh.d_in) : nullptr;
+  w->pb = bwd && bf ? c.take<float>(parts * sh.d_out) : nullptr;
+  w->csum = bwd && bf ? c.take<float>((size_t)multi_colsum_splits(sh.M) * sh.d_out) : nullptr;
   return c.off;
 }
 
 unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
 
-template <typename T>
-cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const T* X, const T* W0, const T* A,
-                    const T* B, const T* bias, Scale s, T* Y, T* Z, cudaStream_t st) {
+cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const float* X, const float* W0,
+                    const float* A, const float* B, const float* bias, Scale s, float* Y, float* Z, cudaStream_t st) {
   const int r = (int)sh.r;
-  cudaError_t e = launch_pdl(multi_proj_kernel<T, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r, X, A, s,
-                             false, w.P, Z);
+  float* P = static_cast<float*>(w.P);
+  const cudaError_t e = launch_pdl(multi_proj_kernel<float, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r,
+                                   X, A, s, false, P, Z);
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_gemm_kernel<T, false>, dim3(blocks(sh.d_out, 64), blocks(sh.M, 64)), dim3(256), 0, st, p,
-                    sh.d_out, sh.d_in, r, X, W0, w.P, B, s, true, bias, Y);
+  return launch_pdl(multi_gemm_kernel<float, false>, dim3(blocks(sh.d_out, 64), blocks(sh.M, 64)), dim3(256), 0, st, p,
+                    sh.d_out, sh.d_in, r, X, W0, (const float*)P, B, s, true, bias, Y);
 }
 
-template <typename T>
-cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const T* X, const T* W0,
-                     const T* A, const T* B, const T* Z, const T* dY, Scale s, T* dX, T* dA, T* dB, T* dbias,
-                     cudaStream_t st) {
+// out [M, N] = S [M, K] W (+ bias) and, for each row, T U_a: the GEMM with the tile's adapters as its tail
+TcGemmDesc gemm(const MultiPlan& p, int mode, int64_t N, int64_t K, int r, int64_t n, const bf16* S, const bf16* W,
+                const bf16* T, const bf16* U, const bf16* bias, bf16* out, uint32_t* err) {
+  TcGemmDesc d;
+  d.mode = mode;
+  d.b0_mn = d.b1_mn = mode == TC_BWD_DX;
+  d.M = (int)p.M;
+  d.N = (int)N;
+  d.K0 = (int)K;
+  d.A0 = S;
+  d.lda0 = K;
+  d.B0 = W;
+  d.ldb0 = d.b0_mn ? N : K;
+  d.b0_rows = d.b0_mn ? (int)K : 0;
+  d.has_tail = true;
+  d.A1 = T;
+  d.lda1 = r;
+  d.K1 = d.K1_a = r;
+  d.B1 = U;
+  d.ad_count = p.tcount;
+  d.ad_list = p.tlist;
+  d.ad_mask = p.tmask;
+  d.ad_total = (int)n;
+  d.out[0] = out;
+  d.ldo = N;
+  d.bias = bias;
+  d.err = err;
+  d.timeout_ns = wait_timeout_ns();
+  return d;
+}
+
+cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
+                    const bf16* A, const bf16* B, const bf16* bias, Scale s, bf16* Y, bf16* Z, cudaStream_t st) {
   const int r = (int)sh.r;
+  bf16* T = static_cast<bf16*>(w.P);
+  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, st);
+  if (e != cudaSuccess) return e;
+  return tc_gemm(gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err), st);
+}
+
+cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const float* X, const float* W0,
+                     const float* A, const float* B, const float* Z, const float* dY, Scale s, float* dX, float* dA,
+                     float* dB, float* dbias, cudaStream_t st) {
+  const int r = (int)sh.r;
+  float* P = static_cast<float*>(w.P);
   cudaError_t e;
   if (!Z) {
-    e = launch_pdl(multi_proj_kernel<T, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r, X, A, s, false,
-                   (float*)nullptr, (T*)w.Z);
+    e = launch_pdl(multi_proj_kernel<float, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r, X, A, s, false,
+                   (float*)nullptr, (float*)w.Z);
     if (e != cudaSuccess) return e;
-    Z = static_cast<const T*>(w.Z);
+    Z = static_cast<const float*>(w.Z);
   }
-  e = launch_pdl(multi_proj_kernel<T, true>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_out, r, dY, B, s, true, w.P,
-                 (T*)nullptr);
+  e = launch_pdl(multi_proj_kernel<float, true>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_out, r, dY, B, s, true, P,
+                 (float*)nullptr);
   if (e != cudaSuccess) return e;
   if (dX) {
-    e = launch_pdl(multi_gemm_kernel<T, true>, dim3(blocks(sh.d_in, 64), blocks(sh.M, 64)), dim3(256), 0, st, p, sh.d_in,
-                   sh.d_out, r, dY, W0, w.P, A, s, false, (const T*)nullptr, dX);
+    e = launch_pdl(multi_gemm_kernel<float, true>, dim3(blocks(sh.d_in, 64), blocks(sh.M, 64)), dim3(256), 0, st, p,
+                   sh.d_in, sh.d_out, r, dY, W0, (const float*)P, A, s, false, (const float*)nullptr, dX);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(multi_reduce_kernel<T, float, false>, dim3(blocks(sh.d_in, 64), (unsigned)sh.n), dim3(256), 0, st, p,
-                 sh.d_in, r, X, w.P, s, false, dA);
+  e = launch_pdl(multi_reduce_kernel<float, float, false>, dim3(blocks(sh.d_in, 64), (unsigned)sh.n), dim3(256), 0, st, p,
+                 sh.d_in, r, X, (const float*)P, s, false, dA);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(multi_reduce_kernel<T, T, true>, dim3(blocks(sh.d_out, 64), (unsigned)sh.n), dim3(256), 0, st, p,
+  e = launch_pdl(multi_reduce_kernel<float, float, true>, dim3(blocks(sh.d_out, 64), (unsigned)sh.n), dim3(256), 0, st, p,
                  sh.d_out, r, dY, Z, s, true, dB);
   if (e != cudaSuccess || !dbias) return e;
-  return launch_pdl(multi_colsum_kernel<T>, dim3(blocks(sh.d_out, 128)), dim3(128), 0, st, sh.M, sh.d_out, dY, dbias);
+  return launch_pdl(colsum_f32_kernel, dim3(blocks(sh.d_out, 128)), dim3(128), 0, st, sh.M, sh.d_out, dY, dbias);
+}
+
+cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
+                     const bf16* A, const bf16* B, const bf16* Z, const bf16* dY, Scale s, bf16* dX, bf16* dA, bf16* dB,
+                     bf16* dbias, cudaStream_t st) {
+  const int r = (int)sh.r;
+  bf16* G = static_cast<bf16*>(w.P);
+  cudaError_t e;
+  if (!Z) {
+    if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, st)) != cudaSuccess) return e;
+    Z = static_cast<const bf16*>(w.Z);
+  }
+  if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, st)) != cudaSuccess) return e;
+  if (dX && (e = tc_gemm(gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err), st)) != cudaSuccess)
+    return e;
+  if ((e = multi_reduce(p, sh.d_in, r, X, G, false, false, 1.f, nullptr, w.pa, dA, st)) != cudaSuccess) return e;
+  if ((e = multi_reduce(p, sh.d_out, r, dY, Z, true, true, s.one, s.each, w.pb, dB, st)) != cudaSuccess) return e;
+  if ((e = multi_sum(p, sh.r * sh.d_in, w.pa, dA, sh.r * sh.d_out, w.pb, dB, st)) != cudaSuccess || !dbias) return e;
+  return multi_colsum(sh.M, sh.d_out, dY, w.csum, dbias, st);
 }
 
 lora_status check(const lora_multi_shape* sh) {

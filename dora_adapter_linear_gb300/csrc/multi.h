@@ -56,4 +56,19 @@ inline size_t multi_plan_layout(int64_t M, int64_t n, char* base, MultiPlan* p) 
 
 cudaError_t multi_plan(const MultiPlan& p, const void* ids, int id_bits, cudaStream_t st);
 
+// bf16 rank-r passes (multi_rank.cu); s_a is each[a], or `one` when each is null.
+// T_i = S_i U_a^T (U_a [r, K], or kr: [K, r]): plain = T, scaled = s_a T, [M, r], either may be null.  Rows without
+// adapter: zeros in plain, nothing in scaled.
+cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
+                       const float* each, bf16* plain, bf16* scaled, cudaStream_t st);
+// out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; adapters with
+// several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero
+cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, bool kr, bool scaled,
+                         float one, const float* each, float* part, bf16* out, cudaStream_t st);
+cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
+                      bf16* out1, cudaStream_t st);
+// out[k] = sum of all rows of S; part [multi_colsum_splits, K]
+int multi_colsum_splits(int64_t M);
+cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, bf16* out, cudaStream_t st);
+
 }  // namespace lg

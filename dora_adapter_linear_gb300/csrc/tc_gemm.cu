@@ -61,6 +61,10 @@ struct TcParams {
   float dn_s;
   int dn_r;
   bf16* dn_z;
+  // many adapters: those of each 256-row tile, and for each the rows that are not its own
+  const int32_t *ad_count, *ad_list;
+  const uint32_t* ad_mask;
+  int ad_chunks;        // 16-column chunks of the rank
   uint32_t* err;
   uint64_t timeout_ns;
 };
@@ -862,9 +866,24 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE, ZF>::THREADS, 1) tc_gemm_k
 //   empty[s]     both CTAs: the leader's MMA commit, multicast to the pair
 //   acc_full[b]  both CTAs: the leader's MMA commit, multicast
 //   acc_empty[b] leader: 4 epilogue warps (8 for the plain scale/bias epilogue) x 2 CTAs
-template <bool B0_MN, bool STACKED, bool HAS_TAIL, bool B1_MN, int EPI, bool KSCALE = false>
+//
+// Many adapters (MULTI): the tail of a tile takes every adapter among its rows in turn, each MMA with the
+// rows of the others switched off (disable-output-lane), so that a row meets its own adapter's operand
+// alone: a NaN in another one stays there, and Z needs no masked copies.  A K-step of the tail holds 64
+// columns of ranks in chunks of 16, those of four adapters up to rank 16, of two up to 32.  A K-major B1 chunk
+// (16 columns, 32 bytes a row) is a tile of its own with the 32-byte swizzle.
+struct MultiTail {
+  int KB, P, chunks, count;     // K-blocks of 64 of the rank; adapters a step; chunks of the rank; adapters
+  __device__ __forceinline__ MultiTail(int chunks_, int count_)
+      : KB((chunks_ + 3) >> 2), P(chunks_ >= 3 ? 1 : 4 / chunks_), chunks(chunks_), count(count_) {}
+  __device__ __forceinline__ int steps() const { return KB * ((count + P - 1) / P); }
+  __device__ __forceinline__ int in_block(int kb) const { return min(4, chunks - 4 * kb); }   // chunks of a K-block
+};
+
+template <bool B0_MN, bool STACKED, bool HAS_TAIL, bool B1_MN, int EPI, bool KSCALE = false, bool MULTI = false>
 __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kernel(const __grid_constant__ TcParams p) {
   static_assert(!KSCALE || (EPI == EPI_SCALE_BIAS && !STACKED), "K-scaling: plain dX products only");
+  static_assert(!MULTI || (EPI == EPI_SCALE_BIAS && !STACKED && HAS_TAIL && !KSCALE), "many adapters: plain products only");
   using C = OneCta<EPI, KSCALE>;
   using L = Layout<EPI, true, KSCALE>;
   constexpr int STAGES = L::STAGES;
@@ -894,7 +913,8 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
   const int num_clusters = gridDim.x >> 1;
   const int num_tiles = p.num_m_tiles * p.num_n_tiles;   // pair tiles (256 rows each)
   const int nk0 = (p.K0 + BK - 1) / BK;
-  const int nk = nk0 + (HAS_TAIL ? (p.K1 + BK - 1) / BK : 0);   // the rank-r tail may span several K-steps
+  // the rank-r tail may span several K-steps; with many adapters the tiles' tails differ
+  const int nk = nk0 + (HAS_TAIL && !MULTI ? (p.K1 + BK - 1) / BK : 0);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
@@ -946,7 +966,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
             ok = false;
             break;
           }
-          const bool tail = HAS_TAIL && ks >= nk0;
+          const bool tail = HAS_TAIL && !MULTI && ks >= nk0;
           uint32_t bar;
           if constexpr (KSCALE) {   // this CTA's bytes (and the scales of a main step) on its own barrier
             mbar_expect_tx(&full[stage], L::STAGE_BYTES + (tail ? 0 : L::KSC_BYTES));
@@ -994,6 +1014,43 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
             phase ^= 1;
           }
         }
+        if constexpr (MULTI) {
+          const MultiTail tail(p.ad_chunks, __ldg(p.ad_count + mt));
+          const int32_t* list = p.ad_list + (int64_t)mt * PM;
+          const int steps = tail.steps();
+          for (int ts = 0; ts < steps && ok; ++ts) {
+            const int kb = ts % tail.KB, q0 = ts / tail.KB * tail.P;
+            const int nq = min(tail.P, tail.count - q0), nc = tail.in_block(kb);
+            int ad[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ad[i] = i < nq ? __ldg(list + q0 + i) : 0;
+            if (!mbar_wait_cl(&empty[stage], phase ^ 1, p.timeout_ns, abort_flag, p.err, 0x201)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bytes = A_STAGE_BYTES + nq * nc * 4096;   // a chunk of this CTA's 128 columns: 4 KB
+            const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+            if (!p.pair_leader_arms) mbar_expect_tx_cluster(bar, bytes);
+            else if (rank == 0) mbar_expect_tx(&full[stage], 2 * bytes);
+            uint8_t* b_dst = sB + stage * L::B_STAGE_BYTES;
+            tma_load_2d_pair(sA + stage * A_STAGE_BYTES, &p.tmA1, bar, kb * BK, m0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              for (int c = 0; i < nq && c < nc; ++c) {
+                const int slot = i * nc + c, k = kb * BK + 16 * c, n = n0 + (int)rank * 128;
+                if (B1_MN) {
+                  tma_load_3d_pair(b_dst + slot * 2048, &p.tmB1, bar, n, k, ad[i]);
+                  tma_load_3d_pair(b_dst + 8192 + slot * 2048, &p.tmB1, bar, n + 64, k, ad[i]);
+                } else {
+                  tma_load_3d_pair(b_dst + slot * 4096, &p.tmB1, bar, k, n, ad[i]);
+                }
+              }
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
       }
       if (!ok) spin_ns(100000ull);  // unwind: give copies already issued time to land
     }
@@ -1010,6 +1067,12 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++it) {
         const int buf = it & 1;
         const uint32_t acc_phase = (it >> 1) & 1;
+        int mt = 0, count = 0;
+        if constexpr (MULTI) {
+          int nt;
+          tile_coords(t, p.num_m_tiles, p.num_n_tiles, p.group_m, mt, nt);
+          count = __ldg(p.ad_count + mt);
+        }
         if (!mbar_wait_cl(&acc_empty[buf], acc_phase ^ 1, p.timeout_ns, abort_flag, p.err, 0x202)) {
           ok = false;
           break;
@@ -1017,7 +1080,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * BN;
         for (int ks = 0; ks < nk; ++ks) {
-          const bool tail = HAS_TAIL && ks >= nk0;
+          const bool tail = HAS_TAIL && !MULTI && ks >= nk0;
           if (!mbar_wait_cl(KSCALE ? &ready[stage] : &full[stage], phase, p.timeout_ns, abort_flag, p.err, 0x203)) {
             ok = false;
             break;
@@ -1037,6 +1100,43 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
+          }
+        }
+        if constexpr (MULTI) {
+          const uint4* masks = reinterpret_cast<const uint4*>(p.ad_mask) + (int64_t)mt * PM * 2;
+          const MultiTail tail(p.ad_chunks, count);
+          const int steps = tail.steps();
+          for (int ts = 0; ts < steps && ok; ++ts) {
+            const int kb = ts % tail.KB, q0 = ts / tail.KB * tail.P;
+            const int nq = min(tail.P, tail.count - q0), nc = tail.in_block(kb);
+            uint4 lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (i < nq) {
+                lo[i] = __ldg(masks + 2 * (q0 + i));
+                hi[i] = __ldg(masks + 2 * (q0 + i) + 1);
+              }
+            if (!mbar_wait_cl(&full[stage], phase, p.timeout_ns, abort_flag, p.err, 0x203)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(sA + stage * A_STAGE_BYTES);
+            const uint32_t b_base = smem_u32(sB + stage * L::B_STAGE_BYTES);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              for (int c = 0; i < nq && c < nc; ++c) {
+                const int slot = i * nc + c;
+                const uint64_t adesc = umma_smem_desc(a_base + c * 32, 16, 1024);
+                const uint64_t bdesc = B1_MN ? umma_smem_desc(b_base + slot * 2048, 8192, 1024)
+                                             : umma_smem_desc_32b(b_base + slot * 4096, 256);
+                umma_bf16_pair_lanes(d_tmem, adesc, bdesc, idesc1, lo[i], hi[i]);
+              }
+            umma_commit_pair_mc(&empty[stage], 0x3);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
         }
         if (!ok) break;
@@ -1133,6 +1233,21 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D bf16 tensor map over a stack of contiguous [outer, inner] matrices, one chunk of 16 rank columns a box: 16
+// rows of 64 elements (128-byte swizzle) where the rank is the outer dimension, else 128 rows of 16 (32-byte
+// swizzle).  What lies outside of a matrix reads as zero, not as the next one.
+static bool make_stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stack, bool rank_outer) {
+  auto enc = get_encode();
+  if (!enc || base == nullptr) return false;
+  cuuint64_t dims[3] = {inner, outer, stack};
+  cuuint64_t strides[2] = {inner * 2, inner * outer * 2};
+  cuuint32_t box[3] = {rank_outer ? 64u : 16u, rank_outer ? 16u : 128u, 1u};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, rank_outer ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
@@ -1235,10 +1350,10 @@ static cudaError_t launch_one(const TcParams& p, cudaStream_t st, int tiles, int
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <bool B0_MN, bool STACKED, bool HAS_TAIL, bool B1_MN, int EPI, bool KSCALE = false>
+template <bool B0_MN, bool STACKED, bool HAS_TAIL, bool B1_MN, int EPI, bool KSCALE = false, bool MULTI = false>
 static cudaError_t launch_pair(const TcParams& p, cudaStream_t st, int tiles, int max_ctas) {
   using L = Layout<EPI, true, KSCALE>;
-  auto kern = tc_pair_kernel<B0_MN, STACKED, HAS_TAIL, B1_MN, EPI, KSCALE>;
+  auto kern = tc_pair_kernel<B0_MN, STACKED, HAS_TAIL, B1_MN, EPI, KSCALE, MULTI>;
   static int max_clusters_dev[64] = {0};   // co-resident clusters, per device
   int& max_clusters = max_clusters_dev[current_device_slot()];
   cudaLaunchConfig_t cfg = {};
@@ -1290,6 +1405,11 @@ static cudaError_t launch_variant(const TcParams& p, cudaStream_t st, int kind, 
 
 static cudaError_t launch_mode(const TcGemmDesc& d, const TcParams& p, cudaStream_t st, int kind, int tiles) {
   const int mc = d.max_ctas;
+  if (d.ad_count) {   // many adapters: the CTA pair, whose 256-row tiles the plan describes
+    if (d.mode == TC_FWD) return launch_pair<false, false, true, false, EPI_SCALE_BIAS, false, true>(p, st, tiles, mc);
+    if (d.mode == TC_BWD_DX) return launch_pair<true, false, true, true, EPI_SCALE_BIAS, false, true>(p, st, tiles, mc);
+    return cudaErrorInvalidValue;
+  }
   switch (d.mode) {
     case TC_FWD:
       if (d.dn_a) return launch_one<false, false, true, false, EPI_SCALE_BIAS, false, true>(p, st, tiles, mc);
@@ -1330,7 +1450,8 @@ cudaError_t tc_gemm(const TcGemmDesc& d, cudaStream_t st) {
   // the down-projection in the GEMM runs on the one-CTA kernel (ranks 8 .. 32, one tail step)
   if (d.dn_a && (d.mode != TC_FWD || !d.has_tail || d.dn_r < 8 || d.dn_r > 32 || d.dn_r % 8 || d.K1 != d.dn_r))
     return cudaErrorInvalidValue;
-  const bool pair = use_pair(d.mode) && d.mode != TC_W8A8K && d.dn_a == nullptr;
+  const bool multi = d.ad_count != nullptr;
+  const bool pair = multi || (use_pair(d.mode) && d.mode != TC_W8A8K && d.dn_a == nullptr);
   TcParams p;
   memset(&p, 0, sizeof(p));
   const bool stacked = d.mode == TC_SWIGLU_FWD;
@@ -1350,7 +1471,8 @@ cudaError_t tc_gemm(const TcGemmDesc& d, cudaStream_t st) {
       if (d.K1_a != d.K1) return cudaErrorInvalidValue;
       ok = ok && make_map(&p.tmA1, d.A1, d.K1_a, d.M, d.lda1, BM);
     }
-    if (d.b1_mn) ok = ok && make_map(&p.tmB1, d.B1, d.N, d.K1, d.ldb1, 64);
+    if (multi) ok = ok && make_stack_map(&p.tmB1, d.B1, d.b1_mn ? d.N : d.K1, d.b1_mn ? d.K1 : d.N, d.ad_total, d.b1_mn);
+    else if (d.b1_mn) ok = ok && make_map(&p.tmB1, d.B1, d.N, d.K1, d.ldb1, 64);
     else {
       ok = ok && make_map(&p.tmB1, d.B1, d.K1_b, d.N, d.ldb1, bnb);
       if (stacked)
@@ -1374,6 +1496,10 @@ cudaError_t tc_gemm(const TcGemmDesc& d, cudaStream_t st) {
   p.dn_s = d.dn_s;
   p.dn_r = d.dn_r;
   p.dn_z = d.dn_z;
+  p.ad_count = d.ad_count;
+  p.ad_list = d.ad_list;
+  p.ad_mask = d.ad_mask;
+  p.ad_chunks = (d.K1 + 15) / 16;
 
   p.M = d.M;
   p.N = d.N;
