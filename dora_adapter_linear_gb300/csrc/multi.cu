@@ -18,144 +18,14 @@ namespace {
 struct Scale {          // s_a: one number, or one for each adapter
   float one;
   const float* each;
-  __device__ __forceinline__ float of(int a) const { return each ? __ldg(each + a) : one; }
 };
-
-// ------------------------------------------------------------------ rank-r products of rows
-// P[i][j] = (scaled) sum_k S[i][k] U_a(j, k), U_a [r, K] or (KR) [K, r]; zeros for a row without adapter.  A
-// warp takes every fourth j of its CTA's row.
-template <typename T, bool KR>
-__global__ void __launch_bounds__(128) multi_proj_kernel(MultiPlan p, int64_t K, int r, const T* S, const T* U, Scale s,
-                                                         bool scaled, float* P, T* Z) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-  const int64_t i = blockIdx.x;
-  const int a = p.ids[i], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* x = S + i * K;
-  const T* u = U + (int64_t)max(a, 0) * r * K;
-  const float f = a >= 0 && scaled ? s.of(a) : 1.f;
-  for (int j = warp; j < r; j += 4) {
-    float t = 0.f;
-    if (a >= 0)
-      for (int64_t k = lane; k < K; k += 32) t = fmaf(to_f(x[k]), to_f(KR ? u[k * r + j] : u[(int64_t)j * K + k]), t);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) {
-      if (P) P[i * r + j] = t * f;
-      if (Z) Z[i * r + j] = from_f<T>(t);
-    }
-  }
-}
-
-// ------------------------------------------------------------------ shared product and rank-r update
-// out[i][c] = sum_k S[i][k] W(c, k) + f_a sum_j P[i][j] U_a(c, j) + bias[c].  W [N, K] and U_a [N, r], or (MN)
-// W [K, N] and U_a [r, N]; f_a = s_a when `scaled`, else 1.
-template <typename T, bool MN>
-__global__ void __launch_bounds__(256) multi_gemm_kernel(MultiPlan p, int64_t N, int64_t K, int r, const T* S, const T* W,
-                                                         const float* P, const T* U, Scale s, bool scaled, const T* bias,
-                                                         T* out) {
-  constexpr int TT = 64, TK = 16;
-  __shared__ float As[TK][TT + 4];
-  __shared__ float Bs[TK][TT + 4];
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = (int64_t)blockIdx.y * TT, n0 = (int64_t)blockIdx.x * TT;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < K; k0 += TK) {
-    for (int i = threadIdx.x; i < TT * TK; i += 256) {
-      const int kk = i % TK, mm = i / TK;
-      const int64_t m = m0 + mm, k = k0 + kk;
-      As[kk][mm] = m < p.M && k < K ? to_f(S[m * K + k]) : 0.f;
-    }
-    for (int i = threadIdx.x; i < TT * TK; i += 256) {
-      const int kk = MN ? i / TT : i % TK, nn = MN ? i % TT : i / TK;
-      const int64_t c = n0 + nn, k = k0 + kk;
-      Bs[kk][nn] = c < N && k < K ? to_f(MN ? W[k * N + c] : W[c * K + k]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < TK; ++kk) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = As[kk][ty * 4 + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = Bs[kk][tx * 4 + j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + ty * 4 + i;
-    if (m >= p.M) continue;
-    const int a = p.ids[m];
-    const float f = a >= 0 && scaled ? s.of(a) : 1.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = n0 + tx * 4 + j;
-      if (c >= N) continue;
-      float v = acc[i][j];
-      if (a >= 0) {
-        const T* u = U + (int64_t)a * r * N;
-        float t = 0.f;
-        for (int q = 0; q < r; ++q) t = fmaf(P[m * r + q], to_f(MN ? u[(int64_t)q * N + c] : u[c * r + q]), t);
-        v = fmaf(f, t, v);
-      }
-      if (bias) v += to_f(bias[c]);
-      out[m * N + c] = from_f<T>(v);
-    }
-  }
-}
-
-// ------------------------------------------------------------------ gradients of the adapters
-// out_a(j, k) = f_a sum over its rows P[i][j] S[i][k], out_a [r, K] or (KR) [K, r]; f_a = s_a when `scaled`.  P
-// fp32 or of the rows' type.  A CTA has 64 columns of one adapter, a thread every fourth j of one; rows in
-// the plan's order.  Zeros for an adapter without rows.
-template <typename T, typename TP, bool KR>
-__global__ void __launch_bounds__(256) multi_reduce_kernel(MultiPlan p, int64_t K, int r, const T* S, const TP* P, Scale s,
-                                                           bool scaled, T* out) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-  const int a = blockIdx.y;
-  const int64_t k = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int j0 = threadIdx.x >> 6;
-  if (k >= K) return;
-  float acc[32] = {};
-  for (int i = p.start[a]; i < p.start[a + 1]; ++i) {
-    const int64_t row = p.order[i];
-    const float x = to_f(S[row * K + k]);
-#pragma unroll
-    for (int q = 0; q < 32; ++q)
-      if (j0 + 4 * q < r) acc[q] = fmaf(to_f(P[row * r + j0 + 4 * q]), x, acc[q]);
-  }
-  const float f = scaled ? s.of(a) : 1.f;
-  T* o = out + (int64_t)a * r * K;
-#pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    const int j = j0 + 4 * q;
-    if (j < r) o[KR ? k * r + j : (int64_t)j * K + k] = from_f<T>(acc[q] * f);
-  }
-}
-
-__global__ void __launch_bounds__(128) colsum_f32_kernel(int64_t M, int64_t K, const float* S, float* out) {
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-  const int64_t k = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (k >= K) return;
-  float t = 0.f;
-  for (int64_t i = 0; i < M; ++i) t += S[i * K + k];
-  out[k] = t;
-}
 
 // ------------------------------------------------------------------ launch sequences
 struct MultiWs {
   uint32_t* err;
   void* P;                    // [M, r] z or s g; bf16: s z or s g
   void* Z;                    // [M, r] z recomputed by the backward
+  float* few;                 // forward of a few bf16 rows: z by stretches of K
   float *pa, *pb, *csum;      // bf16 backward: partials of dA and dB, column sums
 };
 size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
@@ -165,23 +35,39 @@ size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   w->err = c.take<uint32_t>(kErrBytes / 4);
   w->P = c.take<char>(rank);
   w->Z = bwd ? c.take<char>(rank) : nullptr;
+  w->few = !bwd && bf && sh.M <= kFewRows ? c.take<float>((size_t)multi_few_splits(sh.d_in) * sh.M * sh.r) : nullptr;
   w->pa = bwd && bf ? c.take<float>(parts * sh.d_in) : nullptr;
   w->pb = bwd && bf ? c.take<float>(parts * sh.d_out) : nullptr;
   w->csum = bwd && bf ? c.take<float>((size_t)multi_colsum_splits(sh.M) * sh.d_out) : nullptr;
   return c.off;
 }
 
-unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
-
 cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const float* X, const float* W0,
                     const float* A, const float* B, const float* bias, Scale s, float* Y, float* Z, cudaStream_t st) {
   const int r = (int)sh.r;
-  float* P = static_cast<float*>(w.P);
-  const cudaError_t e = launch_pdl(multi_proj_kernel<float, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r,
-                                   X, A, s, false, P, Z);
+  if (!Z) Z = static_cast<float*>(w.P);
+  const cudaError_t e = multi_f32_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, nullptr, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_gemm_kernel<float, false>, dim3(blocks(sh.d_out, 64), blocks(sh.M, 64)), dim3(256), 0, st, p,
-                    sh.d_out, sh.d_in, r, X, W0, (const float*)P, B, s, true, bias, Y);
+  return multi_f32_gemm(p, sh.d_out, sh.d_in, r, X, W0, false, Z, B, bias, true, s.one, s.each, Y, st);
+}
+
+cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const float* X, const float* W0,
+                     const float* A, const float* B, const float* Z, const float* dY, Scale s, float* dX, float* dA,
+                     float* dB, float* dbias, cudaStream_t st) {
+  const int r = (int)sh.r;
+  float* G = static_cast<float*>(w.P);
+  cudaError_t e;
+  if (!Z) {
+    if ((e = multi_f32_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (float*)w.Z, nullptr, st)) != cudaSuccess) return e;
+    Z = static_cast<const float*>(w.Z);
+  }
+  if ((e = multi_f32_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, st)) != cudaSuccess) return e;
+  if (dX && (e = multi_f32_gemm(p, sh.d_in, sh.d_out, r, dY, W0, true, G, A, nullptr, false, 1.f, nullptr, dX, st)) !=
+                cudaSuccess)
+    return e;
+  e = multi_f32_reduce(p, r, sh.d_in, X, G, dA, sh.d_out, dY, Z, dB, s.one, s.each, st);
+  if (e != cudaSuccess || !dbias) return e;
+  return multi_f32_colsum(sh.M, sh.d_out, dY, dbias, st);
 }
 
 // out [M, N] = S [M, K] W (+ bias) and, for each row, T U_a: the GEMM with the tile's adapters as its tail
@@ -218,39 +104,13 @@ TcGemmDesc gemm(const MultiPlan& p, int mode, int64_t N, int64_t K, int r, int64
 cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
                     const bf16* A, const bf16* B, const bf16* bias, Scale s, bf16* Y, bf16* Z, cudaStream_t st) {
   const int r = (int)sh.r;
+  if (sh.M <= kFewRows)
+    return multi_few_fwd(p, sh.d_out, sh.d_in, r, sh.n, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
+                         wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);
   const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, st);
   if (e != cudaSuccess) return e;
   return tc_gemm(gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err), st);
-}
-
-cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const float* X, const float* W0,
-                     const float* A, const float* B, const float* Z, const float* dY, Scale s, float* dX, float* dA,
-                     float* dB, float* dbias, cudaStream_t st) {
-  const int r = (int)sh.r;
-  float* P = static_cast<float*>(w.P);
-  cudaError_t e;
-  if (!Z) {
-    e = launch_pdl(multi_proj_kernel<float, false>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_in, r, X, A, s, false,
-                   (float*)nullptr, (float*)w.Z);
-    if (e != cudaSuccess) return e;
-    Z = static_cast<const float*>(w.Z);
-  }
-  e = launch_pdl(multi_proj_kernel<float, true>, dim3((unsigned)sh.M), dim3(128), 0, st, p, sh.d_out, r, dY, B, s, true, P,
-                 (float*)nullptr);
-  if (e != cudaSuccess) return e;
-  if (dX) {
-    e = launch_pdl(multi_gemm_kernel<float, true>, dim3(blocks(sh.d_in, 64), blocks(sh.M, 64)), dim3(256), 0, st, p,
-                   sh.d_in, sh.d_out, r, dY, W0, (const float*)P, A, s, false, (const float*)nullptr, dX);
-    if (e != cudaSuccess) return e;
-  }
-  e = launch_pdl(multi_reduce_kernel<float, float, false>, dim3(blocks(sh.d_in, 64), (unsigned)sh.n), dim3(256), 0, st, p,
-                 sh.d_in, r, X, (const float*)P, s, false, dA);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(multi_reduce_kernel<float, float, true>, dim3(blocks(sh.d_out, 64), (unsigned)sh.n), dim3(256), 0, st, p,
-                 sh.d_out, r, dY, Z, s, true, dB);
-  if (e != cudaSuccess || !dbias) return e;
-  return launch_pdl(colsum_f32_kernel, dim3(blocks(sh.d_out, 128)), dim3(128), 0, st, sh.M, sh.d_out, dY, dbias);
 }
 
 cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
@@ -277,9 +137,8 @@ lora_status check(const lora_multi_shape* sh) {
   if (sh->M < 0 || sh->d_in <= 0 || sh->d_out <= 0 || sh->r <= 0 || sh->n <= 0) return LORA_ERR_INVALID_ARG;
   if (sh->dtype != LORA_F32 && sh->dtype != LORA_BF16) return LORA_ERR_INVALID_ARG;
   if (sh->d_in % 8 || sh->d_out % 8 || sh->r > 128 || (sh->dtype == LORA_BF16 && sh->r % 8)) return LORA_ERR_UNSUPPORTED;
-  constexpr int64_t top = (1LL << 31) - 1;
-  // rows and columns are counted in 32 bits; 2^24 rows are 2^16 tiles, a launch's limit in its second dimension
-  if (sh->M > 1 << 24 || sh->n > 65535 || sh->d_in > top - 512 || sh->d_out > top - 512) return LORA_ERR_UNSUPPORTED;
+  // the launches' grids are counted for these
+  if (sh->M > 1 << 24 || sh->n > 65535 || sh->d_in > 1 << 20 || sh->d_out > 1 << 20) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 

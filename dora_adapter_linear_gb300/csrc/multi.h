@@ -67,8 +67,27 @@ cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, co
                          float one, const float* each, float* part, bf16* out, cudaStream_t st);
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
                       bf16* out1, cudaStream_t st);
+// The whole bf16 forward of a few rows (multi_few.cu); part: fp32 [multi_few_splits(K), M, r]
+constexpr int kFewRows = 256;
+int multi_few_splits(int64_t K);
+cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64_t n, const bf16* X, const bf16* W0,
+                          const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* part,
+                          bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st);
 // out[k] = sum of all rows of S; part [multi_colsum_splits, K]
 int multi_colsum_splits(int64_t M);
 cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, bf16* out, cudaStream_t st);
+
+
+// fp32 (multi_f32.cu)
+cudaError_t multi_f32_proj(const MultiPlan& p, int64_t K, int r, const float* S, const float* U, bool kr, float one,
+                           const float* each, float* plain, float* scaled, cudaStream_t st);
+// out [M, N] = S [M, K] W (W [N, K], or mn: [K, N]) + (scaled: s_a) P_i U_a (U_a [N, r], or mn: [r, N]) (+ bias)
+cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, const float* S, const float* W, bool mn,
+                           const float* P, const float* U, const float* bias, bool scaled, float one, const float* each,
+                           float* out, cudaStream_t st);
+// dA_a = sum G_i^T X_i, dB_a = s_a sum dY_i^T Z_i
+cudaError_t multi_f32_reduce(const MultiPlan& p, int r, int64_t in, const float* X, const float* G, float* dA, int64_t out,
+                             const float* dY, const float* Z, float* dB, float one, const float* each, cudaStream_t st);
+cudaError_t multi_f32_colsum(int64_t M, int64_t K, const float* S, float* out, cudaStream_t st);
 
 }  // namespace lg

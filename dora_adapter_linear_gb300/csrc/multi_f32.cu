@@ -1,0 +1,391 @@
+// The many-adapter projection in fp32: FMA tiles, no reduced-precision tensor math, as everywhere here for fp32.
+//
+// Sums over long axes are taken in stretches of at most 256 products (or one share of a warp or CTA) that are
+// added up afterwards: their rounding grows with the stretch and not with the whole length.
+#include "common.cuh"
+#include "multi.h"
+#include "vec.cuh"
+
+namespace lg {
+
+namespace {
+
+__device__ __forceinline__ float scale_of(float one, const float* each, int a) { return each ? __ldg(each + a) : one; }
+
+// ------------------------------------------------------------------ rank-r products of rows
+// A CTA has eight rows of an item and all j of their adapter; the rows pass through shared memory 1024 columns
+// at a time, so a factor is read once for eight rows.  Up to eight warps take the j of U_a [r, K] in turn; of
+// U_a [K, r] (KR) a thread keeps one j, and the threads' shares of k meet in shared memory.
+constexpr int kCols = 1024, kRows = 8;
+
+struct F32Proj {
+  MultiPlan p;
+  int64_t K;
+  int r;
+  const float *S, *U;
+  float one;
+  const float* each;
+  float *plain, *scaled;          // [M, r] T and s_a T; either may be null
+};
+
+template <bool KR>
+__global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F32Proj a) {
+  __shared__ float x[kRows][kCols];
+  __shared__ float sum[kRows][128];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int r = a.r, with = a.p.head[kHeadRows];
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.p.M - with) * r; i += (int64_t)gridDim.x * 256) {
+    const int64_t at = (int64_t)a.p.order[with + i / r] * r + i % r;     // rows without adapter
+    if (a.plain) a.plain[at] = 0.f;
+    if (a.scaled) a.scaled[at] = 0.f;
+  }
+  if ((int)blockIdx.x / (kItemRows / kRows) >= a.p.head[kHeadItems]) return;
+  const int4 item = a.p.items[blockIdx.x / (kItemRows / kRows)];
+  const int first = (int)blockIdx.x % (kItemRows / kRows) * kRows, rows = min(kRows, item.z - first);
+  if (rows <= 0) return;
+  const int32_t* order = a.p.order + item.y + first;
+  const float* u = a.U + (int64_t)item.x * r * a.K;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < kRows * 128; i += 256) (&sum[0][0])[i] = 0.f;
+  for (int64_t k0 = 0; k0 < a.K; k0 += kCols) {
+    const int cols = (int)min((int64_t)kCols, a.K - k0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * kCols / 4; i += 256) {
+      const int m = i / (kCols / 4), c = i % (kCols / 4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m < rows && c < cols) v = __ldg(reinterpret_cast<const float4*>(a.S + (int64_t)order[m] * a.K + k0 + c));
+      *reinterpret_cast<float4*>(&x[m][c]) = v;
+    }
+    __syncthreads();
+    if (!KR) {
+      for (int j = warp; j < r; j += 8) {
+        float t[kRows] = {};
+        const float* w = u + (int64_t)j * a.K + k0;
+#pragma unroll 4
+        for (int c = lane * 4; c < cols; c += 128) {
+          const float4 b = __ldg(reinterpret_cast<const float4*>(w + c));
+#pragma unroll
+          for (int m = 0; m < kRows; ++m) {
+            const float4 v = *reinterpret_cast<const float4*>(&x[m][c]);
+            t[m] = fmaf(v.x, b.x, fmaf(v.y, b.y, fmaf(v.z, b.z, fmaf(v.w, b.w, t[m]))));
+          }
+        }
+        const float s = warp_sums_of<8>(t);
+        if (lane % 4 == 0) sum[lane / 4][j] += s;      // this warp's j alone
+      }
+    } else {
+      const int shares = 256 / r, j = threadIdx.x % r, k = threadIdx.x / r;
+      float t[kRows] = {};
+      if (k < shares) {
+#pragma unroll 4
+        for (int c = k; c < cols; c += shares) {
+          const float b = __ldg(u + (k0 + c) * r + j);
+#pragma unroll
+          for (int m = 0; m < kRows; ++m) t[m] = fmaf(x[m][c], b, t[m]);
+        }
+      }
+      __syncthreads();                                 // the rows have been read: their place takes the shares
+      float* red = &x[0][0];
+      if (k < shares)
+#pragma unroll
+        for (int m = 0; m < kRows; ++m) red[(k * kRows + m) * r + j] = t[m];
+      __syncthreads();
+      for (int i = threadIdx.x; i < kRows * r; i += 256) {
+        float s = 0.f;
+        for (int q = 0; q < shares; ++q) s += red[q * kRows * r + i];
+        sum[i / r][i % r] += s;
+      }
+    }
+  }
+  __syncthreads();
+  const float f = scale_of(a.one, a.each, item.x);
+  for (int i = threadIdx.x; i < rows * r; i += 256) {
+    const int64_t at = (int64_t)order[i / r] * r + i % r;
+    const float v = sum[i / r][i % r];
+    if (a.plain) a.plain[at] = v;
+    if (a.scaled) a.scaled[at] = v * f;
+  }
+}
+
+// ------------------------------------------------------------------ shared product and rank-r update
+// 64 x 64 outputs a CTA, 4 x 4 a thread, K in slabs of 16 through two buffers; the CTAs of a cluster share K and add
+// their sums through distributed shared memory, each finishing its share of the rows.  There a thread has one
+// column, and takes its adapter's factor anew only where the next row has another one.
+constexpr int kTile = 64, kSlab = 16;
+
+struct F32Gemm {
+  MultiPlan p;
+  int64_t N, K;
+  int r;
+  const float *S, *W, *P, *U, *bias;
+  float one;
+  const float* each;
+  bool scaled;                    // the update takes s_a
+  float* out;
+};
+
+template <bool MN>
+__global__ void __launch_bounds__(256) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
+  __shared__ float As[2][kSlab][kTile + 4];
+  __shared__ float Bs[2][kSlab][kTile + 4];
+  __shared__ float part[kTile][kTile + 4];
+  __shared__ float ps[kTile][8];
+  __shared__ int ids[kTile];
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t K = a.K, N = a.N;
+  const int tile = (int)(blockIdx.x / ranks), wide = (int)((N + kTile - 1) / kTile);
+  const int64_t m0 = (int64_t)(tile / wide) * kTile, n0 = (int64_t)(tile % wide) * kTile;
+  const int slabs = (int)((K + kSlab - 1) / kSlab), s0 = (int)((int64_t)slabs * rank / ranks),
+            s1 = (int)((int64_t)slabs * (rank + 1) / ranks);
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int lr = threadIdx.x >> 2, lk = (threadIdx.x & 3) * 4;   // a row and four k of a K-major operand
+  const int bk = threadIdx.x >> 4, bc = (threadIdx.x & 15) * 4;  // a k and four columns of W [K, N]
+  auto fetch = [&](int s, float4& x, float4& w) {
+    const int64_t k = (int64_t)s * kSlab + lk;
+    x = s < s1 && m0 + lr < a.p.M && k < K ? __ldg(reinterpret_cast<const float4*>(a.S + (m0 + lr) * K + k)) : none;
+    if (MN) {
+      const int64_t kk = (int64_t)s * kSlab + bk;
+      w = s < s1 && kk < K && n0 + bc < N ? __ldg(reinterpret_cast<const float4*>(a.W + kk * N + n0 + bc)) : none;
+    } else {
+      w = s < s1 && n0 + lr < N && k < K ? __ldg(reinterpret_cast<const float4*>(a.W + (n0 + lr) * K + k)) : none;
+    }
+  };
+  auto put = [&](int b, const float4& x, const float4& w) {
+    As[b][lk][lr] = x.x, As[b][lk + 1][lr] = x.y, As[b][lk + 2][lr] = x.z, As[b][lk + 3][lr] = x.w;
+    if (MN) *reinterpret_cast<float4*>(&Bs[b][bk][bc]) = w;
+    else Bs[b][lk][lr] = w.x, Bs[b][lk + 1][lr] = w.y, Bs[b][lk + 2][lr] = w.z, Bs[b][lk + 3][lr] = w.w;
+  };
+  float acc[4][4] = {}, run[4][4] = {};
+  float4 x, w;
+  fetch(s0, x, w);
+  put(0, x, w);
+  for (int s = s0; s < s1; ++s) {
+    const int b = (s - s0) & 1;
+    fetch(s + 1, x, w);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSlab; ++k) {
+      const float4 u = *reinterpret_cast<const float4*>(&As[b][k][ty * 4]), v = *reinterpret_cast<const float4*>(&Bs[b][k][tx * 4]);
+      const float p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
+    }
+    put(b ^ 1, x, w);
+    if (((s - s0) & 15) == 15 || s + 1 == s1) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += run[i][j], run[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<float4*>(&part[ty * 4 + i][tx * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  if (threadIdx.x < kTile) ids[threadIdx.x] = m0 + threadIdx.x < a.p.M ? a.p.ids[m0 + threadIdx.x] : -1;
+  cluster_sync_all();
+  // column c, every fourth of this CTA's rows
+  const int c = threadIdx.x & 63, own = kTile / (int)ranks, r0 = (int)rank * own + (threadIdx.x >> 6);
+  const uint32_t mine = smem_u32(&part[0][0]);
+  float v[16], t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    v[i] = t[i] = 0.f;
+    if (4 * i < own)
+      for (uint32_t q = 0; q < ranks; ++q) {
+        float f;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(f)
+                     : "r"(mapa_shared(mine + ((r0 + 4 * i) * (kTile + 4) + c) * 4, q)));
+        v[i] += f;
+      }
+  }
+  for (int j0 = 0; j0 < a.r; j0 += 8) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * 8; i += 256) {
+      const int m = i >> 3, j = j0 + (i & 7);
+      ps[m][i & 7] = ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
+    }
+    __syncthreads();
+    if (n0 + c < N) {
+      int have = -1;
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (4 * i >= own) break;
+        const int m = r0 + 4 * i, ad = ids[m];
+        if (ad < 0) continue;
+        if (ad != have) {
+          have = ad;
+          const float* b = a.U + (int64_t)ad * a.r * N;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            u[q] = j0 + q < a.r ? __ldg(MN ? b + (int64_t)(j0 + q) * N + n0 + c : b + (n0 + c) * a.r + j0 + q) : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (j0 + q < a.r) t[i] = fmaf(ps[m][q], u[q], t[i]);
+      }
+    }
+  }
+  if (n0 + c < N) {
+    const float bias = a.bias ? __ldg(a.bias + n0 + c) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t m = m0 + r0 + 4 * i;
+      if (4 * i >= own || m >= a.p.M) break;
+      const int ad = ids[r0 + 4 * i];
+      float y = v[i];
+      if (ad >= 0) y += a.scaled ? scale_of(a.one, a.each, ad) * t[i] : t[i];
+      a.out[m * N + n0 + c] = y + bias;
+    }
+  }
+  cluster_sync_all();           // no CTA leaves while another reads its sums
+}
+
+// ------------------------------------------------------------------ gradients of the adapters
+// out_a(j, k) = f_a sum over its rows T[i][j] S[i][k]: a CTA has 32 columns and 16 of the j of one adapter, its
+// eight warps every eighth row, four at a time.  Both stacks in one launch; zeros for an adapter without rows.
+struct F32Reduce {
+  MultiPlan p;
+  int r;
+  int64_t K[2];                   // columns of S: dA (out [r, K]) and dB (out [K, r], times s_a)
+  const float *S[2], *T[2];
+  float* out[2];
+  float one;
+  const float* each;
+  int blocks0;                    // column blocks of the first
+};
+
+__global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__ F32Reduce a) {
+  __shared__ float red[8][16][33];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int which = (int)blockIdx.x >= a.blocks0, ad = blockIdx.y, j0 = blockIdx.z * 16;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = a.r;
+  const int64_t K = a.K[which], k0 = (int64_t)((int)blockIdx.x - (which ? a.blocks0 : 0)) * 32, k = k0 + lane;
+  const float *S = a.S[which], *T = a.T[which];
+  const int first = a.p.start[ad], last = a.p.start[ad + 1];
+  float acc[16] = {};
+  for (int i0 = first + warp; i0 < last; i0 += 32) {
+    int64_t row[4];
+    float x[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q] = i0 + 8 * q < last ? a.p.order[i0 + 8 * q] : -1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[q] = row[q] >= 0 && k < K ? __ldg(S + row[q] * K + k) : 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (row[q] >= 0) {
+        const float* t = T + row[q] * r + j0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j0 + j < r) acc[j] = fmaf(__ldg(t + j), x[q], acc[j]);
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) red[warp][j][lane] = acc[j];
+  __syncthreads();
+  const float f = which ? scale_of(a.one, a.each, ad) : 1.f;
+  float* out = a.out[which] + (int64_t)ad * r * K;
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    // neighbouring threads write neighbouring elements: columns of dA, j of dB
+    const int c = which ? i >> 4 : i & 31, j = which ? i & 15 : i >> 5;
+    if (k0 + c >= K || j0 + j >= r) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += red[w][j][c];
+    out[which ? (k0 + c) * r + j0 + j : (int64_t)(j0 + j) * K + k0 + c] = s * f;
+  }
+}
+
+// sums of all rows, 32 columns a CTA, a warp every eighth row
+__global__ void __launch_bounds__(256) f32_colsum_kernel(int64_t M, int64_t K, const float* S, float* out) {
+  __shared__ float red[8][32];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t k = (int64_t)blockIdx.x * 32 + lane;
+  float total = 0.f;
+  for (int64_t m0 = warp; m0 < M; m0 += 8 * 256) {
+    float t = 0.f;
+#pragma unroll 8
+    for (int64_t m = m0; m < min(M, m0 + 8 * 256); m += 8)
+      if (k < K) t += __ldg(S + m * K + k);
+    total += t;
+  }
+  red[warp][lane] = total;
+  __syncthreads();
+  if (warp == 0 && k < K) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += red[w][lane];
+    out[k] = t;
+  }
+}
+
+unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+
+template <bool MN>
+cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
+  const int64_t tiles = (int64_t)blocks(a.N, kTile) * blocks(a.p.M, kTile), slabs = blocks(a.K, kSlab), sms = num_sms_current();
+  // the share of K that finishes soonest: whole rounds of a CTA an SM, and what a cluster costs
+  int ranks = 1;
+  double best = 0;
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > 1 && slabs < 8 * s) break;
+    const double t = (double)((tiles * s + sms - 1) / sms) / s + 0.04 * (s - 1);
+    if (s == 1 || t < best) best = t, ranks = s;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(tiles * ranks), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f32_gemm_kernel<MN>, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t multi_f32_proj(const MultiPlan& p, int64_t K, int r, const float* S, const float* U, bool kr, float one,
+                           const float* each, float* plain, float* scaled, cudaStream_t st) {
+  const F32Proj a{p, K, r, S, U, one, each, plain, scaled};
+  const int64_t n = multi_items(p.M, p.n) * (kItemRows / kRows);
+  const dim3 grid((unsigned)(n > 0 ? n : 1));
+  return kr ? launch_pdl(f32_proj_kernel<true>, grid, dim3(256), 0, st, a)
+            : launch_pdl(f32_proj_kernel<false>, grid, dim3(256), 0, st, a);
+}
+
+cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, const float* S, const float* W, bool mn,
+                           const float* P, const float* U, const float* bias, bool scaled, float one, const float* each,
+                           float* out, cudaStream_t st) {
+  const F32Gemm a{p, N, K, r, S, W, P, U, bias, one, each, scaled, out};
+  return mn ? gemm<true>(a, st) : gemm<false>(a, st);
+}
+
+cudaError_t multi_f32_reduce(const MultiPlan& p, int r, int64_t in, const float* X, const float* G, float* dA, int64_t out,
+                             const float* dY, const float* Z, float* dB, float one, const float* each, cudaStream_t st) {
+  const int b0 = (int)blocks(in, 32);
+  const F32Reduce a{p, r, {in, out}, {X, dY}, {G, Z}, {dA, dB}, one, each, b0};
+  return launch_pdl(f32_reduce_kernel, dim3(b0 + blocks(out, 32), (unsigned)p.n, blocks(r, 16)), dim3(256), 0, st, a);
+}
+
+cudaError_t multi_f32_colsum(int64_t M, int64_t K, const float* S, float* out, cudaStream_t st) {
+  return launch_pdl(f32_colsum_kernel, dim3(blocks(K, 32)), dim3(256), 0, st, M, K, S, out);
+}
+
+}  // namespace lg

@@ -1,0 +1,324 @@
+// The many-adapter forward of a few rows (a decode step), bf16.
+//
+// Y [M, N] = X W0^T + the rows' own updates, M small: every byte of W0 is read once, which bounds it.  So the
+// product is turned around: 128 rows of W0 are the M side of the tcgen05 MMA and the batch's rows its N side
+// (16, 32 or 64, zero-filled), and K is shared by the CTAs of a cluster, each with its own stretch of W0, so that
+// some 300 CTAs, two an SM, keep their copies in flight.  The partial accumulators meet through distributed
+// shared memory, in the order of the ranks.  The rank-r part is computed on the side:
+//   multi_few_down   z_i A_a^T in stretches of 512 columns, one CTA a row and stretch (its sums stay apart);
+//   multi_few        while W0 streams in, the epilogue warps add the stretches up and form s z B_a^T.
+// The second kernel starts while the first one runs (programmatic launch): it touches nothing that the first
+// one writes before its wait, and what came before the first one is complete when that lets it start.
+#include "common.cuh"
+#include "multi.h"
+#include "vec.cuh"
+
+namespace lg {
+
+namespace {
+
+constexpr int kStretch = 512;     // columns of x that one CTA of multi_few_down takes
+constexpr int kRowsW = 128, kBK = 64;
+constexpr int kThreads = 192;     // copies, MMA, four epilogue warps
+
+struct FewArgs {
+  CUtensorMap tmW, tmX;
+  int M, N, r, n, nk, stages, splits;
+  const int32_t* ids;
+  const bf16 *X, *A, *B, *bias;
+  float one;
+  const float* each;
+  float* part;                    // [splits, M, r] z by stretches
+  bf16 *Y, *Z;
+  int64_t K;
+  uint32_t* err;
+  uint64_t timeout_ns;
+};
+
+// part[stretch][i][j] = sum over the stretch of X[i][k] A_a[j][k]: a warp takes every fourth group of four j
+__global__ void __launch_bounds__(128) multi_few_down(const __grid_constant__ FewArgs a) {
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int i = blockIdx.x, split = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ad = a.ids[i], r = a.r;
+  float* out = a.part + ((int64_t)split * a.M + i) * r;
+  if (ad < 0) {
+    for (int j = threadIdx.x; j < r; j += 128) out[j] = 0.f;
+    return;
+  }
+  const bf16* u = a.A + (int64_t)ad * r * a.K;
+  int64_t k[2];
+  bool on[2];
+  F2 x[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    k[h] = (int64_t)split * kStretch + h * 256 + lane * 8;
+    on[h] = k[h] < a.K;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) x[h][q] = f2(0.f);
+    if (on[h]) load4x2(a.X + i * a.K + k[h], x[h]);
+  }
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  for (int j0 = warp * 4; j0 < r; j0 += 16) {
+    Raw8<bf16> w[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[j][h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(u + (int64_t)(j0 + j) * a.K + k[h])) : none;
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      F2 t = f2(0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        F2 f[4];
+        w[j][h].get(f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (on[h]) t = fma2(f[q], x[h][q], t);
+      }
+      s[j] = sum2(t);
+    }
+    const float t = warp_sums_of<4>(s);
+    if (lane % 8 == 0) out[j0 + lane / 8] = t;
+  }
+}
+
+template <int T>
+struct Few {
+  static constexpr int STAGE = kRowsW * 128 + T * 128;
+  static constexpr int PITCH = kRowsW + 4;                          // floats of a row of partial outputs
+  static constexpr int OUT = T * PITCH * 4;
+  static constexpr int COLS = T < 32 ? 32 : T;                      // TMEM columns
+};
+// shared memory: the ring (later the partial outputs), the update [T, 128 / ranks], s z [T, r], barriers
+template <int T>
+__host__ __device__ constexpr int few_ring(int stages) {
+  return stages * Few<T>::STAGE > Few<T>::OUT ? stages * Few<T>::STAGE : Few<T>::OUT;
+}
+template <int T>
+__host__ __device__ constexpr int few_smem(int stages, int ranks, int r) {
+  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + T * r * 4 + 8 * (2 * stages + 2) + 32;
+}
+
+template <int T>
+__global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ FewArgs a) {
+  using F = Few<T>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int own = kRowsW / (int)ranks;                              // output columns that this CTA finishes
+  float* update = reinterpret_cast<float*>(smem + few_ring<T>(a.stages));   // [T, own]
+  float* sz = update + T * own;                                     // [T, r]
+  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(sz + T * a.r) + 7) & ~uintptr_t(7));
+  uint64_t* empty = full + a.stages;
+  uint64_t* done = empty + a.stages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = (int)(blockIdx.x / ranks) * kRowsW, m0 = (int)blockIdx.y * T;
+  const int rows = min(T, a.M - m0);
+  const int k0 = (int)((int64_t)a.nk * rank / ranks), k1 = (int)((int64_t)a.nk * (rank + 1) / ranks);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, F::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  if (threadIdx.x == 0) pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&a.tmW);
+      tma_prefetch_desc(&a.tmX);
+      bool ok = true;
+      int last = 0;
+      for (int ks = k0; ks < k1; ++ks) {
+        const int i = ks - k0, s = i % a.stages;
+        if (i >= a.stages && !mbar_wait(&empty[s], (uint32_t)(i / a.stages + 1) & 1, a.timeout_ns, abort_flag, a.err, 0x401)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * F::STAGE;
+        mbar_expect_tx(&full[s], F::STAGE);
+        tma_load_2d(st, &a.tmW, &full[s], ks * kBK, n0);
+        tma_load_2d(st + kRowsW * 128, &a.tmX, &full[s], ks * kBK, m0);
+        last = i + 1;
+      }
+      if (!ok)                  // unwind: what is on its way lands before the CTA goes on
+        for (int i = last > a.stages ? last - a.stages : 0; i < last; ++i)
+          mbar_wait_drain(&full[i % a.stages], (uint32_t)(i / a.stages) & 1, 20000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = umma_idesc_bf16(kRowsW, T, 0, 0);
+      for (int ks = k0; ks < k1; ++ks) {
+        const int i = ks - k0, s = i % a.stages;
+        if (!mbar_wait(&full[s], (uint32_t)(i / a.stages) & 1, a.timeout_ns, abort_flag, a.err, 0x402)) break;
+        tc_fence_after();
+        const uint32_t w = smem_u32(smem + s * F::STAGE), x = w + kRowsW * 128;
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          umma_bf16(tmem, umma_smem_desc(w + kk * 32, 16, 1024), umma_smem_desc(x + kk * 32, 16, 1024), idesc,
+                    (i > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[s]);
+      }
+      umma_commit(done);
+      mbar_wait_drain(done, 0, 20000000ull);
+    }
+    __syncwarp();
+  } else {
+    // the update of this CTA's own columns, while W0 streams in
+    const int e = threadIdx.x - 64;
+    pdl_wait();
+    for (int i = e; i < rows * a.r; i += 128) {
+      const int t = i / a.r, j = i % a.r, row = m0 + t;
+      float z = 0.f;
+      for (int s = 0; s < a.splits; ++s) z += __ldcg(a.part + ((int64_t)s * a.M + row) * a.r + j);
+      if (a.Z && blockIdx.x == 0) a.Z[(int64_t)row * a.r + j] = __float2bfloat16_rn(z);
+      const int ad = __ldg(a.ids + row);
+      sz[i] = ad < 0 ? 0.f : z * (a.each ? __ldg(a.each + ad) : a.one);
+    }
+    named_bar_sync(1, 128);
+    const int f = e % own, c = n0 + (int)rank * own + f;
+    const float b = a.bias && c < a.N ? __bfloat162float(a.bias[c]) : 0.f;
+    for (int t = e / own; t < rows; t += 128 / own) {
+      const int ad = __ldg(a.ids + m0 + t);
+      float v = b;
+      if (ad >= 0 && c < a.N) {
+        const bf16* u = a.B + ((int64_t)ad * a.N + c) * a.r;
+        for (int j = 0; j < a.r; j += 8) {
+          float w[8];
+          load8(u + j, w);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v = fmaf(w[q], sz[t * a.r + j + q], v);
+        }
+      }
+      update[t * own + f] = v;
+    }
+    // the accumulator, once every MMA is done: the ring is free then
+    const int q = warp & 3;
+    const bool ok = mbar_wait(done, 0, a.timeout_ns, abort_flag, a.err, 0x403);
+    tc_fence_after();
+    float* out = reinterpret_cast<float*>(smem);
+    if (__all_sync(0xffffffffu, ok)) {
+#pragma unroll
+      for (int c0 = 0; c0 < T; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + ((uint32_t)(32 * q) << 16) + c0, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) out[(c0 + i) * F::PITCH + 32 * q + lane] = __uint_as_float(v[i]);
+      }
+    }
+    tc_fence_before();
+  }
+  cluster_sync_all();
+  tc_fence_after();
+  // this CTA's columns: the ranks' partial sums in their order, and the update
+  const uint32_t mine = smem_u32(smem);
+  const int pairs = own / 2;
+  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+    const int t = i / pairs, f = i % pairs * 2, c = n0 + (int)rank * own + f;
+    float v0 = 0.f, v1 = 0.f;
+    for (uint32_t s = 0; s < ranks; ++s) {
+      float p0, p1;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(p0), "=f"(p1)
+                   : "r"(mapa_shared(mine + (t * F::PITCH + (int)rank * own + f) * 4, s)));
+      v0 += p0;
+      v1 += p1;
+    }
+    if (c < a.N)
+      *reinterpret_cast<uint32_t*>(a.Y + (int64_t)(m0 + t) * a.N + c) =
+          pack_bf16x2(v0 + update[t * own + f], v1 + update[t * own + f + 1]);
+  }
+  cluster_sync_all();           // no CTA leaves while another reads its sums
+  if (warp == 1) tmem_dealloc(tmem, F::COLS);
+}
+
+template <int T>
+cudaError_t few_launch(FewArgs& a, cudaStream_t st) {
+  constexpr int kMost = 200 * 1024;
+  const int tiles = (a.N + kRowsW - 1) / kRowsW, groups = (a.M + T - 1) / T;
+  const int slots = 2 * num_sms_current();
+  int ranks = 1;
+  while (ranks < 8 && tiles * groups * ranks * 2 <= slots && a.nk >= ranks * 2 * 2) ranks *= 2;
+  // two CTAs an SM where their rings are at least four stages deep so
+  int stages = 12;
+  const int each = a.nk / ranks + (a.nk % ranks != 0);
+  if (stages > each) stages = each;
+  while (stages > 4 && few_smem<T>(stages, ranks, a.r) > 112 * 1024) --stages;
+  while (stages > 2 && few_smem<T>(stages, ranks, a.r) > kMost) --stages;
+  a.stages = stages;
+  const cudaError_t e = allow_smem<multi_few<T>>(kMost);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(tiles * ranks, groups, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = few_smem<T>(stages, ranks, a.r);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, multi_few<T>, a);
+  count_launch();
+  return l != cudaSuccess ? l : cudaGetLastError();
+}
+
+}  // namespace
+
+int multi_few_splits(int64_t K) { return (int)((K + kStretch - 1) / kStretch); }
+
+cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64_t n, const bf16* X, const bf16* W0,
+                          const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* part,
+                          bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st) {
+  FewArgs a;
+  memset(&a, 0, sizeof(a));
+  a.M = (int)p.M;
+  a.N = (int)N;
+  a.r = r;
+  a.n = (int)n;
+  a.K = K;
+  a.nk = (int)((K + kBK - 1) / kBK);
+  a.splits = multi_few_splits(K);
+  a.ids = p.ids;
+  a.X = X;
+  a.A = A;
+  a.B = B;
+  a.bias = bias;
+  a.one = one;
+  a.each = each;
+  a.part = part;
+  a.Y = Y;
+  a.Z = Z;
+  a.err = err;
+  a.timeout_ns = timeout_ns;
+  const int T = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
+  if (!make_tmap_bf16(&a.tmW, W0, K, N, K, kBK, kRowsW, 128) || !make_tmap_bf16(&a.tmX, X, K, p.M, K, kBK, T, 128))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = launch_pdl(multi_few_down, dim3((unsigned)a.M, (unsigned)a.splits), dim3(128), 0, st, a);
+  if (e != cudaSuccess) return e;
+  return T == 16 ? few_launch<16>(a, st) : T == 32 ? few_launch<32>(a, st) : few_launch<64>(a, st);
+}
+
+}  // namespace lg

@@ -199,9 +199,11 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  if ((int)blockIdx.y >= a.p.head[kHeadPieces]) return;
-  const int4 piece = a.p.pieces[blockIdx.y];
-  const int64_t k0 = (int64_t)blockIdx.x * 128, K = a.K;
+  const int64_t K = a.K;
+  const int groups = (int)((K + 127) / 128), mine = (int)blockIdx.x / groups;
+  if (mine >= a.p.head[kHeadPieces]) return;
+  const int4 piece = a.p.pieces[mine];
+  const int64_t k0 = (int64_t)((int)blockIdx.x - mine * groups) * 128;
   const int32_t* order = a.p.order + piece.y;
   const int stages = (piece.z + 31) / 32;
   auto load = [&](int s) {
@@ -359,7 +361,7 @@ cudaError_t reduce_launch(const ReduceArgs& a, int64_t pieces, cudaStream_t st) 
   using C = Reduce<R>;
   const cudaError_t e = allow_smem<multi_reduce_mma<R>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_reduce_mma<R>, dim3((unsigned)((a.K + 127) / 128), (unsigned)pieces), dim3(128), C::SMEM, st, a);
+  return launch_pdl(multi_reduce_mma<R>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::SMEM, st, a);
 }
 
 }  // namespace

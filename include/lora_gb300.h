@@ -612,7 +612,8 @@ lora_status adamw_step(const lora_adamw_tensor* tensors, const void* const* grad
  * gradients.  A row is formed from its own adapter alone: what is not finite in another adapter or in
  * another row does not reach it.
  *   A [n, r, d_in], B [n, d_out, r]: stacks; an adapter of lower rank has zeros in its last rows of A and
- *   columns of B.  1 <= n <= 65535, M <= 2^24, d_in, d_out and r as above (LORA_BF16: r a multiple of 8).
+ *   columns of B.  1 <= n <= 65535, M <= 2^24, d_in and d_out at most 2^20 and, like r, as above
+ *   (LORA_BF16: r a multiple of 8).
  *   s_each: device fp32 [n], read when the call runs, or NULL: s for all. */
 typedef struct {
     int64_t M, d_in, d_out, r, n;
