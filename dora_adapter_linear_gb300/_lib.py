@@ -202,7 +202,7 @@ def host():
         spec.loader.exec_module(module)
         module.bind(*[ctypes.cast(getattr(lib, name), c_void_p).value
                       for name in ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd",
-                                   "grad_clip_workspace_bytes", "grad_clip")])
+                                   "grad_clip_workspace_bytes", "grad_clip", "lora_multi_fwd", "lora_multi_bwd")])
         _HOST = module
     return _HOST
 

@@ -27,6 +27,8 @@ decltype(&rotary_fwd) rotary_fwd_call = nullptr;
 decltype(&rotary_bwd) rotary_bwd_call = nullptr;
 decltype(&grad_clip_workspace_bytes) clip_bytes_call = nullptr;
 decltype(&grad_clip) clip_call = nullptr;
+decltype(&lora_multi_fwd) multi_fwd_call = nullptr;
+decltype(&lora_multi_bwd) multi_bwd_call = nullptr;
 
 // a tensor argument: absent (None), a tensor, or something else
 struct Arg {
@@ -295,6 +297,95 @@ PyObject* py_pair(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The operands that both many-adapter calls share; false: not for here.
+struct Multi {
+  lora_multi_shape sh;
+  float s = 0.f;
+  const float* each = nullptr;
+  // X, W0, A, B, s, plan, its rows, its adapters, workspace
+  bool take(const Arg& X, const Arg& W0, const Arg& A, const Arg& B, PyObject* scale, const Arg& plan, PyObject* rows,
+            PyObject* adapters, const Arg& ws) {
+    if (!X || !W0 || !A || !B || !plan || !ws) return false;
+    const Tensor& x = *X;
+    if (!here(x) || dtype_of(x) < 0 || x.dim() != 2 || (*W0).dim() != 2 || (*A).dim() != 3) return false;
+    const int64_t M = x.size(0), in = x.size(1), out = (*W0).size(0), n = (*A).size(0), r = (*A).size(1);
+    if (M < 1 || !same(X, x, {M, in}) || !same(W0, x, {out, in}) || !same(A, x, {n, r, in}) || !same(B, x, {n, out, r}))
+      return false;
+    if (PyLong_AsLongLong(rows) != M || PyLong_AsLongLong(adapters) != n || (*plan).device() != x.device()) {
+      PyErr_Clear();
+      return false;
+    }
+    if (THPVariable_Check(scale)) {
+      const Tensor& t = THPVariable_Unpack(scale);
+      if (!dense(t, x, at::kFloat, {n})) return false;
+      each = static_cast<const float*>(t.data_ptr());
+    } else {
+      const double v = PyFloat_AsDouble(scale);
+      if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return false;
+      }
+      s = (float)v;
+    }
+    sh = lora_multi_shape{M, in, out, r, n, dtype_of(x)};
+    return true;
+  }
+  static bool same(const Arg& t, const Tensor& x, at::IntArrayRef sizes) {
+    return dense(*t, x, x.scalar_type(), sizes);
+  }
+};
+
+// (X, W0, A, B, s, plan, its rows, its adapters, bias, save_z, workspace)
+PyObject* py_multi_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 11) return not_here();
+  const Arg X(a[0]), W0(a[1]), A(a[2]), B(a[3]), plan(a[5]), bias(a[8]), ws(a[10]);
+  Multi m;
+  bool save;
+  if (!truth(a[9], &save)) return nullptr;
+  if (!bias.ok || !m.take(X, W0, A, B, a[4], plan, a[6], a[7], ws)) return not_here();
+  if (bias && !Multi::same(bias, *X, {m.sh.d_out})) return not_here();
+  Tensor Y, Z;
+  int e;
+  {
+    const Unlocked unlocked;
+    Y = fresh(*X, {m.sh.M, m.sh.d_out});
+    if (save) Z = fresh(*X, {m.sh.M, m.sh.r});
+    e = multi_fwd_call(&m.sh, X.ptr(), W0.ptr(), A.ptr(), B.ptr(), bias.ptr(), m.s, m.each, plan.ptr(), Y.data_ptr(),
+                       save ? Z.data_ptr() : nullptr, ws.ptr(), (*ws).nbytes(), stream());
+  }
+  if (e != LORA_OK) return PyLong_FromLong(e);
+  return tuple_of(Y, Z);
+  END_HANDLE_TH_ERRORS
+}
+
+// (X, W0, A, B, Z, dY, s, plan, its rows, its adapters, need_dx, need_dbias, workspace)
+PyObject* py_multi_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 13) return not_here();
+  const Arg X(a[0]), W0(a[1]), A(a[2]), B(a[3]), Z(a[4]), dY(a[5]), plan(a[7]), ws(a[12]);
+  Multi m;
+  bool need_dx, need_db;
+  if (!truth(a[10], &need_dx) || !truth(a[11], &need_db)) return nullptr;
+  if (!Z.ok || !dY || !m.take(X, W0, A, B, a[6], plan, a[8], a[9], ws)) return not_here();
+  if ((Z && !Multi::same(Z, *X, {m.sh.M, m.sh.r})) || !Multi::same(dY, *X, {m.sh.M, m.sh.d_out})) return not_here();
+  Tensor dX, dA, dB, db;
+  int e;
+  {
+    const Unlocked unlocked;
+    if (need_dx) dX = fresh(*X, {m.sh.M, m.sh.d_in});
+    dA = fresh(*X, {m.sh.n, m.sh.r, m.sh.d_in});
+    dB = fresh(*X, {m.sh.n, m.sh.d_out, m.sh.r});
+    if (need_db) db = fresh(*X, {m.sh.d_out});
+    const auto p = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    e = multi_bwd_call(&m.sh, X.ptr(), W0.ptr(), A.ptr(), B.ptr(), Z.ptr(), dY.ptr(), m.s, m.each, plan.ptr(), p(dX), p(dA),
+                       p(dB), p(db), ws.ptr(), (*ws).nbytes(), stream());
+  }
+  if (e != LORA_OK) return PyLong_FromLong(e);
+  return tuple_of(dX, dA, dB, db);
+  END_HANDLE_TH_ERRORS
+}
+
 // (gradients, groups, count, max_norm): the norms of optim.clip_grads, or a status.  groups: a list with the
 // group of each gradient, or None: each is a stack of `count` groups.
 PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -346,15 +437,15 @@ PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd, grad_clip_workspace_bytes, grad_clip): addresses in the
-// loaded library
+// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd, grad_clip_workspace_bytes, grad_clip, lora_multi_fwd,
+// lora_multi_bwd): addresses in the loaded library
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* at[6];
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "six addresses");
+  void* at[8];
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "eight addresses");
     return nullptr;
   }
-  for (int i = 0; i < 6; ++i)
+  for (int i = 0; i < 8; ++i)
     if (!(at[i] = PyLong_AsVoidPtr(a[i]))) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is zero");
       return nullptr;
@@ -365,6 +456,8 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   rotary_bwd_call = reinterpret_cast<decltype(rotary_bwd_call)>(at[3]);
   clip_bytes_call = reinterpret_cast<decltype(clip_bytes_call)>(at[4]);
   clip_call = reinterpret_cast<decltype(clip_call)>(at[5]);
+  multi_fwd_call = reinterpret_cast<decltype(multi_fwd_call)>(at[6]);
+  multi_bwd_call = reinterpret_cast<decltype(multi_bwd_call)>(at[7]);
   Py_RETURN_NONE;
 }
 
@@ -373,6 +466,8 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), "take the library's entry point
                          {"block_norm_fwd", FAST(py_norm_fwd), "ops.block_norm_fwd"},
                          {"block_norm_bwd", FAST(py_norm_bwd), "ops.block_norm_bwd"},
                          {"rotary", FAST(py_rotary), "ops.rotary_fwd and rotary_bwd"},
+                         {"multi_fwd", FAST(py_multi_fwd), "ops.lora_multi_fwd"},
+                         {"multi_bwd", FAST(py_multi_bwd), "ops.lora_multi_bwd"},
                          {"clip_grads", FAST(py_clip_grads), "optim.clip_grads"},
                          {"pair", FAST(py_pair), "an optimiser's norm and factor"},
                          {"pointers", FAST(py_pointers), "addresses of an optimiser's gradients"},

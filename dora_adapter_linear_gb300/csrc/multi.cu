@@ -24,6 +24,7 @@ struct Scale {          // s_a: one number, or one for each adapter
 struct MultiWs {
   uint32_t* err;
   void* P;                    // [M, r] z or s g; bf16: s z or s g
+  void* P2;                   // bf16 backward: what the rounding of s g leaves
   void* Z;                    // [M, r] z recomputed by the backward
   float* few;                 // forward of a few bf16 rows: z by stretches of K
   float *pa, *pb, *csum;      // bf16 backward: partials of dA and dB, column sums
@@ -35,6 +36,7 @@ size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   w->err = c.take<uint32_t>(kErrBytes / 4);
   w->P = c.take<char>(rank);
   w->Z = bwd ? c.take<char>(rank) : nullptr;
+  w->P2 = bwd && bf ? c.take<char>(rank) : nullptr;
   w->few = !bwd && bf && sh.M <= kFewRows ? c.take<float>((size_t)multi_few_splits(sh.d_in) * sh.M * sh.r) : nullptr;
   w->pa = bwd && bf ? c.take<float>(parts * sh.d_in) : nullptr;
   w->pb = bwd && bf ? c.take<float>(parts * sh.d_out) : nullptr;
@@ -108,7 +110,7 @@ cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiW
     return multi_few_fwd(p, sh.d_out, sh.d_in, r, sh.n, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
                          wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);
-  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, st);
+  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, st);
   if (e != cudaSuccess) return e;
   return tc_gemm(gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err), st);
 }
@@ -120,14 +122,18 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
   bf16* G = static_cast<bf16*>(w.P);
   cudaError_t e;
   if (!Z) {
-    if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, st)) != cudaSuccess) return e;
+    if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, nullptr, st)) != cudaSuccess)
+      return e;
     Z = static_cast<const bf16*>(w.Z);
   }
-  if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, st)) != cudaSuccess) return e;
+  // s g enters dX rounded, like s z the output; as a factor of dA it comes with the rest of its rounding, which would
+  // otherwise add as much to dA's error as dA's own rounding
+  bf16* rest = static_cast<bf16*>(w.P2);
+  if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, st)) != cudaSuccess) return e;
   if (dX && (e = tc_gemm(gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err), st)) != cudaSuccess)
     return e;
-  if ((e = multi_reduce(p, sh.d_in, r, X, G, false, false, 1.f, nullptr, w.pa, dA, st)) != cudaSuccess) return e;
-  if ((e = multi_reduce(p, sh.d_out, r, dY, Z, true, true, s.one, s.each, w.pb, dB, st)) != cudaSuccess) return e;
+  if ((e = multi_reduce(p, sh.d_in, r, X, G, rest, false, false, 1.f, nullptr, w.pa, dA, st)) != cudaSuccess) return e;
+  if ((e = multi_reduce(p, sh.d_out, r, dY, Z, nullptr, true, true, s.one, s.each, w.pb, dB, st)) != cudaSuccess) return e;
   if ((e = multi_sum(p, sh.r * sh.d_in, w.pa, dA, sh.r * sh.d_out, w.pb, dB, st)) != cudaSuccess || !dbias) return e;
   return multi_colsum(sh.M, sh.d_out, dY, w.csum, dbias, st);
 }

@@ -5,7 +5,7 @@
 
 namespace lg {
 
-constexpr int kItemRows = 32;     // rows of an item: consecutive rows of one adapter in the plan's order
+constexpr int kItemRows = 64;     // rows of an item: consecutive rows of one adapter in the plan's order
 constexpr int kPieceRows = 512;   // rows of a piece, the share of one adapter's gradients that is summed at once
 constexpr int kTileRows = 256;    // rows of a tile, whose adapters and row masks the GEMMs take
 
@@ -57,13 +57,14 @@ inline size_t multi_plan_layout(int64_t M, int64_t n, char* base, MultiPlan* p) 
 cudaError_t multi_plan(const MultiPlan& p, const void* ids, int id_bits, cudaStream_t st);
 
 // bf16 rank-r passes (multi_rank.cu); s_a is each[a], or `one` when each is null.
-// T_i = S_i U_a^T (U_a [r, K], or kr: [K, r]): plain = T, scaled = s_a T, [M, r], either may be null.  Rows without
-// adapter: zeros in plain, nothing in scaled.
+// T_i = S_i U_a^T (U_a [r, K], or kr: [K, r]): plain = T, scaled = s_a T, rest = what scaled's rounding left of s_a T,
+// [M, r], each may be null.  Rows without adapter: zeros in plain, nothing in the others.
 cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
-                       const float* each, bf16* plain, bf16* scaled, cudaStream_t st);
-// out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; adapters with
+                       const float* each, bf16* plain, bf16* scaled, bf16* rest, cudaStream_t st);
+// out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; T + T2 where T2 is
+// given; adapters with
 // several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero
-cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, bool kr, bool scaled,
+cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr, bool scaled,
                          float one, const float* each, float* part, bf16* out, cudaStream_t st);
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
                       bf16* out1, cudaStream_t st);

@@ -1,7 +1,7 @@
 // The many-adapter projection in fp32: FMA tiles, no reduced-precision tensor math, as everywhere here for fp32.
 //
-// Sums over long axes are taken in stretches of at most 256 products (or one share of a warp or CTA) that are
-// added up afterwards: their rounding grows with the stretch and not with the whole length.
+// Sums over long axes are taken in shares (of groups of warps, and of the CTAs of a cluster) that are added up
+// afterwards: their rounding grows with the share and not with the whole length.
 #include "common.cuh"
 #include "multi.h"
 #include "vec.cuh"
@@ -16,7 +16,7 @@ __device__ __forceinline__ float scale_of(float one, const float* each, int a) {
 // A CTA has eight rows of an item and all j of their adapter; the rows pass through shared memory 1024 columns
 // at a time, so a factor is read once for eight rows.  Up to eight warps take the j of U_a [r, K] in turn; of
 // U_a [K, r] (KR) a thread keeps one j, and the threads' shares of k meet in shared memory.
-constexpr int kCols = 1024, kRows = 8;
+constexpr int kCols = 1024, kRows = 8;   // kItemRows is a multiple of kRows
 
 struct F32Proj {
   MultiPlan p;
@@ -34,14 +34,14 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
   __shared__ float sum[kRows][128];
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const int r = a.r, with = a.p.head[kHeadRows];
+  const int4 item = a.p.items[blockIdx.x / (kItemRows / kRows)];   // there is room for as many as the grid has
+  const int r = a.r, with = a.p.head[kHeadRows], items = a.p.head[kHeadItems];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.p.M - with) * r; i += (int64_t)gridDim.x * 256) {
     const int64_t at = (int64_t)a.p.order[with + i / r] * r + i % r;     // rows without adapter
     if (a.plain) a.plain[at] = 0.f;
     if (a.scaled) a.scaled[at] = 0.f;
   }
-  if ((int)blockIdx.x / (kItemRows / kRows) >= a.p.head[kHeadItems]) return;
-  const int4 item = a.p.items[blockIdx.x / (kItemRows / kRows)];
+  if ((int)blockIdx.x / (kItemRows / kRows) >= items) return;
   const int first = (int)blockIdx.x % (kItemRows / kRows) * kRows, rows = min(kRows, item.z - first);
   if (rows <= 0) return;
   const int32_t* order = a.p.order + item.y + first;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
       const int shares = 256 / r, j = threadIdx.x % r, k = threadIdx.x / r;
       float t[kRows] = {};
       if (k < shares) {
-#pragma unroll 4
+#pragma unroll 8
         for (int c = k; c < cols; c += shares) {
           const float b = __ldg(u + (k0 + c) * r + j);
 #pragma unroll
@@ -109,10 +109,12 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
 }
 
 // ------------------------------------------------------------------ shared product and rank-r update
-// 64 x 64 outputs a CTA, 4 x 4 a thread, K in slabs of 16 through two buffers; the CTAs of a cluster share K and add
-// their sums through distributed shared memory, each finishing its share of the rows.  There a thread has one
-// column, and takes its adapter's factor anew only where the next row has another one.
-constexpr int kTile = 64, kSlab = 16;
+// 64 x 64 outputs a CTA, 8 x 8 a thread (four shared-memory accesses for 64 FMAs; with 4 x 4 the accesses took as long
+// as the FMAs), K in slabs of 32 through two buffers, of which each of four groups of two warps takes eight.  The
+// CTAs of a cluster share K and add their sums through distributed shared memory, each finishing its share of
+// the rows.  There a thread has one column, and takes its adapter's factor anew only where the next row has
+// another one.
+constexpr int kTile = 64, kSlab = 32, kGroups = 4;
 
 struct F32Gemm {
   MultiPlan p;
@@ -126,43 +128,55 @@ struct F32Gemm {
 };
 
 template <bool MN>
-__global__ void __launch_bounds__(256) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
+__global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
   __shared__ float As[2][kSlab][kTile + 4];
   __shared__ float Bs[2][kSlab][kTile + 4];
-  __shared__ float part[kTile][kTile + 4];
-  __shared__ float ps[kTile][8];
+  float (*part)[kTile + 4] = As[0];                   // the sums, once the slabs are done
   __shared__ int ids[kTile];
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int tid = threadIdx.x, group = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;   // rows 4 ty, 4 ty + 32 and on
   const int64_t K = a.K, N = a.N;
   const int tile = (int)(blockIdx.x / ranks), wide = (int)((N + kTile - 1) / kTile);
   const int64_t m0 = (int64_t)(tile / wide) * kTile, n0 = (int64_t)(tile % wide) * kTile;
   const int slabs = (int)((K + kSlab - 1) / kSlab), s0 = (int)((int64_t)slabs * rank / ranks),
             s1 = (int)((int64_t)slabs * (rank + 1) / ranks);
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int lr = threadIdx.x >> 2, lk = (threadIdx.x & 3) * 4;   // a row and four k of a K-major operand
-  const int bk = threadIdx.x >> 4, bc = (threadIdx.x & 15) * 4;  // a k and four columns of W [K, N]
-  auto fetch = [&](int s, float4& x, float4& w) {
-    const int64_t k = (int64_t)s * kSlab + lk;
-    x = s < s1 && m0 + lr < a.p.M && k < K ? __ldg(reinterpret_cast<const float4*>(a.S + (m0 + lr) * K + k)) : none;
-    if (MN) {
-      const int64_t kk = (int64_t)s * kSlab + bk;
-      w = s < s1 && kk < K && n0 + bc < N ? __ldg(reinterpret_cast<const float4*>(a.W + kk * N + n0 + bc)) : none;
-    } else {
-      w = s < s1 && n0 + lr < N && k < K ? __ldg(reinterpret_cast<const float4*>(a.W + (n0 + lr) * K + k)) : none;
+  // a thread brings four k, and four 16 behind them, of one row of a K-major operand; of W [K, N] four columns of two k
+  const int lr = tid & 63, lk = (tid >> 6) * 4;
+  const bool row = m0 + lr < a.p.M, col = n0 + lr < N;
+  const float* S = a.S + (row ? m0 + lr : 0) * K;
+  const float* W = MN ? a.W : a.W + (col ? n0 + lr : 0) * K;
+  auto fetch = [&](int s, float4 (&x)[2], float4 (&w)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t k = (int64_t)s * kSlab + lk + 16 * i;
+      x[i] = s < s1 && row && k < K ? __ldg(reinterpret_cast<const float4*>(S + k)) : none;
+      if (MN) {
+        const int64_t kk = (int64_t)s * kSlab + (tid >> 4) + 16 * i, c = n0 + (tid & 15) * 4;
+        w[i] = s < s1 && kk < K && c < N ? __ldg(reinterpret_cast<const float4*>(W + kk * N + c)) : none;
+      } else {
+        w[i] = s < s1 && col && k < K ? __ldg(reinterpret_cast<const float4*>(W + k)) : none;
+      }
     }
   };
-  auto put = [&](int b, const float4& x, const float4& w) {
-    As[b][lk][lr] = x.x, As[b][lk + 1][lr] = x.y, As[b][lk + 2][lr] = x.z, As[b][lk + 3][lr] = x.w;
-    if (MN) *reinterpret_cast<float4*>(&Bs[b][bk][bc]) = w;
-    else Bs[b][lk][lr] = w.x, Bs[b][lk + 1][lr] = w.y, Bs[b][lk + 2][lr] = w.z, Bs[b][lk + 3][lr] = w.w;
+  auto put = [&](int b, const float4 (&x)[2], const float4 (&w)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) As[b][lk + 16 * i + j][lr] = p[j];
+      if (MN) *reinterpret_cast<float4*>(&Bs[b][(tid >> 4) + 16 * i][(tid & 15) * 4]) = w[i];
+      else
+#pragma unroll
+        for (int j = 0; j < 4; ++j) Bs[b][lk + 16 * i + j][lr] = q[j];
+    }
   };
-  float acc[4][4] = {}, run[4][4] = {};
-  float4 x, w;
+  float run[8][8] = {};
+  float4 x[2], w[2];
   fetch(s0, x, w);
   put(0, x, w);
   for (int s = s0; s < s1; ++s) {
@@ -170,48 +184,61 @@ __global__ void __launch_bounds__(256) f32_gemm_kernel(const __grid_constant__ F
     fetch(s + 1, x, w);
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kSlab; ++k) {
-      const float4 u = *reinterpret_cast<const float4*>(&As[b][k][ty * 4]), v = *reinterpret_cast<const float4*>(&Bs[b][k][tx * 4]);
-      const float p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+    for (int k = 0; k < kSlab / kGroups; ++k) {
+      float p[8], q[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int h = 0; h < 2; ++h) {
+        const float4 u = *reinterpret_cast<const float4*>(&As[b][group * 8 + k][32 * h + ty * 4]),
+                     v = *reinterpret_cast<const float4*>(&Bs[b][group * 8 + k][32 * h + tx * 4]);
+        p[4 * h] = u.x, p[4 * h + 1] = u.y, p[4 * h + 2] = u.z, p[4 * h + 3] = u.w;
+        q[4 * h] = v.x, q[4 * h + 1] = v.y, q[4 * h + 2] = v.z, q[4 * h + 3] = v.w;
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
     }
     put(b ^ 1, x, w);
-    if (((s - s0) & 15) == 15 || s + 1 == s1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += run[i][j], run[i][j] = 0.f;
-    }
   }
+  // the groups' sums one after another
+  for (int q = 0; q < kGroups; ++q) {
+    __syncthreads();
+    if (group == q)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(&part[ty * 4 + i][tx * 4]) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-  if (threadIdx.x < kTile) ids[threadIdx.x] = m0 + threadIdx.x < a.p.M ? a.p.ids[m0 + threadIdx.x] : -1;
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float4* at = reinterpret_cast<float4*>(&part[32 * (i >> 2) + ty * 4 + (i & 3)][32 * h + tx * 4]);
+          const float4 old = q == 0 ? none : *at;
+          *at = make_float4(old.x + run[i][4 * h], old.y + run[i][4 * h + 1], old.z + run[i][4 * h + 2],
+                            old.w + run[i][4 * h + 3]);
+        }
+  }
+  if (tid < kTile) ids[tid] = m0 + tid < a.p.M ? a.p.ids[m0 + tid] : -1;
   cluster_sync_all();
-  // column c, every fourth of this CTA's rows
-  const int c = threadIdx.x & 63, own = kTile / (int)ranks, r0 = (int)rank * own + (threadIdx.x >> 6);
+  // this thread's column of every fourth of this CTA's rows
+  const int own = kTile / (int)ranks, c = tid & 63, r0 = (int)rank * own + group, each = own / kGroups;
   const uint32_t mine = smem_u32(&part[0][0]);
+  float* ps = &Bs[0][0][0];                           // [64][8] P of eight j
+  const float bias = a.bias && n0 + c < N ? __ldg(a.bias + n0 + c) : 0.f;
   float v[16], t[16];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    v[i] = t[i] = 0.f;
-    if (4 * i < own)
-      for (uint32_t q = 0; q < ranks; ++q) {
+  for (int i = 0; i < 16; ++i) v[i] = t[i] = 0.f;
+  for (uint32_t q = 0; q < ranks; ++q) {
+    const uint32_t from = mapa_shared(mine + (r0 * (kTile + 4) + c) * 4, q);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < each) {
         float f;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(f)
-                     : "r"(mapa_shared(mine + ((r0 + 4 * i) * (kTile + 4) + c) * 4, q)));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(from + i * kGroups * (kTile + 4) * 4));
         v[i] += f;
       }
   }
   for (int j0 = 0; j0 < a.r; j0 += 8) {
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * 8; i += 256) {
-      const int m = i >> 3, j = j0 + (i & 7);
-      ps[m][i & 7] = ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
+    for (int i = tid; i < own * 8; i += 256) {
+      const int m = (int)rank * own + (i >> 3), j = j0 + (i & 7);
+      ps[m * 8 + (i & 7)] = ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
     }
     __syncthreads();
     if (n0 + c < N) {
@@ -219,34 +246,32 @@ __global__ void __launch_bounds__(256) f32_gemm_kernel(const __grid_constant__ F
       float u[8];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (4 * i >= own) break;
-        const int m = r0 + 4 * i, ad = ids[m];
+        if (i >= each) break;
+        const int m = r0 + kGroups * i, ad = ids[m];
         if (ad < 0) continue;
         if (ad != have) {
           have = ad;
-          const float* b = a.U + (int64_t)ad * a.r * N;
+          const float* f = a.U + (int64_t)ad * a.r * N;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            u[q] = j0 + q < a.r ? __ldg(MN ? b + (int64_t)(j0 + q) * N + n0 + c : b + (n0 + c) * a.r + j0 + q) : 0.f;
+            u[q] = j0 + q < a.r ? __ldg(MN ? f + (int64_t)(j0 + q) * N + n0 + c : f + (n0 + c) * a.r + j0 + q) : 0.f;
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (j0 + q < a.r) t[i] = fmaf(ps[m][q], u[q], t[i]);
+          if (j0 + q < a.r) t[i] = fmaf(ps[8 * m + q], u[q], t[i]);
       }
     }
   }
-  if (n0 + c < N) {
-    const float bias = a.bias ? __ldg(a.bias + n0 + c) : 0.f;
+  if (n0 + c < N)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int64_t m = m0 + r0 + 4 * i;
-      if (4 * i >= own || m >= a.p.M) break;
-      const int ad = ids[r0 + 4 * i];
+      const int m = r0 + kGroups * i;
+      if (i >= each || m0 + m >= a.p.M) break;
+      const int ad = ids[m];
       float y = v[i];
       if (ad >= 0) y += a.scaled ? scale_of(a.one, a.each, ad) * t[i] : t[i];
-      a.out[m * N + n0 + c] = y + bias;
+      a.out[(m0 + m) * N + n0 + c] = y + bias;
     }
-  }
   cluster_sync_all();           // no CTA leaves while another reads its sums
 }
 
@@ -340,7 +365,7 @@ cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
   int ranks = 1;
   double best = 0;
   for (int s = 1; s <= 8; s *= 2) {
-    if (s > 1 && slabs < 8 * s) break;
+    if (s > 1 && slabs < 4 * s) break;
     const double t = (double)((tiles * s + sms - 1) / sms) / s + 0.04 * (s - 1);
     if (s == 1 || t < best) best = t, ranks = s;
   }

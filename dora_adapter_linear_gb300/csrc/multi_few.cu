@@ -19,7 +19,8 @@ namespace {
 
 constexpr int kStretch = 512;     // columns of x that one CTA of multi_few_down takes
 constexpr int kRowsW = 128, kBK = 64;
-constexpr int kThreads = 192;     // copies, MMA, four epilogue warps
+constexpr int kUpdate = 256;       // threads of the update; four of their warps read the accumulator
+constexpr int kThreads = 64 + kUpdate;   // copies, MMA
 
 struct FewArgs {
   CUtensorMap tmW, tmX;
@@ -35,53 +36,58 @@ struct FewArgs {
   uint64_t timeout_ns;
 };
 
-// part[stretch][i][j] = sum over the stretch of X[i][k] A_a[j][k]: a warp takes every fourth group of four j
-__global__ void __launch_bounds__(128) multi_few_down(const __grid_constant__ FewArgs a) {
+// part[stretch][i][j] = sum over the stretch of X[i][k] A_a[j][k]: a warp takes every W-th group of J rows of A_a, all of
+// their loads on their way at once
+template <int J, int W>
+__global__ void __launch_bounds__(32 * W) multi_few_down(const __grid_constant__ FewArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   const int i = blockIdx.x, split = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ad = a.ids[i], r = a.r;
   float* out = a.part + ((int64_t)split * a.M + i) * r;
   if (ad < 0) {
-    for (int j = threadIdx.x; j < r; j += 128) out[j] = 0.f;
+    for (int j = threadIdx.x; j < r; j += 32 * W) out[j] = 0.f;
     return;
   }
   const bf16* u = a.A + (int64_t)ad * r * a.K;
+  const uint4 none = make_uint4(0, 0, 0, 0);
   int64_t k[2];
   bool on[2];
-  F2 x[2][4];
+  Raw8<bf16> x[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     k[h] = (int64_t)split * kStretch + h * 256 + lane * 8;
     on[h] = k[h] < a.K;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) x[h][q] = f2(0.f);
-    if (on[h]) load4x2(a.X + i * a.K + k[h], x[h]);
+    x[h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(a.X + i * a.K + k[h])) : none;
   }
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  for (int j0 = warp * 4; j0 < r; j0 += 16) {
-    Raw8<bf16> w[4][2];
+  for (int j0 = warp * J; j0 < r; j0 += W * J) {
+    Raw8<bf16> w[J][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         w[j][h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(u + (int64_t)(j0 + j) * a.K + k[h])) : none;
-    float s[4];
+    float s[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       F2 t = f2(0.f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        F2 f[4];
+        F2 f[4], g[4];
         w[j][h].get(f);
+        x[h].get(g);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (on[h]) t = fma2(f[q], x[h][q], t);
+        for (int q = 0; q < 4; ++q) t = fma2(f[q], g[q], t);
       }
       s[j] = sum2(t);
     }
-    const float t = warp_sums_of<4>(s);
-    if (lane % 8 == 0) out[j0 + lane / 8] = t;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < J; ++j) out[j0 + j] = s[j];
   }
 }
 
@@ -92,14 +98,15 @@ struct Few {
   static constexpr int OUT = T * PITCH * 4;
   static constexpr int COLS = T < 32 ? 32 : T;                      // TMEM columns
 };
-// shared memory: the ring (later the partial outputs), the update [T, 128 / ranks], s z [T, r], barriers
+// shared memory: the ring (later the partial outputs), the update [T, 128 / ranks], s z [T, r], the rows' adapters and
+// scales, barriers
 template <int T>
 __host__ __device__ constexpr int few_ring(int stages) {
   return stages * Few<T>::STAGE > Few<T>::OUT ? stages * Few<T>::STAGE : Few<T>::OUT;
 }
 template <int T>
 __host__ __device__ constexpr int few_smem(int stages, int ranks, int r) {
-  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + T * r * 4 + 8 * (2 * stages + 2) + 32;
+  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + T * r * 4 + T * 8 + 8 * (2 * stages + 2) + 32;
 }
 
 template <int T>
@@ -113,7 +120,9 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   const int own = kRowsW / (int)ranks;                              // output columns that this CTA finishes
   float* update = reinterpret_cast<float*>(smem + few_ring<T>(a.stages));   // [T, own]
   float* sz = update + T * own;                                     // [T, r]
-  uint64_t* full = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(sz + T * a.r) + 7) & ~uintptr_t(7));
+  int* ids = reinterpret_cast<int*>(sz + T * a.r);                  // [T]
+  float* scale = reinterpret_cast<float*>(ids + T);                 // [T]
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale + T);
   uint64_t* empty = full + a.stages;
   uint64_t* done = empty + a.stages;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
@@ -186,38 +195,76 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   } else {
     // the update of this CTA's own columns, while W0 streams in
     const int e = threadIdx.x - 64;
-    pdl_wait();
-    for (int i = e; i < rows * a.r; i += 128) {
-      const int t = i / a.r, j = i % a.r, row = m0 + t;
-      float z = 0.f;
-      for (int s = 0; s < a.splits; ++s) z += __ldcg(a.part + ((int64_t)s * a.M + row) * a.r + j);
-      if (a.Z && blockIdx.x == 0) a.Z[(int64_t)row * a.r + j] = __float2bfloat16_rn(z);
-      const int ad = __ldg(a.ids + row);
-      sz[i] = ad < 0 ? 0.f : z * (a.each ? __ldg(a.each + ad) : a.one);
+    if (e < T) {
+      const int ad = e < rows ? __ldg(a.ids + m0 + e) : -1;
+      ids[e] = ad;
+      scale[e] = ad < 0 ? 0.f : a.each ? __ldg(a.each + ad) : a.one;
     }
-    named_bar_sync(1, 128);
-    const int f = e % own, c = n0 + (int)rank * own + f;
+    named_bar_sync(1, kUpdate);
+    const int f = e % own, c = n0 + (int)rank * own + f, step = kUpdate / own;
     const float b = a.bias && c < a.N ? __bfloat162float(a.bias[c]) : 0.f;
-    for (int t = e / own; t < rows; t += 128 / own) {
-      const int ad = __ldg(a.ids + m0 + t);
-      float v = b;
-      if (ad >= 0 && c < a.N) {
-        const bf16* u = a.B + ((int64_t)ad * a.N + c) * a.r;
-        for (int j = 0; j < a.r; j += 8) {
-          float w[8];
-          load8(u + j, w);
+    // 16 columns of the factor of four rows at a time, the first ones on their way before z is there
+    uint4 w[4][2];
+    auto fetch = [&](int t0, int j0) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v = fmaf(w[q], sz[t * a.r + j + q], v);
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + i * step, ad = t < rows && c < a.N ? ids[t] : -1;
+        const bf16* u = a.B + ((int64_t)max(ad, 0) * a.N + c) * a.r + j0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[i][h] = ad >= 0 && j0 + 8 * h < a.r ? __ldg(reinterpret_cast<const uint4*>(u + 8 * h)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    fetch(e / own, 0);
+    pdl_wait();
+    for (int i = e; i < rows * a.r; i += kUpdate) {
+      const int t = i / a.r, row = m0 + t;
+      const float* p = a.part + (int64_t)row * a.r + (i - t * a.r);
+      const int64_t next = (int64_t)a.M * a.r;
+      float z = 0.f;
+      for (int s = 0; s < a.splits; s += 8) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = s + q < a.splits ? __ldcg(p + (s + q) * next) : 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) z += v[q];
+      }
+      if (a.Z && blockIdx.x == 0) a.Z[(int64_t)row * a.r + (i - t * a.r)] = __float2bfloat16_rn(z);
+      sz[i] = ids[t] < 0 ? 0.f : z * scale[t];
+    }
+    named_bar_sync(1, kUpdate);
+    for (int t0 = e / own; t0 < rows; t0 += 4 * step) {
+      float v[4] = {b, b, b, b};
+      for (int j0 = 0; j0 < a.r; j0 += 16) {
+        if (j0 > 0 || t0 != e / own) fetch(t0, j0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = min(t0 + i * step, rows - 1);
+          const float* z = sz + t * a.r + j0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (j0 + 8 * h < a.r) {
+              const uint32_t x[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float2 p = unpack_bf16x2(x[q]), s = *reinterpret_cast<const float2*>(z + 8 * h + 2 * q);
+                v[i] = fmaf(p.x, s.x, fmaf(p.y, s.y, v[i]));
+              }
+            }
         }
       }
-      update[t * own + f] = v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + i * step;
+        if (t < rows) update[t * own + f] = v[i];
+      }
     }
     // the accumulator, once every MMA is done: the ring is free then
     const int q = warp & 3;
-    const bool ok = mbar_wait(done, 0, a.timeout_ns, abort_flag, a.err, 0x403);
+    const bool ok = warp >= 6 || mbar_wait(done, 0, a.timeout_ns, abort_flag, a.err, 0x403);
     tc_fence_after();
     float* out = reinterpret_cast<float*>(smem);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (warp < 6 && __all_sync(0xffffffffu, ok)) {
 #pragma unroll
       for (int c0 = 0; c0 < T; c0 += 16) {
         uint32_t v[16];
@@ -236,15 +283,17 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   const int pairs = own / 2;
   for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
     const int t = i / pairs, f = i % pairs * 2, c = n0 + (int)rank * own + f;
-    float v0 = 0.f, v1 = 0.f;
-    for (uint32_t s = 0; s < ranks; ++s) {
-      float p0, p1;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(p0), "=f"(p1)
-                   : "r"(mapa_shared(mine + (t * F::PITCH + (int)rank * own + f) * 4, s)));
-      v0 += p0;
-      v1 += p1;
+    float p[8][2], v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (uint32_t s = 0; s < 8; ++s) {
+      p[s][0] = p[s][1] = 0.f;
+      if (s < ranks)
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(p[s][0]), "=f"(p[s][1])
+                     : "r"(mapa_shared(mine + (t * F::PITCH + (int)rank * own + f) * 4, s)));
     }
+#pragma unroll
+    for (int s = 0; s < 8; ++s) v0 += p[s][0], v1 += p[s][1];
     if (c < a.N)
       *reinterpret_cast<uint32_t*>(a.Y + (int64_t)(m0 + t) * a.N + c) =
           pack_bf16x2(v0 + update[t * own + f], v1 + update[t * own + f + 1]);
@@ -316,7 +365,10 @@ cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64
   const int T = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
   if (!make_tmap_bf16(&a.tmW, W0, K, N, K, kBK, kRowsW, 128) || !make_tmap_bf16(&a.tmX, X, K, p.M, K, kBK, T, 128))
     return cudaErrorInvalidValue;
-  const cudaError_t e = launch_pdl(multi_few_down, dim3((unsigned)a.M, (unsigned)a.splits), dim3(128), 0, st, a);
+  const dim3 grid((unsigned)a.M, (unsigned)a.splits);
+  const cudaError_t e = r <= 16   ? launch_pdl(multi_few_down<2, 8>, grid, dim3(256), 0, st, a)
+                        : r <= 32 ? launch_pdl(multi_few_down<4, 8>, grid, dim3(256), 0, st, a)
+                                  : launch_pdl(multi_few_down<4, 16>, grid, dim3(512), 0, st, a);
   if (e != cudaSuccess) return e;
   return T == 16 ? few_launch<16>(a, st) : T == 32 ? few_launch<32>(a, st) : few_launch<64>(a, st);
 }

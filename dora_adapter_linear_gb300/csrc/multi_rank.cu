@@ -10,17 +10,20 @@ namespace lg {
 namespace {
 
 // ------------------------------------------------------------------ products of rows
-// T = S U_a^T of one item (32 rows of one adapter), R columns of U_a [r, K], or (KR) [K, r].  The eight warps share K in
-// stretches of 64 columns and add their sums at the end, in their order.  A lane reads 16 bytes of a row at a
-// time: of 32 columns it holds 8 t .. 8 t + 7 (t = lane % 4), and as a sum over k may run in any order, its
-// words go into the MMA operands as they are, for both factors alike.  U_a [K, R] is turned by ldmatrix: a warp
-// stages 32 rows k at a time, row 8 t + 2 m + e of them as row 8 m + 2 t + e, which gives the same order.
+// T = S U_a^T of one item (64 rows of one adapter), R columns of U_a [r, K], or (KR) [K, r].  The CTAs of a cluster
+// share K and add their sums through distributed shared memory, in the order of the ranks, so that few items
+// still fill the device; 64 rows to a CTA halve the reads of U_a through L2 against 32.  Stages of 128 columns by
+// 16-byte asynchronous copies, three ahead of the one in use; a warp has 32 of the rows and every fourth pair of
+// k16 steps.
 template <int R, bool KR>
 struct Proj {
   static constexpr int NT = R / 8;
-  static constexpr int PITCH = 2 * R + 16;                     // bytes: eight rows of 16 bytes in different banks
-  static constexpr int STAGE = KR ? 32 * PITCH : 0;
-  static constexpr int SMEM = 8 * (2 * STAGE > 32 * R * 4 ? 2 * STAGE : 32 * R * 4);
+  static constexpr int XP = 256 + 16, UP = KR ? 2 * R + 16 : 256 + 16;   // bytes of a row, in different banks
+  static constexpr int STAGE = kItemRows * XP + (KR ? 128 : R) * UP;
+  static constexpr int NST = 4 * STAGE <= 112 * 1024 ? 4 : 3;
+  static constexpr int RED = 4 * kItemRows * R * 4;                      // the warps' sums
+  static constexpr int RING = NST * STAGE > RED ? NST * STAGE : RED;
+  static constexpr int SMEM = RING + kItemRows * 4;
 };
 
 struct ProjArgs {
@@ -29,8 +32,8 @@ struct ProjArgs {
   const bf16 *S, *U;
   float one;
   const float* each;
-  bf16 *plain, *scaled;       // [M, r] T and s_a T; either may be null
-  int r, j0;                  // the rank, and the first of the R columns
+  bf16 *plain, *scaled, *rest;   // [M, r] T, s_a T and what its rounding leaves; each may be null
+  int r, j0;                     // the rank, and the first of the R columns
 };
 
 template <int R, bool KR>
@@ -38,110 +41,96 @@ __global__ void __launch_bounds__(256) multi_proj_mma(const __grid_constant__ Pr
   using C = Proj<R, KR>;
   constexpr int NT = C::NT;
   extern __shared__ __align__(16) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + C::RING);
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int mine = (int)(blockIdx.x / ranks);
   pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+  if (tid == 0) pdl_trigger();
+  const int4 item = a.p.items[mine];               // there is room for as many as there are CTAs
   const int items = a.p.head[kHeadItems], with = a.p.head[kHeadRows];
   if (a.plain) {              // rows without adapter: zeros
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.p.M - with) * NT; i += (int64_t)gridDim.x * 256)
+    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < (a.p.M - with) * NT; i += (int64_t)gridDim.x * 256)
       *reinterpret_cast<uint4*>(a.plain + (int64_t)a.p.order[with + i / NT] * a.r + a.j0 + i % NT * 8) = make_uint4(0, 0, 0, 0);
   }
-  if ((int)blockIdx.x >= items) return;
-  const int4 item = a.p.items[blockIdx.x];
-  const bf16* U = a.U + (int64_t)item.x * a.r * a.K + (KR ? a.j0 : a.j0 * a.K);
-  const bf16* row[4];         // rows g, g + 8, g + 16, g + 24 of the item; past its end its first row, not used
+  if (mine >= items) return;  // the whole cluster
+  const int64_t K = a.K;
+  const bf16* U = a.U + (int64_t)item.x * a.r * K + (KR ? a.j0 : a.j0 * K);
+  if (tid < kItemRows) rows[tid] = a.p.order[item.y + min(tid, item.z - 1)];   // past its end its last row, not used
+  __syncthreads();
+  const int steps = (int)((K + 127) / 128), s0 = (int)((int64_t)steps * rank / ranks),
+            s1 = (int)((int64_t)steps * (rank + 1) / ranks);
+  const int c = tid & 15, r0 = tid >> 4;           // 16 threads a row of 128 columns
+  const bf16* x[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = g + 8 * i;
-    row[i] = a.S + (int64_t)a.p.order[item.y + (k < item.z ? k : 0)] * a.K;
-  }
+  for (int i = 0; i < 4; ++i) x[i] = a.S + (int64_t)rows[r0 + 16 * i] * K + c * 8;
+  auto load = [&](int s) {
+    if (s < s1) {
+      uint8_t* st = smem + (s - s0) % C::NST * C::STAGE;
+      const int64_t k0 = (int64_t)s * 128;
+      const bool on = k0 + c * 8 < K;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cp_async16(st + (r0 + 16 * i) * C::XP + c * 16, on ? x[i] + k0 : a.S, on);
+      st += kItemRows * C::XP;
+      if (KR) {
+        for (int i = tid; i < 128 * NT; i += 256) {
+          const int k = i / NT, q = i % NT;
+          const bool in = k0 + k < K;
+          cp_async16(st + k * C::UP + q * 16, in ? U + (k0 + k) * a.r + q * 8 : a.U, in);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < R; j += 16)
+          if (j + r0 < R) cp_async16(st + (j + r0) * C::UP + c * 16, on ? U + (int64_t)(j + r0) * K + k0 + c * 8 : a.U, on);
+      }
+    }
+    cp_async_commit();
+  };
+  const int mh = warp & 1, kq = warp >> 1;
   float acc[2][NT][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-
-  const int64_t K = a.K;
-  const int halves = (int)((K + 31) / 32);                     // stretches of 32 columns; a warp takes two of 16
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  auto load_rows = [&](int h, uint4 (&x)[4]) {
-    const int64_t k = (int64_t)h * 32 + 8 * t;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = k < K ? __ldcs(reinterpret_cast<const uint4*>(row[i] + k)) : none;
-  };
-  auto mma = [&](const uint4 (&x)[4], int n, uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+  for (int s = 0; s < C::NST - 1; ++s) load(s0 + s);
+  for (int s = s0; s < s1; ++s) {
+    cp_async_wait<C::NST - 2>();
+    __syncthreads();          // stage s is there, and all are done with the one that is loaded next
+    load(s + C::NST - 1);
+    const uint32_t X = smem_u32(smem + (s - s0) % C::NST * C::STAGE), W = X + kItemRows * C::XP;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const uint32_t lo[4] = {x[2 * m].x, x[2 * m + 1].x, x[2 * m].y, x[2 * m + 1].y};
-      const uint32_t hi[4] = {x[2 * m].z, x[2 * m + 1].z, x[2 * m].w, x[2 * m + 1].w};
-      mma_bf16_16816(acc[m][n], lo, b0, b1);
-      mma_bf16_16816(acc[m][n], hi, b2, b3);
-    }
-  };
-  uint8_t* mine = smem + warp * 2 * C::STAGE;
-  auto stage = [&](int h, int buf) {                           // 32 rows of U_a [K, R]; zeros past K
-    if (h < halves)
-      for (int i = lane; i < 32 * NT; i += 32) {
-        const int k = i / NT, c = i % NT, at = 8 * ((k & 7) >> 1) + 2 * (k >> 3) + (k & 1);
-        const int64_t kk = (int64_t)h * 32 + k;
-        cp_async16(mine + buf * C::STAGE + at * C::PITCH + c * 16, U + (kk < K ? kk * a.r + c * 8 : 0), kk < K);
+    for (int h = 0; h < 2; ++h) {
+      const int kk = kq * 2 + h;
+      uint32_t f[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        ldsm_x4(f[m][0], f[m][1], f[m][2], f[m][3],
+                X + (mh * 32 + m * 16 + (lane & 15)) * C::XP + (kk * 2 + (lane >> 4)) * 16);
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b0, b1, b2 = 0, b3 = 0;
+        if (KR) {
+          const uint32_t at = W + (kk * 16 + (lane & 15)) * C::UP + n * 16;
+          if (n + 1 < NT) ldsm_x4_t(b0, b1, b2, b3, at + (lane >> 4) * 16);
+          else ldsm_x2_t(b0, b1, at);
+        } else {
+          const uint32_t at = W + (n * 8 + (lane & 7)) * C::UP + (kk * 2 + ((lane >> 3) & 1)) * 16;
+          if (n + 1 < NT) ldsm_x4(b0, b1, b2, b3, at + (lane >> 4) * 8 * C::UP);
+          else ldsm_x2(b0, b1, at);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          mma_bf16_16816(acc[m][n], f[m], b0, b1);
+          if (n + 1 < NT) mma_bf16_16816(acc[m][n + 1 < NT ? n + 1 : n], f[m], b2, b3);
+        }
       }
-    cp_async_commit();
-  };
-  auto work = [&](int h, int buf, const uint4 (&x)[4]) {
-    if constexpr (KR) {
-      const uint32_t base = smem_u32(mine + buf * C::STAGE) + lane * C::PITCH;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4_t(b0, b1, b2, b3, base + n * 16);
-        mma(x, n, b0, b1, b2, b3);
-      }
-    } else {
-      const int64_t k = (int64_t)h * 32 + 8 * t;
-#pragma unroll
-      for (int n0 = 0; n0 < NT; n0 += 4) {
-        uint4 u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < NT) u[i] = k < K ? __ldg(reinterpret_cast<const uint4*>(U + (int64_t)((n0 + i) * 8 + g) * K + k)) : none;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < NT) mma(x, n0 + i, u[i].x, u[i].y, u[i].z, u[i].w);
-      }
-    }
-  };
-  // stretch j of this warp: the j % 2 half of its 64-column run
-  auto nth = [&](int j) { return (warp + (j >> 1) * 8) * 2 + (j & 1); };
-  uint4 x0[4], x1[4];
-  load_rows(nth(0), x0);
-  load_rows(nth(1), x1);
-  if (KR) {
-    stage(nth(0), 0);
-    stage(nth(1), 1);
-  }
-  for (int j = 0; nth(j) < halves; j += 2) {
-    if (KR) {
-      cp_async_wait<1>();
-      __syncwarp();
-    }
-    work(nth(j), 0, x0);
-    load_rows(nth(j + 2), x0);
-    if (KR) {
-      __syncwarp();
-      stage(nth(j + 2), 0);
-      cp_async_wait<1>();
-      __syncwarp();
-    }
-    if (nth(j + 1) < halves) work(nth(j + 1), 1, x1);
-    load_rows(nth(j + 3), x1);
-    if (KR) {
-      __syncwarp();
-      stage(nth(j + 3), 1);
     }
   }
-  if (KR) cp_async_wait<0>();
-  __syncthreads();            // the sums go where the stages were
+  cp_async_wait<0>();
+  __syncthreads();            // the sums go where the stages were: [4][64][R]
   float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -149,41 +138,74 @@ __global__ void __launch_bounds__(256) multi_proj_mma(const __grid_constant__ Pr
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float2*>(red + (warp * 32 + m * 16 + g + 8 * h) * R + n * 8 + 2 * t) =
+        *reinterpret_cast<float2*>(red + (kq * kItemRows + mh * 32 + m * 16 + g + 8 * h) * R + n * 8 + 2 * t) =
             make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]);
   __syncthreads();
-  const float s = a.each ? __ldg(a.each + item.x) : a.one;
-  for (int i = threadIdx.x; i < item.z * R / 2; i += 256) {
-    float2 v = make_float2(0.f, 0.f);
+  if (ranks > 1) {            // this CTA's sums into the first quarter
+    for (int i = tid; i < kItemRows * R / 2; i += 256) {
+      float2 v = *reinterpret_cast<const float2*>(red + 2 * i);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float2 q = *reinterpret_cast<const float2*>(red + w * 32 * R + 2 * i);
-      v.x += q.x;
-      v.y += q.y;
+      for (int w = 1; w < 4; ++w) {
+        const float2 q = *reinterpret_cast<const float2*>(red + w * kItemRows * R + 2 * i);
+        v.x += q.x;
+        v.y += q.y;
+      }
+      *reinterpret_cast<float2*>(red + 2 * i) = v;
     }
-    const int64_t to = (int64_t)a.p.order[item.y + 2 * i / R] * a.r + a.j0 + 2 * i % R;
-    if (a.plain) *reinterpret_cast<uint32_t*>(a.plain + to) = pack_bf16x2(v.x, v.y);
-    if (a.scaled) *reinterpret_cast<uint32_t*>(a.scaled + to) = pack_bf16x2(v.x * s, v.y * s);
+    cluster_sync_all();
   }
+  const float s = a.each ? __ldg(a.each + item.x) : a.one;
+  const int pairs = item.z * R / 2, p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
+  for (int i = p0 + tid; i < p1; i += 256) {
+    float2 q[8];
+    if (ranks > 1) {
+#pragma unroll
+      for (uint32_t w = 0; w < 8; ++w)
+        if (w < ranks)
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(q[w].x), "=f"(q[w].y)
+                       : "r"(mapa_shared(smem_u32(red + 2 * i), w)));
+        else q[w] = make_float2(0.f, 0.f);
+    } else {
+#pragma unroll
+      for (int w = 0; w < 8; ++w)
+        q[w] = w < 4 ? *reinterpret_cast<const float2*>(red + w * kItemRows * R + 2 * i) : make_float2(0.f, 0.f);
+    }
+    float2 v = q[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      v.x += q[w].x;
+      v.y += q[w].y;
+    }
+    const int64_t to = (int64_t)rows[2 * i / R] * a.r + a.j0 + 2 * i % R;
+    if (a.plain) *reinterpret_cast<uint32_t*>(a.plain + to) = pack_bf16x2(v.x, v.y);
+    const uint32_t hi = pack_bf16x2(v.x * s, v.y * s);
+    if (a.scaled) *reinterpret_cast<uint32_t*>(a.scaled + to) = hi;
+    if (a.rest) {
+      const float2 had = unpack_bf16x2(hi);
+      *reinterpret_cast<uint32_t*>(a.rest + to) = pack_bf16x2(v.x * s - had.x, v.y * s - had.y);
+    }
+  }
+  if (ranks > 1) cluster_sync_all();   // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------ sums over an adapter's rows
 // out[k][j] = f_a sum over the piece's rows S[row][k] T[row][j], of 128 columns k a CTA (a warp 32 of them).  Stages
 // of 32 rows, gathered by 16-byte asynchronous copies; both factors are turned by ldmatrix.  An adapter's only
 // piece gives the gradient itself, others fp32 partials, added by multi_sum in their order.
-template <int R>
+template <int R, bool TWO>
 struct Reduce {
-  static constexpr int NT = R / 8;
+  static constexpr int NT = R / 8, PARTS = TWO ? 2 : 1;
   static constexpr int SP = 256 + 16, TP = 2 * R + 16;
-  static constexpr int STAGE = 32 * (SP + TP);
-  static constexpr int NST = R <= 64 ? 4 : 3;
-  static constexpr int SMEM = NST * STAGE;
+  static constexpr int STAGE = 32 * (SP + PARTS * TP);
+  static constexpr int NST = STAGE <= 14 * 1024 ? 4 : 3;
+  static constexpr int SMEM = NST * STAGE + kPieceRows * 4;
 };
 
 struct ReduceArgs {
   MultiPlan p;
   int64_t K;
-  const bf16 *S, *T;
+  const bf16 *S, *T, *T2;     // T2: what a rounding has left of T, added to it (TWO)
   float one;
   const float* each;          // with scaled: f_a = s_a
   bool scaled, kr;            // kr: out_a [K, R], else [R, K]
@@ -191,38 +213,40 @@ struct ReduceArgs {
   float* part;                // [partials] x [K, R] or [R, K]
 };
 
-template <int R>
+template <int R, bool TWO>
 __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ ReduceArgs a) {
-  using C = Reduce<R>;
+  using C = Reduce<R, TWO>;
   constexpr int NT = C::NT;
   extern __shared__ __align__(16) uint8_t smem[];
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + C::NST * C::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
   const int64_t K = a.K;
   const int groups = (int)((K + 127) / 128), mine = (int)blockIdx.x / groups;
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int4 piece = a.p.pieces[mine];             // there is room for as many as the grid has
   if (mine >= a.p.head[kHeadPieces]) return;
-  const int4 piece = a.p.pieces[mine];
   const int64_t k0 = (int64_t)((int)blockIdx.x - mine * groups) * 128;
-  const int32_t* order = a.p.order + piece.y;
+  for (int i = threadIdx.x; i < piece.z; i += 128) rows[i] = a.p.order[piece.y + i];
+  __syncthreads();
   const int stages = (piece.z + 31) / 32;
+  const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;     // 16 threads a row of S
+  const bool in = k0 + c * 8 < K;
   auto load = [&](int s) {
     if (s < stages) {
       uint8_t* st = smem + s % C::NST * C::STAGE;
-      // 16 threads a row of S: rows threadIdx / 16 + 8 i
-      const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + 8 * i;
-        const bool on = s * 32 + r < piece.z && k0 + c * 8 < K;
-        const int64_t row = on ? order[s * 32 + r] : 0;
-        cp_async16(st + r * C::SP + c * 16, a.S + (on ? row * K + k0 + c * 8 : 0), on);
+        const bool on = in && s * 32 + r < piece.z;
+        cp_async16(st + r * C::SP + c * 16, on ? a.S + (int64_t)rows[s * 32 + r] * K + k0 + c * 8 : a.S, on);
       }
       for (int i = threadIdx.x; i < 32 * NT; i += 128) {
         const int r = i / NT, q = i % NT;
         const bool on = s * 32 + r < piece.z;
-        const int64_t row = on ? order[s * 32 + r] : 0;
-        cp_async16(st + 32 * C::SP + r * C::TP + q * 16, a.T + row * R + q * 8, on);
+        const int64_t at = on ? (int64_t)rows[s * 32 + r] * R + q * 8 : 0;
+        cp_async16(st + 32 * C::SP + r * C::TP + q * 16, a.T + at, on);
+        if (TWO) cp_async16(st + 32 * (C::SP + C::TP) + r * C::TP + q * 16, a.T2 + at, on);
       }
     }
     cp_async_commit();
@@ -247,17 +271,19 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
         ldsm_x4_t(x[m][0], x[m][1], x[m][2], x[m][3],
                   S + (kk * 16 + (lane & 7) + ((lane >> 4) << 3)) * C::SP + (warp * 32 + m * 16 + ((lane >> 3) & 1) * 8) * 2);
 #pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        const uint32_t at = T + (kk * 16 + (lane & 15)) * C::TP + n * 16;
-        uint32_t b0, b1, b2 = 0, b3 = 0;
-        if (n + 1 < NT) ldsm_x4_t(b0, b1, b2, b3, at + (lane >> 4) * 16);
-        else ldsm_x2_t(b0, b1, at);
+      for (int n = 0; n < NT; n += 2)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_bf16_16816(acc[m][n], x[m], b0, b1);
-          if (n + 1 < NT) mma_bf16_16816(acc[m][n + 1 < NT ? n + 1 : n], x[m], b2, b3);
+        for (int w = 0; w < C::PARTS; ++w) {
+          const uint32_t at = T + w * 32 * C::TP + (kk * 16 + (lane & 15)) * C::TP + n * 16;
+          uint32_t b0, b1, b2 = 0, b3 = 0;
+          if (n + 1 < NT) ldsm_x4_t(b0, b1, b2, b3, at + (lane >> 4) * 16);
+          else ldsm_x2_t(b0, b1, at);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma_bf16_16816(acc[m][n], x[m], b0, b1);
+            if (n + 1 < NT) mma_bf16_16816(acc[m][n + 1 < NT ? n + 1 : n], x[m], b2, b3);
+          }
         }
-      }
     }
   }
   cp_async_wait<0>();
@@ -350,18 +376,35 @@ __global__ void __launch_bounds__(256) multi_colsum_kernel(int64_t M, int64_t K,
 }
 
 template <int R, bool KR>
-cudaError_t proj_launch(const ProjArgs& a, int64_t ctas, cudaStream_t st) {
+cudaError_t proj_launch(const ProjArgs& a, int64_t items, cudaStream_t st) {
   using C = Proj<R, KR>;
   const cudaError_t e = allow_smem<multi_proj_mma<R, KR>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_proj_mma<R, KR>, dim3((unsigned)ctas), dim3(256), C::SMEM, st, a);
+  // as many CTAs to a cluster as two an SM have room for, each with two rounds of the ring at least
+  const int64_t steps = (a.K + 127) / 128, slots = 2 * num_sms_current();
+  int ranks = 1;
+  while (ranks < 8 && items * ranks * 2 <= slots && steps >= ranks * 2 * 2 * (C::NST - 1)) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(items * ranks), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t l = cudaLaunchKernelEx(&cfg, multi_proj_mma<R, KR>, a);
+  count_launch();
+  return l != cudaSuccess ? l : cudaGetLastError();
 }
-template <int R>
+template <int R, bool TWO>
 cudaError_t reduce_launch(const ReduceArgs& a, int64_t pieces, cudaStream_t st) {
-  using C = Reduce<R>;
-  const cudaError_t e = allow_smem<multi_reduce_mma<R>>(C::SMEM);
+  using C = Reduce<R, TWO>;
+  const cudaError_t e = allow_smem<multi_reduce_mma<R, TWO>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_reduce_mma<R>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::SMEM, st, a);
+  return launch_pdl(multi_reduce_mma<R, TWO>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::SMEM, st, a);
 }
 
 }  // namespace
@@ -370,16 +413,14 @@ cudaError_t reduce_launch(const ReduceArgs& a, int64_t pieces, cudaStream_t st) 
 #define MORE_RANKS(CASE) CASE(72) CASE(80) CASE(88) CASE(96) CASE(104) CASE(112) CASE(120) CASE(128)
 
 cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
-                       const float* each, bf16* plain, bf16* scaled, cudaStream_t st) {
-  // at least one CTA: with no row that has an adapter the others are still set to zero
-  int64_t ctas = multi_items(p.M, p.n);
-  if (ctas < 1) ctas = 1;
+                       const float* each, bf16* plain, bf16* scaled, bf16* rest, cudaStream_t st) {
+  const int64_t items = multi_items(p.M, p.n);
   for (int j0 = 0; j0 < r; j0 += 64) {   // ranks above 64 take a second pass: their sums do not fit the registers
-    const ProjArgs a{p, K, S, U, one, each, plain, scaled, r, j0};
+    const ProjArgs a{p, K, S, U, one, each, plain, scaled, rest, r, j0};
     cudaError_t e = cudaErrorInvalidValue;
     switch (r - j0 < 64 ? r - j0 : 64) {
 #define CASE(R) \
-  case R: e = kr ? proj_launch<R, true>(a, ctas, st) : proj_launch<R, false>(a, ctas, st); break;
+  case R: e = kr ? proj_launch<R, true>(a, items, st) : proj_launch<R, false>(a, items, st); break;
       RANKS(CASE)
 #undef CASE
     }
@@ -388,12 +429,13 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
   return cudaSuccess;
 }
 
-cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, bool kr, bool scaled,
-                         float one, const float* each, float* part, bf16* out, cudaStream_t st) {
-  const ReduceArgs a{p, K, S, T, one, each, scaled, kr, out, part};
+cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr,
+                         bool scaled, float one, const float* each, float* part, bf16* out, cudaStream_t st) {
+  const ReduceArgs a{p, K, S, T, T2, one, each, scaled, kr, out, part};
+  const int64_t pieces = multi_pieces(p.M, p.n);
   switch (r) {
 #define CASE(R) \
-  case R: return reduce_launch<R>(a, multi_pieces(p.M, p.n), st);
+  case R: return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
     RANKS(CASE) MORE_RANKS(CASE)
 #undef CASE
   }

@@ -657,10 +657,33 @@ def _multi_shape(X, W0, A, B, s, plan, bias=None, Z=None, dY=None):
     return L.LoraMultiShape(M, d_in, d_out, r, n, L.dtype_code(X))
 
 
+@lru_cache(maxsize=1024)
+def _multi_bytes(backward, M, d_in, d_out, r, n, dtype):
+    """Bytes of workspace; 0 for what the calls do not take."""
+    if dtype not in (BF16, F32):
+        return 0
+    sh = L.LoraMultiShape(M, d_in, d_out, r, n, L.LORA_BF16 if dtype == BF16 else L.LORA_F32)
+    return L.lora_multi_workspace_bytes(backward, sh)
+
+
+def _multi_workspace(backward, X, W0, A, plan):
+    """The workspace of a call whose operands look well, or None: what is wrong is for the checks to name."""
+    if X.dim() == 2 and W0.dim() == 2 and A.dim() == 3 and X.is_cuda and isinstance(plan, AdapterPlan):
+        need = _multi_bytes(backward, *X.shape, W0.shape[0], A.shape[1], A.shape[0], X.dtype)
+        if need:
+            return workspace(need, X.device)
+    return None
+
+
 def lora_multi_fwd(X, W0, A, B, s, plan, bias=None, save_z=True):
     """The projection of a batch whose rows have different adapters: row i takes adapter ids[i] of the stacks
     A [n, r, in] and B [n, out, r], or the frozen base alone where it has none; `plan` from
     adapter_plan(ids, n).  s: a number, or an fp32 tensor [n] with one for each adapter.  Returns (Y, Z)."""
+    ws = _multi_workspace(False, X, W0, A, plan)
+    if ws is not None:
+        done = L.host().multi_fwd(X, W0, A, B, s, plan.buffer, plan.rows, plan.adapters, bias, save_z, ws)
+        if done is not None:
+            return _done(done, "lora_multi_fwd")
     sh = _multi_shape(X, W0, A, B, s, plan, bias)
     _need_cuda("X", X)
     Y = torch.empty(sh.M, sh.d_out, dtype=X.dtype, device=X.device)
@@ -673,6 +696,11 @@ def lora_multi_fwd(X, W0, A, B, s, plan, bias=None, save_z=True):
 def lora_multi_bwd(X, W0, A, B, Z, dY, s, plan, need_dx=True, need_dbias=False):
     """Gradients of lora_multi_fwd with W0 frozen: (dX, dA, dB, dbias), dA and dB stacks like A and B, zeros
     for an adapter without rows.  Z: from the forward, or None to recompute it."""
+    ws = _multi_workspace(True, X, W0, A, plan)
+    if ws is not None:
+        done = L.host().multi_bwd(X, W0, A, B, Z, dY, s, plan.buffer, plan.rows, plan.adapters, need_dx, need_dbias, ws)
+        if done is not None:
+            return _done(done, "lora_multi_bwd")
     sh = _multi_shape(X, W0, A, B, s, plan, Z=Z, dY=dY)
     _need_cuda("X", X)
     dX = torch.empty_like(X) if need_dx else None

@@ -3,7 +3,8 @@
 An output's error is at most: half a step of its type; for every sum of k products formed in fp32, k + 4 steps
 of 2^-23 of the sum of the products' magnitudes (a tensor core's sums may be cut off instead of rounded, so a
 whole step each); and, with bf16, half a step (2^-8) of the rank-r values (s z, or s g) that enter the second
-product rounded."""
+product rounded.  As a factor of dA, s g comes in two parts, the second what the first one's rounding left: half
+a step of half a step."""
 import numpy as np
 import torch
 
@@ -71,7 +72,7 @@ def reference_bwd(c, Z, dtype):
         if 0 <= a < len(A):
             rX[i] = abs(G[i]) @ abs(A[a])
             rA[a] += np.outer(abs(G[i]), abs(X[i]))
-    offs = {"dX": (d_out + r + 8) * STEP * mX + round_g * rX, "dA": (M + d_out + 8) * STEP * mA + round_g * rA,
+    offs = {"dX": (d_out + r + 8) * STEP * mX + round_g * rX, "dA": (2 * M + d_out + 8) * STEP * mA + round_g ** 2 * rA,
             "dB": (M + 8) * STEP * mB, "dbias": (M + 4) * STEP * mb}
     return {k: (v, h * (abs(v) + offs[k]) + offs[k]) for k, v in (("dX", dX), ("dA", dA), ("dB", dB), ("dbias", db))}
 

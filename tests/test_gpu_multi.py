@@ -157,7 +157,7 @@ def test_plan(rows, n):
 
     used, tiles = min(rows, n), (rows + 255) // 256
     head, kept, order, _, start, istart, pstart = (take(k) for k in (64, rows, rows, rows, n + 1, n + 1, n + 1))
-    items, pieces = take(rows // 32 + used, 4), take(rows // 512 + used, 4)
+    items, pieces = take(rows // 64 + used, 4), take(rows // 512 + used, 4)
     tcount, tlist, tmask = take(tiles), take(tiles * 256).reshape(tiles, 256), take(tiles * 256 * 8).reshape(tiles, 256, 8)
     assert at == L.lora_multi_plan_bytes(rows, n)
     real = np.where((ids >= 0) & (ids < n), ids, -1)
@@ -166,7 +166,7 @@ def test_plan(rows, n):
     assert (order == np.argsort(key, kind="stable")).all()
     assert (start == np.searchsorted(np.sort(key), np.arange(n + 1))).all()
     slots = 0
-    for first, list_, size in ((istart, items, 32), (pstart, pieces, 512)):
+    for first, list_, size in ((istart, items, 64), (pstart, pieces, 512)):
         count = -(-np.diff(start) // size)
         assert (first == np.concatenate(([0], np.cumsum(count)))).all()
         k = 0
@@ -178,7 +178,7 @@ def test_plan(rows, n):
                     slots += count[a] > 1
                 assert list_[k].tolist() == want
                 k += 1
-        assert head[0 if size == 32 else 1] == k <= len(list_)
+        assert head[0 if size == 64 else 1] == k <= len(list_)
     assert slots <= 2 * (rows // 512) and head[2] == start[n]
     for t in range(tiles):
         mine = np.full(256, -1)
