@@ -4,10 +4,12 @@
 //   norm_g = sqrt(sum over the group's elements x^2),  x = x min(1, max_norm / (norm_g + 1e-6)),
 // and x = 0 throughout a group whose norm is not finite.
 //
-// Three launches.  A CTA of the first sums the squares of one unit (16384 elements of one tensor and group,
-// all its loads on their way at once) in a fixed order; a CTA of the second adds the units' sums of one
-// group (fp64); the third scales the groups whose factor is not 1, last units first, while their elements
-// are still in L2.  Bytes bound large sets: every element read, those above the limit read again and written.
+// A CTA of the first launch sums the squares of one unit (16384 elements of one tensor and group, all its loads on
+// their way at once) in a fixed order.  A CTA of the last one scales a unit whose group's factor is not 1, last
+// units first, while their elements are still in L2.  The units' sums of a group are added in fp64, by one CTA for
+// each group in a launch between, or, where a group has up to 512, by every CTA of the last launch for itself
+// (three adapters of one small block: 10.1 instead of 12 us a call).  Bytes bound large sets: every element
+// read, those above the limit read again and written.
 #include <float.h>
 #include <math.h>
 
@@ -22,7 +24,9 @@ namespace lg {
 namespace {
 
 constexpr int kUnit = 16384;          // elements of a unit
-constexpr int kSmallTable = 64, kTable = 640;
+constexpr int kSmallTable = 64, kMidTable = 192, kTable = 640;
+constexpr int kFew = 512;              // sums of a group that every CTA adds for itself
+constexpr int kGroups = 2048;          // groups of one launch's table of sums
 
 struct ClipEntry {
   void* g;
@@ -31,15 +35,16 @@ struct ClipEntry {
   int32_t units;                      // units of each group
   int32_t at;                         // the first of their sums (stacks: of group 0)
   int32_t group;                      // -1: a stack, one entry of it for each group
-  int32_t sums;                       // sums of the group, on the group's first tensor; 0 elsewhere
-  int32_t dtype;
+  int32_t gfirst, gsums;              // where the group's sums begin, and how many they are (stacks: of group 0)
+  int16_t dtype, leads;               // leads: the group's first tensor
 };
 struct ClipArgs {
   int count;
-  int32_t units, per_group;           // of this launch; sums of each group of stacks
+  int32_t units;                      // of this launch
   float* parts;
-  int32_t *gfirst, *gsums;            // where a group's sums begin and how many there are (lists)
-  const float* factor;                // of each group: 0 a group that is not finite
+  float max_norm;
+  float* norms;
+  float* factor;                      // of each group: 0 a group that is not finite
 };
 template <int N>
 struct ClipTable {
@@ -49,9 +54,8 @@ struct ClipTable {
 struct Unit {
   void* p;                            // its first element
   int n;                              // elements, at most kUnit
-  int group, at, bf;
-  bool leads;                         // the first unit of its group's first tensor
-  int sums;
+  int group, at, gfirst, gsums;
+  bool bf, leads;                     // leads: the first unit of its group
 };
 template <int N>
 __device__ __forceinline__ Unit unit_of(const ClipArgs& a, const ClipTable<N>& t, int i) {
@@ -69,9 +73,10 @@ __device__ __forceinline__ Unit unit_of(const ClipArgs& a, const ClipTable<N>& t
   r.p = static_cast<char*>(e.g) + (k * e.n + off) * (r.bf ? 2 : 4);
   r.n = (int)(e.n - off < kUnit ? e.n - off : kUnit);
   r.group = e.group < 0 ? k : e.group;
-  r.at = e.at + k * a.per_group + u;
-  r.leads = v == 0 && e.sums > 0;
-  r.sums = e.sums;
+  r.gsums = e.gsums;
+  r.gfirst = e.gfirst + k * e.gsums;
+  r.at = e.at + k * e.gsums + u;
+  r.leads = u == 0 && e.leads;
   return r;
 }
 
@@ -112,35 +117,44 @@ __global__ void __launch_bounds__(256) clip_norm_kernel(const __grid_constant__ 
   if (threadIdx.x == 0) pdl_trigger();
   float s[1] = {u.bf ? squares(static_cast<const bf16*>(u.p), u.n) : squares(static_cast<const float*>(u.p), u.n)};
   block_sums<1>(s, red, 0);
-  if (threadIdx.x == 0) {
-    a.parts[u.at] = s[0];
-    if (a.gfirst && u.leads) {
-      a.gfirst[u.group] = u.at;
-      a.gsums[u.group] = u.sums;
-    }
-  }
+  if (threadIdx.x == 0) a.parts[u.at] = s[0];
 }
 
-__global__ void __launch_bounds__(256) clip_factor_kernel(const float* parts, const int32_t* gfirst, const int32_t* gsums,
-                                                          int per_group, float max_norm, float* norms, float* factor) {
-  __shared__ double tot[8];
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
-  const int g = blockIdx.x;
-  const int first = gfirst ? gfirst[g] : g * per_group, sums = gfirst ? gsums[g] : per_group;
+// The norm of the group whose sums are parts[0 .. sums - 1], in every thread of a block of 256.
+__device__ __forceinline__ float norm_of(const float* parts, int sums, double* tot) {
   double t = 0.0;
-  for (int i = threadIdx.x; i < sums; i += 256) t += (double)parts[first + i];
+  for (int i = threadIdx.x; i < sums; i += 256) t += (double)parts[i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if ((threadIdx.x & 31) == 0) tot[threadIdx.x >> 5] = t;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    t = 0.0;
+  t = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += tot[i];
-    const float norm = sqrtf((float)t);
-    norms[g] = norm;
-    factor[g] = isfinite(norm) ? fminf(1.f, max_norm / (norm + 1e-6f)) : 0.f;
+  for (int i = 0; i < 8; ++i) t += tot[i];
+  return sqrtf((float)t);
+}
+__device__ __forceinline__ float factor_of(float norm, float max_norm) {
+  return isfinite(norm) ? fminf(1.f, max_norm / (norm + 1e-6f)) : 0.f;
+}
+
+// where the sums of a launch's groups begin and how many they are: of stacks the same number for each
+template <int N>
+struct Sums {
+  int32_t group0, each;
+  int32_t first[N], sums[N];
+};
+template <int N>
+__global__ void __launch_bounds__(256) clip_factor_kernel(const __grid_constant__ ClipArgs a,
+                                                          const __grid_constant__ Sums<N> table) {
+  __shared__ double tot[8];
+  pdl_wait();
+  if (threadIdx.x == 0) pdl_trigger();
+  const int k = blockIdx.x, g = table.group0 + k;
+  const float norm = N > 1 ? norm_of(a.parts + table.first[N > 1 ? k : 0], table.sums[N > 1 ? k : 0], tot)
+                           : norm_of(a.parts + (int64_t)g * table.each, table.each, tot);
+  if (threadIdx.x == 0) {
+    a.norms[g] = norm;
+    a.factor[g] = factor_of(norm, a.max_norm);
   }
 }
 
@@ -174,13 +188,21 @@ __device__ __forceinline__ void scale(T* p, int n, float f, bool zero) {
   }
 }
 
-template <int N>
+template <int N, bool FEW>
 __global__ void __launch_bounds__(256) clip_scale_kernel(const __grid_constant__ ClipArgs a,
                                                          const __grid_constant__ ClipTable<N> table) {
+  __shared__ double tot[8];
   const Unit u = unit_of(a, table, a.units - 1 - (int)blockIdx.x);
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const float f = a.factor[u.group];
+  float f;
+  if (FEW) {
+    const float norm = norm_of(a.parts + u.gfirst, u.gsums, tot);
+    if (u.leads && threadIdx.x == 0) a.norms[u.group] = norm;
+    f = factor_of(norm, a.max_norm);
+  } else {
+    f = a.factor[u.group];
+  }
   if (f == 1.f) return;
   // a factor of an infinite max_norm's finite group is 1; 0 stands for a group that is not finite
   if (u.bf) scale(static_cast<bf16*>(u.p), u.n, f, f == 0.f);
@@ -191,13 +213,11 @@ int64_t units_of(int64_t n) { return (n + kUnit - 1) / kUnit; }
 
 struct ClipWs {
   float *parts, *factor;
-  int32_t* group;                     // [2, groups] of lists
 };
-size_t carve(int64_t sums, int64_t groups, bool stacked, char* base, ClipWs* w) {
+size_t carve(int64_t sums, int64_t groups, char* base, ClipWs* w) {
   Carve c{base};
   w->parts = c.take<float>(sums);
   w->factor = c.take<float>(groups);
-  w->group = stacked ? nullptr : c.take<int32_t>(2 * groups);
   return c.off;
 }
 
@@ -238,18 +258,52 @@ bool overlap(const lora_grad_tensor* t, int64_t count, int64_t each) {
   return false;
 }
 
+// Where the sums lie: those of a group behind one another, in the order of its tensors.
+struct Place {
+  std::vector<int32_t> at;              // of each tensor's units (stacks: of group 0)
+  std::vector<int32_t> gfirst, gsums;   // of each group; stacks: of group 0 alone
+  std::vector<char> leads;              // the tensor is its group's first
+  int32_t most = 0;                     // sums of the largest group
+  bool none = false;                    // there is a group without elements
+};
+Place place(const lora_grad_tensor* t, int64_t count, int64_t groups, bool stacked) {
+  Place p;
+  const int64_t n = stacked ? 1 : groups;
+  p.at.resize(count);
+  p.leads.assign(count, 0);
+  p.gfirst.assign(n, 0);
+  p.gsums.assign(n, 0);
+  auto group = [&](int64_t i) { return stacked ? 0 : t[i].group; };
+  for (int64_t i = 0; i < count; ++i) {
+    const int32_t u = (int32_t)units_of(t[i].n);
+    p.at[i] = p.gsums[group(i)];
+    p.leads[i] = u > 0 && p.at[i] == 0;
+    p.gsums[group(i)] += u;
+  }
+  int32_t sum = 0;
+  for (int64_t g = 0; g < n; ++g) {
+    p.gfirst[g] = sum;
+    sum += p.gsums[g];
+    if (p.gsums[g] > p.most) p.most = p.gsums[g];
+    if (p.gsums[g] == 0) p.none = true;
+  }
+  for (int64_t i = 0; i < count; ++i) p.at[i] += p.gfirst[group(i)];
+  return p;
+}
+
 template <int N, typename F>
-cudaError_t over_table(const lora_grad_tensor* t, int64_t count, int64_t groups, bool stacked, ClipArgs a,
-                       const std::vector<int32_t>& at, const std::vector<int32_t>& sums, F launch) {
+cudaError_t over_table(const lora_grad_tensor* t, int64_t count, int64_t groups, bool stacked, ClipArgs a, const Place& p,
+                       F launch) {
   ClipTable<N> table;
   int64_t i = 0;
   while (i < count) {
     a.count = 0;
     a.units = 0;
     for (; i < count && a.count < N; ++i) {
-      const int32_t u = (int32_t)units_of(t[i].n);
+      const int32_t u = (int32_t)units_of(t[i].n), g = stacked ? 0 : t[i].group;
       if (u == 0) continue;
-      table.e[a.count++] = ClipEntry{t[i].g, t[i].n, a.units, u, at[i], stacked ? -1 : t[i].group, sums[i], t[i].dtype};
+      table.e[a.count++] = ClipEntry{t[i].g, t[i].n, a.units, u, p.at[i], stacked ? -1 : g, p.gfirst[g], p.gsums[g],
+                                     (int16_t)t[i].dtype, (int16_t)p.leads[i]};
       a.units += (int32_t)(u * (stacked ? groups : 1));
     }
     if (a.count == 0) break;
@@ -260,18 +314,39 @@ cudaError_t over_table(const lora_grad_tensor* t, int64_t count, int64_t groups,
 }
 
 template <int N>
-cudaError_t run(const lora_grad_tensor* t, int64_t count, int64_t groups, bool stacked, float max_norm, float* norms,
-                ClipArgs a, const ClipWs& w, const std::vector<int32_t>& at, const std::vector<int32_t>& sums,
+cudaError_t factors_of(const ClipArgs& a, const Place& p, int64_t groups, cudaStream_t st) {
+  Sums<N> s;
+  for (int64_t g0 = 0; g0 < groups; g0 += N) {
+    const int64_t n = groups - g0 < N ? groups - g0 : N;
+    s.group0 = (int32_t)g0;
+    s.each = 0;
+    for (int64_t g = 0; g < n; ++g) s.first[g] = p.gfirst[g0 + g], s.sums[g] = p.gsums[g0 + g];
+    const cudaError_t e = launch_pdl(clip_factor_kernel<N>, dim3((unsigned)n), dim3(256), 0, st, a, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int N>
+cudaError_t run(const lora_grad_tensor* t, int64_t count, int64_t groups, bool stacked, const ClipArgs& a, const Place& p,
                 cudaStream_t st) {
-  cudaError_t e = over_table<N>(t, count, groups, stacked, a, at, sums, [&](const ClipArgs& b, const ClipTable<N>& table) {
+  cudaError_t e = over_table<N>(t, count, groups, stacked, a, p, [&](const ClipArgs& b, const ClipTable<N>& table) {
     return launch_pdl(clip_norm_kernel<N>, dim3((unsigned)b.units), dim3(256), 0, st, b, table);
   });
   if (e != cudaSuccess) return e;
-  e = launch_pdl(clip_factor_kernel, dim3((unsigned)groups), dim3(256), 0, st, (const float*)w.parts,
-                 (const int32_t*)a.gfirst, (const int32_t*)a.gsums, (int)a.per_group, max_norm, norms, w.factor);
-  if (e != cudaSuccess || !(max_norm > 0.f)) return e;
-  return over_table<N>(t, count, groups, stacked, a, at, sums, [&](const ClipArgs& b, const ClipTable<N>& table) {
-    return launch_pdl(clip_scale_kernel<N>, dim3((unsigned)b.units), dim3(256), 0, st, b, table);
+  const bool scales = a.max_norm > 0.f, few = scales && !p.none && p.most <= kFew;
+  if (!few) {
+    if (stacked) {
+      const Sums<1> s{0, p.gsums[0], {0}, {0}};
+      e = launch_pdl(clip_factor_kernel<1>, dim3((unsigned)groups), dim3(256), 0, st, a, s);
+    } else {
+      e = groups <= 64 ? factors_of<64>(a, p, groups, st) : factors_of<kGroups>(a, p, groups, st);
+    }
+    if (e != cudaSuccess || !scales) return e;
+  }
+  return over_table<N>(t, count, groups, stacked, a, p, [&](const ClipArgs& b, const ClipTable<N>& table) {
+    if (few) return launch_pdl(clip_scale_kernel<N, true>, dim3((unsigned)b.units), dim3(256), 0, st, b, table);
+    return launch_pdl(clip_scale_kernel<N, false>, dim3((unsigned)b.units), dim3(256), 0, st, b, table);
   });
 }
 
@@ -286,7 +361,7 @@ extern "C" {
 size_t grad_clip_workspace_bytes(const lora_grad_tensor* tensors, int64_t count, int64_t groups, int stacked) {
   const int64_t sums = check_tensors(tensors, count, groups, stacked);
   ClipWs w;
-  return sums < 0 ? 0 : carve(sums, groups, stacked != 0, nullptr, &w);
+  return sums < 0 ? 0 : carve(sums, groups, nullptr, &w);
 }
 
 lora_status grad_clip(const lora_grad_tensor* tensors, int64_t count, int64_t groups, int stacked, float max_norm,
@@ -299,40 +374,15 @@ lora_status grad_clip(const lora_grad_tensor* tensors, int64_t count, int64_t gr
   try {
     if (overlap(tensors, count, stacked ? groups : 1)) return LORA_ERR_INVALID_ARG;
     ClipWs w;
-    const lora_status e = check_ws(ws, ws_bytes, carve(total, groups, stacked != 0, nullptr, &w));
+    const lora_status e = check_ws(ws, ws_bytes, carve(total, groups, nullptr, &w));
     if (e != LORA_OK) return e;
-    carve(total, groups, stacked != 0, static_cast<char*>(ws), &w);
+    carve(total, groups, static_cast<char*>(ws), &w);
     cudaStream_t st = (cudaStream_t)stream;
-    ClipArgs a = {};
-    a.parts = w.parts;
-    a.factor = w.factor;
-    // where the sums of each tensor begin, those of a group behind one another
-    std::vector<int32_t> at(count), sums(count, 0);
-    if (stacked) {
-      int32_t n = 0;
-      for (int64_t i = 0; i < count; ++i) at[i] = n, n += (int32_t)units_of(tensors[i].n);
-      a.per_group = n;
-    } else {
-      a.gfirst = w.group;
-      a.gsums = w.group + groups;
-      std::vector<int32_t> next(groups, 0), lead(groups, -1);
-      for (int64_t i = 0; i < count; ++i) {
-        const int32_t u = (int32_t)units_of(tensors[i].n), g = tensors[i].group;
-        if (u > 0 && lead[g] < 0) lead[g] = (int32_t)i;
-        next[g] += u;
-      }
-      int32_t n = 0;
-      for (int64_t g = 0; g < groups; ++g) {
-        if (lead[g] >= 0) sums[lead[g]] = next[g];
-        const int32_t k = next[g];
-        next[g] = n;
-        n += k;
-      }
-      for (int64_t i = 0; i < count; ++i) at[i] = next[tensors[i].group], next[tensors[i].group] += (int32_t)units_of(tensors[i].n);
-      CK(cudaMemsetAsync(w.group, 0, 2 * groups * sizeof(int32_t), st));   // groups without tensors
-    }
-    if (count <= kSmallTable) CK(run<kSmallTable>(tensors, count, groups, stacked, max_norm, norms, a, w, at, sums, st));
-    else CK(run<kTable>(tensors, count, groups, stacked, max_norm, norms, a, w, at, sums, st));
+    const Place p = place(tensors, count, groups, stacked != 0);
+    const ClipArgs a{0, 0, w.parts, max_norm, norms, w.factor};
+    if (count <= kSmallTable) CK(run<kSmallTable>(tensors, count, groups, stacked != 0, a, p, st));
+    else if (count <= kMidTable) CK(run<kMidTable>(tensors, count, groups, stacked != 0, a, p, st));
+    else CK(run<kTable>(tensors, count, groups, stacked != 0, a, p, st));
   } catch (...) {                     // no memory on the host
     return LORA_ERR_WORKSPACE;
   }

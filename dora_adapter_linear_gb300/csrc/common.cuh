@@ -99,6 +99,20 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // Lets the next kernel in the stream be scheduled once every CTA of this one has signalled (or exited).
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A kernel that needs nothing of the kernel launched before it may run beside it (early): that one triggers only
+// after its own wait, so what came before it is complete when this one starts.  So that the completion of this
+// kernel still implies that of all before it, its last CTA waits at its end.  Without `early`: the usual wait.
+struct PdlEarly {
+  const bool at_end;
+  __device__ __forceinline__ PdlEarly(bool early, bool last_cta) : at_end(early && last_cta) {
+    if (!early) pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+  }
+  __device__ __forceinline__ ~PdlEarly() {
+    if (at_end) pdl_wait();
+  }
+};
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_prefetch_desc(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");

@@ -64,19 +64,21 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
 // out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; T + T2 where T2 is
 // given; adapters with
 // several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero
+// early: see PdlEarly; behind: S has just been read by multi_proj
 cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr, bool scaled,
-                         float one, const float* each, float* part, bf16* out, cudaStream_t st);
+                         float one, const float* each, float* part, bf16* out, bool early, bool behind, cudaStream_t st);
+// sums [K]: the column sums from multi_colsum, or null
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
-                      bf16* out1, cudaStream_t st);
+                      bf16* out1, int64_t K, const float* csum, bf16* sums, cudaStream_t st);
 // The whole bf16 forward of a few rows (multi_few.cu); part: fp32 [multi_few_splits(K), M, r]
 constexpr int kFewRows = 256;
 int multi_few_splits(int64_t K);
 cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64_t n, const bf16* X, const bf16* W0,
                           const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* part,
                           bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st);
-// out[k] = sum of all rows of S; part [multi_colsum_splits, K]
+// part [multi_colsum_splits, K]: column sums of all rows of S by stretches of rows (starts early)
 int multi_colsum_splits(int64_t M);
-cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, bf16* out, cudaStream_t st);
+cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, cudaStream_t st);
 
 
 // fp32 (multi_f32.cu)
@@ -88,7 +90,8 @@ cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, cons
                            float* out, cudaStream_t st);
 // dA_a = sum G_i^T X_i, dB_a = s_a sum dY_i^T Z_i
 cudaError_t multi_f32_reduce(const MultiPlan& p, int r, int64_t in, const float* X, const float* G, float* dA, int64_t out,
-                             const float* dY, const float* Z, float* dB, float one, const float* each, cudaStream_t st);
+                             const float* dY, const float* Z, float* dB, float one, const float* each, bool early,
+                             cudaStream_t st);
 cudaError_t multi_f32_colsum(int64_t M, int64_t K, const float* S, float* out, cudaStream_t st);
 
 }  // namespace lg

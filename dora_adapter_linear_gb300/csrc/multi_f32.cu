@@ -13,8 +13,8 @@ namespace {
 __device__ __forceinline__ float scale_of(float one, const float* each, int a) { return each ? __ldg(each + a) : one; }
 
 // ------------------------------------------------------------------ rank-r products of rows
-// A CTA has eight rows of an item and all j of their adapter; the rows pass through shared memory 1024 columns
-// at a time, so a factor is read once for eight rows.  Up to eight warps take the j of U_a [r, K] in turn; of
+// A CTA has eight rows of an item, all j of their adapter and its cluster rank's share of K; the rows pass through
+// shared memory 1024 columns at a time, so a factor is read once for eight rows.  Up to eight warps take the j of U_a [r, K] in turn; of
 // U_a [K, r] (KR) a thread keeps one j, and the threads' shares of k meet in shared memory.
 constexpr int kCols = 1024, kRows = 8;   // kItemRows is a multiple of kRows
 
@@ -32,24 +32,29 @@ template <bool KR>
 __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F32Proj a) {
   __shared__ float x[kRows][kCols];
   __shared__ float sum[kRows][128];
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const int sub = (int)(blockIdx.x / ranks);
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const int4 item = a.p.items[blockIdx.x / (kItemRows / kRows)];   // there is room for as many as the grid has
+  const int4 item = a.p.items[sub / (kItemRows / kRows)];   // there is room for as many as the grid has
   const int r = a.r, with = a.p.head[kHeadRows], items = a.p.head[kHeadItems];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (a.p.M - with) * r; i += (int64_t)gridDim.x * 256) {
     const int64_t at = (int64_t)a.p.order[with + i / r] * r + i % r;     // rows without adapter
     if (a.plain) a.plain[at] = 0.f;
     if (a.scaled) a.scaled[at] = 0.f;
   }
-  if ((int)blockIdx.x / (kItemRows / kRows) >= items) return;
-  const int first = (int)blockIdx.x % (kItemRows / kRows) * kRows, rows = min(kRows, item.z - first);
+  if (sub / (kItemRows / kRows) >= items) return;                  // the whole cluster
+  const int first = sub % (kItemRows / kRows) * kRows, rows = min(kRows, item.z - first);
   if (rows <= 0) return;
+  const int64_t begin = a.K / 8 * rank / ranks * 8, end = a.K / 8 * (rank + 1) / ranks * 8;   // K is a multiple of 8
   const int32_t* order = a.p.order + item.y + first;
   const float* u = a.U + (int64_t)item.x * r * a.K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < kRows * 128; i += 256) (&sum[0][0])[i] = 0.f;
-  for (int64_t k0 = 0; k0 < a.K; k0 += kCols) {
-    const int cols = (int)min((int64_t)kCols, a.K - k0);
+  for (int64_t k0 = begin; k0 < end; k0 += kCols) {
+    const int cols = (int)min((int64_t)kCols, end - k0);
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * kCols / 4; i += 256) {
       const int m = i / (kCols / 4), c = i % (kCols / 4) * 4;
@@ -98,14 +103,20 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
       }
     }
   }
-  __syncthreads();
+  cluster_sync_all();
   const float f = scale_of(a.one, a.each, item.x);
-  for (int i = threadIdx.x; i < rows * r; i += 256) {
+  for (int i = (int)rank * 256 + threadIdx.x; i < rows * r; i += 256 * (int)ranks) {
     const int64_t at = (int64_t)order[i / r] * r + i % r;
-    const float v = sum[i / r][i % r];
+    float v = 0.f;
+    for (uint32_t q = 0; q < ranks; ++q) {
+      float s;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(s) : "r"(mapa_shared(smem_u32(&sum[i / r][i % r]), q)));
+      v += s;
+    }
     if (a.plain) a.plain[at] = v;
     if (a.scaled) a.scaled[at] = v * f;
   }
+  cluster_sync_all();           // no CTA leaves while another reads its sums
 }
 
 // ------------------------------------------------------------------ shared product and rank-r update
@@ -129,9 +140,13 @@ struct F32Gemm {
 
 template <bool MN>
 __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
-  __shared__ float As[2][kSlab][kTile + 4];
-  __shared__ float Bs[2][kSlab][kTile + 4];
-  float (*part)[kTile + 4] = As[0];                   // the sums, once the slabs are done
+  // two buffers of S and of W by k; column c of k lies at c ^ 4 (k / 4 % 8): a row's four k, spread over the lanes, are
+  // stored without bank conflicts, and four columns stay together.  Behind the slabs: the sums, and P of eight j.
+  __shared__ __align__(16) float pool[4 * kSlab * kTile];
+  float (*As)[kSlab][kTile] = reinterpret_cast<float (*)[kSlab][kTile]>(pool);
+  float (*Bs)[kSlab][kTile] = As + 2;
+  float (*part)[kTile + 4] = reinterpret_cast<float (*)[kTile + 4]>(pool);
+  float* ps = pool + kTile * (kTile + 4);
   __shared__ int ids[kTile];
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -145,34 +160,37 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
   const int slabs = (int)((K + kSlab - 1) / kSlab), s0 = (int)((int64_t)slabs * rank / ranks),
             s1 = (int)((int64_t)slabs * (rank + 1) / ranks);
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  // a thread brings four k, and four 16 behind them, of one row of a K-major operand; of W [K, N] four columns of two k
-  const int lr = tid & 63, lk = (tid >> 6) * 4;
-  const bool row = m0 + lr < a.p.M, col = n0 + lr < N;
-  const float* S = a.S + (row ? m0 + lr : 0) * K;
-  const float* W = MN ? a.W : a.W + (col ? n0 + lr : 0) * K;
+  // a thread brings four k of two rows of a K-major operand, eight lanes a row; of W [K, N] four columns of two k
+  const int lr = tid >> 3, lk = (tid & 7) * 4, lc = (tid & 15) * 4;
+  const float *S[2], *W[2];
+  bool row[2], col[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    row[i] = m0 + lr + 32 * i < a.p.M;
+    S[i] = a.S + (row[i] ? m0 + lr + 32 * i : 0) * K;
+    col[i] = MN ? n0 + lc < N : n0 + lr + 32 * i < N;
+    W[i] = MN ? a.W + (col[i] ? n0 + lc : 0) : a.W + (col[i] ? n0 + lr + 32 * i : 0) * K;
+  }
   auto fetch = [&](int s, float4 (&x)[2], float4 (&w)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t k = (int64_t)s * kSlab + lk + 16 * i;
-      x[i] = s < s1 && row && k < K ? __ldg(reinterpret_cast<const float4*>(S + k)) : none;
-      if (MN) {
-        const int64_t kk = (int64_t)s * kSlab + (tid >> 4) + 16 * i, c = n0 + (tid & 15) * 4;
-        w[i] = s < s1 && kk < K && c < N ? __ldg(reinterpret_cast<const float4*>(W + kk * N + c)) : none;
-      } else {
-        w[i] = s < s1 && col && k < K ? __ldg(reinterpret_cast<const float4*>(W + k)) : none;
-      }
+      const int64_t k = (int64_t)s * kSlab + lk, kk = (int64_t)s * kSlab + (tid >> 4) + 16 * i;
+      x[i] = s < s1 && row[i] && k < K ? __ldg(reinterpret_cast<const float4*>(S[i] + k)) : none;
+      if (MN) w[i] = s < s1 && col[i] && kk < K ? __ldg(reinterpret_cast<const float4*>(W[i] + kk * N)) : none;
+      else w[i] = s < s1 && col[i] && k < K ? __ldg(reinterpret_cast<const float4*>(W[i] + k)) : none;
     }
   };
   auto put = [&](int b, const float4 (&x)[2], const float4 (&w)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      const int c = (lr + 32 * i) ^ lk, kk = (tid >> 4) + 16 * i;       // lk = 4 (k / 4 % 8)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) As[b][lk + 16 * i + j][lr] = p[j];
-      if (MN) *reinterpret_cast<float4*>(&Bs[b][(tid >> 4) + 16 * i][(tid & 15) * 4]) = w[i];
+      for (int j = 0; j < 4; ++j) As[b][lk + j][c] = p[j];
+      if (MN) *reinterpret_cast<float4*>(&Bs[b][kk][lc ^ ((kk & 28))]) = w[i];
       else
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Bs[b][lk + 16 * i + j][lr] = q[j];
+        for (int j = 0; j < 4; ++j) Bs[b][lk + j][c] = q[j];
     }
   };
   float run[8][8] = {};
@@ -186,10 +204,11 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kSlab / kGroups; ++k) {
       float p[8], q[8];
+      const int kk = group * 8 + k, swap = kk & 28;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 u = *reinterpret_cast<const float4*>(&As[b][group * 8 + k][32 * h + ty * 4]),
-                     v = *reinterpret_cast<const float4*>(&Bs[b][group * 8 + k][32 * h + tx * 4]);
+        const float4 u = *reinterpret_cast<const float4*>(&As[b][kk][(32 * h + ty * 4) ^ swap]),
+                     v = *reinterpret_cast<const float4*>(&Bs[b][kk][(32 * h + tx * 4) ^ swap]);
         p[4 * h] = u.x, p[4 * h + 1] = u.y, p[4 * h + 2] = u.z, p[4 * h + 3] = u.w;
         q[4 * h] = v.x, q[4 * h + 1] = v.y, q[4 * h + 2] = v.z, q[4 * h + 3] = v.w;
       }
@@ -219,7 +238,6 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
   // this thread's column of every fourth of this CTA's rows
   const int own = kTile / (int)ranks, c = tid & 63, r0 = (int)rank * own + group, each = own / kGroups;
   const uint32_t mine = smem_u32(&part[0][0]);
-  float* ps = &Bs[0][0][0];                           // [64][8] P of eight j
   const float bias = a.bias && n0 + c < N ? __ldg(a.bias + n0 + c) : 0.f;
   float v[16], t[16];
 #pragma unroll
@@ -287,12 +305,12 @@ struct F32Reduce {
   float one;
   const float* each;
   int blocks0;                    // column blocks of the first
+  bool early;                     // see pdl_early
 };
 
 __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__ F32Reduce a) {
   __shared__ float red[8][16][33];
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+  const PdlEarly order(a.early, blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1);
   const int which = (int)blockIdx.x >= a.blocks0, ad = blockIdx.y, j0 = blockIdx.z * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = a.r;
   const int64_t K = a.K[which], k0 = (int64_t)((int)blockIdx.x - (which ? a.blocks0 : 0)) * 32, k = k0 + lane;
@@ -334,8 +352,7 @@ __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__
 // sums of all rows, 32 columns a CTA, a warp every eighth row
 __global__ void __launch_bounds__(256) f32_colsum_kernel(int64_t M, int64_t K, const float* S, float* out) {
   __shared__ float red[8][32];
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+  const PdlEarly order(true, blockIdx.x == gridDim.x - 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t k = (int64_t)blockIdx.x * 32 + lane;
   float total = 0.f;
@@ -389,10 +406,22 @@ cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
 cudaError_t multi_f32_proj(const MultiPlan& p, int64_t K, int r, const float* S, const float* U, bool kr, float one,
                            const float* each, float* plain, float* scaled, cudaStream_t st) {
   const F32Proj a{p, K, r, S, U, one, each, plain, scaled};
-  const int64_t n = multi_items(p.M, p.n) * (kItemRows / kRows);
-  const dim3 grid((unsigned)(n > 0 ? n : 1));
-  return kr ? launch_pdl(f32_proj_kernel<true>, grid, dim3(256), 0, st, a)
-            : launch_pdl(f32_proj_kernel<false>, grid, dim3(256), 0, st, a);
+  const int64_t n = multi_items(p.M, p.n) * (kItemRows / kRows), slots = 3 * num_sms_current();
+  int ranks = 1;                // shares of at least 128 columns, while there is room for their CTAs
+  while (ranks < 8 && n * ranks * 2 <= slots && K >= ranks * 2 * 128) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(n * ranks), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t e = kr ? cudaLaunchKernelEx(&cfg, f32_proj_kernel<true>, a) : cudaLaunchKernelEx(&cfg, f32_proj_kernel<false>, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, const float* S, const float* W, bool mn,
@@ -403,9 +432,10 @@ cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, cons
 }
 
 cudaError_t multi_f32_reduce(const MultiPlan& p, int r, int64_t in, const float* X, const float* G, float* dA, int64_t out,
-                             const float* dY, const float* Z, float* dB, float one, const float* each, cudaStream_t st) {
+                             const float* dY, const float* Z, float* dB, float one, const float* each, bool early,
+                             cudaStream_t st) {
   const int b0 = (int)blocks(in, 32);
-  const F32Reduce a{p, r, {in, out}, {X, dY}, {G, Z}, {dA, dB}, one, each, b0};
+  const F32Reduce a{p, r, {in, out}, {X, dY}, {G, Z}, {dA, dB}, one, each, b0, early};
   return launch_pdl(f32_reduce_kernel, dim3(b0 + blocks(out, 32), (unsigned)p.n, blocks(r, 16)), dim3(256), 0, st, a);
 }
 

@@ -211,6 +211,8 @@ struct ReduceArgs {
   bool scaled, kr;            // kr: out_a [K, R], else [R, K]
   bf16* out;
   float* part;                // [partials] x [K, R] or [R, K]
+  bool early;                 // see PdlEarly
+  int behind;                 // CTAs a cluster of the pass that has just read S, or 0
 };
 
 template <int R, bool TWO>
@@ -221,12 +223,24 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
   int32_t* rows = reinterpret_cast<int32_t*>(smem + C::NST * C::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t K = a.K;
-  const int groups = (int)((K + 127) / 128), mine = (int)blockIdx.x / groups;
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+  const int groups = (int)((K + 127) / 128), all = (int)gridDim.x / groups;
+  const PdlEarly order(a.early, blockIdx.x == gridDim.x - 1);
+  int mine = (int)blockIdx.x / groups, group = (int)blockIdx.x - mine * groups;
+  if (a.behind) {
+    // the columns that the pass before this one read last come first, while they are in L2: it walked along the
+    // rows, each rank of its clusters through its own stretch
+    const int i = (int)blockIdx.x / all, ranks = a.behind, share = (groups + ranks - 1) / ranks;
+    mine = (int)blockIdx.x - i * all;
+    // i-th of the groups, counted down from the ends of the stretches
+    int left = i;
+    group = -1;
+    for (int d = share - 1; d >= 0 && group < 0; --d)
+      for (int q = 0; q < ranks && group < 0; ++q)
+        if (q * share + d < groups && left-- == 0) group = q * share + d;
+  }
   const int4 piece = a.p.pieces[mine];             // there is room for as many as the grid has
   if (mine >= a.p.head[kHeadPieces]) return;
-  const int64_t k0 = (int64_t)((int)blockIdx.x - mine * groups) * 128;
+  const int64_t k0 = (int64_t)group * 128;
   for (int i = threadIdx.x; i < piece.z; i += 128) rows[i] = a.p.order[piece.y + i];
   __syncthreads();
   const int stages = (piece.z + 31) / 32;
@@ -315,17 +329,28 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
 }
 
 // The gradients of adapters with several pieces, and zeros for those without rows; eight elements a thread.
-// Both of a backward's stacks in one launch.
+// Both of a backward's stacks in one launch, and the column sums of dY.
 struct SumArgs {
   MultiPlan p;
   int64_t size[2];            // elements of one adapter
   const float* part[2];
   bf16* out[2];
+  int splits;                 // of the column sums; 0: none
+  int64_t K;
+  const float* csum;
+  bf16* sums;
 };
 __global__ void __launch_bounds__(256) multi_sum_kernel(const __grid_constant__ SumArgs a) {
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   const int ad = blockIdx.y, which = blockIdx.z;
+  if (ad == 0 && which == 0 && a.splits)
+    for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < a.K; k += (int64_t)gridDim.x * 256) {
+      float t = 0.f;
+#pragma unroll 8
+      for (int s = 0; s < a.splits; ++s) t += a.csum[s * a.K + k];
+      a.sums[k] = __float2bfloat16_rn(t);
+    }
   const int first = a.p.pstart[ad], count = a.p.pstart[ad + 1] - first;
   if (count == 1) return;
   const int64_t size = a.size[which];
@@ -347,8 +372,7 @@ __global__ void __launch_bounds__(256) multi_sum_kernel(const __grid_constant__ 
 // column sums of 64 columns and one split of the rows a CTA: part [splits, K]
 __global__ void __launch_bounds__(256) multi_colsum_kernel(int64_t M, int64_t K, int rows, const bf16* S, float* part) {
   __shared__ float red[32][64];
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
+  const PdlEarly order(true, blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1);
   const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const int64_t k = (int64_t)blockIdx.x * 64 + c * 8, m1 = min(M, (int64_t)(blockIdx.y + 1) * rows);
   float v[8] = {};
@@ -375,15 +399,20 @@ __global__ void __launch_bounds__(256) multi_colsum_kernel(int64_t M, int64_t K,
   }
 }
 
+// as many CTAs to a cluster as two an SM have room for, each with two rounds of the ring at least
+template <int R, bool KR>
+int proj_ranks(int64_t items, int64_t K) {
+  const int64_t steps = (K + 127) / 128, slots = 2 * num_sms_current();
+  int ranks = 1;
+  while (ranks < 8 && items * ranks * 2 <= slots && steps >= ranks * 2 * 2 * (Proj<R, KR>::NST - 1)) ranks *= 2;
+  return ranks;
+}
 template <int R, bool KR>
 cudaError_t proj_launch(const ProjArgs& a, int64_t items, cudaStream_t st) {
   using C = Proj<R, KR>;
   const cudaError_t e = allow_smem<multi_proj_mma<R, KR>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  // as many CTAs to a cluster as two an SM have room for, each with two rounds of the ring at least
-  const int64_t steps = (a.K + 127) / 128, slots = 2 * num_sms_current();
-  int ranks = 1;
-  while (ranks < 8 && items * ranks * 2 <= slots && steps >= ranks * 2 * 2 * (C::NST - 1)) ranks *= 2;
+  const int ranks = proj_ranks<R, KR>(items, a.K);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -430,21 +459,30 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
 }
 
 cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr,
-                         bool scaled, float one, const float* each, float* part, bf16* out, cudaStream_t st) {
-  const ReduceArgs a{p, K, S, T, T2, one, each, scaled, kr, out, part};
+                         bool scaled, float one, const float* each, float* part, bf16* out, bool early, bool behind,
+                         cudaStream_t st) {
   const int64_t pieces = multi_pieces(p.M, p.n);
+  ReduceArgs a{p, K, S, T, T2, one, each, scaled, kr, out, part, early, 0};
   switch (r) {
-#define CASE(R) \
-  case R: return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
-    RANKS(CASE) MORE_RANKS(CASE)
+#define CASE(R)                                                                       \
+  case R:                                                                             \
+    if (behind) a.behind = proj_ranks<R, true>(multi_items(p.M, p.n), K);             \
+    return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
+    RANKS(CASE)
+#undef CASE
+#define CASE(R)                                                                       \
+  case R:                                                                             \
+    if (behind) a.behind = proj_ranks<R - 64, true>(multi_items(p.M, p.n), K);        \
+    return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
+    MORE_RANKS(CASE)
 #undef CASE
   }
   return cudaErrorInvalidValue;
 }
 
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
-                      bf16* out1, cudaStream_t st) {
-  const SumArgs a{p, {size0, size1}, {part0, part1}, {out0, out1}};
+                      bf16* out1, int64_t K, const float* csum, bf16* sums, cudaStream_t st) {
+  const SumArgs a{p, {size0, size1}, {part0, part1}, {out0, out1}, sums ? multi_colsum_splits(p.M) : 0, K, csum, sums};
   const int64_t most = size0 > size1 ? size0 : size1, blocks = (most + 2047) / 2048;
   return launch_pdl(multi_sum_kernel, dim3((unsigned)(blocks < 256 ? blocks : 256), (unsigned)p.n, 2), dim3(256), 0, st, a);
 }
@@ -453,11 +491,10 @@ int multi_colsum_splits(int64_t M) {
   const int64_t n = (M + 255) / 256;
   return (int)(n < 64 ? n : 64);
 }
-cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, bf16* out, cudaStream_t st) {
+cudaError_t multi_colsum(int64_t M, int64_t K, const bf16* S, float* part, cudaStream_t st) {
   const int splits = multi_colsum_splits(M), rows = (int)((M + splits - 1) / splits);
-  const cudaError_t e = launch_pdl(multi_colsum_kernel, dim3((unsigned)((K + 63) / 64), (unsigned)splits), dim3(256), 0, st,
-                                   M, K, rows, S, part);
-  return e != cudaSuccess ? e : sum_splits<bf16>(part, splits, K, nullptr, out, st);
+  return launch_pdl(multi_colsum_kernel, dim3((unsigned)((K + 63) / 64), (unsigned)splits), dim3(256), 0, st, M, K, rows, S,
+                    part);
 }
 
 }  // namespace lg
