@@ -26,7 +26,7 @@ struct MultiWs {
   void* P;                    // [M, r] z or s g; bf16: s z or s g
   void* P2;                   // bf16 backward: what the rounding of s g leaves
   void* Z;                    // [M, r] z recomputed by the backward
-  float* few;                 // forward of a few bf16 rows: z by stretches of K
+  float* few;                 // forward of a few bf16 rows: s z in fp32
   float *pa, *pb, *csum;      // bf16 backward: partials of dA and dB, column sums
 };
 size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
@@ -37,7 +37,7 @@ size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   w->P = c.take<char>(rank);
   w->Z = bwd ? c.take<char>(rank) : nullptr;
   w->P2 = bwd && bf ? c.take<char>(rank) : nullptr;
-  w->few = !bwd && bf && sh.M <= kFewRows ? c.take<float>((size_t)multi_few_splits(sh.d_in) * sh.M * sh.r) : nullptr;
+  w->few = !bwd && bf && sh.M <= kFewRows ? c.take<float>((size_t)sh.M * sh.r) : nullptr;
   w->pa = bwd && bf ? c.take<float>(parts * sh.d_in) : nullptr;
   w->pb = bwd && bf ? c.take<float>(parts * sh.d_out) : nullptr;
   w->csum = bwd && bf ? c.take<float>((size_t)multi_colsum_splits(sh.M) * sh.d_out) : nullptr;
@@ -107,7 +107,7 @@ cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiW
                     const bf16* A, const bf16* B, const bf16* bias, Scale s, bf16* Y, bf16* Z, cudaStream_t st) {
   const int r = (int)sh.r;
   if (sh.M <= kFewRows)
-    return multi_few_fwd(p, sh.d_out, sh.d_in, r, sh.n, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
+    return multi_few_fwd(p, sh.d_out, sh.d_in, r, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
                          wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);
   const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, st);

@@ -120,12 +120,12 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
 }
 
 // ------------------------------------------------------------------ shared product and rank-r update
-// 64 x 64 outputs a CTA, 8 x 8 a thread (four shared-memory accesses for 64 FMAs; with 4 x 4 the accesses took as long
-// as the FMAs), K in slabs of 32 through two buffers, of which each of four groups of two warps takes eight.  The
-// CTAs of a cluster share K and add their sums through distributed shared memory, each finishing its share of
-// the rows.  There a thread has one column, and takes its adapter's factor anew only where the next row has
-// another one.
-constexpr int kTile = 64, kSlab = 32, kGroups = 4;
+// 64 x 128 outputs a CTA, 8 x 16 a thread (six 16-byte accesses of shared memory for 128 FMAs: a warp's access takes
+// four cycles of the SM's one port, so that 8 x 8 with four for 64 took as long as the FMAs, and the two did not
+// overlap), K in slabs of 16 through two buffers, of which each of two groups of two warps takes eight.  The CTAs of a
+// cluster share K and add their sums through distributed shared memory, each finishing its share of the rows.
+// There a thread has one column, and takes its adapter's factor anew only where the next row has another one.
+constexpr int kTileM = 64, kTileN = 128, kSlab = 16, kGroups = 2, kGemmThreads = 64 * kGroups;
 
 struct F32Gemm {
   MultiPlan p;
@@ -139,15 +139,16 @@ struct F32Gemm {
 };
 
 template <bool MN>
-__global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
-  // two buffers of S and of W by k; column c of k lies at c ^ 4 (k / 4 % 8): a row's four k, spread over the lanes, are
-  // stored without bank conflicts, and four columns stay together.  Behind the slabs: the sums, and P of eight j.
-  __shared__ __align__(16) float pool[4 * kSlab * kTile];
-  float (*As)[kSlab][kTile] = reinterpret_cast<float (*)[kSlab][kTile]>(pool);
-  float (*Bs)[kSlab][kTile] = As + 2;
-  float (*part)[kTile + 4] = reinterpret_cast<float (*)[kTile + 4]>(pool);
-  float* ps = pool + kTile * (kTile + 4);
-  __shared__ int ids[kTile];
+__global__ void __launch_bounds__(kGemmThreads, 2) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
+  // two buffers of S and of W by k; column c of k lies at c ^ 8 (k / 4 % 4): a row's four k, spread over the lanes, are
+  // stored without bank conflicts, and four columns stay together.  Later the sums lie there.
+  constexpr int kPitch = kTileN + 4;
+  __shared__ __align__(16) float pool[kTileM * kPitch];
+  __shared__ float ps[8][8];                          // P of eight rows and eight j
+  __shared__ int ids[kTileM];
+  float (*As)[kSlab][kTileM] = reinterpret_cast<float (*)[kSlab][kTileM]>(pool);
+  float (*Bs)[kSlab][kTileN] = reinterpret_cast<float (*)[kSlab][kTileN]>(pool + 2 * kSlab * kTileM);
+  float (*part)[kPitch] = reinterpret_cast<float (*)[kPitch]>(pool);
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
@@ -155,46 +156,56 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
   if (threadIdx.x == 0) pdl_trigger();
   const int tid = threadIdx.x, group = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;   // rows 4 ty, 4 ty + 32 and on
   const int64_t K = a.K, N = a.N;
-  const int tile = (int)(blockIdx.x / ranks), wide = (int)((N + kTile - 1) / kTile);
-  const int64_t m0 = (int64_t)(tile / wide) * kTile, n0 = (int64_t)(tile % wide) * kTile;
+  const int tile = (int)(blockIdx.x / ranks), wide = (int)((N + kTileN - 1) / kTileN);
+  const int64_t m0 = (int64_t)(tile / wide) * kTileM, n0 = (int64_t)(tile % wide) * kTileN;
   const int slabs = (int)((K + kSlab - 1) / kSlab), s0 = (int)((int64_t)slabs * rank / ranks),
             s1 = (int)((int64_t)slabs * (rank + 1) / ranks);
   const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  // a thread brings four k of two rows of a K-major operand, eight lanes a row; of W [K, N] four columns of two k
-  const int lr = tid >> 3, lk = (tid & 7) * 4, lc = (tid & 15) * 4;
-  const float *S[2], *W[2];
-  bool row[2], col[2];
+  // a thread brings four k of two rows of S and of four rows of W [N, K], four lanes a row; of W [K, N] four columns
+  // of every fourth k
+  const int lr = tid >> 2, lk = (tid & 3) * 4, lc = (tid & 31) * 4;
+  const float* S[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    row[i] = m0 + lr + 32 * i < a.p.M;
-    S[i] = a.S + (row[i] ? m0 + lr + 32 * i : 0) * K;
-    col[i] = MN ? n0 + lc < N : n0 + lr + 32 * i < N;
-    W[i] = MN ? a.W + (col[i] ? n0 + lc : 0) : a.W + (col[i] ? n0 + lr + 32 * i : 0) * K;
+  for (int i = 0; i < 2; ++i) S[i] = m0 + lr + 32 * i < a.p.M ? a.S + (m0 + lr + 32 * i) * K : nullptr;
+  const float* W[MN ? 1 : 4];
+#pragma unroll
+  for (int i = 0; i < (MN ? 1 : 4); ++i) {
+    const int64_t c = n0 + (MN ? lc : lr + 32 * i);
+    W[i] = c < N ? a.W + (MN ? c : c * K) : nullptr;
   }
-  auto fetch = [&](int s, float4 (&x)[2], float4 (&w)[2]) {
+  auto fetch = [&](int s, float4 (&x)[2], float4 (&w)[4]) {
+    const int64_t k = (int64_t)s * kSlab + lk;
+    const bool on = s < s1 && k < K;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t k = (int64_t)s * kSlab + lk, kk = (int64_t)s * kSlab + (tid >> 4) + 16 * i;
-      x[i] = s < s1 && row[i] && k < K ? __ldg(reinterpret_cast<const float4*>(S[i] + k)) : none;
-      if (MN) w[i] = s < s1 && col[i] && kk < K ? __ldg(reinterpret_cast<const float4*>(W[i] + kk * N)) : none;
-      else w[i] = s < s1 && col[i] && k < K ? __ldg(reinterpret_cast<const float4*>(W[i] + k)) : none;
-    }
+    for (int i = 0; i < 2; ++i) x[i] = on && S[i] ? __ldg(reinterpret_cast<const float4*>(S[i] + k)) : none;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (MN) {
+        const int64_t kk = (int64_t)s * kSlab + (tid >> 5) + 4 * i;
+        w[i] = s < s1 && kk < K && W[0] ? __ldg(reinterpret_cast<const float4*>(W[0] + kk * N)) : none;
+      } else {
+        w[i] = on && W[MN ? 0 : i] ? __ldg(reinterpret_cast<const float4*>(W[MN ? 0 : i] + k)) : none;
+      }
   };
-  auto put = [&](int b, const float4 (&x)[2], const float4 (&w)[2]) {
+  auto put = [&](int b, const float4 (&x)[2], const float4 (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      const int c = (lr + 32 * i) ^ lk, kk = (tid >> 4) + 16 * i;       // lk = 4 (k / 4 % 8)
+      const float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) As[b][lk + j][c] = p[j];
-      if (MN) *reinterpret_cast<float4*>(&Bs[b][kk][lc ^ ((kk & 28))]) = w[i];
+      for (int j = 0; j < 4; ++j) As[b][lk + j][(lr + 32 * i) ^ (2 * lk)] = p[j];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int kk = (tid >> 5) + 4 * i;
+      const float q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if (MN) *reinterpret_cast<float4*>(&Bs[b][kk][lc ^ (2 * (kk & 12))]) = w[i];
       else
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Bs[b][lk + j][c] = q[j];
+        for (int j = 0; j < 4; ++j) Bs[b][lk + j][(lr + 32 * i) ^ (2 * lk)] = q[j];
     }
   };
-  float run[8][8] = {};
-  float4 x[2], w[2];
+  float run[8][16] = {};
+  float4 x[2], w[4];
   fetch(s0, x, w);
   put(0, x, w);
   for (int s = s0; s < s1; ++s) {
@@ -203,19 +214,22 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kSlab / kGroups; ++k) {
-      float p[8], q[8];
-      const int kk = group * 8 + k, swap = kk & 28;
+      float p[8], q[16];
+      const int kk = group * 8 + k, swap = 2 * (kk & 12);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float4 u = *reinterpret_cast<const float4*>(&As[b][kk][(32 * h + ty * 4) ^ swap]),
-                     v = *reinterpret_cast<const float4*>(&Bs[b][kk][(32 * h + tx * 4) ^ swap]);
+        const float4 u = *reinterpret_cast<const float4*>(&As[b][kk][(32 * h + ty * 4) ^ swap]);
         p[4 * h] = u.x, p[4 * h + 1] = u.y, p[4 * h + 2] = u.z, p[4 * h + 3] = u.w;
+      }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float4 v = *reinterpret_cast<const float4*>(&Bs[b][kk][(32 * h + tx * 4) ^ swap]);
         q[4 * h] = v.x, q[4 * h + 1] = v.y, q[4 * h + 2] = v.z, q[4 * h + 3] = v.w;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
+        for (int j = 0; j < 16; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
     }
     put(b ^ 1, x, w);
   }
@@ -226,70 +240,72 @@ __global__ void __launch_bounds__(256, 2) f32_gemm_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 4; ++h) {
           float4* at = reinterpret_cast<float4*>(&part[32 * (i >> 2) + ty * 4 + (i & 3)][32 * h + tx * 4]);
           const float4 old = q == 0 ? none : *at;
           *at = make_float4(old.x + run[i][4 * h], old.y + run[i][4 * h + 1], old.z + run[i][4 * h + 2],
                             old.w + run[i][4 * h + 3]);
         }
   }
-  if (tid < kTile) ids[tid] = m0 + tid < a.p.M ? a.p.ids[m0 + tid] : -1;
+  if (tid < kTileM) ids[tid] = m0 + tid < a.p.M ? a.p.ids[m0 + tid] : -1;
   cluster_sync_all();
-  // this thread's column of every fourth of this CTA's rows
-  const int own = kTile / (int)ranks, c = tid & 63, r0 = (int)rank * own + group, each = own / kGroups;
+  // this thread's column of this CTA's share of the rows, eight rows at a time
+  const int c = tid, r0 = kTileM * (int)rank / (int)ranks, r1 = kTileM * ((int)rank + 1) / (int)ranks;
   const uint32_t mine = smem_u32(&part[0][0]);
   const float bias = a.bias && n0 + c < N ? __ldg(a.bias + n0 + c) : 0.f;
-  float v[16], t[16];
+  for (int e0 = r0; e0 < r1; e0 += 8) {
+    float v[8], t[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = t[i] = 0.f;
-  for (uint32_t q = 0; q < ranks; ++q) {
-    const uint32_t from = mapa_shared(mine + (r0 * (kTile + 4) + c) * 4, q);
+    for (int i = 0; i < 8; ++i) v[i] = t[i] = 0.f;
+    for (uint32_t q = 0; q < ranks; ++q) {
+      const uint32_t from = mapa_shared(mine + (e0 * kPitch + c) * 4, q);
+      float f[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < each) {
-        float f;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(from + i * kGroups * (kTile + 4) * 4));
-        v[i] += f;
+      for (int i = 0; i < 8; ++i) {
+        f[i] = 0.f;
+        if (e0 + i < r1) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f[i]) : "r"(from + i * kPitch * 4));
       }
-  }
-  for (int j0 = 0; j0 < a.r; j0 += 8) {
-    __syncthreads();
-    for (int i = tid; i < own * 8; i += 256) {
-      const int m = (int)rank * own + (i >> 3), j = j0 + (i & 7);
-      ps[m * 8 + (i & 7)] = ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
-    }
-    __syncthreads();
-    if (n0 + c < N) {
-      int have = -1;
-      float u[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i >= each) break;
-        const int m = r0 + kGroups * i, ad = ids[m];
-        if (ad < 0) continue;
-        if (ad != have) {
-          have = ad;
-          const float* f = a.U + (int64_t)ad * a.r * N;
+      for (int i = 0; i < 8; ++i) v[i] += f[i];
+    }
+    for (int j0 = 0; j0 < a.r; j0 += 8) {
+      __syncthreads();
+      if (tid < 64) {
+        const int m = e0 + (tid >> 3), j = j0 + (tid & 7);
+        ps[tid >> 3][tid & 7] = m < r1 && ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
+      }
+      __syncthreads();
+      if (n0 + c < N) {
+        int have = -1;
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (e0 + i >= r1) break;
+          const int ad = ids[e0 + i];
+          if (ad < 0) continue;
+          if (ad != have) {
+            have = ad;
+            const float* f = a.U + (int64_t)ad * a.r * N;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              u[q] = j0 + q < a.r ? __ldg(MN ? f + (int64_t)(j0 + q) * N + n0 + c : f + (n0 + c) * a.r + j0 + q) : 0.f;
+          }
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            u[q] = j0 + q < a.r ? __ldg(MN ? f + (int64_t)(j0 + q) * N + n0 + c : f + (n0 + c) * a.r + j0 + q) : 0.f;
+            if (j0 + q < a.r) t[i] = fmaf(ps[i][q], u[q], t[i]);
         }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (j0 + q < a.r) t[i] = fmaf(ps[8 * m + q], u[q], t[i]);
       }
     }
-  }
-  if (n0 + c < N)
+    if (n0 + c < N)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int m = r0 + kGroups * i;
-      if (i >= each || m0 + m >= a.p.M) break;
-      const int ad = ids[m];
-      float y = v[i];
-      if (ad >= 0) y += a.scaled ? scale_of(a.one, a.each, ad) * t[i] : t[i];
-      a.out[(m0 + m) * N + n0 + c] = y + bias;
-    }
+      for (int i = 0; i < 8; ++i) {
+        if (e0 + i >= r1 || m0 + e0 + i >= a.p.M) break;
+        const int ad = ids[e0 + i];
+        float y = v[i];
+        if (ad >= 0) y += a.scaled ? scale_of(a.one, a.each, ad) * t[i] : t[i];
+        a.out[(m0 + e0 + i) * N + n0 + c] = y + bias;
+      }
+  }
   cluster_sync_all();           // no CTA leaves while another reads its sums
 }
 
@@ -305,7 +321,7 @@ struct F32Reduce {
   float one;
   const float* each;
   int blocks0;                    // column blocks of the first
-  bool early;                     // see pdl_early
+  bool early;                     // see PdlEarly
 };
 
 __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__ F32Reduce a) {
@@ -377,13 +393,15 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 
 template <bool MN>
 cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
-  const int64_t tiles = (int64_t)blocks(a.N, kTile) * blocks(a.p.M, kTile), slabs = blocks(a.K, kSlab), sms = num_sms_current();
-  // the share of K that finishes soonest: whole rounds of a CTA an SM, and what a cluster costs
+  const int64_t tiles = (int64_t)blocks(a.N, kTileN) * blocks(a.p.M, kTileM), slabs = blocks(a.K, kSlab), sms = num_sms_current();
+  // the share of K that finishes soonest: what the fullest SM has, and what a cluster costs; a lone CTA of an SM keeps
+  // little more than half of its FMA units busy
   int ranks = 1;
   double best = 0;
-  for (int s = 1; s <= 8; s *= 2) {
-    if (s > 1 && slabs < 4 * s) break;
-    const double t = (double)((tiles * s + sms - 1) / sms) / s + 0.04 * (s - 1);
+  for (int s = 1; s <= 8; ++s) {
+    if (s > 1 && slabs < 8 * s) break;
+    const int64_t n = (tiles * s + sms - 1) / sms;
+    const double t = (double)n / s / (n == 1 ? 0.6 : 1.0) + 0.02 * (s - 1);
     if (s == 1 || t < best) best = t, ranks = s;
   }
   cudaLaunchConfig_t cfg = {};
@@ -392,7 +410,7 @@ cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
   attr[0].val.clusterDim.x = ranks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(tiles * ranks), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(kGemmThreads, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + pdl_attr(&attr[1]);

@@ -5,8 +5,8 @@
 // (16, 32 or 64, zero-filled), and K is shared by the CTAs of a cluster, each with its own stretch of W0, so that
 // some 300 CTAs, two an SM, keep their copies in flight.  The partial accumulators meet through distributed
 // shared memory, in the order of the ranks.  The rank-r part is computed on the side:
-//   multi_few_down   z_i A_a^T in stretches of 512 columns, one CTA a row and stretch (its sums stay apart);
-//   multi_few        while W0 streams in, the epilogue warps add the stretches up and form s z B_a^T.
+//   multi_few_down   z_i = x_i A_a^T, one cluster a row, its CTAs sharing K;
+//   multi_few        while W0 streams in, eight more warps form s z B_a^T.
 // The second kernel starts while the first one runs (programmatic launch): it touches nothing that the first
 // one writes before its wait, and what came before the first one is complete when that lets it start.
 #include "common.cuh"
@@ -17,78 +17,107 @@ namespace lg {
 
 namespace {
 
-constexpr int kStretch = 512;     // columns of x that one CTA of multi_few_down takes
+constexpr int kStretch = 512;     // columns of x that a CTA of multi_few_down takes at a time
 constexpr int kRowsW = 128, kBK = 64;
 constexpr int kUpdate = 256;       // threads of the update; four of their warps read the accumulator
 constexpr int kThreads = 64 + kUpdate;   // copies, MMA
+constexpr int kAhead = 6;         // pieces of the factor that a thread has on their way
 
 struct FewArgs {
   CUtensorMap tmW, tmX;
-  int M, N, r, n, nk, stages, splits;
+  int M, N, r, nk, stages;
   const int32_t* ids;
   const bf16 *X, *A, *B, *bias;
   float one;
   const float* each;
-  float* part;                    // [splits, M, r] z by stretches
+  float* sz;                      // [M, r] s z
   bf16 *Y, *Z;
   int64_t K;
   uint32_t* err;
   uint64_t timeout_ns;
 };
 
-// part[stretch][i][j] = sum over the stretch of X[i][k] A_a[j][k]: a warp takes every W-th group of J rows of A_a, all of
-// their loads on their way at once
+// sz[i] = s_a x_i A_a^T and Z[i] = x_i A_a^T, zeros for a row without adapter.  A CTA has its rank's share of K, in
+// stretches of 512; of each a warp takes every W-th group of J rows of A_a, all of their loads on their way at once.
 template <int J, int W>
 __global__ void __launch_bounds__(32 * W) multi_few_down(const __grid_constant__ FewArgs a) {
+  __shared__ float sum[128];
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const int i = blockIdx.x, split = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ad = a.ids[i], r = a.r;
-  float* out = a.part + ((int64_t)split * a.M + i) * r;
-  if (ad < 0) {
-    for (int j = threadIdx.x; j < r; j += 32 * W) out[j] = 0.f;
+  const int i = (int)(blockIdx.x / ranks), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = a.r;
+  const int ad = a.ids[i];
+  const int64_t to = (int64_t)i * r;
+  if (ad < 0) {                   // the whole cluster
+    for (int j = threadIdx.x; rank == 0 && j < r; j += 32 * W) {
+      a.sz[to + j] = 0.f;
+      if (a.Z) a.Z[to + j] = __float2bfloat16_rn(0.f);
+    }
     return;
   }
   const bf16* u = a.A + (int64_t)ad * r * a.K;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  int64_t k[2];
-  bool on[2];
-  Raw8<bf16> x[2];
+  const int64_t all = (a.K + kStretch - 1) / kStretch;
+  const int s0 = (int)(all * rank / ranks), s1 = (int)(all * (rank + 1) / ranks);
+  for (int st = s0; st < s1; ++st) {
+    int64_t k[2];
+    bool on[2];
+    Raw8<bf16> x[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    k[h] = (int64_t)split * kStretch + h * 256 + lane * 8;
-    on[h] = k[h] < a.K;
-    x[h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(a.X + i * a.K + k[h])) : none;
-  }
-  for (int j0 = warp * J; j0 < r; j0 += W * J) {
-    Raw8<bf16> w[J][2];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[j][h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(u + (int64_t)(j0 + j) * a.K + k[h])) : none;
-    float s[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      F2 t = f2(0.f);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        F2 f[4], g[4];
-        w[j][h].get(f);
-        x[h].get(g);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) t = fma2(f[q], g[q], t);
-      }
-      s[j] = sum2(t);
+    for (int h = 0; h < 2; ++h) {
+      k[h] = (int64_t)st * kStretch + h * 256 + lane * 8;
+      on[h] = k[h] < a.K;
+      x[h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(a.X + i * a.K + k[h])) : none;
     }
+    for (int j0 = warp * J; j0 < r; j0 += W * J) {
+      Raw8<bf16> w[J][2];
 #pragma unroll
-    for (int j = 0; j < J; ++j)
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
-    if (lane == 0)
+        for (int h = 0; h < 2; ++h)
+          w[j][h].v = on[h] ? __ldg(reinterpret_cast<const uint4*>(u + (int64_t)(j0 + j) * a.K + k[h])) : none;
+      float s[J];
 #pragma unroll
-      for (int j = 0; j < J; ++j) out[j0 + j] = s[j];
+      for (int j = 0; j < J; ++j) {
+        F2 t = f2(0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          F2 f[4], g[4];
+          w[j][h].get(f);
+          x[h].get(g);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) t = fma2(f[q], g[q], t);
+        }
+        s[j] = sum2(t);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < J; ++j) sum[j0 + j] = st > s0 ? sum[j0 + j] + s[j] : s[j];
+    }
   }
+  cluster_sync_all();
+  if (rank == 0) {
+    const float f = a.each ? __ldg(a.each + ad) : a.one;
+    for (int j = threadIdx.x; j < r; j += 32 * W) {
+      float p[8], z = 0.f;
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q) {
+        p[q] = 0.f;
+        if (q < ranks) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[q]) : "r"(mapa_shared(smem_u32(sum + j), q)));
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z += p[q];
+      a.sz[to + j] = z * f;
+      if (a.Z) a.Z[to + j] = __float2bfloat16_rn(z);
+    }
+  }
+  cluster_sync_all();             // no CTA leaves while another reads its sums
 }
 
 template <int T>
@@ -98,15 +127,15 @@ struct Few {
   static constexpr int OUT = T * PITCH * 4;
   static constexpr int COLS = T < 32 ? 32 : T;                      // TMEM columns
 };
-// shared memory: the ring (later the partial outputs), the update [T, 128 / ranks], s z [T, r], the rows' adapters and
-// scales, barriers
+// shared memory: the ring (later the partial outputs), the update [T, 128 / ranks], s z [T, r], the rows'
+// adapters, barriers
 template <int T>
 __host__ __device__ constexpr int few_ring(int stages) {
   return stages * Few<T>::STAGE > Few<T>::OUT ? stages * Few<T>::STAGE : Few<T>::OUT;
 }
 template <int T>
 __host__ __device__ constexpr int few_smem(int stages, int ranks, int r) {
-  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + T * r * 4 + T * 8 + 8 * (2 * stages + 2) + 32;
+  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + T * r * 4 + T * 4 + 8 * (2 * stages + 2) + 32;
 }
 
 template <int T>
@@ -121,8 +150,7 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   float* update = reinterpret_cast<float*>(smem + few_ring<T>(a.stages));   // [T, own]
   float* sz = update + T * own;                                     // [T, r]
   int* ids = reinterpret_cast<int*>(sz + T * a.r);                  // [T]
-  float* scale = reinterpret_cast<float*>(ids + T);                 // [T]
-  uint64_t* full = reinterpret_cast<uint64_t*>(scale + T);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ids + T);
   uint64_t* empty = full + a.stages;
   uint64_t* done = empty + a.stages;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
@@ -132,6 +160,13 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   const int rows = min(T, a.M - m0);
   const int k0 = (int)((int64_t)a.nk * rank / ranks), k1 = (int)((int64_t)a.nk * (rank + 1) / ranks);
 
+  auto copy = [&](int i) {      // K-step k0 + i of this CTA
+    const int s = i % a.stages;
+    uint8_t* st = smem + s * F::STAGE;
+    mbar_expect_tx(&full[s], F::STAGE);
+    tma_load_2d(st, &a.tmW, &full[s], (k0 + i) * kBK, n0);
+    tma_load_2d(st + kRowsW * 128, &a.tmX, &full[s], (k0 + i) * kBK, m0);
+  };
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&full[i], 1);
@@ -140,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
     mbar_init(done, 1);
     *abort_flag = 0;
     mbar_fence_init();
+    for (int i = 0; i < min(a.stages, k1 - k0); ++i) copy(i);   // on their way while the rest is set up
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, F::COLS);
@@ -153,20 +189,14 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&a.tmW);
-      tma_prefetch_desc(&a.tmX);
       bool ok = true;
-      int last = 0;
-      for (int ks = k0; ks < k1; ++ks) {
-        const int i = ks - k0, s = i % a.stages;
-        if (i >= a.stages && !mbar_wait(&empty[s], (uint32_t)(i / a.stages + 1) & 1, a.timeout_ns, abort_flag, a.err, 0x401)) {
+      int last = min(a.stages, k1 - k0);
+      for (int i = last; i < k1 - k0; ++i) {
+        if (!mbar_wait(&empty[i % a.stages], (uint32_t)(i / a.stages + 1) & 1, a.timeout_ns, abort_flag, a.err, 0x401)) {
           ok = false;
           break;
         }
-        uint8_t* st = smem + s * F::STAGE;
-        mbar_expect_tx(&full[s], F::STAGE);
-        tma_load_2d(st, &a.tmW, &full[s], ks * kBK, n0);
-        tma_load_2d(st + kRowsW * 128, &a.tmX, &full[s], ks * kBK, m0);
+        copy(i);
         last = i + 1;
       }
       if (!ok)                  // unwind: what is on its way lands before the CTA goes on
@@ -195,68 +225,53 @@ __global__ void __launch_bounds__(kThreads) multi_few(const __grid_constant__ Fe
   } else {
     // the update of this CTA's own columns, while W0 streams in
     const int e = threadIdx.x - 64;
-    if (e < T) {
-      const int ad = e < rows ? __ldg(a.ids + m0 + e) : -1;
-      ids[e] = ad;
-      scale[e] = ad < 0 ? 0.f : a.each ? __ldg(a.each + ad) : a.one;
-    }
+    if (e < T) ids[e] = e < rows ? __ldg(a.ids + m0 + e) : -1;
     named_bar_sync(1, kUpdate);
     const int f = e % own, c = n0 + (int)rank * own + f, step = kUpdate / own;
     const float b = a.bias && c < a.N ? __bfloat162float(a.bias[c]) : 0.f;
-    // 16 columns of the factor of four rows at a time, the first ones on their way before z is there
-    uint4 w[4][2];
-    auto fetch = [&](int t0, int j0) {
+    // this thread's rows are e / own, + step, ..; it takes their factor's row by 16 columns at a time, kAhead of these on
+    // their way, the first ones before z is there
+    uint4 w[kAhead][2];
+    int ft = e / own, fj = 0;
+    auto fetch = [&](uint4 (&x)[2]) {
+      const int ad = ft < rows && c < a.N ? ids[ft] : -1;
+      const bf16* u = a.B + ((int64_t)max(ad, 0) * a.N + c) * a.r + fj;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + i * step, ad = t < rows && c < a.N ? ids[t] : -1;
-        const bf16* u = a.B + ((int64_t)max(ad, 0) * a.N + c) * a.r + j0;
+      for (int h = 0; h < 2; ++h)
+        x[h] = ad >= 0 && fj + 8 * h < a.r ? __ldg(reinterpret_cast<const uint4*>(u + 8 * h)) : make_uint4(0, 0, 0, 0);
+      fj += 16;
+      if (fj >= a.r) fj = 0, ft += step;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(w[i]);
+    pdl_wait();
+    for (int i = e * 4; i < rows * a.r; i += kUpdate * 4)
+      *reinterpret_cast<float4*>(sz + i) = __ldcg(reinterpret_cast<const float4*>(a.sz + (int64_t)m0 * a.r + i));
+    named_bar_sync(1, kUpdate);
+    float v = b;
+    for (int t = e / own, j = 0; t < rows;) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t >= rows) break;
+        const float* z = sz + t * a.r + j;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          w[i][h] = ad >= 0 && j0 + 8 * h < a.r ? __ldg(reinterpret_cast<const uint4*>(u + 8 * h)) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    fetch(e / own, 0);
-    pdl_wait();
-    for (int i = e; i < rows * a.r; i += kUpdate) {
-      const int t = i / a.r, row = m0 + t;
-      const float* p = a.part + (int64_t)row * a.r + (i - t * a.r);
-      const int64_t next = (int64_t)a.M * a.r;
-      float z = 0.f;
-      for (int s = 0; s < a.splits; s += 8) {
-        float v[8];
+          if (j + 8 * h < a.r) {
+            const uint32_t x[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = s + q < a.splits ? __ldcg(p + (s + q) * next) : 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) z += v[q];
-      }
-      if (a.Z && blockIdx.x == 0) a.Z[(int64_t)row * a.r + (i - t * a.r)] = __float2bfloat16_rn(z);
-      sz[i] = ids[t] < 0 ? 0.f : z * scale[t];
-    }
-    named_bar_sync(1, kUpdate);
-    for (int t0 = e / own; t0 < rows; t0 += 4 * step) {
-      float v[4] = {b, b, b, b};
-      for (int j0 = 0; j0 < a.r; j0 += 16) {
-        if (j0 > 0 || t0 != e / own) fetch(t0, j0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = min(t0 + i * step, rows - 1);
-          const float* z = sz + t * a.r + j0;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (j0 + 8 * h < a.r) {
-              const uint32_t x[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float2 p = unpack_bf16x2(x[q]), s = *reinterpret_cast<const float2*>(z + 8 * h + 2 * q);
-                v[i] = fmaf(p.x, s.x, fmaf(p.y, s.y, v[i]));
-              }
+            for (int q = 0; q < 4; ++q) {
+              const float2 p = unpack_bf16x2(x[q]), s = *reinterpret_cast<const float2*>(z + 8 * h + 2 * q);
+              v = fmaf(p.x, s.x, fmaf(p.y, s.y, v));
             }
+          }
+        fetch(w[i]);
+        j += 16;
+        if (j >= a.r) {
+          update[t * own + f] = v;
+          v = b;
+          j = 0;
+          t += step;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + i * step;
-        if (t < rows) update[t * own + f] = v[i];
       }
     }
     // the accumulator, once every MMA is done: the ring is free then
@@ -334,22 +349,36 @@ cudaError_t few_launch(FewArgs& a, cudaStream_t st) {
   return l != cudaSuccess ? l : cudaGetLastError();
 }
 
+template <int J, int W>
+cudaError_t down_launch(const FewArgs& a, cudaStream_t st) {
+  const int64_t stretches = (a.K + kStretch - 1) / kStretch;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)(stretches < 8 ? stretches : 8);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(a.M * attr[0].val.clusterDim.x, 1, 1);
+  cfg.blockDim = dim3(32 * W, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, multi_few_down<J, W>, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace
 
-int multi_few_splits(int64_t K) { return (int)((K + kStretch - 1) / kStretch); }
-
-cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64_t n, const bf16* X, const bf16* W0,
-                          const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* part,
+cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, const bf16* X, const bf16* W0,
+                          const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* sz,
                           bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st) {
   FewArgs a;
   memset(&a, 0, sizeof(a));
   a.M = (int)p.M;
   a.N = (int)N;
   a.r = r;
-  a.n = (int)n;
   a.K = K;
   a.nk = (int)((K + kBK - 1) / kBK);
-  a.splits = multi_few_splits(K);
   a.ids = p.ids;
   a.X = X;
   a.A = A;
@@ -357,7 +386,7 @@ cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64
   a.bias = bias;
   a.one = one;
   a.each = each;
-  a.part = part;
+  a.sz = sz;
   a.Y = Y;
   a.Z = Z;
   a.err = err;
@@ -365,10 +394,9 @@ cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, int64
   const int T = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 64;
   if (!make_tmap_bf16(&a.tmW, W0, K, N, K, kBK, kRowsW, 128) || !make_tmap_bf16(&a.tmX, X, K, p.M, K, kBK, T, 128))
     return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)a.M, (unsigned)a.splits);
-  const cudaError_t e = r <= 16   ? launch_pdl(multi_few_down<2, 8>, grid, dim3(256), 0, st, a)
-                        : r <= 32 ? launch_pdl(multi_few_down<4, 8>, grid, dim3(256), 0, st, a)
-                                  : launch_pdl(multi_few_down<4, 16>, grid, dim3(512), 0, st, a);
+  const cudaError_t e = r <= 16   ? down_launch<2, 8>(a, st)
+                        : r <= 32 ? down_launch<4, 8>(a, st)
+                                  : down_launch<4, 16>(a, st);
   if (e != cudaSuccess) return e;
   return T == 16 ? few_launch<16>(a, st) : T == 32 ? few_launch<32>(a, st) : few_launch<64>(a, st);
 }
