@@ -123,7 +123,13 @@ __global__ void __launch_bounds__(256) clip_norm_kernel(const __grid_constant__ 
 // The norm of the group whose sums are parts[0 .. sums - 1], in every thread of a block of 256.
 __device__ __forceinline__ float norm_of(const float* parts, int sums, double* tot) {
   double t = 0.0;
-  for (int i = threadIdx.x; i < sums; i += 256) t += (double)parts[i];
+  for (int i = threadIdx.x; i < sums; i += 8 * 256) {
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = i + 256 * q < sums ? parts[i + 256 * q] : 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += (double)v[q];
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   if ((threadIdx.x & 31) == 0) tot[threadIdx.x >> 5] = t;

@@ -120,12 +120,19 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
 }
 
 // ------------------------------------------------------------------ shared product and rank-r update
-// 64 x 128 outputs a CTA, 8 x 16 a thread (six 16-byte accesses of shared memory for 128 FMAs: a warp's access takes
-// four cycles of the SM's one port, so that 8 x 8 with four for 64 took as long as the FMAs, and the two did not
-// overlap), K in slabs of 16 through two buffers, of which each of two groups of two warps takes eight.  The CTAs of a
-// cluster share K and add their sums through distributed shared memory, each finishing its share of the rows.
-// There a thread has one column, and takes its adapter's factor anew only where the next row has another one.
-constexpr int kTileM = 64, kTileN = 128, kSlab = 16, kGroups = 2, kGemmThreads = 64 * kGroups;
+// 64 x 64 outputs a CTA, 8 x 8 a thread, K in slabs of 16, of which each of two groups of two warps takes eight.
+// Operands come by asynchronous copies, three slabs ahead, and lie as they do in memory: rows of 16 k (80 bytes apart,
+// so that eight rows' 16 bytes fall into different banks), W [K, N] by k.  A thread reads four k of a row at once.
+// What counts is warps: with two a scheduler it issues every second cycle (8 x 16 a thread: 60 us at 509 x 1000 x
+// 1496, the FMA units 38% busy), so 128 registers and four CTAs an SM.  The CTAs of a cluster share K and add their
+// sums through distributed shared memory, each finishing its share of the rows.  There a thread has one column, and
+// takes its adapter's factor anew only where the next row has another one.
+constexpr int kTileM = 64, kTileN = 64, kSlab = 16, kGroups = 2, kGemmThreads = 64 * kGroups, kSlabs = 4;
+constexpr int kRowPitch = kSlab + 4, kColPitch = kTileN + 4;          // floats
+constexpr int kSlabA = kTileM * kRowPitch, kSlabB = kTileN * kRowPitch;
+static_assert(kSlab * kColPitch <= kSlabB, "a slab of W [K, N] fits as well");
+constexpr int kGemmSmem = kSlabs * (kSlabA + kSlabB) * 4;
+static_assert(kGemmSmem >= kTileM * (kTileN + 4) * 4, "the sums take the slabs' place");
 
 struct F32Gemm {
   MultiPlan p;
@@ -139,100 +146,98 @@ struct F32Gemm {
 };
 
 template <bool MN>
-__global__ void __launch_bounds__(kGemmThreads, 2) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
-  // two buffers of S and of W by k; column c of k lies at c ^ 8 (k / 4 % 4): a row's four k, spread over the lanes, are
-  // stored without bank conflicts, and four columns stay together.  Later the sums lie there.
+__global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_constant__ F32Gemm a) {
   constexpr int kPitch = kTileN + 4;
-  __shared__ __align__(16) float pool[kTileM * kPitch];
-  __shared__ float ps[8][8];                          // P of eight rows and eight j
+  extern __shared__ __align__(16) float pool[];
+  __shared__ float ps[8 * kGroups][8];                // P of eight rows of each group and eight j
   __shared__ int ids[kTileM];
-  float (*As)[kSlab][kTileM] = reinterpret_cast<float (*)[kSlab][kTileM]>(pool);
-  float (*Bs)[kSlab][kTileN] = reinterpret_cast<float (*)[kSlab][kTileN]>(pool + 2 * kSlab * kTileM);
   float (*part)[kPitch] = reinterpret_cast<float (*)[kPitch]>(pool);
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
-  const int tid = threadIdx.x, group = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;   // rows 4 ty, 4 ty + 32 and on
+  // rows ty + 8 i and columns tx + 8 j of a K-major W, 4 tx + 32 h and on of W [K, N]
+  const int tid = threadIdx.x, group = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;
   const int64_t K = a.K, N = a.N;
   const int tile = (int)(blockIdx.x / ranks), wide = (int)((N + kTileN - 1) / kTileN);
   const int64_t m0 = (int64_t)(tile / wide) * kTileM, n0 = (int64_t)(tile % wide) * kTileN;
   const int slabs = (int)((K + kSlab - 1) / kSlab), s0 = (int)((int64_t)slabs * rank / ranks),
             s1 = (int)((int64_t)slabs * (rank + 1) / ranks);
-  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-  // a thread brings four k of two rows of S and of four rows of W [N, K], four lanes a row; of W [K, N] four columns
-  // of every fourth k
-  const int lr = tid >> 2, lk = (tid & 3) * 4, lc = (tid & 31) * 4;
-  const float* S[2];
+  // a thread brings four k of two rows of S and of W [N, K], four lanes a row; of W [K, N] four columns of every eighth k
+  const int lr = tid >> 2, lk = (tid & 3) * 4, lc = (tid & 15) * 4;
+  auto load = [&](int s) {
+    if (s < s1) {
+      float* A = pool + (s - s0) % kSlabs * (kSlabA + kSlabB);
+      float* B = A + kSlabA;
+      const int64_t k = (int64_t)s * kSlab + lk;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) S[i] = m0 + lr + 32 * i < a.p.M ? a.S + (m0 + lr + 32 * i) * K : nullptr;
-  const float* W[MN ? 1 : 4];
-#pragma unroll
-  for (int i = 0; i < (MN ? 1 : 4); ++i) {
-    const int64_t c = n0 + (MN ? lc : lr + 32 * i);
-    W[i] = c < N ? a.W + (MN ? c : c * K) : nullptr;
-  }
-  auto fetch = [&](int s, float4 (&x)[2], float4 (&w)[4]) {
-    const int64_t k = (int64_t)s * kSlab + lk;
-    const bool on = s < s1 && k < K;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x[i] = on && S[i] ? __ldg(reinterpret_cast<const float4*>(S[i] + k)) : none;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (MN) {
-        const int64_t kk = (int64_t)s * kSlab + (tid >> 5) + 4 * i;
-        w[i] = s < s1 && kk < K && W[0] ? __ldg(reinterpret_cast<const float4*>(W[0] + kk * N)) : none;
-      } else {
-        w[i] = on && W[MN ? 0 : i] ? __ldg(reinterpret_cast<const float4*>(W[MN ? 0 : i] + k)) : none;
+      for (int i = 0; i < 2; ++i) {
+        const bool on = k < K && m0 + lr + 32 * i < a.p.M;
+        cp_async16(A + (lr + 32 * i) * kRowPitch + lk, on ? a.S + (m0 + lr + 32 * i) * K + k : a.S, on);
       }
-  };
-  auto put = [&](int b, const float4 (&x)[2], const float4 (&w)[4]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float p[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) As[b][lk + j][(lr + 32 * i) ^ (2 * lk)] = p[j];
+      for (int i = 0; i < 2; ++i)
+        if (MN) {
+          const int kk = (tid >> 4) + 8 * i;
+          const int64_t row = (int64_t)s * kSlab + kk;
+          const bool on = row < K && n0 + lc < N;
+          cp_async16(B + kk * kColPitch + lc, on ? a.W + row * N + n0 + lc : a.W, on);
+        } else {
+          const bool on = k < K && n0 + lr + 32 * i < N;
+          cp_async16(B + (lr + 32 * i) * kRowPitch + lk, on ? a.W + (n0 + lr + 32 * i) * K + k : a.W, on);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int kk = (tid >> 5) + 4 * i;
-      const float q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      if (MN) *reinterpret_cast<float4*>(&Bs[b][kk][lc ^ (2 * (kk & 12))]) = w[i];
-      else
-#pragma unroll
-        for (int j = 0; j < 4; ++j) Bs[b][lk + j][(lr + 32 * i) ^ (2 * lk)] = q[j];
-    }
+    cp_async_commit();
   };
-  float run[8][16] = {};
-  float4 x[2], w[4];
-  fetch(s0, x, w);
-  put(0, x, w);
+  float run[8][8] = {};
+#pragma unroll
+  for (int s = 0; s < kSlabs - 1; ++s) load(s0 + s);
   for (int s = s0; s < s1; ++s) {
-    const int b = (s - s0) & 1;
-    fetch(s + 1, x, w);
-    __syncthreads();
+    cp_async_wait<kSlabs - 2>();
+    __syncthreads();              // slab s is there, and all are done with the one that is loaded next
+    load(s + kSlabs - 1);
+    const float* A = pool + (s - s0) % kSlabs * (kSlabA + kSlabB) + ty * kRowPitch + group * 8;
+    const float* B = pool + (s - s0) % kSlabs * (kSlabA + kSlabB) + kSlabA;
 #pragma unroll
-    for (int k = 0; k < kSlab / kGroups; ++k) {
-      float p[8], q[16];
-      const int kk = group * 8 + k, swap = 2 * (kk & 12);
+    for (int q = 0; q < 2; ++q) {
+      float p[8][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 u = *reinterpret_cast<const float4*>(&As[b][kk][(32 * h + ty * 4) ^ swap]);
-        p[4 * h] = u.x, p[4 * h + 1] = u.y, p[4 * h + 2] = u.z, p[4 * h + 3] = u.w;
+      for (int i = 0; i < 8; ++i) {
+        const float4 u = *reinterpret_cast<const float4*>(A + 8 * i * kRowPitch + 4 * q);
+        p[i][0] = u.x, p[i][1] = u.y, p[i][2] = u.z, p[i][3] = u.w;
       }
+      if (MN) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const float4 v = *reinterpret_cast<const float4*>(&Bs[b][kk][(32 * h + tx * 4) ^ swap]);
-        q[4 * h] = v.x, q[4 * h + 1] = v.y, q[4 * h + 2] = v.z, q[4 * h + 3] = v.w;
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float4 v = *reinterpret_cast<const float4*>(B + (group * 8 + 4 * q + k) * kColPitch + 32 * h + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              run[i][4 * h] = fmaf(p[i][k], v.x, run[i][4 * h]);
+              run[i][4 * h + 1] = fmaf(p[i][k], v.y, run[i][4 * h + 1]);
+              run[i][4 * h + 2] = fmaf(p[i][k], v.z, run[i][4 * h + 2]);
+              run[i][4 * h + 3] = fmaf(p[i][k], v.w, run[i][4 * h + 3]);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(B + (tx + 8 * j) * kRowPitch + group * 8 + 4 * q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) run[i][j] = fmaf(p[i][0], v.x, run[i][j]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) run[i][j] = fmaf(p[i][1], v.y, run[i][j]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) run[i][j] = fmaf(p[i][2], v.z, run[i][j]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) run[i][j] = fmaf(p[i][3], v.w, run[i][j]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) run[i][j] = fmaf(p[i], q[j], run[i][j]);
     }
-    put(b ^ 1, x, w);
   }
+  cp_async_wait<0>();
   // the groups' sums one after another
   for (int q = 0; q < kGroups; ++q) {
     __syncthreads();
@@ -240,20 +245,21 @@ __global__ void __launch_bounds__(kGemmThreads, 2) f32_gemm_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          float4* at = reinterpret_cast<float4*>(&part[32 * (i >> 2) + ty * 4 + (i & 3)][32 * h + tx * 4]);
-          const float4 old = q == 0 ? none : *at;
-          *at = make_float4(old.x + run[i][4 * h], old.y + run[i][4 * h + 1], old.z + run[i][4 * h + 2],
-                            old.w + run[i][4 * h + 3]);
+        for (int j = 0; j < 8; ++j) {
+          float* at = &part[ty + 8 * i][MN ? 32 * (j >> 2) + 4 * tx + (j & 3) : tx + 8 * j];
+          *at = q == 0 ? run[i][j] : *at + run[i][j];
         }
   }
   if (tid < kTileM) ids[tid] = m0 + tid < a.p.M ? a.p.ids[m0 + tid] : -1;
   cluster_sync_all();
-  // this thread's column of this CTA's share of the rows, eight rows at a time
-  const int c = tid, r0 = kTileM * (int)rank / (int)ranks, r1 = kTileM * ((int)rank + 1) / (int)ranks;
+  // this thread's column of its group's half of this CTA's share of the rows, eight rows at a time
+  const int c = tid & 63, part_of = (int)rank * kGroups + group, parts = (int)ranks * kGroups;
+  const int r0 = kTileM * part_of / parts, r1 = kTileM * (part_of + 1) / parts;
+  const int rounds = ((kTileM + parts - 1) / parts + 7) / 8;          // of the longest share
   const uint32_t mine = smem_u32(&part[0][0]);
   const float bias = a.bias && n0 + c < N ? __ldg(a.bias + n0 + c) : 0.f;
-  for (int e0 = r0; e0 < r1; e0 += 8) {
+  for (int round = 0; round < rounds; ++round) {
+    const int e0 = r0 + 8 * round;
     float v[8], t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = t[i] = 0.f;
@@ -270,9 +276,9 @@ __global__ void __launch_bounds__(kGemmThreads, 2) f32_gemm_kernel(const __grid_
     }
     for (int j0 = 0; j0 < a.r; j0 += 8) {
       __syncthreads();
-      if (tid < 64) {
-        const int m = e0 + (tid >> 3), j = j0 + (tid & 7);
-        ps[tid >> 3][tid & 7] = m < r1 && ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
+      {
+        const int m = e0 + (c >> 3), j = j0 + (c & 7);
+        ps[group * 8 + (c >> 3)][c & 7] = m < r1 && ids[m] >= 0 && j < a.r ? a.P[(m0 + m) * a.r + j] : 0.f;
       }
       __syncthreads();
       if (n0 + c < N) {
@@ -286,13 +292,22 @@ __global__ void __launch_bounds__(kGemmThreads, 2) f32_gemm_kernel(const __grid_
           if (ad != have) {
             have = ad;
             const float* f = a.U + (int64_t)ad * a.r * N;
+            if (!MN && (a.r & 3) == 0) {              // a row of the factor by 16 bytes
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              u[q] = j0 + q < a.r ? __ldg(MN ? f + (int64_t)(j0 + q) * N + n0 + c : f + (n0 + c) * a.r + j0 + q) : 0.f;
+              for (int q = 0; q < 8; q += 4) {
+                const float4 x = j0 + q < a.r ? __ldg(reinterpret_cast<const float4*>(f + (n0 + c) * a.r + j0 + q))
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                u[q] = x.x, u[q + 1] = x.y, u[q + 2] = x.z, u[q + 3] = x.w;
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                u[q] = j0 + q < a.r ? __ldg(MN ? f + (int64_t)(j0 + q) * N + n0 + c : f + (n0 + c) * a.r + j0 + q) : 0.f;
+            }
           }
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (j0 + q < a.r) t[i] = fmaf(ps[i][q], u[q], t[i]);
+            if (j0 + q < a.r) t[i] = fmaf(ps[group * 8 + i][q], u[q], t[i]);
         }
       }
     }
@@ -394,14 +409,16 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 template <bool MN>
 cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
   const int64_t tiles = (int64_t)blocks(a.N, kTileN) * blocks(a.p.M, kTileM), slabs = blocks(a.K, kSlab), sms = num_sms_current();
-  // the share of K that finishes soonest: what the fullest SM has, and what a cluster costs; a lone CTA of an SM keeps
-  // little more than half of its FMA units busy
+  const cudaError_t allowed = allow_smem<f32_gemm_kernel<MN>>(kGemmSmem);
+  if (allowed != cudaSuccess) return allowed;
+  // the share of K that finishes soonest: what the fullest SM has, by how busy so many CTAs keep it, and what a cluster
+  // costs
   int ranks = 1;
   double best = 0;
   for (int s = 1; s <= 8; ++s) {
     if (s > 1 && slabs < 8 * s) break;
     const int64_t n = (tiles * s + sms - 1) / sms;
-    const double t = (double)n / s / (n == 1 ? 0.6 : 1.0) + 0.02 * (s - 1);
+    const double t = (double)n / s / (n == 1 ? 0.3 : n == 2 ? 0.55 : n == 3 ? 0.75 : 0.9) + 0.02 * (s - 1);
     if (s == 1 || t < best) best = t, ranks = s;
   }
   cudaLaunchConfig_t cfg = {};
@@ -411,6 +428,7 @@ cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(tiles * ranks), 1, 1);
   cfg.blockDim = dim3(kGemmThreads, 1, 1);
+  cfg.dynamicSmemBytes = kGemmSmem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + pdl_attr(&attr[1]);

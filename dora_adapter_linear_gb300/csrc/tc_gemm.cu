@@ -947,8 +947,10 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
   cluster_sync_all();   // barriers of both CTAs initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  pdl_wait();      // the operands may come from the previous kernel in the stream
-  if (threadIdx.x == 0) pdl_trigger();
+  if (!MULTI) {
+    pdl_wait();    // the operands may come from the previous kernel in the stream
+    if (threadIdx.x == 0) pdl_trigger();
+  }
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer (both CTAs)
@@ -956,6 +958,8 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      bool waited = !MULTI;   // MULTI: the rank-r pass before this kernel gives the tail alone, and what came before
+                              // that pass is complete, so the main steps begin beside its end
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
         int mt, nt;
         tile_coords(t, p.num_m_tiles, p.num_n_tiles, p.group_m, mt, nt);
@@ -1019,6 +1023,11 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
           const int32_t* list = p.ad_list + (int64_t)mt * PM;
           const int steps = tail.steps();
           for (int ts = 0; ts < steps && ok; ++ts) {
+            if (!waited) {
+              waited = true;
+              pdl_wait();
+              pdl_trigger();
+            }
             const int kb = ts % tail.KB, q0 = ts / tail.KB * tail.P;
             const int nq = min(tail.P, tail.count - q0), nc = tail.in_block(kb);
             int ad[4];
@@ -1052,6 +1061,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
           }
         }
       }
+      if (!waited) pdl_wait();      // the end of this kernel implies that of those before it
       if (!ok) spin_ns(100000ull);  // unwind: give copies already issued time to land
     }
     __syncwarp();
