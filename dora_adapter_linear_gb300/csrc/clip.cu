@@ -6,8 +6,8 @@
 //
 // A CTA of the first launch sums the squares of one unit (16384 elements of one tensor and group, all its loads on
 // their way at once) in a fixed order.  A CTA of the last one scales a unit whose group's factor is not 1, last
-// units first, while their elements are still in L2.  The units' sums of a group are added in fp64, by one CTA for
-// each group in a launch between, or, where a group has up to 512, by every CTA of the last launch for itself
+// units first, while their elements are still in L2.  The units' sums of a group are added by one CTA for each
+// group in a launch between, or, where a group has up to 512, by every CTA of the last launch for itself
 // (three adapters of one small block: 10.1 instead of 12 us a call).  Bytes bound large sets: every element
 // read, those above the limit read again and written.
 #include <float.h>
@@ -109,7 +109,7 @@ __device__ __forceinline__ float squares(const T* p, int n) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(256) clip_norm_kernel(const __grid_constant__ ClipArgs a,
+__global__ void __launch_bounds__(256, 4) clip_norm_kernel(const __grid_constant__ ClipArgs a,
                                                         const __grid_constant__ ClipTable<N> table) {
   __shared__ float red[2 * 32];
   const Unit u = unit_of(a, table, blockIdx.x);
@@ -120,24 +120,27 @@ __global__ void __launch_bounds__(256) clip_norm_kernel(const __grid_constant__ 
   if (threadIdx.x == 0) a.parts[u.at] = s[0];
 }
 
-// The norm of the group whose sums are parts[0 .. sums - 1], in every thread of a block of 256.
-__device__ __forceinline__ float norm_of(const float* parts, int sums, double* tot) {
-  double t = 0.0;
-  for (int i = threadIdx.x; i < sums; i += 8 * 256) {
+// The norm of the group whose sums are parts[0 .. sums - 1], in every thread of a block of 256.  Eight at a time in
+// fp32, longer runs of these in fp64 (whose units are few: with each sum in fp64 this took 4 us of a CTA).
+__device__ __forceinline__ float norm_of(const float* parts, int sums, float* tot) {
+  auto eight = [&](int i) {
     float v[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = i + 256 * q < sums ? parts[i + 256 * q] : 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) t += (double)v[q];
+    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+  };
+  float s = eight(threadIdx.x);
+  if (sums > 2048) {
+    double t = (double)s;
+    for (int i = threadIdx.x + 2048; i < sums; i += 2048) t += (double)eight(i);
+    s = (float)t;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if ((threadIdx.x & 31) == 0) tot[threadIdx.x >> 5] = t;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) tot[threadIdx.x >> 5] = s;
   __syncthreads();
-  t = 0.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t += tot[i];
-  return sqrtf((float)t);
+  s = ((tot[0] + tot[1]) + (tot[2] + tot[3])) + ((tot[4] + tot[5]) + (tot[6] + tot[7]));
+  return sqrtf(s);
 }
 __device__ __forceinline__ float factor_of(float norm, float max_norm) {
   return isfinite(norm) ? fminf(1.f, max_norm / (norm + 1e-6f)) : 0.f;
@@ -152,7 +155,7 @@ struct Sums {
 template <int N>
 __global__ void __launch_bounds__(256) clip_factor_kernel(const __grid_constant__ ClipArgs a,
                                                           const __grid_constant__ Sums<N> table) {
-  __shared__ double tot[8];
+  __shared__ float tot[8];
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();
   const int k = blockIdx.x, g = table.group0 + k;
@@ -197,7 +200,7 @@ __device__ __forceinline__ void scale(T* p, int n, float f, bool zero) {
 template <int N, bool FEW>
 __global__ void __launch_bounds__(256) clip_scale_kernel(const __grid_constant__ ClipArgs a,
                                                          const __grid_constant__ ClipTable<N> table) {
-  __shared__ double tot[8];
+  __shared__ float tot[8];
   const Unit u = unit_of(a, table, a.units - 1 - (int)blockIdx.x);
   pdl_wait();
   if (threadIdx.x == 0) pdl_trigger();

@@ -400,39 +400,49 @@ PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred()) return nullptr;
   if (count < 1 || count > 65535) return not_here();
   std::vector<lora_grad_tensor> table;
-  std::vector<Tensor> kept;           // the list may change while other threads run
+  struct Kept {                       // the list may change while other threads run
+    std::vector<PyObject*> all;
+    ~Kept() {
+      for (PyObject* o : all) Py_DECREF(o);
+    }
+  } kept;
   table.reserve(all);
-  kept.reserve(all);
+  kept.all.reserve(all);
+  const auto device = c10::cuda::current_device();
+  PyObject** grads = PySequence_Fast_ITEMS(a[0]);
   for (Py_ssize_t i = 0; i < all; ++i) {
-    const Arg g(PySequence_Fast_ITEMS(a[0])[i]);
+    const Arg g(grads[i]);
     if (!g.ok) return not_here();
     if (!g) continue;
     const Tensor& t = *g;
-    if (!here(t) || !strided(t) || dtype_of(t) < 0 || !t.is_contiguous()) return not_here();
+    if (!t.is_cuda() || t.device().index() != device || !strided(t) || dtype_of(t) < 0 || !t.is_contiguous())
+      return not_here();
     if (stacked && (t.dim() < 1 || t.size(0) != count)) return not_here();
     int64_t group = 0;
     if (!stacked) {
       group = PyLong_AsLongLong(PyList_GET_ITEM(a[1], i));
-      if (PyErr_Occurred()) return nullptr;
+      if (group == -1 && PyErr_Occurred()) return nullptr;
       if (group < 0 || group >= count) return not_here();
     }
     table.push_back(lora_grad_tensor{t.data_ptr(), stacked ? t.numel() / count : t.numel(), (int32_t)group, dtype_of(t)});
-    kept.push_back(t);
+    Py_INCREF(grads[i]);
+    kept.all.push_back(grads[i]);
   }
-  if (kept.empty()) return not_here();
+  if (kept.all.empty()) return not_here();
   Tensor norms;
   int e;
   {
+    const Tensor& like = THPVariable_Unpack(kept.all[0]);
     const Unlocked unlocked;
-    norms = fresh(kept[0], {count}, at::kFloat);
+    norms = fresh(like, {count}, at::kFloat);
     const size_t need = clip_bytes_call(table.data(), (int64_t)table.size(), count, stacked);
-    const Tensor ws = fresh(kept[0], {(int64_t)(need ? need : 1)}, at::kByte);
+    const Tensor ws = fresh(like, {(int64_t)(need ? need : 1)}, at::kByte);
     e = clip_call(table.data(), (int64_t)table.size(), count, stacked, (float)max_norm,
                   static_cast<float*>(norms.data_ptr()), ws.data_ptr(), need, stream());
   }
   if (e != LORA_OK) return PyLong_FromLong(e);
   if (max_norm > 0)
-    for (const Tensor& t : kept) written(t);
+    for (PyObject* o : kept.all) written(THPVariable_Unpack(o));
   return THPVariable_Wrap(norms);
   END_HANDLE_TH_ERRORS
 }
