@@ -408,15 +408,16 @@ PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } kept;
   table.reserve(all);
   kept.all.reserve(all);
-  const auto device = c10::cuda::current_device();
+  int device = -1;                    // the current one, asked once there is a CUDA tensor
   PyObject** grads = PySequence_Fast_ITEMS(a[0]);
   for (Py_ssize_t i = 0; i < all; ++i) {
     const Arg g(grads[i]);
     if (!g.ok) return not_here();
     if (!g) continue;
     const Tensor& t = *g;
-    if (!t.is_cuda() || t.device().index() != device || !strided(t) || dtype_of(t) < 0 || !t.is_contiguous())
-      return not_here();
+    if (!t.is_cuda()) return not_here();
+    if (device < 0) device = c10::cuda::current_device();
+    if (t.device().index() != device || !strided(t) || dtype_of(t) < 0 || !t.is_contiguous()) return not_here();
     if (stacked && (t.dim() < 1 || t.size(0) != count)) return not_here();
     int64_t group = 0;
     if (!stacked) {
