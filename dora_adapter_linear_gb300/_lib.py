@@ -200,9 +200,9 @@ def host():
         spec = importlib.util.spec_from_file_location("_host", HOST_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(*[ctypes.cast(getattr(lib, name), c_void_p).value
-                      for name in ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd",
-                                   "grad_clip_workspace_bytes", "grad_clip", "lora_multi_fwd", "lora_multi_bwd")])
+        address = lambda name: ctypes.cast(getattr(lib, name), c_void_p).value  # noqa: E731
+        module.bind(*map(address, ("block_norm_fwd", "block_norm_bwd", "rotary_fwd", "rotary_bwd")))
+        module.bind_multi(*map(address, ("lora_multi_fwd", "lora_multi_bwd", "grad_clip_workspace_bytes", "grad_clip")))
         _HOST = module
     return _HOST
 

@@ -448,27 +448,39 @@ PyObject* py_clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd, grad_clip_workspace_bytes, grad_clip, lora_multi_fwd,
-// lora_multi_bwd): addresses in the loaded library
-PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* at[8];
-  if (n != 8) {
-    PyErr_SetString(PyExc_TypeError, "eight addresses");
-    return nullptr;
+// four addresses in the loaded library, from Python numbers
+bool addresses(PyObject* const* a, Py_ssize_t n, void* (&at)[4]) {
+  if (n != 4) {
+    PyErr_SetString(PyExc_TypeError, "four addresses");
+    return false;
   }
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
     if (!(at[i] = PyLong_AsVoidPtr(a[i]))) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "an address is zero");
-      return nullptr;
+      return false;
     }
+  return true;
+}
+
+// (block_norm_fwd, block_norm_bwd, rotary_fwd, rotary_bwd): addresses in the loaded library
+PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* at[4];
+  if (!addresses(a, n, at)) return nullptr;
   norm_fwd_call = reinterpret_cast<decltype(norm_fwd_call)>(at[0]);
   norm_bwd_call = reinterpret_cast<decltype(norm_bwd_call)>(at[1]);
   rotary_fwd_call = reinterpret_cast<decltype(rotary_fwd_call)>(at[2]);
   rotary_bwd_call = reinterpret_cast<decltype(rotary_bwd_call)>(at[3]);
-  clip_bytes_call = reinterpret_cast<decltype(clip_bytes_call)>(at[4]);
-  clip_call = reinterpret_cast<decltype(clip_call)>(at[5]);
-  multi_fwd_call = reinterpret_cast<decltype(multi_fwd_call)>(at[6]);
-  multi_bwd_call = reinterpret_cast<decltype(multi_bwd_call)>(at[7]);
+  Py_RETURN_NONE;
+}
+
+// (lora_multi_fwd, lora_multi_bwd, grad_clip_workspace_bytes, grad_clip): the same
+PyObject* py_bind_multi(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  void* at[4];
+  if (!addresses(a, n, at)) return nullptr;
+  multi_fwd_call = reinterpret_cast<decltype(multi_fwd_call)>(at[0]);
+  multi_bwd_call = reinterpret_cast<decltype(multi_bwd_call)>(at[1]);
+  clip_bytes_call = reinterpret_cast<decltype(clip_bytes_call)>(at[2]);
+  clip_call = reinterpret_cast<decltype(clip_call)>(at[3]);
   Py_RETURN_NONE;
 }
 
@@ -477,6 +489,7 @@ PyMethodDef methods[] = {{"bind", FAST(py_bind), "take the library's entry point
                          {"block_norm_fwd", FAST(py_norm_fwd), "ops.block_norm_fwd"},
                          {"block_norm_bwd", FAST(py_norm_bwd), "ops.block_norm_bwd"},
                          {"rotary", FAST(py_rotary), "ops.rotary_fwd and rotary_bwd"},
+                         {"bind_multi", FAST(py_bind_multi), "take the entry points of many adapters"},
                          {"multi_fwd", FAST(py_multi_fwd), "ops.lora_multi_fwd"},
                          {"multi_bwd", FAST(py_multi_bwd), "ops.lora_multi_bwd"},
                          {"clip_grads", FAST(py_clip_grads), "optim.clip_grads"},

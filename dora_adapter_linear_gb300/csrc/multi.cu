@@ -106,7 +106,7 @@ TcGemmDesc gemm(const MultiPlan& p, int mode, int64_t N, int64_t K, int r, int64
 cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
                     const bf16* A, const bf16* B, const bf16* bias, Scale s, bf16* Y, bf16* Z, cudaStream_t st) {
   const int r = (int)sh.r;
-  if (sh.M <= kFewRows)
+  if (multi_few_fits(sh.M, sh.d_out))
     return multi_few_fwd(p, sh.d_out, sh.d_in, r, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
                          wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);

@@ -71,7 +71,8 @@ cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, co
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
                       bf16* out1, int64_t K, const float* csum, bf16* sums, cudaStream_t st);
 // The whole bf16 forward of a few rows (multi_few.cu); sz: fp32 [M, r]
-constexpr int kFewRows = 256;
+constexpr int kFewRows = 256;                        // the most that it takes
+bool multi_few_fits(int64_t M, int64_t N);           // whether it is the faster way
 cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, const bf16* X, const bf16* W0,
                           const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* sz,
                           bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st);

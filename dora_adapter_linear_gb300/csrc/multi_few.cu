@@ -547,6 +547,14 @@ cudaError_t down_launch(const FewArgs& a, int* beside, cudaStream_t st) {
 
 }  // namespace
 
+// Measured (4096 x 4096, 128 rows: 21 us, the GEMM of 256-row tiles 28; 192: 30 and 29; 4096 x 11008, 64 rows: 31 and
+// 51, 128: 55 and 51; 4096 x 1024, 256: 23 and 28, 512: 31 and 28): up to 128 rows while two CTAs share K, more only
+// where eight do.
+bool multi_few_fits(int64_t M, int64_t N) {
+  const int64_t groups = (M + 63) / 64, ctas = (N + kRowsW - 1) / kRowsW * groups;
+  return M <= kFewRows && ctas * (groups <= 2 ? 2 : 8) <= 2 * num_sms_current();
+}
+
 cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, const bf16* X, const bf16* W0,
                           const bf16* A, const bf16* B, const bf16* bias, float one, const float* each, float* sz,
                           bf16* Y, bf16* Z, uint32_t* err, uint64_t timeout_ns, cudaStream_t st) {
