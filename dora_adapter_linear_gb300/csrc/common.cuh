@@ -472,6 +472,13 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return __bfloat1622float2(b);
 }
 
+// Two fp32 numbers in two bf16 parts: the first rounded, the second what that left (nothing of what is not finite)
+__device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  const float2 had = unpack_bf16x2(hi);
+  lo = pack_bf16x2(isfinite(had.x) ? x - had.x : 0.f, isfinite(had.y) ? y - had.y : 0.f);
+}
+
 // Input dropout on one bf16x2 operand register: each half becomes bf16(x k) where its mask byte
 // is nonzero and 0 where it is zero (k = 1 / (1 - p)); m0 belongs to the low half.
 __device__ __forceinline__ uint32_t mask_bf16x2(uint32_t v, uint32_t m0, uint32_t m1, float k) {

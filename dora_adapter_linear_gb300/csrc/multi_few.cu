@@ -364,12 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) multi_few(const __grid_constant__
     fetch(w[0]);
     fetch(w[1]);
     // s z, two words: hi and lo of a pair
-    auto put_z = [&](int i, float z0, float z1) {
-      const uint32_t hi = pack_bf16x2(z0, z1);
-      const float2 had = unpack_bf16x2(hi);
-      szh[i / 2] = hi;
-      szl[i / 2] = pack_bf16x2(z0 - had.x, z1 - had.y);
-    };
+    auto put_z = [&](int i, float z0, float z1) { split_bf16x2(z0, z1, szh[i / 2], szl[i / 2]); };
     if (OWN) {
       cluster_wait();
       for (int i = e * 2; i < rows * a.r; i += kUpdate * 2) {

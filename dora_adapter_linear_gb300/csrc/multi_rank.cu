@@ -179,12 +179,10 @@ __global__ void __launch_bounds__(256) multi_proj_mma(const __grid_constant__ Pr
     }
     const int64_t to = (int64_t)rows[2 * i / R] * a.r + a.j0 + 2 * i % R;
     if (a.plain) *reinterpret_cast<uint32_t*>(a.plain + to) = pack_bf16x2(v.x, v.y);
-    const uint32_t hi = pack_bf16x2(v.x * s, v.y * s);
+    uint32_t hi, lo;
+    split_bf16x2(v.x * s, v.y * s, hi, lo);
     if (a.scaled) *reinterpret_cast<uint32_t*>(a.scaled + to) = hi;
-    if (a.rest) {
-      const float2 had = unpack_bf16x2(hi);
-      *reinterpret_cast<uint32_t*>(a.rest + to) = pack_bf16x2(v.x * s - had.x, v.y * s - had.y);
-    }
+    if (a.rest) *reinterpret_cast<uint32_t*>(a.rest + to) = lo;
   }
   if (ranks > 1) cluster_sync_all();   // no CTA leaves while another reads its sums
 }

@@ -154,3 +154,22 @@ def test_a_tensor_past_32_bits():
     assert abs(float(norm) - 43 ** 0.5) < 1e-5
     want = (torch.tensor([3.0, 4.0]) / (43 ** 0.5 + 1e-6)).bfloat16().tolist()
     assert g[-3:].tolist() == want[:1] * 3 and float(g[0]) == want[1] and not g[1:-3].any()
+
+
+def test_shared_memory_is_refused():
+    buf = torch.ones(100, device="cuda")
+    for grads in ([buf, buf], [buf[:60], buf[50:]], [buf[60:], buf[:61]], [buf[90:], buf[:10], buf[5:20]]):
+        with pytest.raises(ValueError, match="share memory"):
+            optim.clip_grads(grads, 1.0)
+    assert (buf == 1).all()
+    optim.clip_grads([buf[50:], buf[:50]], 1.0)
+
+
+def test_what_it_does_not_take_is_named():
+    g = torch.ones(4, 6, device="cuda")
+    for grads, groups, what in (([g.t()], None, "contiguous"), ([g.double()], None, "fp32 or bf16"), ([g], 3, "stack of 3"),
+                                ([g, 1.0], None, "tensor or None"), ([g], [-1], "1 to 65535"), ([g, g[0]], [1, -1], "not in 0 to 1"),
+                                ([g, torch.ones(3)], None, "CUDA")):
+        with pytest.raises(ValueError, match=what):
+            optim.clip_grads(grads, 1.0, groups)
+    assert (g == 1).all()

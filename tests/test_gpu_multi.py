@@ -259,3 +259,27 @@ def test_offsets_past_32_bits():
     ref = C.reference_fwd(c, "bf16")
     C.near(Y[-64:], ref["Y"], "Y")
     assert torch.equal(Y[:M - 64:4099], g["bias"].expand(len(Y[:M - 64:4099]), -1))
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_infinite_values_stay_infinite(M):
+    """A z that overflows gives its row infinities of the formula's signs, as one product would, and no NaN."""
+    c = C.inputs(M, 64, 72, 8, 2, "one", "bf16", bias=False)
+    c["A"][:], c["B"][:] = 0, 1
+    c["A"][1, 3, 5], c["X"][:, 5], c["s"][:] = 2.0 ** 100, 1, 1
+    c["X"][1, 5], c["X"][2, 5] = 3e38, -3e38
+    g = cuda(c)
+    Y, Z = fwd(g)
+    # the base's own product of 3e38 overflows too where its weight is above 1.13: the other way, the sum is NaN
+    base = g["X"][:3, 5].float()[:, None] * g["W0"][:, 5].float()
+    want = base + torch.tensor([0, float("inf"), -float("inf")], device="cuda")[:, None]
+    assert Y[0].isfinite().all()
+    for i in (1, 2):
+        assert torch.equal(Y[i].isnan(), want[i].isnan())
+        assert torch.equal(Y[i].float()[~want[i].isnan()], want[i][~want[i].isnan()])
+    assert Z[1, 3] == float("inf") and Z[2, 3] == -float("inf")
+    g["dY"][:] = 0
+    g["dY"][1, 0], g["B"][1, 0] = 1, 0                   # g_1 has one element, which overflows times the scale
+    g["B"][1, 0, 2], g["s"][1], g["X"][1] = 3e38, 4.0, 1
+    dX, dA, dB, _ = bwd(g, torch.ones_like(Z))
+    assert (dA[1, 2] == float("inf")).all() and dA[1, [0, 1, 3]].isfinite().all()
