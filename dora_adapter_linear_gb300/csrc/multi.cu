@@ -130,13 +130,13 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
   // otherwise add as much to dA's error as dA's own rounding
   bf16* rest = static_cast<bf16*>(w.P2);
   if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, st)) != cudaSuccess) return e;
-  // dB needs nothing of that pass, dA and the column sums nothing of the product between: they fill the
-  // multiprocessors that those leave free
-  e = multi_reduce(p, sh.d_out, r, dY, Z, nullptr, true, true, s.one, s.each, w.pb, dB, true, true, st);
-  if (e != cudaSuccess) return e;
   if (dX && (e = tc_gemm(gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err), st)) != cudaSuccess)
     return e;
-  e = multi_reduce(p, sh.d_in, r, X, G, rest, false, false, 1.f, nullptr, w.pa, dA, dX != nullptr, false, st);
+  // the sums need nothing of that product: they run beside it, or where it leaves multiprocessors free
+  const bool beside = dX && (sh.M + 255) / 256 * ((sh.d_in + 255) / 256) > num_sms_current() / 2;
+  e = multi_reduce(p, sh.d_out, r, dY, Z, nullptr, true, true, s.one, s.each, w.pb, dB, true, beside, st);
+  if (e != cudaSuccess) return e;
+  e = multi_reduce(p, sh.d_in, r, X, G, rest, false, false, 1.f, nullptr, w.pa, dA, dX != nullptr, beside, st);
   if (e == cudaSuccess && dbias) e = multi_colsum(sh.M, sh.d_out, dY, w.csum, st);
   if (e != cudaSuccess) return e;
   return multi_sum(p, sh.r * sh.d_in, w.pa, dA, sh.r * sh.d_out, w.pb, dB, sh.d_out, w.csum, dbias, st);

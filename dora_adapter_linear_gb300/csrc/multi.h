@@ -64,9 +64,9 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
 // out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; T + T2 where T2 is
 // given; adapters with
 // several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero
-// early: see PdlEarly; behind: S has just been read by multi_proj
+// early: see PdlEarly; beside: with little shared memory, to run on the multiprocessors of a large product
 cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr, bool scaled,
-                         float one, const float* each, float* part, bf16* out, bool early, bool behind, cudaStream_t st);
+                         float one, const float* each, float* part, bf16* out, bool early, bool beside, cudaStream_t st);
 // sums [K]: the column sums from multi_colsum, or null
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
                       bf16* out1, int64_t K, const float* csum, bf16* sums, cudaStream_t st);

@@ -196,8 +196,8 @@ struct Reduce {
   static constexpr int NT = R / 8, PARTS = TWO ? 2 : 1;
   static constexpr int SP = 256 + 16, TP = 2 * R + 16;
   static constexpr int STAGE = 32 * (SP + PARTS * TP);
-  static constexpr int NST = STAGE <= 14 * 1024 ? 4 : 3;
-  static constexpr int SMEM = NST * STAGE + kPieceRows * 4;
+  static constexpr int NST = STAGE <= 14 * 1024 ? 4 : 3;     // stages, or two
+  static constexpr int smem(int stages) { return stages * STAGE + kPieceRows * 4; }
 };
 
 struct ReduceArgs {
@@ -210,7 +210,7 @@ struct ReduceArgs {
   bf16* out;
   float* part;                // [partials] x [K, R] or [R, K]
   bool early;                 // see PdlEarly
-  int behind;                 // CTAs a cluster of the pass that has just read S, or 0
+  int stages;                 // NST, or two
 };
 
 template <int R, bool TWO>
@@ -218,24 +218,13 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
   using C = Reduce<R, TWO>;
   constexpr int NT = C::NT;
   extern __shared__ __align__(16) uint8_t smem[];
-  int32_t* rows = reinterpret_cast<int32_t*>(smem + C::NST * C::STAGE);
+  const int nst = a.stages;
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + nst * C::STAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t K = a.K;
-  const int groups = (int)((K + 127) / 128), all = (int)gridDim.x / groups;
+  const int groups = (int)((K + 127) / 128);
   const PdlEarly order(a.early, blockIdx.x == gridDim.x - 1);
-  int mine = (int)blockIdx.x / groups, group = (int)blockIdx.x - mine * groups;
-  if (a.behind) {
-    // the columns that the pass before this one read last come first, while they are in L2: it walked along the
-    // rows, each rank of its clusters through its own stretch
-    const int i = (int)blockIdx.x / all, ranks = a.behind, share = (groups + ranks - 1) / ranks;
-    mine = (int)blockIdx.x - i * all;
-    // i-th of the groups, counted down from the ends of the stretches
-    int left = i;
-    group = -1;
-    for (int d = share - 1; d >= 0 && group < 0; --d)
-      for (int q = 0; q < ranks && group < 0; ++q)
-        if (q * share + d < groups && left-- == 0) group = q * share + d;
-  }
+  const int mine = (int)blockIdx.x / groups, group = (int)blockIdx.x - mine * groups;
   const int4 piece = a.p.pieces[mine];             // there is room for as many as the grid has
   if (mine >= a.p.head[kHeadPieces]) return;
   const int64_t k0 = (int64_t)group * 128;
@@ -244,9 +233,9 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
   const int stages = (piece.z + 31) / 32;
   const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;     // 16 threads a row of S
   const bool in = k0 + c * 8 < K;
-  auto load = [&](int s) {
+  auto load = [&](int s, int at_stage) {
     if (s < stages) {
-      uint8_t* st = smem + s % C::NST * C::STAGE;
+      uint8_t* st = smem + at_stage * C::STAGE;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + 8 * i;
@@ -268,13 +257,13 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-#pragma unroll
-  for (int s = 0; s < C::NST - 1; ++s) load(s);
-  for (int s = 0; s < stages; ++s) {
-    cp_async_wait<C::NST - 2>();
+  for (int s = 0; s < nst - 1; ++s) load(s, s);
+  for (int s = 0, now = 0; s < stages; ++s) {
+    if (nst == 2) cp_async_wait<0>();
+    else cp_async_wait<C::NST - 2>();
     __syncthreads();          // stage s is there, and all are done with the one that is loaded next
-    load(s + C::NST - 1);
-    const uint32_t S = smem_u32(smem + s % C::NST * C::STAGE), T = S + 32 * C::SP;
+    load(s + nst - 1, now == 0 ? nst - 1 : now - 1);
+    const uint32_t S = smem_u32(smem + now * C::STAGE), T = S + 32 * C::SP;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       uint32_t x[2][4];
@@ -297,6 +286,7 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
           }
         }
     }
+    if (++now == nst) now = 0;
   }
   cp_async_wait<0>();
   const float f = !a.scaled ? 1.f : a.each ? __ldg(a.each + piece.x) : a.one;
@@ -427,11 +417,12 @@ cudaError_t proj_launch(const ProjArgs& a, int64_t items, cudaStream_t st) {
   return l != cudaSuccess ? l : cudaGetLastError();
 }
 template <int R, bool TWO>
-cudaError_t reduce_launch(const ReduceArgs& a, int64_t pieces, cudaStream_t st) {
+cudaError_t reduce_launch(ReduceArgs a, int64_t pieces, cudaStream_t st) {
   using C = Reduce<R, TWO>;
-  const cudaError_t e = allow_smem<multi_reduce_mma<R, TWO>>(C::SMEM);
+  const cudaError_t e = allow_smem<multi_reduce_mma<R, TWO>>(C::smem(C::NST));
   if (e != cudaSuccess) return e;
-  return launch_pdl(multi_reduce_mma<R, TWO>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::SMEM, st, a);
+  if (a.stages == 0) a.stages = C::NST;
+  return launch_pdl(multi_reduce_mma<R, TWO>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::smem(a.stages), st, a);
 }
 
 }  // namespace
@@ -457,21 +448,14 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
 }
 
 cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr,
-                         bool scaled, float one, const float* each, float* part, bf16* out, bool early, bool behind,
+                         bool scaled, float one, const float* each, float* part, bf16* out, bool early, bool beside,
                          cudaStream_t st) {
   const int64_t pieces = multi_pieces(p.M, p.n);
-  ReduceArgs a{p, K, S, T, T2, one, each, scaled, kr, out, part, early, 0};
+  const ReduceArgs a{p, K, S, T, T2, one, each, scaled, kr, out, part, early, beside ? 2 : 0};
   switch (r) {
-#define CASE(R)                                                                       \
-  case R:                                                                             \
-    if (behind) a.behind = proj_ranks<R, true>(multi_items(p.M, p.n), K);             \
-    return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
+#define CASE(R) \
+  case R: return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
     RANKS(CASE)
-#undef CASE
-#define CASE(R)                                                                       \
-  case R:                                                                             \
-    if (behind) a.behind = proj_ranks<R - 64, true>(multi_items(p.M, p.n), K);        \
-    return T2 ? reduce_launch<R, true>(a, pieces, st) : reduce_launch<R, false>(a, pieces, st);
     MORE_RANKS(CASE)
 #undef CASE
   }

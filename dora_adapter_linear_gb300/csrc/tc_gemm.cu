@@ -82,12 +82,14 @@ template <> struct EpiCfg<EPI_SWIGLU_BWD, false> { static constexpr int STAGES =
 template <> struct EpiCfg<EPI_SCALE_BIAS, true> { static constexpr int STAGES = 6, STG_BUFS = 2; };
 template <> struct EpiCfg<EPI_SWIGLU, true> { static constexpr int STAGES = 5, STG_BUFS = 3; };
 template <> struct EpiCfg<EPI_SWIGLU_BWD, true> { static constexpr int STAGES = 6, STG_BUFS = 2; };
+// many adapters: a stage less, as fast, leaves room for the rank-r passes beside the product
+constexpr int kMultiStages = 5;
 template <> struct EpiCfg<EPI_W8A8K, false> { static constexpr int STAGES = 4, STG_BUFS = 2; };
 template <> struct EpiCfg<EPI_W8A8K, true> { static constexpr int STAGES = 6, STG_BUFS = 2; };
 
-template <int EPI, bool PAIR, bool KSCALE = false>
+template <int EPI, bool PAIR, bool KSCALE = false, bool MULTI = false>
 struct Layout {
-  static constexpr int STAGES = EpiCfg<EPI, PAIR>::STAGES;
+  static constexpr int STAGES = MULTI ? kMultiStages : EpiCfg<EPI, PAIR>::STAGES;
   static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // B rows (N) staged by one CTA
   static constexpr int B_STAGE_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_STAGE_BYTES + B_STAGE_BYTES;
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
   static_assert(!KSCALE || (EPI == EPI_SCALE_BIAS && !STACKED), "K-scaling: plain dX products only");
   static_assert(!MULTI || (EPI == EPI_SCALE_BIAS && !STACKED && HAS_TAIL && !KSCALE), "many adapters: plain products only");
   using C = OneCta<EPI, KSCALE>;
-  using L = Layout<EPI, true, KSCALE>;
+  using L = Layout<EPI, true, KSCALE, MULTI>;
   constexpr int STAGES = L::STAGES;
   constexpr int N_OUT = STACKED ? BN / 2 : BN;        // logical output columns per tile
   constexpr uint32_t TMEM_COLS = 2 * BN;
@@ -1362,7 +1364,7 @@ static cudaError_t launch_one(const TcParams& p, cudaStream_t st, int tiles, int
 
 template <bool B0_MN, bool STACKED, bool HAS_TAIL, bool B1_MN, int EPI, bool KSCALE = false, bool MULTI = false>
 static cudaError_t launch_pair(const TcParams& p, cudaStream_t st, int tiles, int max_ctas) {
-  using L = Layout<EPI, true, KSCALE>;
+  using L = Layout<EPI, true, KSCALE, MULTI>;
   auto kern = tc_pair_kernel<B0_MN, STACKED, HAS_TAIL, B1_MN, EPI, KSCALE, MULTI>;
   static int max_clusters_dev[64] = {0};   // co-resident clusters, per device
   int& max_clusters = max_clusters_dev[current_device_slot()];
