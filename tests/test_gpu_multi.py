@@ -52,6 +52,26 @@ def test_forward_and_backward(M, d_in, d_out, r, n, style, dtype):
     ops.check_device_errors()
 
 
+@pytest.mark.parametrize("M,d_in,d_out,r,n,style", [
+    (2570, 1800, 1816, 8, 5, "bare"), (2570, 1816, 1800, 16, 300, "rows"), (2600, 1800, 2048, 24, 9, "runs"),
+    (2561, 2568, 1800, 32, 40, "rows"), (2820, 1800, 1832, 32, 1, "one"), (2600, 1800, 1800, 72, 3, "runs")])
+def test_products_that_fill_the_device(M, d_in, d_out, r, n, style):
+    """Enough tiles for every multiprocessor: the gradients' sums run beside the product.  Z recomputed has the same bits."""
+    c = C.inputs(M, d_in, d_out, r, n, style, "bf16", seed=M + r)
+    g = cuda(c)
+    Y, Z = fwd(g)
+    ref = C.reference_fwd(c, "bf16")
+    C.near(Y, ref["Y"], "Y")
+    C.near(Z, ref["Z"], "Z")
+    first = bwd(g, Z)
+    grads = dict(zip(("dX", "dA", "dB", "dbias"), first))
+    for k, v in C.reference_bwd(c, Z, "bf16").items():
+        C.near(grads[k], v, k)
+    for other in (Z, None):
+        assert all(torch.equal(a, b) for a, b in zip(first, bwd(g, other)))
+    ops.check_device_errors()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_options(dtype):
     """No bias, a number as scale, 32-bit ids, no saved Z, no dX, Z recomputed."""
