@@ -150,10 +150,48 @@ __device__ __forceinline__ void gate_act_grad(float e, int act, float& a, float&
 
 // ---------------------------------------------------------------------------- epilogue of one tile
 // One warp drains its 32 TMEM lanes (rows row0 .. row0 + 31) of the accumulator at t_row.
-template <int EPI, int N_OUT>
+template <int EPI, int N_OUT, bool MULTI = false>
 __device__ __forceinline__ void epilogue_tile(const TcParams& p, uint32_t t_row, int row0, int n0, int lane,
                                               uint8_t* my_stg, uint32_t& chunk_ctr) {
-  if constexpr (EPI == EPI_SCALE_BIAS) {
+  if constexpr (EPI == EPI_SCALE_BIAS && MULTI) {
+    // a product with one tile a CTA has nothing to hide its epilogue behind: all 64 columns of a chunk are read at
+    // once, and the bias comes by 16 bytes
+#pragma unroll 1
+    for (int c = 0; c < N_OUT / 64; ++c) {
+      uint32_t v[64];
+      tmem_ld_32x32b_x32(t_row + c * 64, *reinterpret_cast<uint32_t(*)[32]>(v));
+      tmem_ld_32x32b_x32(t_row + c * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+      if (lane == 0) tma_store_wait_read<0>();
+      __syncwarp();
+      tmem_ld_wait();
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 64; j += 8) {
+          const int col = n0 + c * 64 + j;             // N is a multiple of 8
+          if (col >= p.N) break;
+          const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+          const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 f = unpack_bf16x2(w[q]);
+            v[j + 2 * q] = __float_as_uint(u2f(v[j + 2 * q]) + f.x);
+            v[j + 2 * q + 1] = __float_as_uint(u2f(v[j + 2 * q + 1]) + f.y);
+          }
+        }
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) w[j] = pack_bf16x2(u2f(v[2 * j]), u2f(v[2 * j + 1]));
+      stage_row(my_stg, lane, w, 0);
+      stage_row(my_stg, lane, w + 16, 4);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&p.tmOut[0], my_stg, n0 + c * 64, row0);
+        tma_store_commit();
+      }
+    }
+  } else if constexpr (EPI == EPI_SCALE_BIAS) {
 #pragma unroll 1
     for (int c = 0; c < N_OUT / 64; ++c, ++chunk_ctr) {
       // a whole-tile epilogue warp double-buffers its staging; a half-tile one has a single buffer
@@ -1176,7 +1214,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
       const uint32_t t_row = tmem_base + ((uint32_t)(32 * q) << 16) + buf * BN + half * (N_OUT / 2);
       const int row0 = mt * PM + (int)rank * BM + 32 * q;
       if constexpr (EPI8)
-        epilogue_tile<EPI, N_OUT / 2>(p, t_row, row0, nt * N_OUT + half * (N_OUT / 2), lane, my_stg, chunk_ctr);
+        epilogue_tile<EPI, N_OUT / 2, MULTI>(p, t_row, row0, nt * N_OUT + half * (N_OUT / 2), lane, my_stg, chunk_ctr);
       else
         epilogue_tile<EPI, N_OUT>(p, t_row, row0, nt * N_OUT, lane, my_stg, chunk_ctr);
       tc_fence_before();
