@@ -103,6 +103,9 @@ TcGemmDesc gemm(const MultiPlan& p, int mode, int64_t N, int64_t K, int r, int64
   return d;
 }
 
+// whether a product [M, N] has a tile for every pair of multiprocessors
+bool fills(int64_t M, int64_t N) { return (M + 255) / 256 * ((N + 255) / 256) >= num_sms_current() / 2; }
+
 cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
                     const bf16* A, const bf16* B, const bf16* bias, Scale s, bf16* Y, bf16* Z, cudaStream_t st) {
   const int r = (int)sh.r;
@@ -110,7 +113,7 @@ cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiW
     return multi_few_fwd(p, sh.d_out, sh.d_in, r, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
                          wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);
-  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, st);
+  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, fills(sh.M, sh.d_out), st);
   if (e != cudaSuccess) return e;
   return tc_gemm(gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err), st);
 }
@@ -122,18 +125,19 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
   bf16* G = static_cast<bf16*>(w.P);
   cudaError_t e;
   if (!Z) {
-    if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, nullptr, st)) != cudaSuccess)
+    if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, nullptr, fills(sh.M, sh.d_out),
+                        st)) != cudaSuccess)      // as the forward has it
       return e;
     Z = static_cast<const bf16*>(w.Z);
   }
+  const bool beside = dX && fills(sh.M, sh.d_in);
   // s g enters dX rounded, like s z the output; as a factor of dA it comes with the rest of its rounding, which would
   // otherwise add as much to dA's error as dA's own rounding
   bf16* rest = static_cast<bf16*>(w.P2);
-  if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, st)) != cudaSuccess) return e;
+  if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, beside, st)) != cudaSuccess) return e;
   if (dX && (e = tc_gemm(gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err), st)) != cudaSuccess)
     return e;
   // the sums need nothing of that product: they run beside it, or where it leaves multiprocessors free
-  const bool beside = dX && (sh.M + 255) / 256 * ((sh.d_in + 255) / 256) > num_sms_current() / 2;
   e = multi_reduce(p, sh.d_out, r, dY, Z, nullptr, true, true, s.one, s.each, w.pb, dB, true, beside, st);
   if (e != cudaSuccess) return e;
   e = multi_reduce(p, sh.d_in, r, X, G, rest, false, false, 1.f, nullptr, w.pa, dA, dX != nullptr, beside, st);

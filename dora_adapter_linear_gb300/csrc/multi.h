@@ -59,8 +59,9 @@ cudaError_t multi_plan(const MultiPlan& p, const void* ids, int id_bits, cudaStr
 // bf16 rank-r passes (multi_rank.cu); s_a is each[a], or `one` when each is null.
 // T_i = S_i U_a^T (U_a [r, K], or kr: [K, r]): plain = T, scaled = s_a T, rest = what scaled's rounding left of s_a T,
 // [M, r], each may be null.  Rows without adapter: zeros in plain, nothing in the others.
+// all: the product that follows has tiles for all multiprocessors
 cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
-                       const float* each, bf16* plain, bf16* scaled, bf16* rest, cudaStream_t st);
+                       const float* each, bf16* plain, bf16* scaled, bf16* rest, bool all, cudaStream_t st);
 // out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; T + T2 where T2 is
 // given; adapters with
 // several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero

@@ -387,20 +387,23 @@ __global__ void __launch_bounds__(256) multi_colsum_kernel(int64_t M, int64_t K,
   }
 }
 
-// as many CTAs to a cluster as two an SM have room for, each with two rounds of the ring at least
+// as many CTAs to a cluster as two an SM have room for (about half of the adapters end in a part of an item).  Before a
+// product that needs all multiprocessors a CTA has four stages at least (3001 x 2568: 61.2 us, with six 62.9), before a
+// smaller one six: that one begins on multiprocessors that have none of these CTAs (1999 x 2568, 32 tiles: 37.7 us,
+// with four 41.7)
 template <int R, bool KR>
-int proj_ranks(int64_t items, int64_t K) {
-  const int64_t steps = (K + 127) / 128, slots = 2 * num_sms_current();
+int proj_ranks(const MultiPlan& p, int64_t K, bool all) {
+  const int64_t steps = (K + 127) / 128, slots = 2 * num_sms_current(), items = p.M / kItemRows + (p.n + 1) / 2;
   int ranks = 1;
-  while (ranks < 8 && items * ranks * 2 <= slots && steps >= ranks * 2 * 2 * (Proj<R, KR>::NST - 1)) ranks *= 2;
+  while (ranks < 8 && items * ranks * 2 <= slots && steps >= ranks * 2 * (all ? 4 : 6)) ranks *= 2;
   return ranks;
 }
 template <int R, bool KR>
-cudaError_t proj_launch(const ProjArgs& a, int64_t items, cudaStream_t st) {
+cudaError_t proj_launch(const ProjArgs& a, int64_t items, bool all, cudaStream_t st) {
   using C = Proj<R, KR>;
   const cudaError_t e = allow_smem<multi_proj_mma<R, KR>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  const int ranks = proj_ranks<R, KR>(items, a.K);
+  const int ranks = proj_ranks<R, KR>(a.p, a.K, all);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -431,14 +434,15 @@ cudaError_t reduce_launch(ReduceArgs a, int64_t pieces, cudaStream_t st) {
 #define MORE_RANKS(CASE) CASE(72) CASE(80) CASE(88) CASE(96) CASE(104) CASE(112) CASE(120) CASE(128)
 
 cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
-                       const float* each, bf16* plain, bf16* scaled, bf16* rest, cudaStream_t st) {
+                       const float* each, bf16* plain, bf16* scaled, bf16* rest, bool all,
+                       cudaStream_t st) {
   const int64_t items = multi_items(p.M, p.n);
   for (int j0 = 0; j0 < r; j0 += 64) {   // ranks above 64 take a second pass: their sums do not fit the registers
     const ProjArgs a{p, K, S, U, one, each, plain, scaled, rest, r, j0};
     cudaError_t e = cudaErrorInvalidValue;
     switch (r - j0 < 64 ? r - j0 : 64) {
 #define CASE(R) \
-  case R: e = kr ? proj_launch<R, true>(a, items, st) : proj_launch<R, false>(a, items, st); break;
+  case R: e = kr ? proj_launch<R, true>(a, items, all, st) : proj_launch<R, false>(a, items, all, st); break;
       RANKS(CASE)
 #undef CASE
     }
