@@ -8,8 +8,9 @@
 // their way at once) in a fixed order.  A CTA of the last one scales a unit whose group's factor is not 1, last
 // units first, while their elements are still in L2.  The units' sums of a group are added by one CTA for each
 // group in a launch between, or, where a group has up to 512, by every CTA of the last launch for itself
-// (three adapters of one small block: 10.1 instead of 12 us a call).  Bytes bound large sets: every element
-// read, those above the limit read again and written.
+// (three adapters of one small block: 3.4 us on the device, 9.2 a call, 12 with the launch between).  Bytes bound large
+// sets: every element read, those above the limit read again and written.  168 M bf16 elements, half of them scaled: norms
+// 53 us (6.3 TB/s), scaling 44, together 100 us of 74 at the rate of a long copy.
 #include <float.h>
 #include <math.h>
 

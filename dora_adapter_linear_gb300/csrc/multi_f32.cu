@@ -14,8 +14,9 @@ __device__ __forceinline__ float scale_of(float one, const float* each, int a) {
 
 // ------------------------------------------------------------------ rank-r products of rows
 // A CTA has eight rows of an item, all j of their adapter and its cluster rank's share of K; the rows pass through
-// shared memory 1024 columns at a time, so a factor is read once for eight rows.  Up to eight warps take the j of U_a [r, K] in turn; of
-// U_a [K, r] (KR) a thread keeps one j, and the threads' shares of k meet in shared memory.
+// shared memory 1024 columns at a time, so a factor is read once for eight rows.  Up to eight warps take the j of
+// U_a [r, K] in turn; of U_a [K, r] (KR) a thread keeps one j, and the threads' shares of k meet in shared memory.
+// Latency: 10 us for 509 x 1000, rank 12, as for 300 x 1376, rank 8.
 constexpr int kCols = 1024, kRows = 8;   // kItemRows is a multiple of kRows
 
 struct F32Proj {
@@ -124,7 +125,9 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
 // Operands come by asynchronous copies, three slabs ahead, and lie as they do in memory: rows of 16 k (80 bytes apart,
 // so that eight rows' 16 bytes fall into different banks), W [K, N] by k.  A thread reads four k of a row at once.
 // What counts is warps: with two a scheduler it issues every second cycle (8 x 16 a thread: 60 us at 509 x 1000 x
-// 1496, the FMA units 38% busy), so 128 registers and four CTAs an SM.  The CTAs of a cluster share K and add their
+// 1496, the FMA units 38% busy), so 128 registers and four CTAs an SM: 55 us, 28 TFLOP/s.  Two products an
+// instruction (fma.rn.f32x2) do not help: a 16-byte read of shared memory takes four cycles of an SM, 16 of these
+// feed 256 FMA, and the pairs of k they come in would need twice the accumulators (4 x 8 a thread: 5 us more).  The CTAs of a cluster share K and add their
 // sums through distributed shared memory, each finishing its share of the rows.  There a thread has one column, and
 // takes its adapter's factor anew only where the next row has another one.
 constexpr int kTileM = 64, kTileN = 64, kSlab = 16, kGroups = 2, kGemmThreads = 64 * kGroups, kSlabs = 4;
@@ -327,6 +330,7 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
 // ------------------------------------------------------------------ gradients of the adapters
 // out_a(j, k) = f_a sum over its rows T[i][j] S[i][k]: a CTA has 32 columns and 16 of the j of one adapter, its
 // eight warps every eighth row, four at a time.  Both stacks in one launch; zeros for an adapter without rows.
+// 300 rows of three adapters, 512 and 1376 columns: 17 us alone, beside the product's end: latency.
 struct F32Reduce {
   MultiPlan p;
   int r;

@@ -4,7 +4,10 @@
 // product is turned around: 128 rows of W0 are the M side of the tcgen05 MMA and the batch's rows its N side
 // (16, 32 or 64, zero-filled), and K is shared by the CTAs of a cluster, each with its own stretch of W0, so that
 // some 300 CTAs, two an SM, keep their copies in flight.  The partial accumulators meet through distributed
-// shared memory, in the order of the ranks.  The rank-r part is computed on the side:
+// shared memory, in the order of the ranks.  Measured (rank 16): one row of 4096 x 4096 10.1 us (W0 alone at the rate of
+// a long copy: 5.0), 64 rows 18.5, 19 rows of 4096 x 11008 at rank 64 24.1 (15.0): a first read of 67 MB takes 16 us with
+// nothing but loads, and a decode step is not long enough to get past that start.  The rank-r part is computed on the
+// side:
 //   multi_few_down   z_i = x_i A_a^T, one cluster a row, its CTAs sharing K;
 //   multi_few        while W0 streams in, eight more warps form s z B_a^T.
 // The second kernel starts while the first one runs (programmatic launch): it touches nothing that the first
@@ -542,12 +545,12 @@ cudaError_t down_launch(const FewArgs& a, int* beside, cudaStream_t st) {
 
 }  // namespace
 
-// Measured (4096 x 4096, 128 rows: 21 us, the GEMM of 256-row tiles 28; 192: 30 and 29; 4096 x 11008, 64 rows: 31 and
-// 51, 128: 55 and 51; 4096 x 1024, 256: 23 and 28, 512: 31 and 28): up to 128 rows while two CTAs share K, more only
-// where eight do.
+// Measured against the GEMM of 256-row tiles (K = 4096, us here and there): N 4096, 64 rows: 17.6, 29.6; 128: 20.4, 30.1;
+// 192: 29.4, 30.1; N 11008, 64: 30.5, 33.2; 128: 48.6, 34.2; 256 rows, N 1024: 23.8, 28.4; 2048: 24.7, 29.9; 512 rows, N
+// 1024: 31, 28.  Up to 128 rows while two CTAs share K, more only where four do.
 bool multi_few_fits(int64_t M, int64_t N) {
   const int64_t groups = (M + 63) / 64, ctas = (N + kRowsW - 1) / kRowsW * groups;
-  return M <= kFewRows && ctas * (groups <= 2 ? 2 : 8) <= 2 * num_sms_current();
+  return M <= kFewRows && ctas * (groups <= 2 ? 2 : 4) <= 2 * num_sms_current();
 }
 
 cudaError_t multi_few_fwd(const MultiPlan& p, int64_t N, int64_t K, int r, const bf16* X, const bf16* W0,
