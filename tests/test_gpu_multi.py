@@ -1,10 +1,12 @@
 """The many-adapter projection against its fp64 reference, element by element."""
+import threading
+
 import numpy as np
 import pytest
 import torch
 
 from dora_adapter_linear_gb300 import _lib as L
-from dora_adapter_linear_gb300 import ops
+from dora_adapter_linear_gb300 import ops, optim
 import multi_cases as C
 
 pytestmark = pytest.mark.gpu
@@ -303,3 +305,38 @@ def test_infinite_values_stay_infinite(M):
     g["B"][1, 0, 2], g["s"][1], g["X"][1] = 3e38, 4.0, 1
     dX, dA, dB, _ = bwd(g, torch.ones_like(Z))
     assert (dA[1, 2] == float("inf")).all() and dA[1, [0, 1, 3]].isfinite().all()
+
+
+@pytest.mark.parametrize("own_streams", [False, True])
+def test_threads(own_streams):
+    """Calls of four threads, on one stream, where their launches come in any order, or on one each."""
+    cases = [cuda(C.inputs(M, d, d + 16, r, 5, "rows", "bf16", seed=M)) for M, d, r in
+             ((5, 520, 16), (150, 136, 24), (700, 264, 8), (2570, 1800, 32))]
+    plans = [ops.adapter_plan(g["ids"], 5) for g in cases]
+
+    def step(i):
+        Y, Z = fwd(cases[i], plans[i])
+        grads = bwd(cases[i], Z, plans[i])
+        norms = optim.clip_grads([grads[1], grads[2]], 1.0, groups=5)
+        return (Y, Z, norms) + grads
+
+    want = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(i):
+        stream = torch.cuda.Stream() if own_streams else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                got = step(i)
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    ops.check_device_errors()
