@@ -146,6 +146,11 @@ struct F32Gemm {
   const float* each;
   bool scaled;                    // the update takes s_a
   float* out;
+  // The rank-r pass before this kernel gives P alone, and what came before that pass is complete when this kernel
+  // starts: its sums may begin beside that pass.  Half way they wait for it, so that the kernels behind this one start
+  // beside the rest.  With one or two CTAs an SM (backward of 300 x 512 -> 1376 39.7 -> 37.3 us); more are spread
+  // unevenly around that pass's (509 x 1000 -> 1496 58 -> 67).
+  bool ahead;
 };
 
 template <bool MN>
@@ -158,8 +163,6 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  pdl_wait();
-  if (threadIdx.x == 0) pdl_trigger();
   // rows ty + 8 i and columns tx + 8 j of a K-major W, 4 tx + 32 h and on of W [K, N]
   const int tid = threadIdx.x, group = tid >> 6, tx = tid & 7, ty = (tid >> 3) & 7;
   const int64_t K = a.K, N = a.N;
@@ -194,9 +197,18 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
     cp_async_commit();
   };
   float run[8][8] = {};
+  const int wait_at = a.ahead ? (s0 + s1) / 2 : s1;
+  if (!a.ahead) {
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_trigger();
+  }
 #pragma unroll
   for (int s = 0; s < kSlabs - 1; ++s) load(s0 + s);
   for (int s = s0; s < s1; ++s) {
+    if (s == wait_at) {
+      pdl_wait();
+      if (threadIdx.x == 0) pdl_trigger();
+    }
     cp_async_wait<kSlabs - 2>();
     __syncthreads();              // slab s is there, and all are done with the one that is loaded next
     load(s + kSlabs - 1);
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(256) f32_colsum_kernel(int64_t M, int64_t K, c
 unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
 
 template <bool MN>
-cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
+cudaError_t gemm(F32Gemm a, cudaStream_t st) {
   const int64_t tiles = (int64_t)blocks(a.N, kTileN) * blocks(a.p.M, kTileM), slabs = blocks(a.K, kSlab), sms = num_sms_current();
   const cudaError_t allowed = allow_smem<f32_gemm_kernel<MN>>(kGemmSmem);
   if (allowed != cudaSuccess) return allowed;
@@ -425,6 +437,7 @@ cudaError_t gemm(const F32Gemm& a, cudaStream_t st) {
     const double t = (double)n / s / (n == 1 ? 0.3 : n == 2 ? 0.55 : n == 3 ? 0.75 : 0.9) + 0.02 * (s - 1);
     if (s == 1 || t < best) best = t, ranks = s;
   }
+  a.ahead = tiles * ranks <= 2 * sms;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -467,7 +480,7 @@ cudaError_t multi_f32_proj(const MultiPlan& p, int64_t K, int r, const float* S,
 cudaError_t multi_f32_gemm(const MultiPlan& p, int64_t N, int64_t K, int r, const float* S, const float* W, bool mn,
                            const float* P, const float* U, const float* bias, bool scaled, float one, const float* each,
                            float* out, cudaStream_t st) {
-  const F32Gemm a{p, N, K, r, S, W, P, U, bias, one, each, scaled, out};
+  const F32Gemm a{p, N, K, r, S, W, P, U, bias, one, each, scaled, out, false};
   return mn ? gemm<true>(a, st) : gemm<false>(a, st);
 }
 
