@@ -17,6 +17,7 @@ class AdapterPlan:
             raise ValueError(f"a plan has 0 to 2^24 rows and 1 to 65535 adapters, got {rows} and {adapters}")
         self.rows, self.adapters = rows, adapters
         self.buffer = torch.empty(need, dtype=torch.uint8, device=device)
+        self.filled = False               # calls refuse a plan before its first update
 
     def update(self, ids):
         """ids [rows], a contiguous int32 or int64 CUDA tensor: the adapter of each row, anything outside
@@ -26,6 +27,7 @@ class AdapterPlan:
             raise ValueError(f"ids must be [{self.rows}] on {self.buffer.device}, got {tuple(ids.shape)} on {ids.device}")
         L.need_current("ids", ids.device)
         L.lora_multi_plan(self.rows, self.adapters, ids, self.buffer)
+        self.filled = True
         return self
 
 

@@ -657,6 +657,11 @@ def _multi_shape(X, W0, A, B, s, plan, bias=None, Z=None, dY=None):
     return L.LoraMultiShape(M, d_in, d_out, r, n, L.dtype_code(X))
 
 
+def _need_filled(plan):
+    if not plan.filled:
+        raise ValueError("the plan holds no ids yet: make it by adapter_plan() or call update()")
+
+
 @lru_cache(maxsize=1024)
 def _multi_bytes(backward, M, d_in, d_out, r, n, dtype):
     """Bytes of workspace; 0 for what the calls do not take."""
@@ -668,7 +673,8 @@ def _multi_bytes(backward, M, d_in, d_out, r, n, dtype):
 
 def _multi_workspace(backward, X, W0, A, plan):
     """The workspace of a call whose operands look well, or None: what is wrong is for the checks to name."""
-    if X.dim() == 2 and W0.dim() == 2 and A.dim() == 3 and X.is_cuda and isinstance(plan, AdapterPlan):
+    if X.dim() == 2 and W0.dim() == 2 and A.dim() == 3 and X.is_cuda and isinstance(plan, AdapterPlan) \
+            and plan.filled:
         need = _multi_bytes(backward, *X.shape, W0.shape[0], A.shape[1], A.shape[0], X.dtype)
         if need:
             return workspace(need, X.device)
@@ -686,6 +692,7 @@ def lora_multi_fwd(X, W0, A, B, s, plan, bias=None, save_z=True):
             return _done(done, "lora_multi_fwd")
     sh = _multi_shape(X, W0, A, B, s, plan, bias)
     _need_cuda("X", X)
+    _need_filled(plan)
     Y = torch.empty(sh.M, sh.d_out, dtype=X.dtype, device=X.device)
     Z = torch.empty(sh.M, sh.r, dtype=X.dtype, device=X.device) if save_z else None
     ws = workspace(L.lora_multi_workspace_bytes(False, sh), X.device)
@@ -703,6 +710,7 @@ def lora_multi_bwd(X, W0, A, B, Z, dY, s, plan, need_dx=True, need_dbias=False):
             return _done(done, "lora_multi_bwd")
     sh = _multi_shape(X, W0, A, B, s, plan, Z=Z, dY=dY)
     _need_cuda("X", X)
+    _need_filled(plan)
     dX = torch.empty_like(X) if need_dx else None
     dA, dB = torch.empty_like(A), torch.empty_like(B)
     dbias = torch.empty(sh.d_out, dtype=X.dtype, device=X.device) if need_dbias else None

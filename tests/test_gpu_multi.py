@@ -240,6 +240,17 @@ def test_captured_step_follows_its_ids():
                 C.near(dict(zip(("dX", "dA", "dB", "dbias"), grads))[k], v, k)
 
 
+def test_a_plan_without_ids_is_refused():
+    c = C.inputs(8, 64, 72, 8, 3, "rows", "bf16")
+    g = cuda(c)
+    plan = ops.AdapterPlan(8, 3, g["X"].device)
+    for call in (lambda: fwd(g, plan), lambda: bwd(g, None, plan)):
+        with pytest.raises(ValueError, match="no ids yet"):
+            call()
+    plan.update(g["ids"])
+    C.near(fwd(g, plan)[0], C.reference_fwd(c, "bf16")["Y"], "Y")
+
+
 def test_another_stream():
     c = C.inputs(300, 136, 264, 16, 5, "runs", "bf16")
     g = cuda(c)
