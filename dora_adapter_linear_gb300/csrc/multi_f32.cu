@@ -148,7 +148,8 @@ struct F32Gemm {
   float* out;
   // The rank-r pass before this kernel gives P alone, and what came before that pass is complete when this kernel
   // starts: its sums may begin beside that pass.  Half way they wait for it, so that the kernels behind this one start
-  // beside the rest.  With one or two CTAs an SM (backward of 300 x 512 -> 1376 39.7 -> 37.3 us); more are spread
+  // beside the rest (a quarter earlier or later: the same).  With one or two CTAs an SM (backward of 300 x 512 -> 1376
+  // 39.7 -> 37.3 us); more are spread
   // unevenly around that pass's (509 x 1000 -> 1496 58 -> 67).
   bool ahead;
 };
@@ -341,8 +342,9 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
 
 // ------------------------------------------------------------------ gradients of the adapters
 // out_a(j, k) = f_a sum over its rows T[i][j] S[i][k]: a CTA has 32 columns and 16 of the j of one adapter, its
-// eight warps every eighth row, four at a time.  Both stacks in one launch; zeros for an adapter without rows.
-// 300 rows of three adapters, 512 and 1376 columns: 17 us alone, beside the product's end: latency.
+// eight warps every eighth row, four at a time, asked for a round ahead; their T passes through shared memory.  Both
+// stacks in one launch; zeros for an adapter without rows.  Latency: 10.5 us for 300 rows of three adapters, 512 and
+// 1376 columns, 16 us for 1000 of four, 2048 and 2048 (47 with T by uniform loads and nothing ahead).
 struct F32Reduce {
   MultiPlan p;
   int r;
@@ -357,27 +359,48 @@ struct F32Reduce {
 
 __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__ F32Reduce a) {
   __shared__ float red[8][16][33];
+  __shared__ __align__(16) float ts[2][32][16];        // T of 32 rows, zeros past the last row and j
   const PdlEarly order(a.early, blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1);
   const int which = (int)blockIdx.x >= a.blocks0, ad = blockIdx.y, j0 = blockIdx.z * 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = a.r;
   const int64_t K = a.K[which], k0 = (int64_t)((int)blockIdx.x - (which ? a.blocks0 : 0)) * 32, k = k0 + lane;
   const float *S = a.S[which], *T = a.T[which];
   const int first = a.p.start[ad], last = a.p.start[ad + 1];
-  float acc[16] = {};
-  for (int i0 = first + warp; i0 < last; i0 += 32) {
-    int64_t row[4];
-    float x[4];
+  const int tr = threadIdx.x >> 3, tj = (threadIdx.x & 7) * 2;       // the row and the two j of T that a thread brings
+  int64_t row[4], trow;                                // of the 32 rows that are loaded next
+  float x[4], t[2];
+  auto rows = [&](int i0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) row[q] = i0 + 8 * q < last ? a.p.order[i0 + 8 * q] : -1;
+    for (int q = 0; q < 4; ++q) row[q] = i0 + warp + 8 * q < last ? a.p.order[i0 + warp + 8 * q] : -1;
+    trow = i0 + tr < last ? a.p.order[i0 + tr] : -1;
+  };
+  auto load = [&] {
 #pragma unroll
     for (int q = 0; q < 4; ++q) x[q] = row[q] >= 0 && k < K ? __ldg(S + row[q] * K + k) : 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (row[q] >= 0) {
-        const float* t = T + row[q] * r + j0;
+    for (int q = 0; q < 2; ++q) t[q] = trow >= 0 && j0 + tj + q < r ? __ldg(T + trow * r + j0 + tj + q) : 0.f;
+  };
+  float acc[16] = {};
+  rows(first);
+  load();
+  rows(first + 32);
+  for (int i0 = first, flip = 0; i0 < last; i0 += 32, flip ^= 1) {
+    *reinterpret_cast<float2*>(&ts[flip][tr][tj]) = make_float2(t[0], t[1]);
+    float now[4];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j0 + j < r) acc[j] = fmaf(__ldg(t + j), x[q], acc[j]);
+    for (int q = 0; q < 4; ++q) now[q] = x[q];
+    __syncthreads();          // T is there, and all are done with the half that is written next
+    load();
+    rows(i0 + 64);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 u = *reinterpret_cast<const float4*>(&ts[flip][warp + 8 * q][j]);
+        acc[j] = fmaf(u.x, now[q], acc[j]);
+        acc[j + 1] = fmaf(u.y, now[q], acc[j + 1]);
+        acc[j + 2] = fmaf(u.z, now[q], acc[j + 2]);
+        acc[j + 3] = fmaf(u.w, now[q], acc[j + 3]);
       }
   }
 #pragma unroll
@@ -396,28 +419,43 @@ __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__
   }
 }
 
-// sums of all rows, 32 columns a CTA, a warp every eighth row
+// sums of all rows, 32 columns a cluster, whose CTAs have a stretch of the rows each and their warps every eighth of it;
+// added up through distributed shared memory, in the order of the ranks.  1000 x 2048: 9 us, 36 by one CTA for all rows.
 __global__ void __launch_bounds__(256) f32_colsum_kernel(int64_t M, int64_t K, const float* S, float* out) {
   __shared__ float red[8][32];
+  uint32_t rank, ranks;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const PdlEarly order(true, blockIdx.x == gridDim.x - 1);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t k = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t k = (int64_t)(blockIdx.x / ranks) * 32 + lane, m0 = M * rank / ranks, m1 = M * (rank + 1) / ranks;
   float total = 0.f;
-  for (int64_t m0 = warp; m0 < M; m0 += 8 * 256) {
+  for (int64_t b = m0 + warp; b < m1; b += 8 * 256) {
     float t = 0.f;
 #pragma unroll 8
-    for (int64_t m = m0; m < min(M, m0 + 8 * 256); m += 8)
+    for (int64_t m = b; m < min(m1, b + 8 * 256); m += 8)
       if (k < K) t += __ldg(S + m * K + k);
     total += t;
   }
   red[warp][lane] = total;
   __syncthreads();
-  if (warp == 0 && k < K) {
+  if (warp == 0) {
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) t += red[w][lane];
+    red[0][lane] = t;         // read by this warp alone until the cluster meets
+  }
+  cluster_sync_all();
+  if (warp == 0 && rank == 0 && k < K) {
+    float t = 0.f;
+    for (uint32_t q = 0; q < ranks; ++q) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(&red[0][lane]), q)));
+      t += v;
+    }
     out[k] = t;
   }
+  cluster_sync_all();         // no CTA leaves while another reads its sums
 }
 
 unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
@@ -493,7 +531,22 @@ cudaError_t multi_f32_reduce(const MultiPlan& p, int r, int64_t in, const float*
 }
 
 cudaError_t multi_f32_colsum(int64_t M, int64_t K, const float* S, float* out, cudaStream_t st) {
-  return launch_pdl(f32_colsum_kernel, dim3(blocks(K, 32)), dim3(256), 0, st, M, K, S, out);
+  const int64_t columns = blocks(K, 32);
+  int ranks = 1;                // stretches of at least 64 rows, while there is room for their CTAs
+  while (ranks < 8 && M >= ranks * 2 * 64 && columns * ranks * 2 <= 4 * num_sms_current()) ranks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(columns * ranks), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1 + pdl_attr(&attr[1]);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f32_colsum_kernel, M, K, S, out);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace lg
