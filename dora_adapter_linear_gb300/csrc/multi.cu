@@ -28,7 +28,17 @@ struct MultiWs {
   void* Z;                    // [M, r] z recomputed by the backward
   float* few;                 // forward of a few bf16 rows: s z in fp32
   float *pa, *pb, *csum;      // bf16 backward: partials of dA and dB, column sums
+  bf16 *S, *W;                // copies of X and W0, or of dY, in longer rows, where these are odd multiples of 16 bytes
 };
+// Whether copies of operands in longer rows pay.  Measured (rank 16, us without and with): forward 3001 x 2568 x 2568 58.3,
+// 54.6, 8192 x 4104 x 4104 291, 240, 1999 x 2568 -> 1000 35.2, 32.2, but 1999 x 1000 -> 2568 27.6, 29.2, 600 x 2568 x 2568
+// 28.4, 30.5; backward, dY alone, 3001 x 2568 x 2568 71.2, 68.8, 1000 x 4104 x 4104 59.8, 53.2, 600 x 2568 x 2568 33.1,
+// 35.2 (W0 [K, N] as well: 74.3, 60.3, 36.3).  So: with some steps for a pair of multiprocessors, of 1000 rows or so.
+bool pads(const lora_multi_shape& sh, bool bwd) {
+  const int64_t mt = (sh.M + 255) / 256, tiles = mt * (((bwd ? sh.d_in : sh.d_out) + 255) / 256),
+                steps = ((bwd ? sh.d_out : sh.d_in) + 63) / 64;
+  return mt >= 4 && (tiles + 75) / 76 * steps >= 40;
+}
 size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   Carve c{base};
   const bool bf = sh.dtype == LORA_BF16;
@@ -40,6 +50,10 @@ size_t carve(const lora_multi_shape& sh, bool bwd, char* base, MultiWs* w) {
   w->few = !bwd && bf && sh.M <= kFewRows ? c.take<float>((size_t)sh.M * sh.r) : nullptr;
   w->pa = bwd && bf ? c.take<float>(parts * sh.d_in) : nullptr;
   w->pb = bwd && bf ? c.take<float>(parts * sh.d_out) : nullptr;
+  const int64_t len = bwd ? sh.d_out : sh.d_in;
+  const bool pad = bf && multi_pad_odd(len) && pads(sh, bwd);
+  w->S = pad ? c.take<bf16>((size_t)sh.M * multi_pad_ld(len)) : nullptr;
+  w->W = pad && !bwd ? c.take<bf16>((size_t)sh.d_out * multi_pad_ld(sh.d_in)) : nullptr;
   w->csum = bwd && bf ? c.take<float>((size_t)multi_colsum_splits(sh.M) * sh.d_out) : nullptr;
   return c.off;
 }
@@ -103,6 +117,16 @@ TcGemmDesc gemm(const MultiPlan& p, int mode, int64_t N, int64_t K, int r, int64
   return d;
 }
 
+// the product's operands in longer rows, where there is room for these
+cudaError_t pad(const lora_multi_shape& sh, const MultiWs& w, const bf16* S, int64_t len, const bf16* W0, TcGemmDesc* d,
+                cudaStream_t st) {
+  if (!w.S && !w.W) return cudaSuccess;
+  if (w.S) d->A0 = w.S, d->lda0 = multi_pad_ld(len);
+  if (w.W) d->B0 = w.W, d->ldb0 = multi_pad_ld(sh.d_in);
+  d->ad_wait = true;
+  return multi_pad({S, w.S, sh.M, len}, {W0, w.W, sh.d_out, sh.d_in}, st);
+}
+
 // whether a product [M, N] has a tile for every pair of multiprocessors
 bool fills(int64_t M, int64_t N) { return (M + 255) / 256 * ((N + 255) / 256) >= num_sms_current() / 2; }
 
@@ -113,9 +137,11 @@ cudaError_t forward(const lora_multi_shape& sh, const MultiPlan& p, const MultiW
     return multi_few_fwd(p, sh.d_out, sh.d_in, r, X, W0, A, B, bias, s.one, s.each, w.few, Y, Z, w.err,
                          wait_timeout_ns(), st);
   bf16* T = static_cast<bf16*>(w.P);
-  const cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, fills(sh.M, sh.d_out), st);
+  cudaError_t e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, Z, T, nullptr, fills(sh.M, sh.d_out), st);
   if (e != cudaSuccess) return e;
-  return tc_gemm(gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err), st);
+  TcGemmDesc d = gemm(p, TC_FWD, sh.d_out, sh.d_in, r, sh.n, X, W0, T, B, bias, Y, w.err);
+  if ((e = pad(sh, w, X, sh.d_in, W0, &d, st)) != cudaSuccess) return e;
+  return tc_gemm(d, st);
 }
 
 cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const MultiWs& w, const bf16* X, const bf16* W0,
@@ -135,8 +161,10 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
   // otherwise add as much to dA's error as dA's own rounding
   bf16* rest = static_cast<bf16*>(w.P2);
   if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, beside, st)) != cudaSuccess) return e;
-  if (dX && (e = tc_gemm(gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err), st)) != cudaSuccess)
-    return e;
+  if (dX) {
+    TcGemmDesc d = gemm(p, TC_BWD_DX, sh.d_in, sh.d_out, r, sh.n, dY, W0, G, A, nullptr, dX, w.err);
+    if ((e = pad(sh, w, dY, sh.d_out, W0, &d, st)) != cudaSuccess || (e = tc_gemm(d, st)) != cudaSuccess) return e;
+  }
   // the sums need nothing of that product: they run beside it, or where it leaves multiprocessors free
   e = multi_reduce(p, sh.d_out, r, dY, Z, nullptr, true, true, s.one, s.each, w.pb, dB, true, beside, st);
   if (e != cudaSuccess) return e;

@@ -68,6 +68,15 @@ cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, cons
 // early: see PdlEarly; beside: with little shared memory, to run on the multiprocessors of a large product
 cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr, bool scaled,
                          float one, const float* each, float* part, bf16* out, bool early, bool beside, cudaStream_t st);
+// copies of matrices [rows, K] in rows of multi_pad_ld(K) elements, `to` null: none; beside the kernel before it
+struct MultiPad {
+  const bf16* from;
+  bf16* to;
+  int64_t rows, K;
+};
+inline bool multi_pad_odd(int64_t K) { return K % 16 == 8; }
+inline int64_t multi_pad_ld(int64_t K) { return (K + 63) / 64 * 64; }
+cudaError_t multi_pad(const MultiPad& S, const MultiPad& W, cudaStream_t st);
 // sums [K]: the column sums from multi_colsum, or null
 cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf16* out0, int64_t size1, const float* part1,
                       bf16* out1, int64_t K, const float* csum, bf16* sums, cudaStream_t st);

@@ -394,6 +394,34 @@ __global__ void __launch_bounds__(256) multi_colsum_kernel(int64_t M, int64_t K,
   }
 }
 
+// Rows of an odd multiple of 16 bytes slow the product's copies by a third (each 128 bytes of them lie across two lines),
+// so a product that reads them often enough takes copies in rows of whole lines, made beside the pass before it.
+struct PadArgs {
+  const bf16* from[2];
+  bf16* to[2];
+  int64_t rows[2], K[2], ld[2];
+};
+__global__ void __launch_bounds__(256) multi_pad_kernel(const __grid_constant__ PadArgs a) {
+  const PdlEarly order(true, blockIdx.x == gridDim.x - 1);
+  const int lane = threadIdx.x & 31, warps = (int)gridDim.x * 8;
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows[w]; row += warps) {   // a warp a row
+      const uint4* from = reinterpret_cast<const uint4*>(a.from[w] + row * a.K[w]);
+      uint4* to = reinterpret_cast<uint4*>(a.to[w] + row * a.ld[w]);
+      const int all = (int)(a.K[w] / 8);
+      for (int c = lane; c < all; c += 256) {
+        uint4 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c + 32 * q < all) v[q] = __ldg(from + c + 32 * q);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (c + 32 * q < all) to[c + 32 * q] = v[q];
+      }
+    }
+}
+
 // as many CTAs to a cluster as two an SM have room for (about half of the adapters end in a part of an item).  Before a
 // product that needs all multiprocessors a CTA has four stages at least (3001 x 2568: 61.2 us, with six 62.9), before a
 // smaller one six: that one begins on multiprocessors that have none of these CTAs (1999 x 2568, 32 tiles: 37.7 us,
@@ -478,6 +506,11 @@ cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf1
   const SumArgs a{p, {size0, size1}, {part0, part1}, {out0, out1}, sums ? multi_colsum_splits(p.M) : 0, K, csum, sums};
   const int64_t most = size0 > size1 ? size0 : size1, blocks = (most + 2047) / 2048;
   return launch_pdl(multi_sum_kernel, dim3((unsigned)(blocks < 256 ? blocks : 256), (unsigned)p.n, 2), dim3(256), 0, st, a);
+}
+
+cudaError_t multi_pad(const MultiPad& S, const MultiPad& W, cudaStream_t st) {
+  const PadArgs a{{S.from, W.from}, {S.to, W.to}, {S.to ? S.rows : 0, W.to ? W.rows : 0}, {S.K, W.K}, {multi_pad_ld(S.K), multi_pad_ld(W.K)}};
+  return launch_pdl(multi_pad_kernel, dim3((unsigned)(2 * num_sms_current())), dim3(256), 0, st, a);
 }
 
 int multi_colsum_splits(int64_t M) {

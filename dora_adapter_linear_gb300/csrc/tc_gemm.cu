@@ -65,6 +65,7 @@ struct TcParams {
   const int32_t *ad_count, *ad_list;
   const uint32_t* ad_mask;
   int ad_chunks;        // 16-column chunks of the rank
+  int ad_wait;          // the main operands come from the kernel before this one, too
   uint32_t* err;
   uint64_t timeout_ns;
 };
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE, ZF>::THREADS, 1) tc_gemm_k
 // no change): an adapter costs its tile 0.2 us for every 16 columns of rank.
 // 8192 x 4096 x 4096, rank 16: 162 us, 1.70 PFLOP/s; dX of 8192 x 11008 x 4096, rank 32: 438 us, 1.69.  Few tiles are
 // slower: 3001 x 2568 x 2568 takes 57 us, two rounds of 76 pairs, and rows of an odd multiple of 16 bytes slow its copies
-// (K 2576: 38 us without adapters, K 2568: 48).  Tiles of 128 columns were no faster (300 x 4096 x 4096: 34 us, 29).
+// (K 2576: 38 us without adapters, K 2568: 48; larger products get copies in longer rows).  Tiles of 128 columns were no faster (300 x 4096 x 4096: 34 us, 29).
 struct MultiTail {
   int KB, P, chunks, count;     // K-blocks of 64 of the rank; adapters a step; chunks of the rank; adapters
   __device__ __forceinline__ MultiTail(int chunks_, int count_)
@@ -1006,6 +1007,11 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE>::THREADS, 1) tc_pair_kerne
       bool ok = true;
       bool waited = !MULTI;   // MULTI: the rank-r pass before this kernel gives the tail alone, and what came before
                               // that pass is complete, so the main steps begin beside its end
+      if (MULTI && p.ad_wait) {
+        waited = true;
+        pdl_wait();
+        pdl_trigger();
+      }
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
         int mt, nt;
         tile_coords(t, p.num_m_tiles, p.num_n_tiles, p.group_m, mt, nt);
@@ -1556,6 +1562,7 @@ cudaError_t tc_gemm(const TcGemmDesc& d, cudaStream_t st) {
   p.ad_list = d.ad_list;
   p.ad_mask = d.ad_mask;
   p.ad_chunks = (d.K1 + 15) / 16;
+  p.ad_wait = d.ad_wait;
 
   p.M = d.M;
   p.N = d.N;
