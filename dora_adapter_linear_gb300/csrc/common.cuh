@@ -472,11 +472,19 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v) {
   return __bfloat1622float2(b);
 }
 
-// Two fp32 numbers in two bf16 parts: the first rounded, the second what that left (nothing of what is not finite)
+// Two fp32 numbers in two bf16 parts: the first rounded, the second what that left (nothing of what is not finite).
+// The other factor meets the first part as it is and the second by finite_bf16x2: an infinity times the number has the
+// first part's sign, which the rest need not have, and times a rest of zero it would be NaN.
 __device__ __forceinline__ void split_bf16x2(float x, float y, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
   const float2 had = unpack_bf16x2(hi);
   lo = pack_bf16x2(isfinite(had.x) ? x - had.x : 0.f, isfinite(had.y) ? y - had.y : 0.f);
+}
+// zeros in place of infinities and NaN
+__device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v) {
+  const uint32_t most = 0x7f7f7f7fu;                    // the largest number, twice
+  return v & __hle2_mask(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)),
+                         *reinterpret_cast<const __nv_bfloat162*>(&most));
 }
 
 // Input dropout on one bf16x2 operand register: each half becomes bf16(x k) where its mask byte

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) multi_few(const __grid_constant__
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         if (it >= items) break;
-        const int u = it / groups, f = (it - u * groups) * 16;
+        const int u = it / groups, c = (it - u * groups) * 16;
         const uint2 rows8 = *reinterpret_cast<const uint2*>(units + u * 8);
         const uint32_t half = lane & 16 ? rows8.y : rows8.x;
         const int row = (half >> (8 * (g & 3))) & 255;
@@ -416,14 +416,15 @@ __global__ void __launch_bounds__(kThreads, 2) multi_few(const __grid_constant__
         const uint32_t r0 = __shfl_xor_sync(0xffffffffu, up ? x[i].x : x[i].z, 2),
                        r1 = __shfl_xor_sync(0xffffffffu, up ? x[i].y : x[i].w, 2);
         const uint32_t m[4] = {up ? r0 : x[i].x, up ? x[i].z : r0, up ? r1 : x[i].y, up ? x[i].w : r1};
+        const uint32_t f[4] = {finite_bf16x2(m[0]), finite_bf16x2(m[1]), finite_bf16x2(m[2]), finite_bf16x2(m[3])};
         mma_bf16_16816(d, m, hi.x, hi.y);
-        mma_bf16_16816(d, m, lo.x, lo.y);
+        mma_bf16_16816(d, f, lo.x, lo.y);
         j += 16;
         if (j >= a.r) {
           const uint32_t pair = ((lane & 2 ? rows8.y : rows8.x) >> (16 * (lane & 1))) & 0xffffu;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {                // columns g and g + 8, the unit's rows 2 (lane % 4) and + 1
-            const int t = (pair >> (8 * (k & 1))) & 255, at = f + g + (k >> 1) * 8;
+            const int t = (pair >> (8 * (k & 1))) & 255, at = c + g + (k >> 1) * 8;
             if (t != 255) update[t * own + at] = d[k] + bias[at];
             d[k] = 0.f;
           }

@@ -277,9 +277,14 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
         ldsm_x4_t(x[m][0], x[m][1], x[m][2], x[m][3],
                   S + (kk * 16 + (lane & 7) + ((lane >> 4) << 3)) * C::SP + (warp * 32 + m * 16 + ((lane >> 3) & 1) * 8) * 2);
 #pragma unroll
-      for (int n = 0; n < NT; n += 2)
+      for (int w = 0; w < C::PARTS; ++w) {
+        if (w == 1)
 #pragma unroll
-        for (int w = 0; w < C::PARTS; ++w) {
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[m][i] = finite_bf16x2(x[m][i]);
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
           const uint32_t at = T + w * 32 * C::TP + (kk * 16 + (lane & 15)) * C::TP + n * 16;
           uint32_t b0, b1, b2 = 0, b3 = 0;
           if (n + 1 < NT) ldsm_x4_t(b0, b1, b2, b3, at + (lane >> 4) * 16);
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
             if (n + 1 < NT) mma_bf16_16816(acc[m][n + 1 < NT ? n + 1 : n], x[m], b2, b3);
           }
         }
+      }
     }
     if (++now == nst) now = 0;
   }

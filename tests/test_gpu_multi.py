@@ -8,6 +8,7 @@ import torch
 from dora_adapter_linear_gb300 import _lib as L
 from dora_adapter_linear_gb300 import ops, optim
 import multi_cases as C
+from oracle import multi_oracle as O
 
 pytestmark = pytest.mark.gpu
 
@@ -351,3 +352,85 @@ def test_threads(own_streams):
         t.join()
     assert not wrong
     ops.check_device_errors()
+
+
+def same_kinds(got, want, what):
+    """NaN and signed infinities where the formula has them."""
+    got = C.f64(got)
+    for kind in (np.isnan, np.isposinf, np.isneginf):
+        assert (kind(got) == kind(want)).all(), f"{what}: {kind.__name__}"
+
+
+def one_infinity(M, dtype, where):
+    """A case of 16 columns of rank and three adapters in turn, and the same with an infinity at each of `where`:
+    (name, index, sign).  Values of z and g that meet one are far enough from zero to have a sign."""
+    c = C.inputs(M, 72, 136, 16, 3, "rows", dtype, seed=6)
+    c["ids"] = np.arange(M) % 3
+    X, W0, A, B, s, dY = (C.f64(c[k]) for k in ("X", "W0", "A", "B", "s", "dY"))
+    Z = O.multi_fwd(X, W0, A, B, s, c["ids"])[1]
+    G = O.multi_bwd(X, W0, A, B, s, c["ids"], Z, dY)[4]
+    mZ = O.multi_fwd(abs(X), W0, abs(A), B, s, c["ids"])[1]
+    mG = O.multi_bwd(X, W0, A, abs(B), abs(s), c["ids"], Z, abs(dY))[4]
+    for at in ((1, slice(None)), (slice(1, None, 3), [3, 9, 15])):
+        assert (abs(Z) > 80 * C.STEP * mZ)[at].all() and (abs(G) > 144 * C.STEP * mG)[at].all()
+    d = {k: v.clone() if torch.is_tensor(v) else v for k, v in c.items()}
+    for name, at, sign in where:
+        d[name][at] = sign * float("inf")
+    return c, d
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("where", [[("B", (1, 5, 3), 1)], [("B", (1, 5, 3), -1), ("B", (1, 70, 9), 1)], [("B", (1, 135, 15), -1)]])
+def test_an_infinity_in_B(M, dtype, where):
+    """Its column of the adapter's rows is the infinity of the formula's sign, all else keeps its bits."""
+    c, d = one_infinity(M, dtype, where)
+    Y0, Z0 = fwd(cuda(c))
+    Y, Z = fwd(cuda(d))
+    assert torch.equal(Z, Z0)
+    with np.errstate(all="ignore"):
+        want = O.multi_fwd(*(C.f64(d[k]) for k in ("X", "W0", "A", "B", "s")), c["ids"], C.f64(c["bias"]))[0]
+    assert np.isinf(want).sum() == len(where) * len(range(1, M, 3)) and not np.isnan(want).any()
+    same_kinds(Y, want, "Y")
+    fine = torch.from_numpy(np.isfinite(want)).cuda()
+    assert torch.equal(Y[fine], Y0[fine])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [3, 40, 300, 1600])
+@pytest.mark.parametrize("where", [[("X", (1, 7), 1)], [("X", (1, 7), -1), ("X", (1, 71), 1)], [("A", (1, 3, 7), 1)],
+                                   [("B", (1, 5, 3), 1)], [("dY", (1, 5), -1)]])
+def test_an_infinity_in_the_backward(M, dtype, where):
+    """dA is a sum of g x: infinite, with the formula's sign, where an infinity meets numbers; and dX and dB likewise."""
+    c, d = one_infinity(M, dtype, where)
+    Z = fwd(cuda(c))[1]
+    first, got = bwd(cuda(c), Z), bwd(cuda(d), Z)
+    with np.errstate(all="ignore"):
+        want = O.multi_bwd(*(C.f64(d[k]) for k in ("X", "W0", "A", "B", "s")), c["ids"], C.f64(Z), C.f64(d["dY"]))
+    for name, a, b, v in zip(("dX", "dA", "dB", "dbias"), first, got, want):
+        same_kinds(b, v, name)
+        fine = torch.from_numpy(np.isfinite(v)).cuda()
+        assert torch.equal(a[fine], b[fine]), name
+
+
+@pytest.mark.parametrize("e", [10, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_products_that_overflow(M, sign, e):
+    """Finite factors, z or g of 2^50 or 2^80, whose product does not fit in fp32, let alone bf16: the infinity of its
+    sign, as one product of the rounded factor gives, whatever the sign of its rounding's rest."""
+    for frac in (1 + 3 * 2.0 ** -7, 1 + 100 * 2.0 ** -7, 1):         # times 1 + 2^-7: rests of both signs and none
+        c = C.inputs(M, 64, 72, 8, 2, "one", "bf16", bias=False)
+        for k in ("A", "B", "W0", "X", "dY"):
+            c[k][:] = 0
+        c["s"][:] = 1
+        c["A"][1, 3, 5], c["X"][:, 5], c["B"][1, 9, 3] = 2.0 ** e * (1 + 2.0 ** -7), 2.0 ** 40 * frac, sign * 2.0 ** (120 - e)
+        g = cuda(c)
+        Y, Z = fwd(g)
+        assert (Y[:, 9] == sign * float("inf")).all() and not Y[:, :9].any() and not Y[:, 10:].any()
+        g["dY"][0, 9], g["X"][0, 5], g["A"][:] = 2.0 ** (2 * e - 80) * frac, 2.0 ** (120 - e), 0
+        g["s"][1] = 1 + 2.0 ** -7                        # g_0 = sign 2^(40 + e) (1 + 2^-7) frac
+        dX, dA, dB, _ = bwd(g, torch.zeros_like(Z))
+        assert dA[1, 3, 5] == sign * float("inf")
+        dA[1, 3, 5] = 0
+        assert not dA.any() and not dB.any() and not dX.any()
