@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__
 #pragma unroll
   for (int j = 0; j < 16; ++j) red[warp][j][lane] = acc[j];
   __syncthreads();
-  const float f = which ? scale_of(a.one, a.each, ad) : 1.f;
+  // without rows the gradient is zero, whatever the slot's scale
+  const float f = which && first < last ? scale_of(a.one, a.each, ad) : 1.f;
   float* out = a.out[which] + (int64_t)ad * r * K;
   for (int i = threadIdx.x; i < 512; i += 256) {
     // neighbouring threads write neighbouring elements: columns of dA, j of dB

@@ -434,3 +434,43 @@ def test_products_that_overflow(M, sign, e):
         assert dA[1, 3, 5] == sign * float("inf")
         dA[1, 3, 5] = 0
         assert not dA.any() and not dB.any() and not dX.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,r", [(40, 16), (300, 24), (1600, 72)])
+def test_adapters_without_rows_have_zero_gradients(M, r, dtype):
+    """Whatever their slots hold: scales, factors.  The others' bits are as with numbers there."""
+    c = C.inputs(M, 136, 264, r, 5, "rows", dtype)
+    c["ids"] = np.asarray([0, 2, -1, 4, 2])[np.arange(M) % 5]        # 1 and 3 have none
+    g = cuda(c)
+    Y0, Z0 = fwd(g)
+    first = bwd(g, Z0)
+    for k in ("A", "B", "s"):
+        g[k][1], g[k][3] = float("nan"), float("inf")
+    Y, Z = fwd(g)
+    assert torch.equal(Y, Y0) and torch.equal(Z, Z0)
+    for a, b in zip(first, bwd(g, Z)):
+        assert torch.equal(a, b)
+    for t in first[1:3]:
+        assert not t[1].any() and not t[3].any() and t[[0, 2, 4]].any(-1).any(-1).all()
+
+
+@pytest.mark.parametrize("M,r", [(40, 13), (300, 16), (600, 72)])
+def test_what_is_not_finite_stays_with_its_adapter_in_fp32(M, r):
+    c = C.inputs(M, 136, 264, r, 4, "rows", "f32")
+    g = cuda(c)
+    plan = ops.adapter_plan(g["ids"], 4)
+    Y0, Z0 = fwd(g, plan)
+    d0 = bwd(g, Z0, plan)
+    g2 = {k: v.clone() if torch.is_tensor(v) else v for k, v in g.items()}
+    g2["A"][1, :, ::3], g2["B"][1, ::2], g2["s"][1] = float("nan"), float("inf"), float("nan")
+    sick = int(np.flatnonzero(c["ids"] == 2)[1])
+    g2["X"][sick], g2["dY"][sick] = float("inf"), float("nan")
+    Y, Z = fwd(g2, plan)
+    fine = torch.from_numpy(c["ids"] != 1).cuda()
+    fine[sick] = False
+    assert torch.equal(Y[fine], Y0[fine]) and torch.equal(Z[fine], Z0[fine])
+    dX, dA, dB, _ = bwd(g2, torch.where(fine[:, None], Z0, float("nan")), plan)
+    assert torch.equal(dX[fine], d0[0][fine])
+    for a in (0, 3):
+        assert torch.equal(dA[a], d0[1][a]) and torch.equal(dB[a], d0[2][a])
