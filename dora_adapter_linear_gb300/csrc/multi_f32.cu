@@ -1,7 +1,7 @@
 // The many-adapter projection in fp32: FMA tiles, no reduced-precision tensor math, as everywhere here for fp32.
 //
-// Sums over long axes are taken in shares (of groups of warps, and of the CTAs of a cluster) that are added up
-// afterwards: their rounding grows with the share and not with the whole length.
+// Sums over long axes are taken in shares that are added up afterwards, so that their rounding grows with the share:
+// those over rows in shares of a fixed length, the product's over K in one for each group of warps and CTA of a cluster.
 #include "common.cuh"
 #include "multi.h"
 #include "vec.cuh"
@@ -342,9 +342,13 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
 
 // ------------------------------------------------------------------ gradients of the adapters
 // out_a(j, k) = f_a sum over its rows T[i][j] S[i][k]: a CTA has 32 columns and 16 of the j of one adapter, its
-// eight warps every eighth row, four at a time, asked for a round ahead; their T passes through shared memory.  Both
-// stacks in one launch; zeros for an adapter without rows.  Latency: 10.5 us for 300 rows of three adapters, 512 and
-// 1376 columns, 16 us for 1000 of four, 2048 and 2048 (47 with T by uniform loads and nothing ahead).
+// eight warps every eighth row, four at a time, asked for a round ahead; their T passes through shared memory.  Every
+// 1024 rows a thread adds its sums, of 128 rows then, to those before.  Both stacks in one launch; zeros for an adapter
+// without rows.  Latency: 10.5 us for 300 rows of three adapters, 512 and 1376 columns, 16 us for 1000 of four, 2048 and
+// 2048 (47 with T by uniform loads and nothing ahead).  The rows of one adapter are not shared by CTAs: few and long
+// batches are slow (with the pass for g: 8192 rows of one adapter, 4096 and 4096 columns, rank 64: 960 us; of four, 1024
+// and 1024, rank 16: 94).
+constexpr int kShareRows = 1024;
 struct F32Reduce {
   MultiPlan p;
   int r;
@@ -384,27 +388,36 @@ __global__ void __launch_bounds__(256) f32_reduce_kernel(const __grid_constant__
   rows(first);
   load();
   rows(first + 32);
-  for (int i0 = first, flip = 0; i0 < last; i0 += 32, flip ^= 1) {
-    *reinterpret_cast<float2*>(&ts[flip][tr][tj]) = make_float2(t[0], t[1]);
-    float now[4];
+  int i0 = first, flip = 0;
+  do {
+    const int end = min(last, i0 + kShareRows);
+    const bool more = i0 > first;
+#pragma unroll 2
+    for (; i0 < end; i0 += 32, flip ^= 1) {
+      *reinterpret_cast<float2*>(&ts[flip][tr][tj]) = make_float2(t[0], t[1]);
+      float now[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) now[q] = x[q];
-    __syncthreads();          // T is there, and all are done with the half that is written next
-    load();
-    rows(i0 + 64);
+      for (int q = 0; q < 4; ++q) now[q] = x[q];
+      __syncthreads();          // T is there, and all are done with the half that is written next
+      load();
+      rows(i0 + 64);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 u = *reinterpret_cast<const float4*>(&ts[flip][warp + 8 * q][j]);
-        acc[j] = fmaf(u.x, now[q], acc[j]);
-        acc[j + 1] = fmaf(u.y, now[q], acc[j + 1]);
-        acc[j + 2] = fmaf(u.z, now[q], acc[j + 2]);
-        acc[j + 3] = fmaf(u.w, now[q], acc[j + 3]);
-      }
-  }
+        for (int j = 0; j < 16; j += 4) {
+          const float4 u = *reinterpret_cast<const float4*>(&ts[flip][warp + 8 * q][j]);
+          acc[j] = fmaf(u.x, now[q], acc[j]);
+          acc[j + 1] = fmaf(u.y, now[q], acc[j + 1]);
+          acc[j + 2] = fmaf(u.z, now[q], acc[j + 2]);
+          acc[j + 3] = fmaf(u.w, now[q], acc[j + 3]);
+        }
+    }
 #pragma unroll
-  for (int j = 0; j < 16; ++j) red[warp][j][lane] = acc[j];
+    for (int j = 0; j < 16; ++j) {                     // a thread meets its own places alone
+      red[warp][j][lane] = more ? red[warp][j][lane] + acc[j] : acc[j];
+      acc[j] = 0.f;
+    }
+  } while (i0 < last);
   __syncthreads();
   // without rows the gradient is zero, whatever the slot's scale
   const float f = which && first < last ? scale_of(a.one, a.each, ad) : 1.f;

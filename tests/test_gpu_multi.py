@@ -474,3 +474,22 @@ def test_what_is_not_finite_stays_with_its_adapter_in_fp32(M, r):
     assert torch.equal(dX[fine], d0[0][fine])
     for a in (0, 3):
         assert torch.equal(dA[a], d0[1][a]) and torch.equal(dB[a], d0[2][a])
+
+
+@pytest.mark.parametrize("rows", [1000, 65536 + 37])
+def test_fp32_gradients_of_many_rows(rows):
+    """One adapter's rows are summed in shares: a sum whose every step would round down by almost half a step
+    is off by the roundings of a share and of the shares' sum, not by one for each row.  Steps of a thread: 128 in
+    a share, one for each 1024 rows; then 7 for the warps and one for the scale."""
+    n, d, low = 3, 8, 1 + 0.98 * 2.0 ** -12
+    v = float(np.float32(low))
+    g = {"X": torch.full((rows, d), v), "W0": torch.zeros(d, d), "A": torch.zeros(n, 2, d), "B": torch.zeros(n, d, 2),
+         "s": torch.ones(n), "dY": torch.ones(rows, d), "ids": torch.ones(rows, dtype=torch.int64)}
+    g["B"][1, 0, 0] = g["B"][1, 3, 1] = 1                # g of both is one
+    g = {k: t.cuda() for k, t in g.items()}
+    Z = torch.full((rows, 2), v, device="cuda")
+    dX, dA, dB, db = bwd(g, Z)
+    off = (128 + rows // 1024 + 1 + 8) * 2.0 ** -24 * rows * v
+    assert abs(C.f64(dA[1]) - rows * v).max() <= off
+    assert abs(C.f64(dB[1]) - rows * v).max() <= off
+    assert not dA[[0, 2]].any() and not dB[[0, 2]].any() and (db == rows).all()
