@@ -151,8 +151,10 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
   bf16* G = static_cast<bf16*>(w.P);
   cudaError_t e;
   if (!Z) {
+    // as the forward has it where that takes the GEMM; multi_few sums in another order, and its z may be rounded the
+    // other way
     if ((e = multi_proj(p, sh.d_in, r, X, A, false, s.one, s.each, (bf16*)w.Z, nullptr, nullptr, fills(sh.M, sh.d_out),
-                        st)) != cudaSuccess)      // as the forward has it
+                        st)) != cudaSuccess)
       return e;
     Z = static_cast<const bf16*>(w.Z);
   }

@@ -702,7 +702,8 @@ def lora_multi_fwd(X, W0, A, B, s, plan, bias=None, save_z=True):
 
 def lora_multi_bwd(X, W0, A, B, Z, dY, s, plan, need_dx=True, need_dbias=False):
     """Gradients of lora_multi_fwd with W0 frozen: (dX, dA, dB, dbias), dA and dB stacks like A and B, zeros
-    for an adapter without rows.  Z: from the forward, or None to recompute it."""
+    for an adapter without rows.  Z: from the forward, or None to recompute it (bf16 with up to 256 rows: an
+    element may then be the forward's neighbour, its fp32 sum being formed in another order)."""
     ws = _multi_workspace(True, X, W0, A, plan)
     if ws is not None:
         done = L.host().multi_bwd(X, W0, A, B, Z, dY, s, plan.buffer, plan.rows, plan.adapters, need_dx, need_dbias, ws)

@@ -637,7 +637,8 @@ lora_status lora_multi_fwd(const lora_multi_shape* sh, const void* X, const void
                            const void* bias, float s, const float* s_each, const void* plan, void* Y, void* Z_save,
                            void* ws, size_t ws_bytes, void* stream);
 
-/* Z_saved [M, r] from the forward, or NULL to recompute it; dX [M, d_in] or NULL; dA, dB as A, B;
+/* Z_saved [M, r] from the forward, or NULL to recompute it (LORA_BF16 with up to 256 rows: an element may then be
+ * the forward's neighbour, its fp32 sum being formed in another order); dX [M, d_in] or NULL; dA, dB as A, B;
  * dbias [d_out] or NULL.  The sums over rows are fp32 in a fixed order. */
 lora_status lora_multi_bwd(const lora_multi_shape* sh, const void* X, const void* W0, const void* A, const void* B,
                            const void* Z_saved, const void* dY, float s, const float* s_each, const void* plan, void* dX,
