@@ -511,3 +511,41 @@ def test_recomputed_z_of_a_few_rows(M):
     ref["dB"] = (ref["dB"][0], ref["dB"][1] + more * (1 + 2 * C.half_step("bf16")))
     for k, v in zip(("dX", "dA", "dB", "dbias"), bwd(g, None)):
         C.near(v, ref[k], k)
+
+
+@pytest.mark.parametrize("one_stream", [False, True])
+def test_every_thread_comes_to_its_end(one_stream):
+    """As test_threads; what a thread raises counts, and each has to finish its rounds."""
+    cases = [cuda(C.inputs(M, d, d + 16, r, 5, "rows", dtype, seed=M)) for M, d, r, dtype in
+             ((3, 520, 16, "bf16"), (90, 136, 24, "f32"), (400, 264, 72, "bf16"), (2570, 1800, 32, "bf16"))]
+    plans = [ops.adapter_plan(g["ids"], 5) for g in cases]
+
+    def step(i):
+        Y, Z = fwd(cases[i], plans[i])
+        grads = bwd(cases[i], Z, plans[i])
+        return (Y, Z, optim.clip_grads([grads[1], grads[2]], 1.0, groups=5)) + grads
+
+    want = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+    said = [None] * 4
+
+    def run(i):
+        try:
+            stream = torch.cuda.default_stream() if one_stream else torch.cuda.Stream()
+            rounds = 0
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    got = step(i)
+                    stream.synchronize()
+                    rounds += all(torch.equal(a, b) for a, b in zip(got, want[i]))
+            said[i] = rounds
+        except BaseException as e:  # noqa: BLE001
+            said[i] = e
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert said == [20] * 4
+    ops.check_device_errors()
