@@ -142,7 +142,7 @@ def clip_grads(grads, max_norm, groups=None):
     norms before that, fp32 [groups] on the device; nothing waits.  grads: contiguous fp32 or bf16 CUDA
     tensors (or None); groups: None, one group of all; a list with the number of each tensor's group, 0 to
     the largest; or a number G: every tensor is a stack of G groups along its first dimension, as the
-    gradients of ops.lora_multi_bwd are.  A group whose norm is not finite (from about 2^63 on) becomes
+    gradients of ops.lora_multi_bwd are.  A group whose norm is not finite (from 2^64 on) becomes
     zeros, the others go on.  max_norm None: the norms alone; infinity: only such groups change."""
     grads = grads if isinstance(grads, (list, tuple)) else list(grads)
     each = None

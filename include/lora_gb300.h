@@ -649,10 +649,10 @@ lora_status lora_multi_bwd(const lora_multi_shape* sh, const void* X, const void
  * elements of group k: one group for each adapter of a set that is trained together, so that one adapter's
  * spike does not scale the others.  A group whose norm is not finite becomes zeros (its norm shows it, the
  * others go on).  max_norm <= 0: the norms alone; infinity: only such groups change.
- * Squares are summed in fp32 in a fixed order, long runs of their sums in fp64: a norm from about 2^63 on counts as
- * not finite, values below about 2^-75 add nothing.
+ * Squares are summed in fp32 in a fixed order, long runs of their sums in fp64: a norm from 2^64 on counts as not
+ * finite; below a mean square of 2^-126 a norm loses its last bits, and values below 2^-75 add nothing.
  * `tensors` is a host array of `count` entries, read during the call; g: contiguous device array, aligned to
- * its element (16-byte aligned ones are faster), of one dtype.  stacked 0: n elements of group `group`.
+ * its element (16-byte aligned ones are faster); a group's tensors may differ in dtype.  stacked 0: n elements of group `group`.
  * stacked 1: a stack of all `groups` groups behind one another, n elements each (`group` is not read).  No two
  * tensors share memory (LORA_ERR_INVALID_ARG).  1 <= groups <= 65535; norms: device fp32 [groups]. */
 typedef struct {

@@ -173,3 +173,26 @@ def test_what_it_does_not_take_is_named():
         with pytest.raises(ValueError, match=what):
             optim.clip_grads(grads, 1.0, groups)
     assert (g == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_ends_of_a_norms_range(dtype):
+    """A norm below 2^64 counts as finite.  Values whose mean square is at least 2^-126 give a norm as exact as any:
+    a square below 2^-126 is off by half of 2^-149, which is 2^-24 of that mean.  A factor below 2^-126 is off by half
+    of 2^-149 itself, and so an element by its own size times 2^-150."""
+    off = 48 * 2.0 ** -24
+    for g in ([torch.full((16,), 1.3 * 2.0 ** 61).to(dtype)],                    # 1.3 * 2^63
+              [torch.full((3 * 16384,), 1.01 * 2.0 ** 56).to(dtype)],            # sums of several units: 1.75 * 2^63
+              [torch.full((64,), 1.3 * 2.0 ** -63).to(dtype)],
+              [normal(5000, dtype=dtype, scale=1.5 * 2.0 ** -63)],
+              [torch.cat((torch.full((999,), 1.7 * 2.0 ** -72), torch.full((1,), 1.9 * 2.0 ** -58))).to(dtype)]):
+        for max_norm in (None, 2.0 ** -70, 1.0):
+            x = [t.cuda() for t in g]
+            norms = f64(optim.clip_grads(x, max_norm))
+            want, clipped = O.clip([f64(t) for t in g], max_norm, [0], 1)
+            assert abs(norms[0] - want[0]) <= off * want[0]
+            h = torch.finfo(dtype).eps / 2 + off + 8 * 2.0 ** -24
+            most = abs(clipped[0]) * h + abs(f64(g[0])) * 2.0 ** -150 * (1 + h) + 2.0 ** (-150 if dtype == torch.float32 else -134)
+            assert (abs(f64(x[0]) - clipped[0]) <= (0 if max_norm is None else most)).all()
+    g = [torch.full((16,), 1.01 * 2.0 ** 62, device="cuda").to(dtype)]           # 1.01 * 2^64
+    assert optim.clip_grads(g, 1.0).isinf().all() and not g[0].any()
