@@ -9,7 +9,8 @@ from . import _lib as L
 class AdapterPlan:
     """Rows by adapter and adapters by tile of one batch, on the device.  `update` refills it in place for
     a batch of as many rows, as a captured graph needs it; calls that read the plan run behind it on the
-    same stream."""
+    same stream.  One whose only updates were captured holds its ids from the graph's first replay on: calls
+    outside of the graph wait for that."""
 
     def __init__(self, rows, adapters, device):
         need = L.lora_multi_plan_bytes(rows, adapters)

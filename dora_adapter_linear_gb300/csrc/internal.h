@@ -129,13 +129,13 @@ struct TcGemmDesc {
   bf16* dn_z = nullptr;
   int act = 0;                 // gated MLP activation: 0 SwiGLU, 1 GeGLU
   // many adapters (TC_FWD, TC_BWD_DX; has_tail, K1 the rank): B1 is a stack of ad_total matrices, and the tail of a
-  bool ad_wait = false;            // its operands come from the kernel before it, too
   // 256-row tile takes those of ad_list [tiles, 256] (ad_count [tiles] of them), each for the rows whose bit in
   // ad_mask [tiles, 256, 8] is 0
   const int32_t* ad_count = nullptr;
   const int32_t* ad_list = nullptr;
   const uint32_t* ad_mask = nullptr;
   int ad_total = 0;
+  bool ad_wait = false;        // the main operands come from the kernel before this one, too
 };
 cudaError_t tc_gemm(const TcGemmDesc& d, cudaStream_t st);
 

@@ -34,6 +34,7 @@ struct MultiWs {
 // 54.6, 8192 x 4104 x 4104 291, 240, 1999 x 2568 -> 1000 35.2, 32.2, but 1999 x 1000 -> 2568 27.6, 29.2, 600 x 2568 x 2568
 // 28.4, 30.5; backward, dY alone, 3001 x 2568 x 2568 71.2, 68.8, 1000 x 4104 x 4104 59.8, 53.2, 600 x 2568 x 2568 33.1,
 // 35.2 (W0 [K, N] as well: 74.3, 60.3, 36.3).  So: with some steps for a pair of multiprocessors, of 1000 rows or so.
+// 76 pairs are written down here: a workspace is sized on hosts without a device as well.
 bool pads(const lora_multi_shape& sh, bool bwd) {
   const int64_t mt = (sh.M + 255) / 256, tiles = mt * (((bwd ? sh.d_in : sh.d_out) + 255) / 256),
                 steps = ((bwd ? sh.d_out : sh.d_in) + 63) / 64;
@@ -159,8 +160,11 @@ cudaError_t backward(const lora_multi_shape& sh, const MultiPlan& p, const Multi
     Z = static_cast<const bf16*>(w.Z);
   }
   const bool beside = dX && fills(sh.M, sh.d_in);
-  // s g enters dX rounded, like s z the output; as a factor of dA it comes with the rest of its rounding, which would
-  // otherwise add as much to dA's error as dA's own rounding
+  // s g enters dX rounded, like s z the output: a half step of the update, as the one-adapter layer has it (the
+  // output's error beside its own rounding: 4% more at rank 16, where the update is 28% of the output, 12% at rank
+  // 64, where it is half); a second part would double the tail's MMAs, 0.2 us for each adapter of a tile and 16 of
+  // the rank.  As a factor of dA it comes with the rest of its rounding, which would otherwise add as much to dA's
+  // error as dA's own rounding
   bf16* rest = static_cast<bf16*>(w.P2);
   if ((e = multi_proj(p, sh.d_out, r, dY, B, true, s.one, s.each, nullptr, G, rest, beside, st)) != cudaSuccess) return e;
   if (dX) {

@@ -6,7 +6,9 @@
 namespace lg {
 
 constexpr int kItemRows = 64;     // rows of an item: consecutive rows of one adapter in the plan's order
-constexpr int kPieceRows = 512;   // rows of a piece, the share of one adapter's gradients that is summed at once
+// rows of a piece, the share of one adapter's gradients that is summed at once; the partial sums of adapters with several
+// are up to M / 256 of [r, d_in + d_out] in fp32 in the backward's workspace
+constexpr int kPieceRows = 512;
 constexpr int kTileRows = 256;    // rows of a tile, whose adapters and row masks the GEMMs take
 
 enum { kHeadItems = 0, kHeadPieces = 1, kHeadRows = 2, kHeadWords = 64 };
@@ -63,11 +65,12 @@ cudaError_t multi_plan(const MultiPlan& p, const void* ids, int id_bits, cudaStr
 cudaError_t multi_proj(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* U, bool kr, float one,
                        const float* each, bf16* plain, bf16* scaled, bf16* rest, bool all, cudaStream_t st);
 // out_a(j, k) = sum over its rows S[i][k] T[i][j] (scaled: times s_a), out_a [r, K], or kr: [K, r]; T + T2 where T2 is
-// given; adapters with
-// several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows to zero
+// given; adapters with several pieces leave part [multi_partials, ...] for multi_sum, which also sets those without rows
+// to zero
 // early: see PdlEarly; beside: with little shared memory, to run on the multiprocessors of a large product
-cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr, bool scaled,
-                         float one, const float* each, float* part, bf16* out, bool early, bool beside, cudaStream_t st);
+cudaError_t multi_reduce(const MultiPlan& p, int64_t K, int r, const bf16* S, const bf16* T, const bf16* T2, bool kr,
+                         bool scaled, float one, const float* each, float* part, bf16* out, bool early, bool beside,
+                         cudaStream_t st);
 // copies of matrices [rows, K] in rows of multi_pad_ld(K) elements, `to` null: none; beside the kernel before it
 struct MultiPad {
   const bf16* from;

@@ -127,9 +127,10 @@ __global__ void __launch_bounds__(256) f32_proj_kernel(const __grid_constant__ F
 // What counts is warps: with two a scheduler it issues every second cycle (8 x 16 a thread: 60 us at 509 x 1000 x
 // 1496, the FMA units 38% busy), so 128 registers and four CTAs an SM: 55 us, 28 TFLOP/s.  Two products an
 // instruction (fma.rn.f32x2) do not help: a 16-byte read of shared memory takes four cycles of an SM, 16 of these
-// feed 256 FMA, and the pairs of k they come in would need twice the accumulators (4 x 8 a thread: 5 us more).  The CTAs of a cluster share K and add their
-// sums through distributed shared memory, each finishing its share of the rows.  There a thread has one column, and
-// takes its adapter's factor anew only where the next row has another one.
+// feed 256 FMA, and the pairs of k they come in would need twice the accumulators (4 x 8 a thread: 5 us more).  The CTAs
+// of a cluster share K and add their sums through distributed shared memory, each finishing its share of the rows.
+// There a thread has one column, and takes its adapter's factor anew only where the next row has another one.  A tile
+// computes 64 rows whatever the batch has: one row of 4096 x 4096 takes 80 us, 64 take 92.
 constexpr int kTileM = 64, kTileN = 64, kSlab = 16, kGroups = 2, kGemmThreads = 64 * kGroups, kSlabs = 4;
 constexpr int kRowPitch = kSlab + 4, kColPitch = kTileN + 4;          // floats
 constexpr int kSlabA = kTileM * kRowPitch, kSlabB = kTileN * kRowPitch;
@@ -148,9 +149,10 @@ struct F32Gemm {
   float* out;
   // The rank-r pass before this kernel gives P alone, and what came before that pass is complete when this kernel
   // starts: its sums may begin beside that pass.  Half way they wait for it, so that the kernels behind this one start
-  // beside the rest (a quarter earlier or later: the same).  With one or two CTAs an SM (backward of 300 x 512 -> 1376
-  // 39.7 -> 37.3 us); more are spread
-  // unevenly around that pass's (509 x 1000 -> 1496 58 -> 67).
+  // beside the rest (a quarter earlier or later: the same).  With one or two CTAs an SM (us without and with: backward of
+  // 300 x 512 -> 1376 41.7, 40.1; 16 x 1024 -> 1024 20.0, 16.4, backward 22.8, 19.1); more are spread unevenly around that
+  // pass's: 509 x 1000 -> 1496 60.4, 63.5, elsewhere up to a tenth is left (1 x 4096 -> 4096 80.1, 72.7; 200 x 1000 ->
+  // 1000 33.9, 31.4; 1000 x 2048 -> 2048 261.7, 252.1; 1024 x 4096 -> 4096 834, 822).
   bool ahead;
 };
 
@@ -476,11 +478,16 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 
 template <bool MN>
 cudaError_t gemm(F32Gemm a, cudaStream_t st) {
-  const int64_t tiles = (int64_t)blocks(a.N, kTileN) * blocks(a.p.M, kTileM), slabs = blocks(a.K, kSlab), sms = num_sms_current();
+  const int64_t tiles = (int64_t)blocks(a.N, kTileN) * blocks(a.p.M, kTileM), slabs = blocks(a.K, kSlab),
+                sms = num_sms_current();
   const cudaError_t allowed = allow_smem<f32_gemm_kernel<MN>>(kGemmSmem);
   if (allowed != cudaSuccess) return allowed;
-  // the share of K that finishes soonest: what the fullest SM has, by how busy so many CTAs keep it, and what a cluster
-  // costs
+  // the share of K that finishes soonest: what the fullest SM has, by how busy so many CTAs keep it (1 CTA 0.3 of
+  // four's rate, 2 0.55, 3 0.75), and what a cluster costs.  Measured, us with 1 to 8 shares and what this takes: 300
+  // x 512 -> 1376 74 41 36 29 28 39 38 36: 4; 509 x 1000 -> 1496 140 81 62 75 73 76 79 76: 3; 256 x 4096 -> 1024 362
+  // 239 166 125 114 99 88 87: 7; 1000 x 2048 -> 2048 264 234 263 249 263 261 275 265: 5; 700 x 768 -> 3000 109 100
+  // 115 112 123 124 134 132: 2; 1 x 4096 -> 4096 163 86 96 80 84 74 80 72: 7.  Backward, furthest from the best: 509
+  // x 1000 -> 1496 140 107 85 66 87 84 82 77: 7.
   int ranks = 1;
   double best = 0;
   for (int s = 1; s <= 8; ++s) {
@@ -524,7 +531,8 @@ cudaError_t multi_f32_proj(const MultiPlan& p, int64_t K, int r, const float* S,
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1 + pdl_attr(&attr[1]);
-  const cudaError_t e = kr ? cudaLaunchKernelEx(&cfg, f32_proj_kernel<true>, a) : cudaLaunchKernelEx(&cfg, f32_proj_kernel<false>, a);
+  const cudaError_t e = kr ? cudaLaunchKernelEx(&cfg, f32_proj_kernel<true>, a)
+                           : cudaLaunchKernelEx(&cfg, f32_proj_kernel<false>, a);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
 }

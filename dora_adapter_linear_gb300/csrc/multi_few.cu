@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(128) multi_few_down(const __grid_constant__ Fe
 #pragma unroll
       for (uint32_t q = 0; q < 8; ++q) {
         p[q] = 0.f;
-        if (q < ranks) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[q]) : "r"(mapa_shared(smem_u32(sum + j), q)));
+        if (q < ranks)
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[q]) : "r"(mapa_shared(smem_u32(sum + j), q)));
       }
 #pragma unroll
       for (int q = 0; q < 8; ++q) z += p[q];
@@ -161,7 +162,8 @@ __host__ __device__ constexpr int few_ring(int stages) {
 }
 template <int T>
 __host__ __device__ constexpr int few_smem(int stages, int ranks, int r, bool own) {
-  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + (own ? 2 : 1) * T * r * 4 + T * 12 + 16 + kRowsW * 4 + 8 * (2 * stages + 2) + 32;
+  return 1024 + few_ring<T>(stages) + T * (kRowsW / ranks) * 4 + (own ? 2 : 1) * T * r * 4 + T * 12 + 16 + kRowsW * 4 +
+         8 * (2 * stages + 2) + 32;
 }
 
 // zp[t][j] = sum over K-steps k0 .. k1 - 1 of x[t] A_a[j]: a warp takes every eighth group of four j of a row
@@ -184,7 +186,8 @@ __device__ __forceinline__ void own_z(const FewArgs& a, const int* ids, int rows
           const bool on = k + 256 * h < end;
           xr[h].v = on ? __ldg(reinterpret_cast<const uint4*>(x + k + 256 * h)) : none;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) ur[h][j].v = on ? __ldg(reinterpret_cast<const uint4*>(u + j * a.K + k + 256 * h)) : none;
+          for (int j = 0; j < 4; ++j)
+            ur[h][j].v = on ? __ldg(reinterpret_cast<const uint4*>(u + j * a.K + k + 256 * h)) : none;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 2) multi_few(const __grid_constant__
   const int own = kRowsW / (int)ranks;                              // output columns that this CTA finishes
   float* update = reinterpret_cast<float*>(smem + few_ring<T>(a.stages));   // [T, own]
   uint32_t* szh = reinterpret_cast<uint32_t*>(update + T * own);    // [T, r / 2] s z, pairs
-  uint32_t* szl = szh + T * a.r / 2;                                // what their rounding left; OWN: then [T, r] z of this CTA's K
+  uint32_t* szl = szh + T * a.r / 2;    // what their rounding left; OWN: then [T, r] z of this CTA's K
   int* ids = reinterpret_cast<int*>(szl + T * a.r / 2 + (OWN ? T * a.r : 0));   // [T]
   uint32_t* leaders = reinterpret_cast<uint32_t*>(ids + T);         // rows that begin a unit; two more words unused
   float* bias = reinterpret_cast<float*>(leaders + 4);              // [128] of this CTA's columns
@@ -546,9 +549,14 @@ cudaError_t down_launch(const FewArgs& a, int* beside, cudaStream_t st) {
 
 }  // namespace
 
-// Measured against the GEMM of 256-row tiles (K = 4096, us here and there): N 4096, 64 rows: 17.6, 29.6; 128: 20.4, 30.1;
-// 192: 29.4, 30.1; N 11008, 64: 30.5, 33.2; 128: 48.6, 34.2; 256 rows, N 1024: 23.8, 28.4; 2048: 24.7, 29.9; 512 rows, N
-// 1024: 31, 28.  Up to 128 rows while two CTAs share K, more only where four do.
+// Measured against the GEMM of 256-row tiles (K = 4096, us here and there): N 4096, 64 rows: 17.6, 29.6; 128: 20.4,
+// 30.1; 192: 29.4, 30.1; N 11008, 64: 30.5, 33.2; 128: 48.6, 34.2; 256 rows, N 1024: 23.8, 28.4; 2048: 24.7, 29.9;
+// 512 rows, N 1024: 31, 28.  Up to 128 rows while two CTAs share K, more only where four do: 256 rows up to N 2432,
+// 192 up to 3200, 128 up to 9728, 64 up to 19456.  These figures are of 16 adapters at rank 16.  What the rule does
+// not see is the GEMM's tail, 0.2 us for each adapter of a tile and 16 of the rank: behind its border a batch with an
+// adapter for every row is slow (4096 x 4096, rank 16: 128 rows 29 us, 129 rows 69, 256 rows 102, at rank 64 271;
+// with eight adapters 21, 29, 29, 34), and so is a single row of more than 19456 columns (28672: 83 us for 35 of
+// reads).
 bool multi_few_fits(int64_t M, int64_t N) {
   const int64_t groups = (M + 63) / 64, ctas = (N + kRowsW - 1) / kRowsW * groups;
   return M <= kFewRows && ctas * (groups <= 2 ? 2 : 4) <= 2 * num_sms_current();

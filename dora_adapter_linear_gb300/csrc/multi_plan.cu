@@ -4,8 +4,10 @@
 // One launch.  Block 0 sorts: a counting sort by 8 bits of the adapter's number a pass (one pass up to
 // 255 adapters), stable, so that every sum over an adapter's rows has one fixed order.  Each warp counts
 // and places a run of consecutive rows; rows of equal digit within 32 find their order by a warp match.
-// The other blocks take four tiles each.  Latency bound: a few microseconds, once for all projections
-// of a batch.
+// The other blocks take four tiles each.  Once for all projections of a batch, bound by latency: 6 us for a row of eight
+// adapters, 15 for 8192 rows of eight, 34 of 256 in any order (two passes).  One block sorts and lists whatever the sizes
+// are: 106 us for 65536 rows of eight adapters, 1.6 ms for 2^20, 41 ms for 2^24 (104 of 65535 adapters); and one thread
+// writes where the adapters between two neighbouring numbers begin: 211 us for a row of one of 65535.
 #include "common.cuh"
 #include "multi.h"
 

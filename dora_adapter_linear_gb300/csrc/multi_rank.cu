@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(256) multi_proj_mma(const __grid_constant__ Pr
   const int items = a.p.head[kHeadItems], with = a.p.head[kHeadRows];
   if (a.plain) {              // rows without adapter: zeros
     for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < (a.p.M - with) * NT; i += (int64_t)gridDim.x * 256)
-      *reinterpret_cast<uint4*>(a.plain + (int64_t)a.p.order[with + i / NT] * a.r + a.j0 + i % NT * 8) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(a.plain + (int64_t)a.p.order[with + i / NT] * a.r + a.j0 + i % NT * 8) =
+          make_uint4(0, 0, 0, 0);
   }
   if (mine >= items) return;  // the whole cluster
   const int64_t K = a.K;
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(256) multi_proj_mma(const __grid_constant__ Pr
     cluster_sync_all();
   }
   const float s = a.each ? __ldg(a.each + item.x) : a.one;
-  const int pairs = item.z * R / 2, p0 = (int)((int64_t)pairs * rank / ranks), p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
+  const int pairs = item.z * R / 2, p0 = (int)((int64_t)pairs * rank / ranks),
+            p1 = (int)((int64_t)pairs * (rank + 1) / ranks);
   for (int i = p0 + tid; i < p1; i += 256) {
     float2 q[8];
     if (ranks > 1) {
@@ -275,7 +277,8 @@ __global__ void __launch_bounds__(128) multi_reduce_mma(const __grid_constant__ 
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         ldsm_x4_t(x[m][0], x[m][1], x[m][2], x[m][3],
-                  S + (kk * 16 + (lane & 7) + ((lane >> 4) << 3)) * C::SP + (warp * 32 + m * 16 + ((lane >> 3) & 1) * 8) * 2);
+                  S + (kk * 16 + (lane & 7) + ((lane >> 4) << 3)) * C::SP +
+                      (warp * 32 + m * 16 + ((lane >> 3) & 1) * 8) * 2);
 #pragma unroll
       for (int w = 0; w < C::PARTS; ++w) {
         if (w == 1)
@@ -428,10 +431,15 @@ __global__ void __launch_bounds__(256) multi_pad_kernel(const __grid_constant__ 
     }
 }
 
-// as many CTAs to a cluster as two an SM have room for (about half of the adapters end in a part of an item).  Before a
-// product that needs all multiprocessors a CTA has four stages at least (3001 x 2568: 61.2 us, with six 62.9), before a
-// smaller one six: that one begins on multiprocessors that have none of these CTAs (1999 x 2568, 32 tiles: 37.7 us,
-// with four 41.7)
+// as many CTAs to a cluster as two an SM have room for (about half of the adapters end in a part of an item).  Before
+// a product that needs all multiprocessors a CTA has four stages at least, before a smaller one six: that one begins
+// on multiprocessors that have none of these CTAs.  Whole calls with four and with six, us (adapters' rows behind one
+// another):
+//   smaller: 600 x 4096 -> 4096 33.0, 28.7, backward 40.4, 39.3; 1000 rows 33.2, 33.6, 42.4, 41.6; 1999 x 2568 -> 1000
+//     28.9, 30.0; backward of 1999 x 1000 -> 2568 34.8, 36.7 (another batch 41.7, 37.7)
+//   all: 2048 x 4096 -> 4096 55.8, 56.4, backward 65.1, 64.8; 3001 x 2568 -> 2568 57.0, 54.6, 70.0, 68.1 (another batch
+//     61.2, 62.9); 4000 x 2048 -> 4096 59.9, 54.2, 68.8, 68.9; 3001 x 4096 and 1500 x 11008 -> 4096 the same
+// It is a matter of a tenth either way, and of the batch.
 template <int R, bool KR>
 int proj_ranks(const MultiPlan& p, int64_t K, bool all) {
   const int64_t steps = (K + 127) / 128, slots = 2 * num_sms_current(), items = p.M / kItemRows + (p.n + 1) / 2;
@@ -466,7 +474,8 @@ cudaError_t reduce_launch(ReduceArgs a, int64_t pieces, cudaStream_t st) {
   const cudaError_t e = allow_smem<multi_reduce_mma<R, TWO>>(C::smem(C::NST));
   if (e != cudaSuccess) return e;
   if (a.stages == 0) a.stages = C::NST;
-  return launch_pdl(multi_reduce_mma<R, TWO>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::smem(a.stages), st, a);
+  return launch_pdl(multi_reduce_mma<R, TWO>, dim3((unsigned)((a.K + 127) / 128 * pieces)), dim3(128), C::smem(a.stages),
+                    st, a);
 }
 
 }  // namespace
@@ -515,7 +524,8 @@ cudaError_t multi_sum(const MultiPlan& p, int64_t size0, const float* part0, bf1
 }
 
 cudaError_t multi_pad(const MultiPad& S, const MultiPad& W, cudaStream_t st) {
-  const PadArgs a{{S.from, W.from}, {S.to, W.to}, {S.to ? S.rows : 0, W.to ? W.rows : 0}, {S.K, W.K}, {multi_pad_ld(S.K), multi_pad_ld(W.K)}};
+  const PadArgs a{{S.from, W.from}, {S.to, W.to}, {S.to ? S.rows : 0, W.to ? W.rows : 0}, {S.K, W.K},
+                  {multi_pad_ld(S.K), multi_pad_ld(W.K)}};
   return launch_pdl(multi_pad_kernel, dim3((unsigned)(2 * num_sms_current())), dim3(256), 0, st, a);
 }
 

@@ -909,16 +909,16 @@ __global__ void __launch_bounds__(OneCta<EPI, KSCALE, ZF>::THREADS, 1) tc_gemm_k
 //   acc_full[b]  both CTAs: the leader's MMA commit, multicast
 //   acc_empty[b] leader: 4 epilogue warps (8 for the plain scale/bias epilogue) x 2 CTAs
 //
-// Many adapters (MULTI): the tail of a tile takes every adapter among its rows in turn, each MMA with the
-// rows of the others switched off (disable-output-lane), so that a row meets its own adapter's operand
-// alone: a NaN in another one stays there, and Z needs no masked copies.  A K-step of the tail holds 64
-// columns of ranks in chunks of 16, those of four adapters up to rank 16, of two up to 32.  A K-major B1 chunk
-// (16 columns, 32 bytes a row) is a tile of its own with the 32-byte swizzle.  A masked MMA of 16 columns takes
-// about 0.21 us where another takes 0.084, whatever feeds it (masks asked for earlier, wider tiles of B1, halves of N:
-// no change): an adapter costs its tile 0.2 us for every 16 columns of rank.
-// 8192 x 4096 x 4096, rank 16: 162 us, 1.70 PFLOP/s; dX of 8192 x 11008 x 4096, rank 32: 438 us, 1.69.  Few tiles are
-// slower: 3001 x 2568 x 2568 takes 57 us, two rounds of 76 pairs, and rows of an odd multiple of 16 bytes slow its copies
-// (K 2576: 38 us without adapters, K 2568: 48; larger products get copies in longer rows).  Tiles of 128 columns were no faster (300 x 4096 x 4096: 34 us, 29).
+// Many adapters (MULTI): the tail of a tile takes every adapter among its rows in turn, each MMA with the rows of the
+// others switched off (disable-output-lane), so that a row meets its own adapter's operand alone: a NaN in another
+// one stays there, and Z needs no masked copies.  A K-step of the tail holds 64 columns of ranks in chunks of 16,
+// those of four adapters up to rank 16, of two up to 32.  A K-major B1 chunk (16 columns, 32 bytes a row) is a tile
+// of its own with the 32-byte swizzle.  A masked MMA of 16 columns takes about 0.21 us where another takes 0.084,
+// whatever feeds it (masks asked for earlier, wider tiles of B1, halves of N: no change): an adapter costs its tile
+// 0.2 us for every 16 columns of rank. 8192 x 4096 x 4096, rank 16: 162 us, 1.70 PFLOP/s; dX of 8192 x 11008 x 4096,
+// rank 32: 438 us, 1.69.  Few tiles are slower: 3001 x 2568 x 2568 takes 57 us, two rounds of 76 pairs, and rows of
+// an odd multiple of 16 bytes slow its copies (K 2576: 38 us without adapters, K 2568: 48; larger products get copies
+// in longer rows).  Tiles of 128 columns were no faster (300 x 4096 x 4096: 34 us, 29).
 struct MultiTail {
   int KB, P, chunks, count;     // K-blocks of 64 of the rank; adapters a step; chunks of the rank; adapters
   __device__ __forceinline__ MultiTail(int chunks_, int count_)

@@ -143,7 +143,8 @@ def clip_grads(grads, max_norm, groups=None):
     tensors (or None); groups: None, one group of all; a list with the number of each tensor's group, 0 to
     the largest; or a number G: every tensor is a stack of G groups along its first dimension, as the
     gradients of ops.lora_multi_bwd are.  A group whose norm is not finite (from 2^64 on) becomes
-    zeros, the others go on.  max_norm None: the norms alone; infinity: only such groups change."""
+    zeros, the others go on.  max_norm None: the norms alone; infinity: only such groups change.  A list without
+    any tensor is refused: it has no device."""
     grads = grads if isinstance(grads, (list, tuple)) else list(grads)
     each = None
     if groups is None:
