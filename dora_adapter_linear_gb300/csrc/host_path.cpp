@@ -12,6 +12,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <vector>
 
 #include "../../include/lora_gb300.h"
@@ -326,6 +327,7 @@ struct Multi {
         return false;
       }
       s = (float)v;
+      if (!std::isfinite(s)) return false;
     }
     sh = lora_multi_shape{M, in, out, r, n, dtype_of(x)};
     return true;

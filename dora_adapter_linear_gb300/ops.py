@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import math
 import threading
+from ctypes import c_float
 from functools import lru_cache
 
 import torch
@@ -648,7 +649,7 @@ def _multi_shape(X, W0, A, B, s, plan, bias=None, Z=None, dY=None):
         _check_like(name, t, shape, X)
     if isinstance(s, torch.Tensor):
         _check_vec("s", s, n, X, F32)
-    elif not math.isfinite(s):
+    elif not math.isfinite(c_float(s).value):           # as the kernels have it
         raise ValueError(f"s must be finite, got {s}")
     if plan.rows != M or plan.adapters != n:
         raise ValueError(f"the plan is of {plan.rows} rows and {plan.adapters} adapters, the call has {M} and {n}")

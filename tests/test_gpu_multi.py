@@ -549,3 +549,14 @@ def test_every_thread_comes_to_its_end(one_stream):
         t.join()
     assert said == [20] * 4
     ops.check_device_errors()
+
+
+@pytest.mark.parametrize("s", [float("nan"), float("inf"), -float("inf"), 1e39])
+def test_a_scale_that_is_not_finite_in_fp32_is_named(s):
+    """As it is without a GPU: a ValueError, before anything is launched."""
+    g = cuda(C.inputs(8, 64, 72, 8, 3, "rows", "bf16"))
+    plan, args = ops.adapter_plan(g["ids"], 3), (g["X"], g["W0"], g["A"], g["B"])
+    with pytest.raises(ValueError, match="s must be finite"):
+        ops.lora_multi_fwd(*args, s, plan)
+    with pytest.raises(ValueError, match="s must be finite"):
+        ops.lora_multi_bwd(*args, None, g["dY"], s, plan)

@@ -94,6 +94,12 @@ def test_cpu_tensors_are_refused():
         ops.lora_multi_bwd(**_ok(), Z=None, dY=_t(8, 16))
 
 
+@pytest.mark.parametrize("s", [1e39, -1e300, 2 ** 200])
+def test_a_scale_beyond_fp32_is_refused(s):
+    with pytest.raises(ValueError, match="s must be finite"):
+        ops.lora_multi_fwd(**dict(_ok(), s=s))
+
+
 @pytest.mark.parametrize("ids", [torch.zeros(4), torch.zeros(2, 2, dtype=torch.int64),
                                  torch.zeros(8, dtype=torch.int64)[::2], torch.zeros(4, dtype=torch.int16),
                                  torch.zeros(4, dtype=torch.int64)])
