@@ -346,10 +346,10 @@ __global__ void __launch_bounds__(kGemmThreads, 4) f32_gemm_kernel(const __grid_
 // out_a(j, k) = f_a sum over its rows T[i][j] S[i][k]: a CTA has 32 columns and 16 of the j of one adapter, its
 // eight warps every eighth row, four at a time, asked for a round ahead; their T passes through shared memory.  Every
 // 1024 rows a thread adds its sums, of 128 rows then, to those before.  Both stacks in one launch; zeros for an adapter
-// without rows.  Latency: 9.7 us for 300 rows of three adapters, 512 and 1376 columns, 15 us for 1000 of four, 2048 and
-// 2048 (47 with T by uniform loads and nothing ahead).  The rows of one adapter are not shared by CTAs: few and long
-// batches are slow (with the pass for g: 8192 rows of one adapter, 4096 and 4096 columns, rank 64: 960 us; of four, 1024
-// and 1024, rank 16: 94).
+// without rows.  Latency: 9.7 us for 300 rows of three adapters, 512 and 1376 columns; with the pass for g 28.6 us for
+// 1000 of four, 2048 and 2048 (T by uniform loads and nothing ahead: 31 more).  The rows of one adapter are not shared
+// by CTAs: few adapters with many rows are slow (with the pass for g: 8192 rows of one, 4096 and 4096 columns, rank 64:
+// 960 us; of four, 1024 and 1024, rank 16: 94).
 constexpr int kShareRows = 1024;
 struct F32Reduce {
   MultiPlan p;
