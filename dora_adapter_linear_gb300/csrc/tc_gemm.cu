@@ -1282,64 +1282,62 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
+// A tiled tensor map of up to three dimensions, elements next to one another, what lies outside reads as zero.  The
+// encoder wants a current context, which a thread has only after a call of the runtime that makes one current, such as
+// a launch: where it is a thread's first call, the current device's context is made current here.
+static bool encode(CUtensorMap* m, CUtensorMapDataType type, uint32_t rank, const void* base, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  auto enc = get_encode();
+  if (!enc || base == nullptr) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
+  auto call = [&] {
+    return enc(m, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult e = call();
+  int dev = 0;
+  if (e == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    e = call();
+  return e == CUDA_SUCCESS;
+}
+
 // 2-D bf16 tensor map, inner extent `inner` (contiguous), `outer` rows of `ld` elements,
 // box {64, box_rows}, 128-byte swizzle, out-of-bounds elements read as zero.
 static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
                      uint32_t box_rows) {
-  auto enc = get_encode();
-  if (!enc || base == nullptr) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // 3-D bf16 tensor map over a stack of contiguous [outer, inner] matrices, one chunk of 16 rank columns a box: 16
 // rows of 64 elements (128-byte swizzle) where the rank is the outer dimension, else 128 rows of 16 (32-byte
 // swizzle).  What lies outside of a matrix reads as zero, not as the next one.
-static bool make_stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stack, bool rank_outer) {
-  auto enc = get_encode();
-  if (!enc || base == nullptr) return false;
-  cuuint64_t dims[3] = {inner, outer, stack};
-  cuuint64_t strides[2] = {inner * 2, inner * outer * 2};
-  cuuint32_t box[3] = {rank_outer ? 64u : 16u, rank_outer ? 16u : 128u, 1u};
-  cuuint32_t es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, rank_outer ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+static bool make_stack_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t stack,
+                           bool rank_outer) {
+  const cuuint64_t dims[3] = {inner, outer, stack}, strides[2] = {inner * 2, inner * outer * 2};
+  const cuuint32_t box[3] = {rank_outer ? 64u : 16u, rank_outer ? 16u : 128u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                rank_outer ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B);
 }
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
                     uint32_t box_inner, uint32_t box_outer, int swizzle_bytes) {
-  auto enc = get_encode();
-  if (!enc || base == nullptr) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld * 2};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  const CUtensorMapSwizzle sw = swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                                      : CU_TENSOR_MAP_SWIZZLE_NONE;
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {ld * 2};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
+                swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                      : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
                   uint32_t box_outer) {
-  auto enc = get_encode();
-  if (!enc || base == nullptr || ld % 16 != 0) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t es[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (ld % 16 != 0) return false;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {ld};
+  const cuuint32_t box[2] = {box_inner, box_outer};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 int num_sms_current() {

@@ -67,3 +67,68 @@ def test_threads_on_one_stream(ops):
     for t in threads:
         t.join()
     assert not wrong
+
+
+def first_call(f, threads=2):
+    """What f raises as the first call of a new thread, in several threads one after another: later ones get an
+    earlier one's number and find its workspace, so that nothing but f comes before f."""
+    said = []
+
+    def run():
+        try:
+            f()
+        except Exception as e:  # noqa: BLE001
+            said.append(e)
+
+    for _ in range(threads):
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    return said
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+def test_many_adapters_as_a_threads_first_call(ops, M):
+    """A new thread has no CUDA context until a call makes one current."""
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    n = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(BF16)  # noqa: E731
+    X, W0, A, B, dY = n(M, 136), n(264, 136), n(3, 16, 136), n(3, 264, 16), n(M, 264)
+    plan = ops.adapter_plan(torch.arange(M, device=DEV) % 3, 3)
+    Y, Z = ops.lora_multi_fwd(X, W0, A, B, 0.5, plan)
+    grads = ops.lora_multi_bwd(X, W0, A, B, Z, dY, 0.5, plan)
+    got = {}
+    assert first_call(lambda: got.update(f=ops.lora_multi_fwd(X, W0, A, B, 0.5, plan)), 4) == []
+    assert torch.equal(got["f"][0], Y) and torch.equal(got["f"][1], Z)
+    assert first_call(lambda: got.update(b=ops.lora_multi_bwd(X, W0, A, B, Z, dY, 0.5, plan)), 4) == []
+    assert all(torch.equal(a, b) for a, b in zip(got["b"][:3], grads[:3]))
+
+
+def test_entry_points_as_a_threads_first_call(ops):
+    """With everything in hand before, workspaces too: nothing but the entry point runs in the thread."""
+    L = ops.L
+    M, d, o, r = 1024, 512, 384, 16
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    n = lambda *s: torch.randn(*s, generator=gen, device=DEV).to(BF16)  # noqa: E731
+    X, W0, A, B, dY = n(M, d), n(o, d), n(r, d), n(o, r), n(M, o)
+    ws, stream = torch.zeros(1 << 26, dtype=torch.uint8, device=DEV), int(torch.cuda.current_stream().cuda_stream)
+    Y, Z, dX, dA, dB = (torch.empty_like(t) for t in (dY, n(M, r), X, A, B))
+    sh = L.shape(M, d, o, r, L.dtype_code(X))
+    A3, B3, plan = torch.stack((A, A, A)), torch.stack((B, B, B)), ops.adapter_plan(torch.zeros(M, dtype=torch.int64, device=DEV), 3)
+    ms, few = L.LoraMultiShape(M, d, o, r, 3, L.LORA_BF16), L.LoraMultiShape(20, d, o, r, 3, L.LORA_BF16)
+    plan20 = ops.adapter_plan(torch.zeros(20, dtype=torch.int64, device=DEV), 3)
+    dA3, dB3 = torch.empty_like(A3), torch.empty_like(B3)
+    Xq, Wq = (torch.randint(-127, 128, t.shape, generator=gen, device=DEV, dtype=torch.int8) for t in (X, W0))
+    sx, sw = torch.rand(M, device=DEV), torch.rand(o, device=DEV)
+    calls = {
+        "lora_linear_fwd": lambda: L.lora_linear_fwd(sh, X, W0, A, B, None, 0.5, Y, Z, ws, stream),
+        "lora_linear_bwd": lambda: L.lora_linear_bwd(sh, X, W0, A, B, Z, dY, 0.5, dX, dA, dB, None, ws, stream),
+        "w8a8_lora_fwd": lambda: L.w8a8_lora_fwd(M, d, o, r, Xq, sx, Wq, sw, Z, B, 0.5, None, Y, None, ws, stream),
+        "lora_multi_fwd": lambda: L.lora_multi_fwd(ms, X, W0, A3, B3, None, 0.5, plan.buffer, Y, Z, ws, stream),
+        "few rows": lambda: L.lora_multi_fwd(few, X, W0, A3, B3, None, 0.5, plan20.buffer, Y, Z, ws, stream),
+        "lora_multi_bwd": lambda: L.lora_multi_bwd(ms, X, W0, A3, B3, Z, dY, 0.5, plan.buffer, dX, dA3, dB3, None, ws, stream),
+    }
+    for call in calls.values():
+        call()
+    torch.cuda.synchronize()
+    assert {k: first_call(f, 1) for k, f in calls.items()} == {k: [] for k in calls}
